@@ -2,14 +2,23 @@
 on AMD MI355X.
 
 The computation lives in the HIP library ``libozgemm.so`` (C-ABI in
-``include/ozgemm.h``); :mod:`.ozgemm` is its ctypes binding and
-:mod:`.synthetic` draws seeded inputs.  Importing the package loads nothing;
-the library is opened on first use and its absence is an error.
+``include/ozgemm.h``); :mod:`.ozgemm` is its ctypes binding,
+:mod:`.synthetic` draws seeded inputs and :mod:`.layers` holds the products
+of expert layers on torch tensors.  Importing the package loads nothing; the
+library is opened on first use and its absence is an error.
 """
 from . import ozgemm  # noqa: F401
 from .ozgemm import OzgemmError  # noqa: F401
 
-__all__ = ["ozgemm", "OzgemmError", "dgemm_colmajor"]
+__all__ = ["ozgemm", "OzgemmError", "dgemm_colmajor", "grouped_linear", "grouped_linear_grads"]
+
+
+def __getattr__(name):
+    # torch is imported with the first use of a function that takes tensors
+    if name in ("grouped_linear", "grouped_linear_grads"):
+        from . import layers
+        return getattr(layers, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def dgemm_colmajor(A_cm, B_cm, m: int, n: int, q: int, s: int, C_cm=None):

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "oz_internal.h"
+#include "products.h"
 
 namespace oz {
 namespace {
@@ -803,6 +804,9 @@ int noalloc_scratch(char** out) {
 }
 
 }  // namespace
+
+int record_hip_error(hipError_t err) { return hip_fail(err); }
+
 }  // namespace oz
 
 using namespace oz;

@@ -1,0 +1,67 @@
+// Internal declarations of the grouped products and the orthogonalisation.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/ozgemm.h"
+
+namespace oz {
+
+inline size_t elem_bytes(int type) {
+  return type == OZGEMM_F64 ? 8 : type == OZGEMM_F32 ? 4 : 2;
+}
+
+inline size_t up(size_t x, size_t r) { return (x + r - 1) / r * r; }
+
+// An operand of a 16-bit product as the kernels read it.
+struct Operand16 {
+  const uint16_t* p;
+  long ld;     // elements between rows (K-contiguous) or between k (K-strided)
+  long batch;  // elements between the matrices of two groups (0: one matrix for all)
+  long plane;  // elements between the two slices (0: one slice)
+  bool ks;     // K-strided
+  long last;   // entries that may be read of the last row (K-strided: of the last k)
+  const int32_t* ex;  // exponents of the rows (nullptr: none), ex_batch apart between groups
+  long ex_batch;
+};
+
+struct Grouped16 {
+  Operand16 A, B;
+  int bf16;   // the slices' type: 1 bfloat16, 0 half
+  int nprod;  // 1, or 3 for two slices each
+  int m, n, q, groups;
+  const int32_t* offsets;
+  void* C;
+  int ctype;
+  long ldc, cbatch;
+};
+
+// Whether the launches below have at most 2^31 - 1 tiles.
+bool grouped_n_fits(const Grouped16& g);
+bool grouped_k_fits(const Grouped16& g);
+// C(:, J_e) = A_e B(:, J_e): B's rows are the n columns of the call.
+hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st);
+// C_e (m x q) = sum over j in J_e: A's and B's inner dimension is the n columns.
+hipError_t launch_grouped_k(const Grouped16& g, hipStream_t st);
+
+// slices.hip ---------------------------------------------------------------
+// Operands laid out for the 16-bit products: K-contiguous planes whose rows
+// are padded with zeros to a multiple of 64.
+
+// rows x K, element (r, k) at src[r ld + k]; `batches` of them, `sbatch` apart
+hipError_t launch_slice_rows(int type, const void* src, long ld, long sbatch, int batches, int rows, int K,
+                             uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st);
+// element (r, k) at src[k ld + r], `batches` of them, `sbatch` apart
+hipError_t launch_slice_cols(int type, const void* src, long ld, long sbatch, int batches, int rows, int K,
+                             uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st);
+// element (r, k) at src[k ld + r], k in groups that begin at offsets[e]; group
+// e's rows begin at 64 x (its 64-tiles before); ex[e rows + r]
+hipError_t launch_slice_groups(int type, const void* src, long ld, int rows, int n, const int32_t* offsets,
+                               int groups, uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st);
+
+// Keep the name of a HIP error for ozgemm_strerror and return OZGEMM_HIP_ERROR.
+int record_hip_error(hipError_t err);
+
+}  // namespace oz

@@ -1,0 +1,221 @@
+// One output tile of a product of 16-bit operands on gfx950 matrix cores:
+//   acc[i][j] = sum over k of A[i][k] B[j][k]
+// with the accumulators in FP32.  Shared by the grouped products
+// (gemm16.hip) and the Newton-Schulz steps (ortho.hip).
+//
+// An operand lies "K-contiguous" (row i at i ld, its entries next to each
+// other) or "K-strided" (entry (i, k) at k ld + i).  K slices of 64 entries
+// go from HBM straight into LDS (16 bytes per lane) through two buffers, in
+// the operand's own order; a K-strided tile is transposed on its way from
+// LDS into registers (ds_read_b64_tr_b16: 16 lanes read 4 x 16 entries and
+// each receives a column of 4).  The loads carry a range check: what lies
+// past the operand's end arrives as zero, and entries past the inner
+// dimension of a K-contiguous row are sent past the end, so ragged edges
+// cost no branch and never meet their neighbours' values.
+//
+// An operand may come as two slices (hi + lo, see slices.hip); three slice
+// products lo hi, hi lo, hi hi (smallest first) are then walked as one long
+// K loop into the same accumulators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace oz {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+
+struct Half {
+  static __device__ __forceinline__ v4f mfma(v8s a, v8s b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  }
+};
+struct Bfloat {
+  static __device__ __forceinline__ v4f mfma(v8s a, v8s b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0,
+                                                   0);
+  }
+};
+
+// Where one operand's tile begins and what may be read from there on.
+struct Source16 {
+  const uint16_t* base;  // first entry of the tile at k = 0
+  long plane;            // distance to the second slice
+  long entries;          // entries from `base` to the end of what may be read
+  int ld;
+};
+
+constexpr int BK16 = 64;  // K entries per slice: 128 bytes of a K-contiguous row
+
+// Largest leading dimension the 32-bit offsets within a tile allow:
+// 256 rows of 2 ld bytes stay below 2^30.
+constexpr long LD16_MAX = 1L << 21;
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+
+// This wave's LDS reads are done and its loads into LDS have landed; then
+// every wave's.
+__device__ __forceinline__ void slice_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  wait_loads<0>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <class T, int BM, int BN, int WM, int WN, bool AKS, bool BKS>
+struct Tile16 {
+  static constexpr int NW = WM * WN, WAVES_N = WN;
+  static constexpr int THREADS = NW * 64;
+  static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+  static constexpr int A_BYTES = BM * BK16 * 2, B_BYTES = BN * BK16 * 2;
+  static constexpr int BUF = A_BYTES + B_BYTES;
+  static constexpr int SMEM = 2 * BUF;
+  static constexpr int A_LOADS = A_BYTES / 1024 / NW, B_LOADS = B_BYTES / 1024 / NW;
+  static_assert(A_LOADS * NW * 1024 == A_BYTES && B_LOADS * NW * 1024 == B_BYTES, "whole wave loads");
+  static_assert(FM * WM * 16 == BM && FN * WN * 16 == BN, "whole matrix-core tiles");
+
+  // K-contiguous rows of 128 bytes: 16-byte chunk c of row r sits at chunk
+  // c ^ swz(r), so that the 16 rows of an operand read fall in different
+  // 16-byte bank slots (as in the int8 product).
+  static __device__ __forceinline__ int swz(int row) { return ((row >> 1) ^ (row << 2)) & 7; }
+
+  // K-strided rows of ROWS 16-bit entries (one row per k): 32-byte piece p of
+  // row k sits at piece p ^ kswz(k).  A transposing read takes 8 rows k (0..3
+  // and 8..11 past a multiple of 4) of one piece per 32 lanes; kswz sends
+  // them to 8 different bank slots.
+  template <int ROWS>
+  static __device__ __forceinline__ int kswz(int k) {
+    return ROWS >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
+  }
+
+  // The loads of one operand.  Within a slice, wave load number blk fills
+  // LDS bytes [blk 1024, + 1024).
+  template <int ROWS, bool KS, int LOADS>
+  struct Loader {
+    Source16 s;
+    int off[2];  // lane's byte offset in an even and an odd load (K-contiguous)
+    int kin[2];  // lane's first k within the slice
+    int lane, wave;
+
+    __device__ __forceinline__ void init(const Source16& src, int lane_, int wave_) {
+      s = src;
+      lane = lane_;
+      wave = wave_;
+      if (!KS) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int r = lane >> 3, c = (lane & 7) ^ swz(p * 8 + r);
+          off[p] = (r * s.ld + c * 8) * 2;
+          kin[p] = c * 8;
+        }
+      }
+    }
+
+    // slice at k0 of an inner dimension of q entries, from slice plane `hi` (0) or `lo` (1)
+    __device__ __forceinline__ void load(int plane, int k0, int q, char* lds) const {
+      const long skip = KS ? (long)k0 * s.ld : (long)k0;
+      const long left = (s.entries - skip) * 2;
+      const uint16_t* p = s.base + plane * s.plane + skip;
+      const int records = (int)(left < 0 ? 0 : left > 0x7fffffffL ? 0x7fffffffL : left);
+      const __amdgpu_buffer_rsrc_t rsrc =
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, records, 0x00020000);
+      int base[2] = {0, 0};
+      if (!KS) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) base[e] = kin[e] < q - k0 ? off[e] : (int)0x80000000;
+      }
+#pragma unroll
+      for (int li = 0; li < LOADS; ++li) {
+        const int blk = wave * LOADS + li;
+        int voff;
+        if (KS) {
+          constexpr int CPR = ROWS / 8;         // 16-byte chunks per row
+          constexpr int KPL = 64 / CPR;         // rows k per wave load
+          const int k = blk * KPL + lane / CPR;
+          const int c = (lane % CPR) ^ (kswz<ROWS>(k) << 1);
+          voff = (k * s.ld + c * 8) * 2;
+        } else {
+          voff = base[blk & 1] + blk * 16 * s.ld;
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + blk * 1024),
+                                                 16, voff, 0, 0, 0);
+      }
+    }
+  };
+
+  // 16 rows x 32 k of an operand: lane l gets row l mod 16, k = 8 (l / 16) .. + 7
+  template <int ROWS, bool KS>
+  static __device__ __forceinline__ v8s fragment(const char* lds, int lane, int row0, int ks) {
+    if (!KS) {
+      const int row = row0 + (lane & 15);
+      const int c = (ks * 4 + (lane >> 4)) ^ swz(row);
+      return *reinterpret_cast<const v8s*>(lds + row * 128 + c * 16);
+    } else {
+      const int k = ks * 32 + 8 * (lane >> 4) + ((lane & 15) >> 2);
+      const char* p = lds + k * (ROWS * 2) + (((row0 >> 4) ^ kswz<ROWS>(k)) << 5) + (lane & 3) * 8;
+      typedef __attribute__((address_space(3))) v4s* lds4;
+      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p));
+      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * ROWS * 2));
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+
+  // The whole product of one tile; nprod is 1, or 3 for operands in two slices.
+  static __device__ __forceinline__ void run(v4f (&acc)[FM][FN], char* smem, const Source16& A, const Source16& B,
+                                             int q, int nprod) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    Loader<BM, AKS, A_LOADS> la;
+    Loader<BN, BKS, B_LOADS> lb;
+    la.init(A, lane, wave);
+    lb.init(B, lane, wave);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    const int nk = (q + BK16 - 1) / BK16;
+    const int total = nk * nprod;
+    int u = 0, kt = 0;  // the slice to load next
+    auto load = [&](int buf) {
+      char* d = smem + buf * BUF;
+      la.load(nprod == 3 && u == 0, kt * BK16, q, d);
+      lb.load(nprod == 3 && u == 1, kt * BK16, q, d + A_BYTES);
+      if (++kt == nk) {
+        kt = 0;
+        ++u;
+      }
+    };
+    if (total > 0) load(0);
+    for (int t = 0; t < total; ++t) {
+      slice_barrier();
+      if (t + 1 < total) load((t + 1) & 1);
+      const char* As = smem + (t & 1) * BUF;
+      const char* Bs = As + A_BYTES;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        v8s b[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) b[j] = fragment<BN, BKS>(Bs, lane, wn * (BN / WN) + j * 16, ks);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const v8s a = fragment<BM, AKS>(As, lane, wm * (BM / WM) + i * 16, ks);
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = T::mfma(a, b[j], acc[i][j]);
+        }
+      }
+    }
+  }
+};
+
+}  // namespace oz

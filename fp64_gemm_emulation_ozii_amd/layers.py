@@ -1,0 +1,142 @@
+"""Products of expert layers on torch tensors (row-major): the calls of
+:mod:`.ozgemm` with their shapes, strides and types taken from the tensors.
+
+Nothing here is recorded by autograd: the gradients are calls of their own.
+Work goes on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import ozgemm as L
+
+_TYPES = {torch.float64: L.OZGEMM_F64, torch.float32: L.OZGEMM_F32, torch.bfloat16: L.OZGEMM_BF16,
+          torch.float16: L.OZGEMM_F16}
+
+
+def _type_of(t, what: str, allowed=(torch.float32, torch.bfloat16, torch.float16)) -> int:
+    if t.dtype not in allowed:
+        raise TypeError(f"{what}: {t.dtype} is not supported (one of {', '.join(map(str, allowed))})")
+    return _TYPES[t.dtype]
+
+
+def _no_grad(*tensors) -> None:
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise RuntimeError("this call is not recorded by autograd: make it under torch.no_grad() and take the "
+                           "gradients from grouped_linear_grads")
+
+
+def _rows(t, what: str):
+    """A 2-d tensor with its rows' entries next to each other, and their distance."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions, got {tuple(t.shape)}")
+    n, q = t.shape
+    if (q > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < max(1, q)):
+        t = t.contiguous()
+    return t, max(1, q, t.stride(0) if n > 1 else 0)
+
+
+def _weights(W):
+    """(tensor, transa, lda, stridea) of weights [g, m, q] as op(A_e) = W[e]:
+    in place when either q or m runs contiguously, otherwise from a copy."""
+    if W.dim() != 3:
+        raise ValueError(f"the weights must have three dimensions [groups, out, in], got {tuple(W.shape)}")
+    g, m, q = W.shape
+    s0, s1, s2 = W.stride()
+    s0 = s0 if g > 1 else 0
+    if (q <= 1 or s2 == 1) and (m <= 1 or s1 >= max(1, q)):
+        return W, 1, max(1, q, s1 if m > 1 else 0), s0
+    if (m <= 1 or s1 == 1) and (q <= 1 or s2 >= max(1, m)):
+        return W, 0, max(1, m, s2 if q > 1 else 0), s0
+    W = W.contiguous()
+    return W, 1, max(1, q), m * q
+
+
+def _offsets(offsets, groups: int, device):
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != groups + 1:
+        raise ValueError(f"offsets must be {groups + 1} int32 values, got {offsets.dtype} {tuple(offsets.shape)}")
+    if offsets.device != device:
+        raise ValueError(f"offsets are on {offsets.device}, the operands on {device}")
+    return offsets.contiguous()
+
+
+def _same(a, b, what: str) -> None:
+    if a.dtype != b.dtype or a.device != b.device:
+        raise ValueError(f"{what} are {a.dtype} on {a.device} and {b.dtype} on {b.device}")
+
+
+def _target(out, shape, dtypes, like, what: str):
+    """The tensor a result goes to: `out`, checked, or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtypes[0], device=like.device)
+    if tuple(out.shape) != tuple(shape) or out.dtype not in dtypes or out.device != like.device:
+        raise ValueError(f"{what} must be {tuple(shape)} of {dtypes[0]} on {like.device}, got {tuple(out.shape)} of "
+                         f"{out.dtype} on {out.device}")
+    s = out.stride()
+    if (out.shape[-1] > 1 and s[-1] != 1) or (out.shape[-2] > 1 and s[-2] < max(1, out.shape[-1])) or (
+            out.dim() == 3 and out.shape[0] > 1 and s[0] < max(1, out.shape[1]) * max(s[1], out.shape[2])):
+        raise ValueError(f"{what} must have its rows' entries next to each other and its rows apart, strides {s}")
+    return out
+
+
+def _ld(t) -> int:
+    return max(1, t.shape[-1], t.stride(-2) if t.shape[-2] > 1 else 0)
+
+
+def grouped_linear(X, W, offsets, out=None, out_dtype=None):
+    """``Y[j] = W[e] @ X[j]`` for the rows j of every group e:
+    ``offsets[e] <= j < offsets[e + 1]``.
+
+    X is [n, q], W [g, m, q] (either inner dimension contiguous), offsets
+    int32 [g + 1] on the device, Y [n, m] in X's type or float32
+    (``out_dtype``).  Rows of no group are left as they were in ``out``;
+    without ``out`` they are not written.
+    """
+    _same(X, W, "X and W")
+    _no_grad(X, W)
+    t = _type_of(X, "grouped_linear")
+    if X.dim() != 2 or W.dim() != 3 or X.shape[1] != W.shape[2]:
+        raise ValueError(f"X {tuple(X.shape)} and W {tuple(W.shape)} do not go together")
+    g, m, q = W.shape
+    n = X.shape[0]
+    offsets = _offsets(offsets, g, X.device)
+    Y = _target(out, (n, m), (X.dtype, torch.float32) if out is not None else (out_dtype or X.dtype,), X, "out")
+    if Y.dtype not in (X.dtype, torch.float32):
+        raise TypeError(f"grouped_linear: results are {X.dtype} or float32, not {Y.dtype}")
+    with torch.cuda.device(X.device):
+        X, ldb = _rows(X, "X")
+        W, transa, lda, stridea = _weights(W)
+        L.ozgemm_grouped_gemm(t, _TYPES[Y.dtype], g, m, n, q, transa, W, lda, stridea, X, ldb, offsets, Y, _ld(Y))
+    return Y
+
+
+def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
+    """The gradients of :func:`grouped_linear`: ``dX[j] = W[e]^T @ dY[j]`` and
+    ``dW[e] = sum over j of dY[j] X[j]^T``; returns (dX, dW).
+
+    dX is [n, q] in X's type (rows of no group as in ``out`` there), dW
+    [g, m, q] in X's type or float32 (``dw_dtype``), zeros for a group
+    without rows.
+    """
+    _same(X, W, "X and W")
+    _same(dY, X, "dY and X")
+    t = _type_of(X, "grouped_linear_grads")
+    _no_grad(dY, X, W)
+    if X.dim() != 2 or W.dim() != 3 or dY.dim() != 2 or X.shape[1] != W.shape[2] or (
+            dY.shape != (X.shape[0], W.shape[1])):
+        raise ValueError(f"dY {tuple(dY.shape)}, X {tuple(X.shape)} and W {tuple(W.shape)} do not go together")
+    g, m, q = W.shape
+    n = X.shape[0]
+    offsets = _offsets(offsets, g, X.device)
+    dX = _target(dX, (n, q), (X.dtype,), X, "dX")
+    dW = _target(dW, (g, m, q), (X.dtype, torch.float32) if dW is not None else (dw_dtype or X.dtype,), X, "dW")
+    if dW.dtype not in (X.dtype, torch.float32):
+        raise TypeError(f"grouped_linear_grads: dW is {X.dtype} or float32, not {dW.dtype}")
+    with torch.cuda.device(X.device):
+        X, ldx = _rows(X, "X")
+        dY, ldy = _rows(dY, "dY")
+        W, transa, lda, stridea = _weights(W)
+        L.ozgemm_grouped_gemm(t, t, g, q, n, m, 1 - transa, W, lda, stridea, dY, ldy, offsets, dX, _ld(dX))
+        L.ozgemm_grouped_outer(t, _TYPES[dW.dtype], g, q, m, n, X, ldx, dY, ldy, offsets, dW, _ld(dW),
+                               max(dW.stride(0) if g > 1 else 0, _ld(dW) * m))
+    return dX, dW

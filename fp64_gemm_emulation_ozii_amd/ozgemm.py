@@ -39,6 +39,11 @@ OZGEMM_S1_RN = 0
 OZGEMM_S1_HYBRID = 1
 OZGEMM_S1_K_MAX = 16
 OZGEMM_S1_MAX_OUT = 136
+OZGEMM_F64 = 0
+OZGEMM_F32 = 1
+OZGEMM_BF16 = 2
+OZGEMM_F16 = 3
+OZGEMM_GROUPS_MAX = 65536
 
 #: every symbol the header declares
 EXPORTS = (
@@ -49,6 +54,8 @@ EXPORTS = (
     "ozgemm_scheme1_stage_split", "ozgemm_scheme1_stage_products", "ozgemm_scheme1_stage_accumulate",
     "ozgemm_set_bound", "ozgemm_bound_budget", "ozgemm_gemm_parts", "ozgemm_phase_calls",
     "ozgemm_dgemm_noalloc", "ozgemm_set_panels", "ozgemm_mfma_ceiling",
+    "ozgemm_grouped_gemm", "ozgemm_grouped_gemm_workspace_bytes", "ozgemm_grouped_outer",
+    "ozgemm_grouped_outer_workspace_bytes",
 )
 
 _lib = None
@@ -103,6 +110,13 @@ def lib():
         "ozgemm_scheme1_stage_products": (c_int, [c_int, c_int, c_int, c_int, c_int, vp, vp, vp]),
         "ozgemm_scheme1_stage_accumulate": (c_int, [c_int, c_int, c_int, c_int, c_int, vp, vp, vp, vp, c_int]),
     }
+    ll = ctypes.c_longlong
+    sig.update({
+        "ozgemm_grouped_gemm": (c_int, [c_int] * 7 + [vp, c_int, ll, vp, c_int, vp, vp, c_int, vp, c_size, vp]),
+        "ozgemm_grouped_gemm_workspace_bytes": (c_size, [c_int] * 6 + [vp, c_int, ll, vp, c_int]),
+        "ozgemm_grouped_outer": (c_int, [c_int] * 6 + [vp, c_int, vp, c_int, vp, vp, c_int, ll, vp, c_size, vp]),
+        "ozgemm_grouped_outer_workspace_bytes": (c_size, [c_int] * 5 + [vp, c_int, vp, c_int]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
         fn.restype = res
@@ -344,3 +358,50 @@ def ozgemm_phase_calls():
     buf = (ctypes.c_double * max(4 * n, 1))()
     _check(lib().ozgemm_phase_calls(buf, n, ctypes.byref(calls)), "ozgemm_phase_calls")
     return [list(buf[4 * c:4 * c + 4]) for c in range(n)]
+
+
+# --------------------------------------------------------------------------
+# products over ragged groups (raw C-ABI signatures; column-major)
+# --------------------------------------------------------------------------
+
+def _room(workspace, nbytes: int, device):
+    """(tensor kept alive, pointer, bytes) of a call's workspace: the given
+    one, or one from torch's allocator on the current stream (which hands it
+    out again only to work queued after this call)."""
+    if workspace is not None:
+        return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+    if nbytes == 0:
+        return None, None, 0
+    import torch
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), nbytes
+
+
+def ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, A, lda, stridea, B, ldb) -> int:
+    return int(lib().ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, _ptr(A), lda, stridea,
+                                                         _ptr(B), ldb))
+
+
+def ozgemm_grouped_gemm(type, ctype, groups, m, n, q, transa, A, lda, stridea, B, ldb, offsets, C, ldc,
+                        workspace=None, stream=None, check: bool = True) -> int:
+    """With ``workspace=None`` the bytes the call needs come from torch's
+    allocator; a given workspace (a device tensor) stays the caller's."""
+    need = ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, A, lda, stridea, B, ldb)
+    keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"))
+    st = lib().ozgemm_grouped_gemm(type, ctype, groups, m, n, q, transa, _ptr(A), lda, stridea, _ptr(B), ldb,
+                                   _ptr(offsets), _ptr(C), ldc, ws, nbytes, _stream(stream))
+    return _check(st, "ozgemm_grouped_gemm") if check else st
+
+
+def ozgemm_grouped_outer_workspace_bytes(type, groups, m, q, n, A, lda, B, ldb) -> int:
+    return int(lib().ozgemm_grouped_outer_workspace_bytes(type, groups, m, q, n, _ptr(A), lda, _ptr(B), ldb))
+
+
+def ozgemm_grouped_outer(type, ctype, groups, m, q, n, A, lda, B, ldb, offsets, C, ldc, stridec, workspace=None,
+                         stream=None, check: bool = True) -> int:
+    """Workspace as for :func:`ozgemm_grouped_gemm`."""
+    need = ozgemm_grouped_outer_workspace_bytes(type, groups, m, q, n, A, lda, B, ldb)
+    keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"))
+    st = lib().ozgemm_grouped_outer(type, ctype, groups, m, q, n, _ptr(A), lda, _ptr(B), ldb, _ptr(offsets),
+                                    _ptr(C), ldc, stridec, ws, nbytes, _stream(stream))
+    return _check(st, "ozgemm_grouped_outer") if check else st

@@ -416,6 +416,88 @@ int ozgemm_phase_calls(double *ms_out, int max_calls, int *calls);
  * OZGEMM_HIP_ERROR. */
 int ozgemm_mfma_ceiling(int blocks, int steps, unsigned seed, unsigned *sink, void *hip_stream);
 
+/* ---------------------------------------------------------------------- */
+/* Products over ragged groups, and orthogonalisation by products          */
+/* ---------------------------------------------------------------------- */
+/* What the layers of a mixture of experts and the optimiser of their
+ * matrices need next to C = A B.  Conventions that differ from the calls
+ * above: these calls keep no state and need no ozgemm_config; each takes its
+ * stream (a hipStream_t, NULL for the null stream) and its workspace, so
+ * calls with different workspaces may overlap, from any streams and host
+ * threads, and be captured into graphs.  They allocate nothing, never
+ * synchronise and copy nothing from the host.  The workspace (device memory,
+ * 256-byte aligned) is scratch: its contents do not matter before the call
+ * and mean nothing after it; calls that share one must not overlap.  Device
+ * pointers belong to the current device.
+ *
+ * Element types.  Products of OZGEMM_BF16 and OZGEMM_F16 operands are formed
+ * on matrix cores with FP32 accumulators and rounded once, to nearest-even.
+ * OZGEMM_F32 operands are cut into two half-precision slices per entry on
+ * power-of-two grids by row (of the inner dimension), three slice products
+ * accumulate in FP32: an entry's error is about that of an FP32 product,
+ * |dC| <= (2^-22 + q' 2^-24) (|A||B|) with q' = 3 q / 32 accumulation steps, plus
+ * 2^-38 of the product of the two rows' largest entries per term; a row that
+ * holds Inf or NaN makes the outputs it touches NaN, as in ozgemm_dgemm.
+ * (BF16 and F16 follow the usual rules for Inf and NaN.)  Results do not
+ * depend on the order in which blocks run. */
+#define OZGEMM_F64  0
+#define OZGEMM_F32  1
+#define OZGEMM_BF16 2
+#define OZGEMM_F16  3
+
+#define OZGEMM_GROUPS_MAX 65536 /* most groups of one call */
+
+/* Groups.  n columns, of which group e < groups owns those from offsets[e]
+ * up to offsets[e + 1]; offsets is a DEVICE array of groups + 1 integers in
+ * increasing order (equal neighbours make an empty group) within [0, n].
+ * Columns before offsets[0] and from offsets[groups] on belong to no group.
+ * Offsets out of order or out of range are read as the nearest ordered ones
+ * (running maximum, cut to [0, n]): nothing outside the operands is touched. */
+
+/* C(:, j) = op(A_e) B(:, j) for the columns j of every group e: the product
+ * of a layer of experts (columns are tokens, sorted by expert), and, with
+ * transa turned over and m and q swapped, its gradient for B.
+ *   type    OZGEMM_F32, OZGEMM_BF16 or OZGEMM_F16 (-1)
+ *   op(A_e) m x q; with transa = 0 A_e is m x q (lda >= max(1, m)), with
+ *           transa = 1 it is q x m (lda >= max(1, q)), e.g. the row-major
+ *           [m][q] weight of a linear layer.  A_e begins at A + e stridea
+ *   B       q x n, ldb >= max(1, q);  C  m x n, ldc >= max(1, m), type
+ *           ctype: `type` itself or OZGEMM_F32
+ * Columns of no group are left as they were.  q = 0 gives zeros.  C must not
+ * overlap A or B.  16-bit operands are read in place where rows begin on
+ * 16-byte boundaries and K-contiguous ones (A with transa = 1, B) have q a
+ * multiple of 8, K-strided ones (A with transa = 0) m a multiple of 8; others,
+ * and F32 operands, pass through the workspace.
+ * Errors: -i for argument i; OZGEMM_RANGE for m, n or q above
+ * OZGEMM_MAX_ROWS, groups above OZGEMM_GROUPS_MAX or a grid of more than
+ * 2^31 tiles; OZGEMM_WORKSPACE_TOO_SMALL. */
+int ozgemm_grouped_gemm(int type, int ctype, int groups, int m, int n, int q, int transa,
+                        const void *A, int lda, long long stridea, const void *B, int ldb,
+                        const int32_t *offsets, void *C, int ldc,
+                        void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace the call above needs for these operands (the pointers
+ * are looked at for their alignment alone); 0 where it needs none or the
+ * arguments are invalid.  Host only. */
+size_t ozgemm_grouped_gemm_workspace_bytes(int type, int groups, int m, int n, int q, int transa,
+                                           const void *A, int lda, long long stridea,
+                                           const void *B, int ldb);
+
+/* C_e = sum over the columns j of group e of A(:, j) B(:, j)^T: the gradient
+ * of a layer of experts for its weights.  A is m x n (lda >= max(1, m)), B
+ * q x n (ldb >= max(1, q)), C_e m x q (ldc >= max(1, m)), beginning at
+ * C + e stridec (stridec >= ldc q where groups > 1).  An empty group gives
+ * zeros.  Types, errors and workspace as above; 16-bit operands are read in
+ * place where columns begin on 16-byte boundaries and m and q are multiples
+ * of 8. */
+int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n,
+                         const void *A, int lda, const void *B, int ldb,
+                         const int32_t *offsets, void *C, int ldc, long long stridec,
+                         void *workspace, size_t workspace_bytes, void *hip_stream);
+
+size_t ozgemm_grouped_outer_workspace_bytes(int type, int groups, int m, int q, int n,
+                                            const void *A, int lda, const void *B, int ldb);
+
 #ifdef __cplusplus
 }
 #endif
