@@ -4,18 +4,18 @@ on AMD MI355X.
 The computation lives in the HIP library ``libozgemm.so`` (C-ABI in
 ``include/ozgemm.h``); :mod:`.ozgemm` is its ctypes binding,
 :mod:`.synthetic` draws seeded inputs and :mod:`.layers` holds the products
-of expert layers on torch tensors.  Importing the package loads nothing; the
+of expert layers and the orthogonalisation of updates on torch tensors.  Importing the package loads nothing; the
 library is opened on first use and its absence is an error.
 """
 from . import ozgemm  # noqa: F401
 from .ozgemm import OzgemmError  # noqa: F401
 
-__all__ = ["ozgemm", "OzgemmError", "dgemm_colmajor", "grouped_linear", "grouped_linear_grads"]
+__all__ = ["ozgemm", "OzgemmError", "dgemm_colmajor", "grouped_linear", "grouped_linear_grads", "orthogonalize"]
 
 
 def __getattr__(name):
     # torch is imported with the first use of a function that takes tensors
-    if name in ("grouped_linear", "grouped_linear_grads"):
+    if name in ("grouped_linear", "grouped_linear_grads", "orthogonalize"):
         from . import layers
         return getattr(layers, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

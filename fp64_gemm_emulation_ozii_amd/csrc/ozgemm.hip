@@ -807,6 +807,40 @@ int noalloc_scratch(char** out) {
 
 int record_hip_error(hipError_t err) { return hip_fail(err); }
 
+// Scheme II products inside a caller's region, for paths that are a sequence
+// of them (products.h).  The W_t limbs of one s travel as a kernel argument,
+// so nothing is copied from the host.
+namespace {
+
+struct CrtTable {
+  double w[OZGEMM_S_MAX * MAX_LIMBS];
+};
+
+__global__ __launch_bounds__(128) void crt_table_kernel(CrtTable t, double* __restrict__ out) {
+  if (threadIdx.x < OZGEMM_S_MAX * MAX_LIMBS) out[threadIdx.x] = t.w[threadIdx.x];
+}
+
+}  // namespace
+
+size_t dgemm_region_bytes(int r, int c, int s) {
+  return std::max({make_layout(r, r, c, s).total, make_layout(r, r, r, s).total, make_layout(r, c, r, s).total});
+}
+
+hipError_t dgemm_region_table(char* region, int s, hipStream_t st) {
+  CrtTable t;
+  crt_weights(s, t.w);
+  hipLaunchKernelGGL(crt_table_kernel, dim3(1), dim3(128), 0, st, t, reinterpret_cast<double*>(region));
+  return hipGetLastError();
+}
+
+int dgemm_region(char* region, int m, int n, int q, const double* A, int lda, const double* B, int ldb, double* C,
+                 int ldc, int s, hipStream_t st) {
+  int mp, np, qp;
+  dims(m, n, q, &mp, &np, &qp);
+  const Ctx x{region, make_layout(m, n, q, s), mp, st, OZGEMM_BOUND_CONSERVATIVE};
+  return run_dgemm(x, reinterpret_cast<const double*>(region), m, n, q, A, lda, B, ldb, C, ldc, s, nullptr);
+}
+
 }  // namespace oz
 
 using namespace oz;

@@ -61,6 +61,14 @@ hipError_t launch_slice_cols(int type, const void* src, long ld, long sbatch, in
 hipError_t launch_slice_groups(int type, const void* src, long ld, int rows, int n, const int32_t* offsets,
                                int groups, uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st);
 
+// ozgemm.hip: Scheme II products in a region of a caller's workspace
+// (conservative budget, no configuration; the region holds every product of
+// an r x c matrix's iteration).
+size_t dgemm_region_bytes(int r, int c, int s);
+hipError_t dgemm_region_table(char* region, int s, hipStream_t st);  // once before the products of a call
+int dgemm_region(char* region, int m, int n, int q, const double* A, int lda, const double* B, int ldb, double* C,
+                 int ldc, int s, hipStream_t st);
+
 // Keep the name of a HIP error for ozgemm_strerror and return OZGEMM_HIP_ERROR.
 int record_hip_error(hipError_t err);
 

@@ -3,15 +3,15 @@
 // and for 16-bit operands whose rows do not lie on 16-byte boundaries.
 //
 // FP32 slices.  With 2^(e-1) <= max |x| < 2^e over a row, y = x 2^(15-e) is
-// exact, hi = RN16(y) and lo = RN16(y - hi).  |y - hi| <= 2^-12 2^E for
-// y in [2^E, 2^(E+1)) (11-bit significand), y - hi is exact in FP32, and
-// lo is off by at most 2^-12 of it: hi + lo is y up to 2^-24 relative, as
-// near as FP32 itself holds a value, while |y| >= 2^-3 (half's subnormal
-// spacing is 2^-24); below that up to 2^-25 absolute, 2^-39 of the row's
-// largest entry.  hi hi, hi lo and lo hi give the product up to the dropped
-// lo lo, at most 2^-24 of each term.  The rows' scaling is the library's own
-// (a power of two per row of A and column of B); as there, a row holding
-// Inf or NaN gets OZGEMM_EXP_NONFINITE and zero slices.
+// exact, hi = RN16(y) and lo = RN16(y - hi).  For y in [2^E, 2^(E+1)) half's
+// step is 2^(E-10), so |y - hi| <= 2^(E-11); y - hi is exact in FP32, and lo
+// is off by at most 2^(E-23): hi + lo is y up to 2^-23 relative (FP32 itself
+// rounds to 2^-24) while |y| >= 2^-2, where lo's step is half's smallest,
+// 2^-24; below that up to 2^-25 absolute, 2^-39 of the row's largest entry.
+// hi hi, hi lo and lo hi give the product up to the dropped lo lo, at most
+// 2^-22 of each term.  The rows' scaling is the library's own (a power of two
+// per row of A and column of B); as there, a row holding Inf or NaN gets
+// OZGEMM_EXP_NONFINITE and zero slices.
 //
 // The passes are bound by HBM: each entry is read once (the row maxima of
 // K-contiguous rows twice, the second time from L2) and each plane written

@@ -1,5 +1,5 @@
-"""Products of expert layers on torch tensors (row-major): the calls of
-:mod:`.ozgemm` with their shapes, strides and types taken from the tensors.
+"""Products of expert layers and the orthogonalisation of their updates on
+torch tensors (row-major): the calls of :mod:`.ozgemm` with their shapes, strides and types taken from the tensors.
 
 Nothing here is recorded by autograd: the gradients are calls of their own.
 Work goes on the current stream of the tensors' device.
@@ -140,3 +140,69 @@ def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
         L.ozgemm_grouped_outer(t, _TYPES[dW.dtype], g, q, m, n, X, ldx, dY, ldy, offsets, dW, _ld(dW),
                                max(dW.stride(0) if g > 1 else 0, _ld(dW) * m))
     return dX, dW
+
+
+#: Muon's quintic, for every step
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(G, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7, out=None, s: int = 14):
+    """``steps`` Newton-Schulz steps on every matrix of G [..., rows, cols]:
+    ``X = G / (norm + eps)``, then ``X = a X + (b P + c P P) X`` with
+    ``P = X X^T`` (of the smaller side).
+
+    G is float64, float32, bfloat16 or float16 and the result of its type;
+    ``coeffs`` is one triple (a, b, c) or one for each step.  ``out`` may be G
+    itself.  ``s`` is the number of moduli of the float64 products.
+    """
+    t = _type_of(G, "orthogonalize", tuple(_TYPES))
+    if G.dim() < 2:
+        raise ValueError(f"orthogonalize needs matrices, got {tuple(G.shape)}")
+    if steps < 0:
+        raise ValueError("steps must not be negative")
+    co = list(coeffs)
+    if len(co) == 3 and not any(hasattr(c, "__len__") for c in co):
+        co = [co] * steps
+    elif not all(hasattr(c, "__len__") for c in co):
+        co = []
+    if len(co) != steps or any(len(c) != 3 for c in co):
+        raise ValueError(f"coeffs must be one triple or {steps} of them")
+    if torch.is_grad_enabled() and G.requires_grad:
+        raise RuntimeError("orthogonalize is not recorded by autograd: call it under torch.no_grad()")
+    r, c = G.shape[-2:]
+    if out is None:
+        out = torch.empty(G.shape, dtype=G.dtype, device=G.device)
+    elif out.shape != G.shape or out.dtype != G.dtype or out.device != G.device:
+        raise ValueError(f"out must be {tuple(G.shape)} of {G.dtype} on {G.device}, got {tuple(out.shape)} of "
+                         f"{out.dtype} on {out.device}")
+    if G.numel() == 0:
+        return out
+    with torch.cuda.device(G.device):
+        g = _matrices(G)
+        o = _matrices(out)
+        if o is None:
+            raise ValueError(f"out must be matrices of contiguous rows evenly apart, strides {out.stride()}")
+        if g is None:
+            g = _matrices(G.contiguous())
+        L.ozgemm_orthogonalize(t, g[1], c, r, g[0], g[2], g[3], steps, [v for x in co for v in x], eps, s, o[0], o[2],
+                               o[3])
+    return out
+
+
+def _matrices(t):
+    """(tensor, batch, row distance, matrix distance) of a batch of matrices
+    with contiguous rows, all evenly apart; None if it is none."""
+    r, c = t.shape[-2:]
+    ld = max(1, c, t.stride(-2) if r > 1 else 0)
+    if (c > 1 and t.stride(-1) != 1) or (r > 1 and t.stride(-2) < c):
+        return None
+    batch, step = 1, 0
+    for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if size == 1:
+            continue
+        if batch > 1 and stride != step * batch:
+            return None
+        if batch == 1:
+            step = stride
+        batch *= size
+    return t, batch, ld, step

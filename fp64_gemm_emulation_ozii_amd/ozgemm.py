@@ -44,6 +44,8 @@ OZGEMM_F32 = 1
 OZGEMM_BF16 = 2
 OZGEMM_F16 = 3
 OZGEMM_GROUPS_MAX = 65536
+OZGEMM_ORTHO_MAX = 65536
+OZGEMM_ORTHO_STEPS_MAX = 64
 
 #: every symbol the header declares
 EXPORTS = (
@@ -55,7 +57,7 @@ EXPORTS = (
     "ozgemm_set_bound", "ozgemm_bound_budget", "ozgemm_gemm_parts", "ozgemm_phase_calls",
     "ozgemm_dgemm_noalloc", "ozgemm_set_panels", "ozgemm_mfma_ceiling",
     "ozgemm_grouped_gemm", "ozgemm_grouped_gemm_workspace_bytes", "ozgemm_grouped_outer",
-    "ozgemm_grouped_outer_workspace_bytes",
+    "ozgemm_grouped_outer_workspace_bytes", "ozgemm_orthogonalize", "ozgemm_orthogonalize_workspace_bytes",
 )
 
 _lib = None
@@ -115,6 +117,9 @@ def lib():
         "ozgemm_grouped_gemm": (c_int, [c_int] * 7 + [vp, c_int, ll, vp, c_int, vp, vp, c_int, vp, c_size, vp]),
         "ozgemm_grouped_gemm_workspace_bytes": (c_size, [c_int] * 6 + [vp, c_int, ll, vp, c_int]),
         "ozgemm_grouped_outer": (c_int, [c_int] * 6 + [vp, c_int, vp, c_int, vp, vp, c_int, ll, vp, c_size, vp]),
+        "ozgemm_orthogonalize": (c_int, [c_int] * 4 + [vp, c_int, ll, c_int, ctypes.POINTER(ctypes.c_double),
+                                         ctypes.c_double, c_int, vp, c_int, ll, vp, c_size, vp]),
+        "ozgemm_orthogonalize_workspace_bytes": (c_size, [c_int] * 5),
         "ozgemm_grouped_outer_workspace_bytes": (c_size, [c_int] * 5 + [vp, c_int, vp, c_int]),
     })
     for name, (res, args) in sig.items():
@@ -405,3 +410,19 @@ def ozgemm_grouped_outer(type, ctype, groups, m, q, n, A, lda, B, ldb, offsets, 
     st = lib().ozgemm_grouped_outer(type, ctype, groups, m, q, n, _ptr(A), lda, _ptr(B), ldb, _ptr(offsets),
                                     _ptr(C), ldc, stridec, ws, nbytes, _stream(stream))
     return _check(st, "ozgemm_grouped_outer") if check else st
+
+
+def ozgemm_orthogonalize_workspace_bytes(type, batch, m, n, s) -> int:
+    return int(lib().ozgemm_orthogonalize_workspace_bytes(type, batch, m, n, s))
+
+
+def ozgemm_orthogonalize(type, batch, m, n, G, ldg, strideg, steps, coeffs, eps, s, O, ldo, strideo, workspace=None,
+                         stream=None, check: bool = True) -> int:
+    """``coeffs``: 3 * steps host numbers.  Workspace as for
+    :func:`ozgemm_grouped_gemm`."""
+    co = (ctypes.c_double * max(3 * steps, 1))(*coeffs) if coeffs is not None else None
+    need = ozgemm_orthogonalize_workspace_bytes(type, batch, m, n, s)
+    keep, ws, nbytes = _room(workspace, need, getattr(G, "device", "cuda"))
+    st = lib().ozgemm_orthogonalize(type, batch, m, n, _ptr(G), ldg, strideg, steps, co, eps, s, _ptr(O), ldo,
+                                    strideo, ws, nbytes, _stream(stream))
+    return _check(st, "ozgemm_orthogonalize") if check else st

@@ -433,11 +433,12 @@ int ozgemm_mfma_ceiling(int blocks, int steps, unsigned seed, unsigned *sink, vo
  * Element types.  Products of OZGEMM_BF16 and OZGEMM_F16 operands are formed
  * on matrix cores with FP32 accumulators and rounded once, to nearest-even.
  * OZGEMM_F32 operands are cut into two half-precision slices per entry on
- * power-of-two grids by row (of the inner dimension), three slice products
- * accumulate in FP32: an entry's error is about that of an FP32 product,
- * |dC| <= (2^-22 + q' 2^-24) (|A||B|) with q' = 3 q / 32 accumulation steps, plus
- * 2^-38 of the product of the two rows' largest entries per term; a row that
- * holds Inf or NaN makes the outputs it touches NaN, as in ozgemm_dgemm.
+ * power-of-two grids by row (of the inner dimension); three slice products
+ * accumulate in FP32.  An entry's error is that of an FP32 product in blocks:
+ * the slices hold an entry to 2^-23 and the products drop at most 2^-22 of a
+ * term (2^-39 of the row's largest entry where that is more), under the
+ * rounding of the FP32 sums.  A row that holds Inf or NaN makes the outputs
+ * it touches NaN, as in ozgemm_dgemm.
  * (BF16 and F16 follow the usual rules for Inf and NaN.)  Results do not
  * depend on the order in which blocks run. */
 #define OZGEMM_F64  0
@@ -497,6 +498,40 @@ int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n,
 
 size_t ozgemm_grouped_outer_workspace_bytes(int type, int groups, int m, int q, int n,
                                             const void *A, int lda, const void *B, int ldb);
+
+/* O = the result of `steps` Newton-Schulz steps on every m x n matrix G of a
+ * batch:  X = G / (|G|_F + eps), then with P = X X^T (X^T X where m > n)
+ *         X <- a X + (b P + c P^2) X     (X <- a X + X (b P + c P^2)),
+ * the polynomial that takes X's singular values towards 1 and leaves its
+ * singular vectors: the orthogonalised update of the Muon optimiser, with
+ * (a, b, c) = (3.4445, -4.7750, 2.0315) five times.
+ *   type    OZGEMM_F64, F32, BF16 or F16: G's and O's
+ *   G, O    batches of column-major m x n matrices strideg, strideo apart; a
+ *           row-major [n][m] array is the same thing and is orthogonalised as
+ *           such.  O may be G itself (with its ldg and strideg), and must not
+ *           overlap it otherwise.  strideg may be 0
+ *   coeffs  HOST array of 3 steps numbers a, b, c, read before the call
+ *           returns; |.| < 1e6
+ *   s       moduli of the Scheme II products of OZGEMM_F64 (conservative
+ *           budget whatever ozgemm_set_bound says); not looked at otherwise
+ * The states between the products keep 22 bits or more (F64: 53); BF16
+ * products are formed from 11-bit operands, F16 and F32 ones as the grouped
+ * products of F32 operands are.  steps = 0 gives the normalised G.  A matrix
+ * of zeros gives zeros where eps > 0 (NaN where it is 0); one that holds Inf
+ * or NaN gives NaN throughout (steps > 0).
+ * Errors: -i for argument i; OZGEMM_RANGE for m or n above OZGEMM_ORTHO_MAX,
+ * batch above 65535, coefficients whose steps may leave 1e18, or an s that
+ * leaves no bits; OZGEMM_WORKSPACE_TOO_SMALL. */
+#define OZGEMM_ORTHO_MAX 65536
+#define OZGEMM_ORTHO_STEPS_MAX 64
+int ozgemm_orthogonalize(int type, int batch, int m, int n, const void *G, int ldg, long long strideg,
+                         int steps, const double *coeffs, double eps, int s,
+                         void *O, int ldo, long long strideo,
+                         void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace the call above needs; 0 for invalid or empty arguments.
+ * Host only. */
+size_t ozgemm_orthogonalize_workspace_bytes(int type, int batch, int m, int n, int s);
 
 #ifdef __cplusplus
 }

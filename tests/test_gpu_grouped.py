@@ -5,11 +5,13 @@ and P = (|A||B|) the product of the absolute values:
   16-bit operands: products of two entries are exact in FP32; q additions, each
     off by at most one step (2^-23) of a partial sum <= P, whatever order and
     rounding the matrix cores use:           u |C| + q 2^-23 P
-  FP32 operands: each entry is two half slices, off by <= 2^-24 of itself or
-    2^-40 of its row's largest entry (half of half's smallest step under a grid
-    maximum of 2^15); the dropped product of the low slices <= 2^-24 of a term;
-    3 q additions of terms whose absolute sum is <= P (1 + 2^-10):
-                      2^-24 |C| + (3 + 6.01 q) 2^-24 P + 4 q 2^-40 max max
+  FP32 operands: each entry is two half slices.  Half's step in [2^E, 2^(E+1))
+    is 2^(E-10), so hi is off by <= 2^(E-11), and lo, below 2^(E-11), by
+    <= 2^(E-23): 2^-23 relative for each operand, or 2^-40 of the row's largest
+    entry (half of half's smallest step under a grid maximum of 2^15).  The
+    dropped lo lo is <= 2^-22 of a term.  Together 2^-23 + 2^-23 + 2^-22 = 8 2^-24
+    of P; 3 q additions of terms whose absolute sum is <= P (1 + 2^-10), 2^-23 each:
+                      2^-24 |C| + (8 + 6.01 q) 2^-24 P + 4 q 2^-40 max max
   plus the type's smallest step for results below its normal range.
 Whole numbers whose sums stay below 2^24 have to come out exactly.
 """
@@ -29,7 +31,7 @@ TINY = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -24, torch.float32: 2
 def bound(C, P, q, operand, result, big=0.0):
     u = torch.finfo(result).eps / 2
     if operand == torch.float32:
-        return u * C.abs() + (3 + 6.01 * q) * 2.0 ** -24 * P + 4 * q * 2.0 ** -40 * big + TINY[result]
+        return u * C.abs() + (8 + 6.01 * q) * 2.0 ** -24 * P + 4 * q * 2.0 ** -40 * big + TINY[result]
     return u * C.abs() + q * 2.0 ** -23 * P + TINY[result]
 
 

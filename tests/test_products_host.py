@@ -101,3 +101,50 @@ def test_grouped_linear_refusals(change, error):
 def test_grouped_linear_grads_refusals(change, error):
     with pytest.raises(error):
         oz.grouped_linear_grads(**_args(**{"dY": torch.zeros(10, 4), **change}))
+
+
+def ortho(type=L.OZGEMM_F32, batch=2, m=64, n=32, G=A, ldg=64, strideg=64 * 32, steps=5, co=(3.4445, -4.775, 2.0315),
+          eps=1e-7, s=14, O=C, ldo=64, strideo=64 * 32, ws=WS, nbytes=1 << 33):
+    import ctypes
+    c = None if co is None else (ctypes.c_double * max(1, 3 * steps))(*(list(co) * steps))
+    return L.lib().ozgemm_orthogonalize(type, batch, m, n, G, ldg, strideg, steps, c, eps, s, O, ldo, strideo, ws,
+                                        nbytes, None)
+
+
+@pytest.mark.parametrize("change, status", [
+    (dict(type=4), -1), (dict(type=-1), -1), (dict(batch=-1), -2), (dict(m=-1), -3), (dict(n=-1), -4),
+    (dict(G=None), -5), (dict(ldg=63), -6), (dict(strideg=-1), -7), (dict(steps=-1, co=None), -8),
+    (dict(steps=L.OZGEMM_ORTHO_STEPS_MAX + 1), -8), (dict(co=None), -9), (dict(co=(1e6, 0, 0)), -9),
+    (dict(co=(float("nan"), 0, 0)), -9), (dict(eps=-1.0), -10), (dict(eps=float("nan")), -10),
+    (dict(eps=float("inf")), -10), (dict(type=L.OZGEMM_F64, s=0), -11), (dict(type=L.OZGEMM_F64, s=21), -11),
+    (dict(O=None), -12), (dict(ldo=63), -13), (dict(strideo=64 * 32 - 1), -14), (dict(O=A + 4), -12),
+    (dict(O=A, ldo=65, strideo=65 * 32), -12), (dict(O=A + 64 * 32 * 4), -12), (dict(ws=None), -15),
+    (dict(ws=WS + 16), -15), (dict(nbytes=1000), L.OZGEMM_WORKSPACE_TOO_SMALL),
+    (dict(m=L.OZGEMM_ORTHO_MAX + 1, ldg=1 << 20, ldo=1 << 20, strideo=1 << 40), L.OZGEMM_RANGE),
+    (dict(batch=65536), L.OZGEMM_RANGE), (dict(co=(1e5, 0, 0)), L.OZGEMM_RANGE),
+    (dict(type=L.OZGEMM_F64, s=1), L.OZGEMM_RANGE),
+    (dict(batch=0), 0), (dict(m=0), 0), (dict(n=0, G=None, O=None), 0),
+])
+def test_orthogonalize_refusals(change, status):
+    assert ortho(**change) == status
+
+
+def test_orthogonalize_workspace_bytes():
+    w = L.ozgemm_orthogonalize_workspace_bytes
+    assert w(L.OZGEMM_F32, 2, 100, 50, 0) == w(L.OZGEMM_F32, 2, 50, 100, 0) >= 2 * 12 * 100 * 50
+    assert w(L.OZGEMM_BF16, 1, 16384, 16384, 0) > 1 << 32
+    assert w(L.OZGEMM_F64, 1, 512, 512, 14) >= 5 * 512 * 512 * 8 + L.ozgemm_workspace_bytes(512, 512, 512, 14)
+    for bad in ((4, 1, 8, 8, 14), (L.OZGEMM_F32, 0, 8, 8, 14), (L.OZGEMM_F64, 1, 8, 8, 0), (L.OZGEMM_F64, 1, 8, 8, 21)):
+        assert w(*bad) == 0
+
+
+@pytest.mark.parametrize("how, error", [
+    (dict(G=torch.zeros(4)), ValueError), (dict(G=torch.zeros(4, 4, dtype=torch.int32)), TypeError),
+    (dict(steps=-1), ValueError), (dict(coeffs=(1.0, 2.0)), ValueError),
+    (dict(coeffs=[(1.0, 2.0, 3.0)] * 4), ValueError), (dict(out=torch.zeros(4, 5)), ValueError),
+    (dict(out=torch.zeros(8, 8, dtype=torch.float64)), ValueError),
+    (dict(G=torch.zeros(8, 8, requires_grad=True)), RuntimeError),
+])
+def test_orthogonalize_python_refusals(how, error):
+    with pytest.raises(error):
+        oz.orthogonalize(**{"G": torch.zeros(8, 8), **how})
