@@ -120,37 +120,48 @@ struct Tile16 {
       }
     }
 
-    // slice at k0 of an inner dimension of q entries, from slice plane `hi` (0) or `lo` (1)
-    __device__ __forceinline__ void load(int plane, int k0, int q, char* lds) const {
+    __amdgpu_buffer_rsrc_t rsrc;
+    int base[2];  // off, or past the end for a lane whose k lies past the inner dimension
+
+    // The slice at k0 of an inner dimension of q entries, of the high (0) or
+    // low (1) slices; past the last slice (!any) every load brings zeros.
+    __device__ __forceinline__ void aim(int plane, int k0, int q, bool any) {
       const long skip = KS ? (long)k0 * s.ld : (long)k0;
       const long left = (s.entries - skip) * 2;
       const uint16_t* p = s.base + plane * s.plane + skip;
-      const int records = (int)(left < 0 ? 0 : left > 0x7fffffffL ? 0x7fffffffL : left);
-      const __amdgpu_buffer_rsrc_t rsrc =
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, records, 0x00020000);
-      int base[2] = {0, 0};
+      const int records = (int)(!any || left < 0 ? 0 : left > 0x7fffffffL ? 0x7fffffffL : left);
+      rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, records, 0x00020000);
       if (!KS) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) base[e] = kin[e] < q - k0 ? off[e] : (int)0x80000000;
       }
-#pragma unroll
-      for (int li = 0; li < LOADS; ++li) {
-        const int blk = wave * LOADS + li;
-        int voff;
-        if (KS) {
-          constexpr int CPR = ROWS / 8;         // 16-byte chunks per row
-          constexpr int KPL = 64 / CPR;         // rows k per wave load
-          const int k = blk * KPL + lane / CPR;
-          const int c = (lane % CPR) ^ (kswz<ROWS>(k) << 1);
-          voff = (k * s.ld + c * 8) * 2;
-        } else {
-          voff = base[blk & 1] + blk * 16 * s.ld;
-        }
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + blk * 1024),
-                                                 16, voff, 0, 0, 0);
+    }
+
+    __device__ __forceinline__ void load1(int li, char* lds) const {
+      const int blk = wave * LOADS + li;
+      int voff;
+      if (KS) {
+        constexpr int CPR = ROWS / 8;         // 16-byte chunks per row
+        constexpr int KPL = 64 / CPR;         // rows k per wave load
+        const int k = blk * KPL + lane / CPR;
+        const int c = (lane % CPR) ^ (kswz<ROWS>(k) << 1);
+        voff = (k * s.ld + c * 8) * 2;
+      } else {
+        voff = base[blk & 1] + blk * 16 * s.ld;
       }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + blk * 1024), 16,
+                                               voff, 0, 0, 0);
     }
   };
+
+  // Four entries of a column (see above).  The restrict-qualified argument
+  // gives the read an alias scope; without one the compiler takes it to
+  // depend on every load into LDS in flight and waits for them all before it.
+  // What it does depend on is waited for at slice_barrier.
+  static __device__ __forceinline__ v4s read_tr(const char* __restrict__ p) {
+    typedef __attribute__((address_space(3))) v4s* lds4;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
+  }
 
   // 16 rows x 32 k of an operand: lane l gets row l mod 16, k = 8 (l / 16) .. + 7
   template <int ROWS, bool KS>
@@ -162,16 +173,22 @@ struct Tile16 {
     } else {
       const int k = ks * 32 + 8 * (lane >> 4) + ((lane & 15) >> 2);
       const char* p = lds + k * (ROWS * 2) + (((row0 >> 4) ^ kswz<ROWS>(k)) << 5) + (lane & 3) * 8;
-      typedef __attribute__((address_space(3))) v4s* lds4;
-      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p));
-      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * ROWS * 2));
+      const v4s a = read_tr(p), b = read_tr(p + 4 * ROWS * 2);
       return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   }
 
   // The whole product of one tile; nprod is 1, or 3 for operands in two slices.
+  //
+  // Order of a slice t (two steps of 32 k): the MFMAs of a step run in fixed
+  // slots, and after each slot go the LDS reads of the next step's fragments
+  // (an A fragment right after its last use) and, in the second step, the
+  // loads of slice t + 2.  One barrier per slice, before the second step's
+  // MFMAs: by then this wave's reads of buffer t mod 2 are in registers and
+  // its loads of slice t + 1, issued a whole slice earlier, have landed.
   static __device__ __forceinline__ void run(v4f (&acc)[FM][FN], char* smem, const Source16& A, const Source16& B,
                                              int q, int nprod) {
+    constexpr int SLOTS = FM * FN, LPW = A_LOADS + B_LOADS;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -186,33 +203,71 @@ struct Tile16 {
 
     const int nk = (q + BK16 - 1) / BK16;
     const int total = nk * nprod;
+    if (total == 0) return;
     int u = 0, kt = 0;  // the slice to load next
-    auto load = [&](int buf) {
-      char* d = smem + buf * BUF;
-      la.load(nprod == 3 && u == 0, kt * BK16, q, d);
-      lb.load(nprod == 3 && u == 1, kt * BK16, q, d + A_BYTES);
+    auto aim = [&]() {
+      la.aim(nprod == 3 && u == 0, kt * BK16, q, u < nprod);
+      lb.aim(nprod == 3 && u == 1, kt * BK16, q, u < nprod);
       if (++kt == nk) {
         kt = 0;
         ++u;
       }
     };
-    if (total > 0) load(0);
+    auto load1 = [&](int buf, int li) {
+      char* d = smem + buf * BUF;
+      if (li < A_LOADS)
+        la.load1(li, d);
+      else
+        lb.load1(li - A_LOADS, d + A_BYTES);
+    };
+    // fragment f of step ks in buffer buf: f < FN are B's, the rest A's
+    auto read1 = [&](int buf, int ks, int f) -> v8s {
+      const char* As = smem + buf * BUF;
+      if (f < FN) return fragment<BN, BKS>(As + A_BYTES, lane, wn * (BN / WN) + f * 16, ks);
+      return fragment<BM, AKS>(As, lane, wm * (BM / WM) + (f - FN) * 16, ks);
+    };
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      aim();
+#pragma unroll
+      for (int li = 0; li < LPW; ++li) load1(b, li);
+    }
+    wait_loads<LPW>();  // slice 0 (loads return in order)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    v8s cur[FM + FN], nxt[FM + FN];
+#pragma unroll
+    for (int f = 0; f < FM + FN; ++f) cur[f] = read1(0, 0, f);
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+
     for (int t = 0; t < total; ++t) {
-      slice_barrier();
-      if (t + 1 < total) load((t + 1) & 1);
-      const char* As = smem + (t & 1) * BUF;
-      const char* Bs = As + A_BYTES;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        v8s b[FN];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) b[j] = fragment<BN, BKS>(Bs, lane, wn * (BN / WN) + j * 16, ks);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          const v8s a = fragment<BM, AKS>(As, lane, wm * (BM / WM) + i * 16, ks);
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = T::mfma(a, b[j], acc[i][j]);
+        const int rbuf = ks ? (t + 1) & 1 : t & 1;  // (past the end: zeros, not used)
+        if (ks) {
+          slice_barrier();
+          aim();
         }
+#pragma unroll
+        for (int r = 0; r < SLOTS; ++r) {
+          const int i = r / FN, j = r % FN;
+          acc[i][j] = T::mfma(cur[FN + i], cur[j], acc[i][j]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int f = 0; f < FM + FN; ++f) {
+            const int slot = f < FN ? f * (SLOTS / FN) + 1 : (f - FN) * FN + FN - 1;
+            if (slot == r) nxt[f] = read1(rbuf, 1 - ks, f);
+          }
+          if (ks) {
+#pragma unroll
+            for (int li = 0; li < LPW; ++li)
+              if (li * SLOTS / LPW + (SLOTS > LPW) == r) load1(t & 1, li);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (ks) __builtin_amdgcn_s_waitcnt(0xc07f);
+#pragma unroll
+        for (int f = 0; f < FM + FN; ++f) cur[f] = nxt[f];
       }
     }
   }
