@@ -136,11 +136,13 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_n_kernel(Grouped16 g) {
   A.ld = (int)g.A.ld;
   A.plane = g.A.plane;
   A.base = g.A.p + gt.group * g.A.batch + (AKS ? (long)m0 : (long)m0 * g.A.ld);
-  A.entries = AKS ? (long)(g.q - 1) * g.A.ld + g.A.last - m0 : (long)(g.m - 1 - m0) * g.A.ld + g.A.last;
+  A.rows = g.m - m0;
+  A.last = (int)g.A.last - (AKS ? m0 : 0);
   B.ld = (int)g.B.ld;
   B.plane = g.B.plane;
   B.base = g.B.p + (long)n0 * g.B.ld;
-  B.entries = (long)(g.n - 1 - n0) * g.B.ld + g.B.last;
+  B.rows = g.n - n0;
+  B.last = (int)g.B.last;
   v4f acc[Tile::FM][Tile::FN];
   Tile::run(acc, smem, A, B, g.q, g.nprod);
   store_tile<Tile>(acc, smem,
@@ -166,19 +168,21 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_k_kernel(Grouped16 g) {
   A.plane = g.A.plane;
   B.ld = (int)g.B.ld;
   B.plane = g.B.plane;
+  A.rows = g.m - m0;
+  B.rows = g.q - q0;
   int inner = len;
   if (KS) {
     A.base = g.A.p + gt.begin * g.A.ld + m0;
-    A.entries = (long)(len - 1) * g.A.ld + g.A.last - m0;
+    A.last = (int)g.A.last - m0;
     B.base = g.B.p + gt.begin * g.B.ld + q0;
-    B.entries = (long)(len - 1) * g.B.ld + g.B.last - q0;
+    B.last = (int)g.B.last - q0;
   } else {  // padded planes: the group's rows begin at 64 x its tiles before
-    const long k0 = (long)gt.first * BK16;
+    const int k0 = gt.first * BK16;
     inner = (len + BK16 - 1) / BK16 * BK16;
     A.base = g.A.p + (long)m0 * g.A.ld + k0;
-    A.entries = (long)(g.m - 1 - m0) * g.A.ld + g.A.last - k0;
+    A.last = (int)g.A.last - k0;
     B.base = g.B.p + (long)q0 * g.B.ld + k0;
-    B.entries = (long)(g.q - 1 - q0) * g.B.ld + g.B.last - k0;
+    B.last = (int)g.B.last - k0;
   }
   v4f acc[Tile::FM][Tile::FN];
   Tile::run(acc, smem, A, B, inner, g.nprod);

@@ -167,7 +167,7 @@ struct Step {
 };
 
 template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64) void step_kernel(Step p) {
+__global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
   using Tile = Tile16<Half, BM, BN, WM, WN, false, false>;
   __shared__ __attribute__((aligned(1024))) char smem[Tile::SMEM];
   const int tm = p.m / BM, tn = p.n / BN;
@@ -185,8 +185,8 @@ __global__ __launch_bounds__(WM* WN * 64) void step_kernel(Step p) {
   (void)tn;
   const long b = blockIdx.y;
   const int m0 = mi * BM, n0 = nj * BN;
-  const Source16 A{p.A + b * p.a_batch + (long)m0 * p.k, p.a_plane, (long)(p.m - m0) * p.k, p.k};
-  const Source16 B{p.B + b * p.b_batch + (long)n0 * p.k, p.b_plane, (long)(p.n - n0) * p.k, p.k};
+  const Source16 A{p.A + b * p.a_batch + (long)m0 * p.k, p.a_plane, p.k, p.m - m0, p.k};
+  const Source16 B{p.B + b * p.b_batch + (long)n0 * p.k, p.b_plane, p.k, p.n - n0, p.k};
   v4f acc[Tile::FM][Tile::FN];
   Tile::run(acc, smem, A, B, p.k, p.nprod);
 

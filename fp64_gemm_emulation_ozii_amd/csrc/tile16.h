@@ -45,8 +45,9 @@ struct Bfloat {
 struct Source16 {
   const uint16_t* base;  // first entry of the tile at k = 0
   long plane;            // distance to the second slice
-  long entries;          // entries from `base` to the end of what may be read
   int ld;
+  int rows;  // K-contiguous: rows from `base` on that exist (more than a tile has: as many as it has)
+  int last;  // entries that may be read of the last row (K-contiguous) or of the last k (K-strided) from `base` on
 };
 
 constexpr int BK16 = 64;  // K entries per slice: 128 bytes of a K-contiguous row
@@ -101,43 +102,57 @@ struct Tile16 {
   // LDS bytes [blk 1024, + 1024).
   template <int ROWS, bool KS, int LOADS>
   struct Loader {
-    Source16 s;
-    int off[2];  // lane's byte offset in an even and an odd load (K-contiguous)
-    int kin[2];  // lane's first k within the slice
+    const char* p;   // the slice to load: its base,
+    int records;     // the bytes that may be read from there
+    int ld;
+    int off[2];      // lane's byte offset in an even and an odd load (K-contiguous)
+    int kin[2];      // lane's first k within the slice
+    int base[2];     // off, or past the end for a lane whose k lies past the inner dimension
+    int last, rows;
     int lane, wave;
 
-    __device__ __forceinline__ void init(const Source16& src, int lane_, int wave_) {
-      s = src;
+    __device__ __forceinline__ void init(const Source16& s, int lane_, int wave_) {
+      ld = s.ld;
+      last = s.last;
+      rows = min(s.rows, ROWS);
       lane = lane_;
       wave = wave_;
       if (!KS) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int r = lane >> 3, c = (lane & 7) ^ swz(p * 8 + r);
-          off[p] = (r * s.ld + c * 8) * 2;
-          kin[p] = c * 8;
+        for (int e = 0; e < 2; ++e) {
+          const int r = lane >> 3, c = (lane & 7) ^ swz(e * 8 + r);
+          off[e] = (r * ld + c * 8) * 2;
+          kin[e] = c * 8;
         }
       }
     }
 
-    __amdgpu_buffer_rsrc_t rsrc;
-    int base[2];  // off, or past the end for a lane whose k lies past the inner dimension
-
-    // The slice at k0 of an inner dimension of q entries, of the high (0) or
-    // low (1) slices; past the last slice (!any) every load brings zeros.
-    __device__ __forceinline__ void aim(int plane, int k0, int q, bool any) {
-      const long skip = KS ? (long)k0 * s.ld : (long)k0;
-      const long left = (s.entries - skip) * 2;
-      const uint16_t* p = s.base + plane * s.plane + skip;
-      const int records = (int)(!any || left < 0 ? 0 : left > 0x7fffffffL ? 0x7fffffffL : left);
-      rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, records, 0x00020000);
-      if (!KS) {
+    // The first slice of an inner dimension of which `left` entries remain,
+    __device__ __forceinline__ void start(const uint16_t* at, int left) {
+      p = reinterpret_cast<const char*>(at);
+      if (!KS) records = ((rows - 1) * ld + last) * 2;
+      edge(left);
+    }
+    // and the one after it.
+    __device__ __forceinline__ void next(int left) {
+      p += KS ? (long)ld * (BK16 * 2) : (long)(BK16 * 2);
+      if (!KS) records -= BK16 * 2;
+      edge(left);
+    }
+    __device__ __forceinline__ void edge(int left) {
+      if (KS) {  // rows k past the inner dimension lie past the end
+        records = left > 0 ? ((min(left, BK16) - 1) * ld + last) * 2 : 0;
+      } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) base[e] = kin[e] < q - k0 ? off[e] : (int)0x80000000;
+        for (int e = 0; e < 2; ++e) base[e] = kin[e] < left ? off[e] : (int)0x80000000;
       }
     }
+    // Past the last slice every load brings zeros.
+    __device__ __forceinline__ void stop() { records = 0; }
 
     __device__ __forceinline__ void load1(int li, char* lds) const {
+      const __amdgpu_buffer_rsrc_t rsrc =
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, records, 0x00020000);
       const int blk = wave * LOADS + li;
       int voff;
       if (KS) {
@@ -145,9 +160,9 @@ struct Tile16 {
         constexpr int KPL = 64 / CPR;         // rows k per wave load
         const int k = blk * KPL + lane / CPR;
         const int c = (lane % CPR) ^ (kswz<ROWS>(k) << 1);
-        voff = (k * s.ld + c * 8) * 2;
+        voff = (k * ld + c * 8) * 2;
       } else {
-        voff = base[blk & 1] + blk * 16 * s.ld;
+        voff = base[blk & 1] + blk * 16 * ld;
       }
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + blk * 1024), 16,
                                                voff, 0, 0, 0);
@@ -183,9 +198,14 @@ struct Tile16 {
   // Order of a slice t (two steps of 32 k): the MFMAs of a step run in fixed
   // slots, and after each slot go the LDS reads of the next step's fragments
   // (an A fragment right after its last use) and, in the second step, the
-  // loads of slice t + 2.  One barrier per slice, before the second step's
-  // MFMAs: by then this wave's reads of buffer t mod 2 are in registers and
-  // its loads of slice t + 1, issued a whole slice earlier, have landed.
+  // loads of slice t + 2.  One barrier per slice, a quarter into the second
+  // step, whose MFMAs cover the latency of the last reads of buffer t mod 2;
+  // this wave's loads of slice t + 1, issued a whole slice earlier, have
+  // landed by then.  Reads of buffer t + 1 and loads into buffer t follow it.
+  static constexpr int BAR = FM * FN / 4 - 1;
+  // slot r of FM FN pressed into those after the barrier
+  static constexpr int after_barrier(int r) { return BAR + 1 + r * (FM * FN - BAR - 1) / (FM * FN); }
+
   static __device__ __forceinline__ void run(v4f (&acc)[FM][FN], char* smem, const Source16& A, const Source16& B,
                                              int q, int nprod) {
     constexpr int SLOTS = FM * FN, LPW = A_LOADS + B_LOADS;
@@ -204,15 +224,28 @@ struct Tile16 {
     const int nk = (q + BK16 - 1) / BK16;
     const int total = nk * nprod;
     if (total == 0) return;
-    int u = 0, kt = 0;  // the slice to load next
-    auto aim = [&]() {
-      la.aim(nprod == 3 && u == 0, kt * BK16, q, u < nprod);
-      lb.aim(nprod == 3 && u == 1, kt * BK16, q, u < nprod);
-      if (++kt == nk) {
-        kt = 0;
-        ++u;
+    // The slices in the order they are loaded: `left` entries of the inner
+    // dimension remain of product u.
+    int u = 0, left = q;
+    auto planes = [&]() {
+      la.start(A.base + (nprod == 3 && u == 0 ? A.plane : 0), q);
+      lb.start(B.base + (nprod == 3 && u == 1 ? B.plane : 0), q);
+    };
+    auto advance = [&]() {
+      left -= BK16;
+      la.next(left);
+      lb.next(left);
+      if (left <= 0) {
+        if (++u < nprod) {
+          left = q;
+          planes();
+        } else {
+          la.stop();
+          lb.stop();
+        }
       }
     };
+    planes();
     auto load1 = [&](int buf, int li) {
       char* d = smem + buf * BUF;
       if (li < A_LOADS)
@@ -228,9 +261,9 @@ struct Tile16 {
     };
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      aim();
 #pragma unroll
       for (int li = 0; li < LPW; ++li) load1(b, li);
+      advance();
     }
     wait_loads<LPW>();  // slice 0 (loads return in order)
     __builtin_amdgcn_s_barrier();
@@ -244,24 +277,25 @@ struct Tile16 {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int rbuf = ks ? (t + 1) & 1 : t & 1;  // (past the end: zeros, not used)
-        if (ks) {
-          slice_barrier();
-          aim();
-        }
 #pragma unroll
         for (int r = 0; r < SLOTS; ++r) {
           const int i = r / FN, j = r % FN;
           acc[i][j] = T::mfma(cur[FN + i], cur[j], acc[i][j]);
           __builtin_amdgcn_sched_barrier(0);
+          if (ks && r == BAR) {
+            slice_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+          }
 #pragma unroll
           for (int f = 0; f < FM + FN; ++f) {
             const int slot = f < FN ? f * (SLOTS / FN) + 1 : (f - FN) * FN + FN - 1;
-            if (slot == r) nxt[f] = read1(rbuf, 1 - ks, f);
+            if ((ks ? after_barrier(slot) : slot) == r) nxt[f] = read1(rbuf, 1 - ks, f);
           }
           if (ks) {
 #pragma unroll
             for (int li = 0; li < LPW; ++li)
-              if (li * SLOTS / LPW + (SLOTS > LPW) == r) load1(t & 1, li);
+              if (after_barrier(li * SLOTS / LPW + (SLOTS > LPW)) == r) load1(t & 1, li);
+            if (r == SLOTS - 1) advance();
           }
           __builtin_amdgcn_sched_barrier(0);
         }
