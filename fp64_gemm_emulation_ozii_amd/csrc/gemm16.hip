@@ -46,7 +46,7 @@ template <class Tile>
 __device__ __forceinline__ void store_tile(const v4f (&acc)[Tile::FM][Tile::FN], char* smem, const Target& t) {
   constexpr int WTM = Tile::FM * 16, PITCH = WTM + 4, RUNS = WTM / 8;
   static_assert(Tile::NW * 16 * PITCH * 4 <= Tile::SMEM, "staging fits the operand buffers");
-  slice_barrier();  // every wave has read its last operands
+  slice_barrier<0>();  // every wave has read its last operands
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* stage = reinterpret_cast<float*>(smem) + wave * 16 * PITCH;
@@ -102,26 +102,9 @@ __device__ __forceinline__ void store_tile(const v4f (&acc)[Tile::FM][Tile::FN],
   }
 }
 
-// Block b of `total` tiles, each XCD (b mod 8) taking a contiguous eighth.
-__device__ __forceinline__ int xcd_order(int b, int total) {
-  const int x = b & 7, per = total >> 3, rest = total & 7;
-  return x * per + min(x, rest) + (b >> 3);
-}
-
-// Inside its run an XCD walks `major` panels GROUP at a time against all of
-// `minor`, so the blocks running together share both operands' panels in L2.
-template <int GROUP>
-__device__ __forceinline__ void panel_order(int w, int major, int minor, int& a, int& b) {
-  const int first = w / (GROUP * minor) * GROUP;
-  const int in = w % (GROUP * minor);
-  const int g = min(GROUP, major - first);
-  a = first + in % g;
-  b = in / g;
-}
-
-template <class T, int BM, int BN, int WM, int WN, bool AKS>
+template <class T, int BM, int BN, int WM, int WN, bool AKS, bool PAIR>
 __global__ __launch_bounds__(WM* WN * 64) void grouped_n_kernel(Grouped16 g) {
-  using Tile = Tile16<T, BM, BN, WM, WN, AKS, false>;
+  using Tile = Tile16<T, BM, BN, WM, WN, AKS, false, 2, PAIR>;
   __shared__ __attribute__((aligned(1024))) char smem[Tile::SMEM];
   const int tiles_m = (g.m + BM - 1) / BM;
   const int tiles_n = count_group_tiles(g.offsets, g.groups, g.n, BN);
@@ -144,15 +127,15 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_n_kernel(Grouped16 g) {
   B.rows = g.n - n0;
   B.last = (int)g.B.last;
   v4f acc[Tile::FM][Tile::FN];
-  Tile::run(acc, smem, A, B, g.q, g.nprod);
+  Tile::run(acc, smem, A, B, g.q);
   store_tile<Tile>(acc, smem,
                    Target{g.C, g.ctype, g.ldc, m0, g.m, n0, gt.end,
                           g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr, g.B.ex});
 }
 
-template <class T, int BM, int BN, int WM, int WN, bool KS>
+template <class T, int BM, int BN, int WM, int WN, bool KS, bool PAIR>
 __global__ __launch_bounds__(WM* WN * 64) void grouped_k_kernel(Grouped16 g) {
-  using Tile = Tile16<T, BM, BN, WM, WN, KS, KS>;
+  using Tile = Tile16<T, BM, BN, WM, WN, KS, KS, 2, PAIR>;
   __shared__ __attribute__((aligned(1024))) char smem[Tile::SMEM];
   const int tiles_m = (g.m + BM - 1) / BM, tiles_q = (g.q + BN - 1) / BN;
   const int per = tiles_m * tiles_q;
@@ -185,26 +168,24 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_k_kernel(Grouped16 g) {
     B.last = (int)g.B.last - k0;
   }
   v4f acc[Tile::FM][Tile::FN];
-  Tile::run(acc, smem, A, B, inner, g.nprod);
+  Tile::run(acc, smem, A, B, inner);
   char* C = (char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2);
   store_tile<Tile>(acc, smem,
                    Target{C, g.ctype, g.ldc, m0, g.m, q0, g.q, g.A.ex ? g.A.ex + e * g.A.ex_batch : nullptr,
                           g.B.ex ? g.B.ex + e * g.B.ex_batch : nullptr});
 }
 
-template <class T, bool AKS>
+template <class T, int BT, bool AKS, bool PAIR>
 hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
-  constexpr int BM = 256, BN = 256;
-  const long blocks = group_tiles_max(g.n, g.groups, BN) * ((g.m + BM - 1) / BM);
-  hipLaunchKernelGGL((grouped_n_kernel<T, BM, BN, 2, 4, AKS>), dim3((unsigned)blocks), dim3(512), 0, st, g);
+  const long blocks = group_tiles_max(g.n, g.groups, BT) * ((g.m + BT - 1) / BT);
+  hipLaunchKernelGGL((grouped_n_kernel<T, BT, BT, 2, 4, AKS, PAIR>), dim3((unsigned)blocks), dim3(512), 0, st, g);
   return hipGetLastError();
 }
 
-template <class T, bool KS>
+template <class T, int BT, bool KS, bool PAIR>
 hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
-  constexpr int BM = 256, BN = 256;
-  const long blocks = (long)((g.m + BM - 1) / BM) * ((g.q + BN - 1) / BN) * g.groups;
-  hipLaunchKernelGGL((grouped_k_kernel<T, BM, BN, 2, 4, KS>), dim3((unsigned)blocks), dim3(512), 0, st, g);
+  const long blocks = (long)((g.m + BT - 1) / BT) * ((g.q + BT - 1) / BT) * g.groups;
+  hipLaunchKernelGGL((grouped_k_kernel<T, BT, BT, 2, 4, KS, PAIR>), dim3((unsigned)blocks), dim3(512), 0, st, g);
   return hipGetLastError();
 }
 
@@ -220,15 +201,17 @@ bool grouped_k_fits(const Grouped16& g) {
 }
 
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
-  if (g.B.ks) return hipErrorInvalidValue;
-  if (g.bf16) return g.A.ks ? grouped_n<Bfloat, true>(g, st) : grouped_n<Bfloat, false>(g, st);
-  return g.A.ks ? grouped_n<Half, true>(g, st) : grouped_n<Half, false>(g, st);
+  if (g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
+  if (g.f32) return grouped_n<Half, 128, false, true>(g, st);
+  if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, true, false>(g, st) : grouped_n<Bfloat, 256, false, false>(g, st);
+  return g.A.ks ? grouped_n<Half, 256, true, false>(g, st) : grouped_n<Half, 256, false, false>(g, st);
 }
 
 hipError_t launch_grouped_k(const Grouped16& g, hipStream_t st) {
-  if (g.A.ks != g.B.ks) return hipErrorInvalidValue;
-  if (g.bf16) return g.A.ks ? grouped_k<Bfloat, true>(g, st) : grouped_k<Bfloat, false>(g, st);
-  return g.A.ks ? grouped_k<Half, true>(g, st) : grouped_k<Half, false>(g, st);
+  if (g.A.ks != g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
+  if (g.f32) return grouped_k<Half, 128, false, true>(g, st);
+  if (g.bf16) return g.A.ks ? grouped_k<Bfloat, 256, true, false>(g, st) : grouped_k<Bfloat, 256, false, false>(g, st);
+  return g.A.ks ? grouped_k<Half, 256, true, false>(g, st) : grouped_k<Half, 256, false, false>(g, st);
 }
 
 }  // namespace oz

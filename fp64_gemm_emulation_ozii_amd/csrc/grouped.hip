@@ -150,7 +150,7 @@ int ozgemm_grouped_gemm(int type, int ctype, int groups, int m, int n, int q, in
   char* ws = (char*)workspace;
   Grouped16 g{};
   g.bf16 = type == OZGEMM_BF16;
-  g.nprod = type == OZGEMM_F32 ? 3 : 1;
+  g.f32 = type == OZGEMM_F32;
   g.m = m;
   g.n = n;
   g.q = q;
@@ -159,7 +159,8 @@ int ozgemm_grouped_gemm(int type, int ctype, int groups, int m, int n, int q, in
   g.C = C;
   g.ctype = ctype;
   g.ldc = ldc;
-  g.A = in_place(A, lda, (long)stridea, transa == 0, ar);
+  // (F32 operands stay here only where nothing is read: no inner dimension)
+  g.A = in_place(A, lda, (long)stridea, transa == 0 && !g.f32, ar);
   g.B = in_place(B, ldb, 0, false, q);
   if (!grouped_n_fits(g)) return OZGEMM_RANGE;
   if (r.A.used) {
@@ -219,7 +220,7 @@ int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n, c
   char* ws = (char*)workspace;
   Grouped16 g{};
   g.bf16 = type == OZGEMM_BF16;
-  g.nprod = type == OZGEMM_F32 ? 3 : 1;
+  g.f32 = type == OZGEMM_F32;
   g.m = m;
   g.n = n;
   g.q = q;
@@ -229,8 +230,8 @@ int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n, c
   g.ctype = ctype;
   g.ldc = ldc;
   g.cbatch = (long)stridec;
-  g.A = in_place(A, lda, 0, true, m);
-  g.B = in_place(B, ldb, 0, true, q);
+  g.A = in_place(A, lda, 0, !g.f32, m);
+  g.B = in_place(B, ldb, 0, !g.f32, q);
   if (!grouped_k_fits(g)) return OZGEMM_RANGE;
   if (r.A.used) {  // then B's too
     g.A = sliced(type, r.A, ws, 0, m);

@@ -12,13 +12,15 @@
 // a step, uses both slices, so rounding is not amplified with them).  F16 and
 // F32 use three.  F64 runs the library's Scheme II products.
 //
-// X is kept both ways round (Xr: r x c, Xc: c x r), so that every product
-// has both operands K-contiguous; the step that writes X writes both.  P
-// and P^2 are symmetric: tiles on and below the diagonal are computed and
-// written twice.
+// X stays as G lies: wide (r rows of c entries next to each other) or tall (c
+// rows of r).  P = X X^T runs along the c entries, Q X along the r rows; the
+// product kernel reads an operand K-contiguous or K-strided (tile16.h), so no
+// transposed copy is kept.  P and P^2 are symmetric: tiles on and below the
+// diagonal are computed and written twice.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <cstdlib>
 
 #include "products.h"
 #include "tile16.h"
@@ -60,26 +62,120 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
   return ((part[0] + part[1]) + (part[2] + part[3]));
 }
 
+// Eight entries next to each other, as FP64 (16-byte loads where `wide`).
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* p, long at, int left, bool wide, float (&v)[8]) {
+  if (TYPE == OZGEMM_F32) {
+    const float* q = (const float*)p + at;
+    if (wide && left >= 8) {
+      *reinterpret_cast<v4f*>(v) = *reinterpret_cast<const v4f*>(q);
+      *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f*>(q + 4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < left ? q[e] : 0.f;
+    }
+  } else {
+    const short* q = (const short*)p + at;
+    v8s h = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (wide && left >= 8) {
+      h = *reinterpret_cast<const v8s*>(q);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) h[e] = q[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = TYPE == OZGEMM_BF16 ? (float)__builtin_bit_cast(__bf16, (short)h[e])
+                                 : (float)__builtin_bit_cast(_Float16, (short)h[e]);
+  }
+}
+
+template <class V>
+__device__ __forceinline__ void store8(void* p, int type, long at, int left, bool wide, const V (&v)[8]) {
+  if (type == OZGEMM_F32) {
+    float* q = (float*)p + at;
+    if (wide && left >= 8) {
+      *reinterpret_cast<v4f*>(q) = v4f{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<v4f*>(q + 4) = v4f{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) q[e] = v[e];
+    }
+    return;
+  }
+  v8s h;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    h[e] = type == OZGEMM_BF16 ? __builtin_bit_cast(short, (__bf16)v[e]) : __builtin_bit_cast(short, (_Float16)v[e]);
+  short* q = (short*)p + at;
+  if (wide && left >= 8) {
+    *reinterpret_cast<v8s*>(q) = h;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) q[e] = h[e];
+  }
+}
+
+__device__ __forceinline__ bool wide_rows(const void* G, long base, long ld, int size) {
+  return ((uintptr_t)G & 15) == 0 && base * size % 16 == 0 && ld * size % 16 == 0;
+}
+
 // Sums of squares in FP64 (no square of an FP32 value leaves its range):
-// block (p, b) adds its share of the rows of matrix b.
-__global__ __launch_bounds__(256) void square_sum_kernel(const void* __restrict__ G, int type, int rows, int cols,
-                                                         long ld, long batch, double* __restrict__ part) {
+// block (p, b) adds the pieces of 2048 entries p, p + parts, ... of matrix b's rows.
+template <int TYPE>
+__global__ __launch_bounds__(256) void square_sum_kernel(const void* __restrict__ G, int rows, int cols, long ld,
+                                                         long batch, double* __restrict__ part) {
   __shared__ double s[4];
   const long base = blockIdx.y * batch;
+  const bool wide = wide_rows(G, base, ld, TYPE == OZGEMM_F32 ? 4 : 2);
+  const int per = (cols + 2047) / 2048;
+  const long pieces = (long)rows * per;
+  // narrow rows: each wavefront takes a row of its own
+  const bool narrow = cols <= 512;
   double sum = 0;
-  const long total = (long)rows * cols;
-  for (long at = (long)blockIdx.x * 256 + threadIdx.x; at < total; at += (long)gridDim.x * 256) {
-    const long r = at / cols;
-    const double v = load_value(G, type, base + r * ld + (at - r * cols));
-    sum += v * v;
+  const long first = narrow ? (long)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const long step = narrow ? (long)gridDim.x * 4 : gridDim.x;
+  const int lane8 = (narrow ? (threadIdx.x & 63) : threadIdx.x) * 8;
+  for (long i = first; i < pieces; i += step) {
+    const long r = i / per;
+    const int c = (int)(i - r * per) * 2048 + lane8;
+    if (c >= cols) continue;
+    if (TYPE == OZGEMM_F64) {
+      const double* q = (const double*)G + base + r * ld + c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < cols) sum = __builtin_fma(q[e], q[e], sum);
+    } else {
+      float v[8];
+      load8<TYPE>(G, base + r * ld + c, cols - c, wide, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)v[e], (double)v[e], sum);
+    }
   }
   sum = block_sum(sum, s);
   if (threadIdx.x == 0) part[blockIdx.y * gridDim.x + blockIdx.x] = sum;
 }
 
+hipError_t launch_square_sum(int type, const void* G, int rows, int cols, long ld, long batch, int batches, int parts,
+                             double* part, hipStream_t st) {
+  const dim3 g(parts, batches), t(256);
+  switch (type) {
+    case OZGEMM_F64: hipLaunchKernelGGL(square_sum_kernel<OZGEMM_F64>, g, t, 0, st, G, rows, cols, ld, batch, part); break;
+    case OZGEMM_F32: hipLaunchKernelGGL(square_sum_kernel<OZGEMM_F32>, g, t, 0, st, G, rows, cols, ld, batch, part); break;
+    case OZGEMM_BF16: hipLaunchKernelGGL(square_sum_kernel<OZGEMM_BF16>, g, t, 0, st, G, rows, cols, ld, batch, part); break;
+    default: hipLaunchKernelGGL(square_sum_kernel<OZGEMM_F16>, g, t, 0, st, G, rows, cols, ld, batch, part);
+  }
+  return hipGetLastError();
+}
+
 // 1 / (|G_b|_F + eps) from the partial sums of matrix b, in every thread of the block.
 __device__ __forceinline__ double inverse_norm(const double* part, int parts, long b, double eps, double* s) {
-  const double v = block_sum((int)threadIdx.x < parts ? part[b * parts + threadIdx.x] : 0.0, s);
+  double v = 0;
+  for (int i = threadIdx.x; i < parts; i += 256) v += part[b * parts + i];
+  v = block_sum(v, s);
   return 1.0 / (sqrt(v) + eps);
 }
 
@@ -93,43 +189,47 @@ __device__ __forceinline__ float joined(uint16_t hi, uint16_t lo) {
   return (float)__builtin_bit_cast(_Float16, hi) + (float)__builtin_bit_cast(_Float16, lo);
 }
 
-// G (rows x cols) scaled and cut into slices, as it lies (N: np x kp) and
-// transposed (T: kp x np), zeros in the padding.
+// G (rows x cols) scaled and cut into slices, zeros in the padding.
+constexpr int PREPARE_RUNS = 4;  // runs of 8 entries per thread
+
 struct Prepare {
   const void* G;
-  int type;
   int rows, cols;
   long ld, batch;
   const double* part;
   int parts;
   double eps, scale;
-  uint16_t* N;   // [batch][2][rows_pad][cols_pad]
-  uint16_t* T;   // [batch][2][cols_pad][rows_pad]
+  uint16_t* X;   // [batch][2][rows_pad][cols_pad]
   int rows_pad, cols_pad;
 };
 
+template <int TYPE>
 __global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
   __shared__ double s[4];
-  __shared__ uint32_t tile[64][65];
-  const long b = blockIdx.z;
+  const long b = blockIdx.y;
   const double f = inverse_norm(p.part, p.parts, b, p.eps, s) * p.scale;
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  const long plane = (long)p.rows_pad * p.cols_pad;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int r = r0 + (i >> 6), c = c0 + (i & 63);
-    uint16_t hi = 0, lo = 0;
-    if (r < p.rows && c < p.cols) split((float)(load_value(p.G, p.type, b * p.batch + r * p.ld + c) * f), hi, lo);
-    const long at = b * 2 * plane + (long)r * p.cols_pad + c;
-    p.N[at] = hi;
-    p.N[at + plane] = lo;
-    tile[i >> 6][i & 63] = hi | ((uint32_t)lo << 16);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int c = i >> 6, r = i & 63;
-    const long at = b * 2 * plane + (long)(c0 + c) * p.rows_pad + r0 + r;
-    p.T[at] = (uint16_t)tile[r][c];
-    p.T[at + plane] = (uint16_t)(tile[r][c] >> 16);
+  const long plane = (long)p.rows_pad * p.cols_pad, base = b * p.batch;
+  const bool wide = wide_rows(p.G, base, p.ld, TYPE == OZGEMM_F32 ? 4 : 2);
+  const int per = p.cols_pad / 8;
+#pragma unroll
+  for (int i = 0; i < PREPARE_RUNS; ++i) {
+    const long at = ((long)blockIdx.x * PREPARE_RUNS + i) * 256 + threadIdx.x;
+    if (at * 8 >= plane) return;
+    const int r = (int)(at / per), c = (int)(at - (long)r * per) * 8;
+    float v[8];
+    load8<TYPE>(p.G, base + r * p.ld + c, r < p.rows ? p.cols - c : 0, wide, v);
+    v8s h, l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint16_t hi, lo;
+      split((float)(v[e] * f), hi, lo);
+      if (r >= p.rows || c + e >= p.cols) hi = lo = 0;  // (0 f is NaN where the norm is)
+      h[e] = (short)hi;
+      l[e] = (short)lo;
+    }
+    uint16_t* out = p.X + b * 2 * plane + at * 8;
+    *reinterpret_cast<v8s*>(out) = h;
+    *reinterpret_cast<v8s*>(out + plane) = l;
   }
 }
 
@@ -146,91 +246,104 @@ __global__ __launch_bounds__(256) void normalise_kernel(const void* G, int type,
 }
 
 // One product of a step: D = A B^T on padded planes, then
-// v = alpha D + beta S, rounded to slices of N ([j][i]) and of T ([i][j]),
-// or, last, to the result.
+// v = alpha D + beta S, rounded to slices of N ([j][i]; a symmetric result is
+// computed on and below the diagonal and written on both sides of it) or, in
+// the last step, to the result.
 struct Step {
-  const uint16_t* A;  // [batch] a_batch apart, two slices a_plane apart, rows of k entries
+  const uint16_t* A;  // [batch] a_batch apart, two slices a_plane apart
   const uint16_t* B;
   long a_batch, a_plane, b_batch, b_plane;
+  int a_ld, b_ld;
   int m, n, k;        // padded
-  int nprod, symmetric;
+  int batch;
   float alpha, beta;
   const uint16_t* S;  // like N; nullptr: beta = 0
   uint16_t* N;
-  uint16_t* T;
-  long s_batch, s_plane;  // of S, N and T alike
-  int s_lo, n_lo, t_lo;   // whether the low slices are there
+  long s_batch, s_plane;  // of S and N alike
+  int s_lo, n_lo;         // whether the low slices are there
   void* O;
   int otype;
   long ldo, batcho;
   int om, on;         // the result's own size
 };
 
-template <int BM, int BN, int WM, int WN>
+template <int BT, int WM, int WN, int NB, bool PAIR, bool AKS, bool BKS, bool SYM>
 __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
-  using Tile = Tile16<Half, BM, BN, WM, WN, false, false>;
+  using Tile = Tile16<Half, BT, BT, WM, WN, AKS, BKS, NB, PAIR>;
   __shared__ __attribute__((aligned(1024))) char smem[Tile::SMEM];
-  const int tm = p.m / BM, tn = p.n / BN;
+  const int tm = p.m / BT, tn = p.n / BT;
+  const int per = SYM ? tm * (tm + 1) / 2 : tm * tn;
+  const int w = xcd_order(blockIdx.x, per * p.batch);
+  const long b = w / per;
+  const int t = w % per;
   int mi, nj;
-  if (p.symmetric) {  // tiles (mi, nj), nj <= mi, by rows of the triangle
-    const int t = blockIdx.x;
+  if (SYM) {  // tiles (mi, nj), nj <= mi, by rows of the triangle
     mi = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
     while ((mi + 1) * (mi + 2) / 2 <= t) ++mi;
     while (mi * (mi + 1) / 2 > t) --mi;
     nj = t - mi * (mi + 1) / 2;
   } else {
-    mi = blockIdx.x % tm;
-    nj = blockIdx.x / tm;
+    panel_order<4>(t, tm, tn, mi, nj);
   }
-  (void)tn;
-  const long b = blockIdx.y;
-  const int m0 = mi * BM, n0 = nj * BN;
-  const Source16 A{p.A + b * p.a_batch + (long)m0 * p.k, p.a_plane, p.k, p.m - m0, p.k};
-  const Source16 B{p.B + b * p.b_batch + (long)n0 * p.k, p.b_plane, p.k, p.n - n0, p.k};
+  const int m0 = mi * BT, n0 = nj * BT;
+  const Source16 A{p.A + b * p.a_batch + (AKS ? (long)m0 : (long)m0 * p.a_ld), p.a_plane, p.a_ld, p.m - m0,
+                   AKS ? p.m - m0 : p.k};
+  const Source16 B{p.B + b * p.b_batch + (BKS ? (long)n0 : (long)n0 * p.b_ld), p.b_plane, p.b_ld, p.n - n0,
+                   BKS ? p.n - n0 : p.k};
   v4f acc[Tile::FM][Tile::FN];
-  Tile::run(acc, smem, A, B, p.k, p.nprod);
+  Tile::run(acc, smem, A, B, p.k);
 
-  constexpr int WTM = Tile::FM * 16, PITCH = WTM + 4, RUNS = WTM / 8;
+  // Each wavefront passes its accumulators 16 columns at a time through a
+  // piece of LDS of its own; a lane then holds runs of 8 rows.  S's runs for
+  // the next 16 columns are on their way meanwhile.
+  constexpr int WTM = Tile::FM * 16, PITCH = WTM + 4, RUNS = WTM / 8, CH = (16 * RUNS + 63) / 64;
+  static_assert(16 * RUNS % 64 == 0, "whole wavefronts of runs");
   static_assert(Tile::NW * 16 * PITCH * 4 <= Tile::SMEM, "staging fits the operand buffers");
-  slice_barrier();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* stage = reinterpret_cast<float*>(smem) + wave * 16 * PITCH;
   const int mw = m0 + wave / WN * WTM, nw = n0 + wave % WN * (Tile::FN * 16);
   const uint16_t* S = p.S ? p.S + b * p.s_batch : nullptr;
   uint16_t* N = p.N + b * p.s_batch;
-  uint16_t* T = p.T + b * p.s_batch;
-  const bool mirror = !(p.symmetric && mi == nj);  // a diagonal tile holds both halves itself
+  const bool mirror = SYM && mi != nj;  // a diagonal tile holds both halves itself
+  auto offset = [&](int j, int ch) {
+    const int at = ch * 64 + lane;
+    return (long)(nw + j * 16 + at / RUNS) * p.m + mw + at % RUNS * 8;
+  };
+  v8s sh[2][CH] = {}, sl[2][CH] = {};
+  auto fetch = [&](int j) {
+    if (S == nullptr) return;
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      const long off = offset(j, ch);
+      sh[j & 1][ch] = *reinterpret_cast<const v8s*>(S + off);
+      if (p.s_lo) sl[j & 1][ch] = *reinterpret_cast<const v8s*>(S + p.s_plane + off);
+    }
+  };
+  fetch(0);
+  slice_barrier<0>();  // every wave has read its last operands, and no load into LDS is in flight
 #pragma unroll
   for (int j = 0; j < Tile::FN; ++j) {
+    if (j + 1 < Tile::FN) fetch(j + 1);
 #pragma unroll
     for (int i = 0; i < Tile::FM; ++i)
       *reinterpret_cast<v4f*>(stage + (lane & 15) * PITCH + i * 16 + 4 * (lane >> 4)) = acc[i][j];
     __builtin_amdgcn_s_waitcnt(0xc07f);
     asm volatile("" ::: "memory");
-#pragma unroll 1
-    for (int at = lane; at < 16 * RUNS; at += 64) {
-      const int c = at / RUNS, r = at % RUNS * 8;
-      const int col = nw + j * 16 + c, row = mw + r;
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      const int at = ch * 64 + lane, c = at / RUNS, r = at % RUNS * 8;
       float v[8];
       *reinterpret_cast<v4f*>(v) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r);
       *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r + 4);
-      const long off = (long)col * p.m + row;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= p.alpha;
-      if (S != nullptr) {
-        const v8s h = *reinterpret_cast<const v8s*>(S + off);
-        v8s l = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (p.s_lo) l = *reinterpret_cast<const v8s*>(S + p.s_plane + off);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(p.beta, joined((uint16_t)h[e], (uint16_t)l[e]), v[e]);
-      }
-      if (p.O != nullptr) {
+      for (int e = 0; e < 8; ++e)
+        v[e] = __builtin_fmaf(p.beta, joined((uint16_t)sh[j & 1][ch][e], (uint16_t)sl[j & 1][ch][e]), v[e] * p.alpha);
+      if (!SYM && p.O != nullptr) {
+        const int col = nw + j * 16 + c, row = mw + r;
         if (col < p.on) {
           const long to = b * p.batcho + (long)col * p.ldo + row;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (row + e < p.om) store_value(p.O, p.otype, to + e, v[e]);
+          store8(p.O, p.otype, to, p.om - row, wide_rows(p.O, to, 0, p.otype == OZGEMM_F32 ? 4 : 2), v);
         }
         continue;
       }
@@ -242,9 +355,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
         h[e] = (short)hi;
         l[e] = (short)lo;
       }
+      const long off = offset(j, ch);
       *reinterpret_cast<v8s*>(N + off) = h;
       if (p.n_lo) *reinterpret_cast<v8s*>(N + p.s_plane + off) = l;
-      // the rounded slices go back to the staging piece for the transposed copy
+      // the rounded slices go back to the staging piece for the other side
       if (mirror) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -253,21 +367,20 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);
     asm volatile("" ::: "memory");
-    if (p.O == nullptr && mirror) {
-      // 16 columns of one row: 32 bytes
-#pragma unroll 1
-      for (int at = lane; at < WTM * 2; at += 64) {
-        const int r = at >> 1, c = (at & 1) * 8;
+    if (mirror) {  // 16 columns of one row: 32 bytes
+#pragma unroll
+      for (int ch = 0; ch < (WTM * 2 + 63) / 64; ++ch) {
+        const int at = ch * 64 + lane, r = at >> 1, c = (at & 1) * 8;
         v8s h, l;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const uint32_t w = reinterpret_cast<const uint32_t*>(stage)[(c + e) * PITCH + r];
-          h[e] = (short)w;
-          l[e] = (short)(w >> 16);
+          const uint32_t x = reinterpret_cast<const uint32_t*>(stage)[(c + e) * PITCH + r];
+          h[e] = (short)x;
+          l[e] = (short)(x >> 16);
         }
         const long off = (long)(mw + r) * p.n + nw + j * 16 + c;
-        *reinterpret_cast<v8s*>(T + off) = h;
-        if (p.t_lo) *reinterpret_cast<v8s*>(T + p.s_plane + off) = l;
+        *reinterpret_cast<v8s*>(N + off) = h;
+        if (p.n_lo) *reinterpret_cast<v8s*>(N + p.s_plane + off) = l;
       }
       __builtin_amdgcn_s_waitcnt(0xc07f);
       asm volatile("" ::: "memory");
@@ -275,12 +388,19 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
   }
 }
 
-template <int BT, int WM, int WN>
-hipError_t launch_step_t(const Step& p, int batch, hipStream_t st) {
+template <int BT, int WM, int WN, int NB, bool PAIR>
+hipError_t launch_step_t(const Step& p, bool aks, bool bks, bool sym, hipStream_t st) {
   const long tm = p.m / BT, tn = p.n / BT;
-  const long tiles = p.symmetric ? tm * (tm + 1) / 2 : tm * tn;
-  hipLaunchKernelGGL((step_kernel<BT, BT, WM, WN>), dim3((unsigned)tiles, (unsigned)batch), dim3(WM * WN * 64), 0, st,
-                     p);
+  const dim3 grid((unsigned)((sym ? tm * (tm + 1) / 2 : tm * tn) * p.batch)), block(WM * WN * 64);
+  if (sym && aks)
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, true, true, true>), grid, block, 0, st, p);
+  else if (sym)
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, false, false, true>), grid, block, 0, st, p);
+  else if (aks)
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, true, false, false>), grid, block, 0, st, p);
+  else
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, false, false, false>), grid, block, 0, st, p);
+  (void)bks;
   return hipGetLastError();
 }
 
@@ -342,9 +462,9 @@ __global__ __launch_bounds__(256) void update64_kernel(double* __restrict__ X, d
 // Host side
 // ---------------------------------------------------------------------------
 
-constexpr int SQUARE_PARTS = 256;
+constexpr int SQUARE_PARTS = 1024;
 
-// Blocks that sum one matrix's squares: 16 entries a thread, SQUARE_PARTS at most.
+// Blocks that sum one matrix's squares: 16 entries a thread, up to SQUARE_PARTS.
 int square_parts(int m, int n) {
   const long blocks = ((long)m * n + 4095) / 4096;
   return (int)(blocks < 1 ? 1 : blocks > SQUARE_PARTS ? SQUARE_PARTS : blocks);
@@ -353,13 +473,14 @@ int square_parts(int m, int n) {
 // Tile size of the step products: the padded matrix is cut into whole tiles.
 int step_tile(int batch, int r, int c) {
   (void)batch;
+  if (getenv("OZP")) return atoi(getenv("OZP"));
   if (r <= 64 || c <= 64) return 64;
   return 128;
 }
 
 struct OrthoLayout {
   int tile, rp, cp;
-  size_t part, Xr, Xc, Xc2, P, Q, total;   // 16-bit types
+  size_t part, X1, X2, P, Q, total;        // 16-bit slices
   size_t X, XT, Y, dgemm;                  // FP64
 };
 
@@ -386,9 +507,8 @@ OrthoLayout ortho_layout(int type, int batch, int m, int n, int s) {
   L.rp = (int)up(r, L.tile);
   L.cp = (int)up(c, L.tile);
   const size_t rc = (size_t)batch * 2 * L.rp * L.cp * 2, rr = (size_t)batch * 2 * L.rp * L.rp * 2;
-  L.Xr = take(rc);
-  L.Xc = take(rc);
-  L.Xc2 = take(rc);
+  L.X1 = take(rc);
+  L.X2 = take(rc);
   L.P = take(rr);
   L.Q = take(rr);
   return L;
@@ -482,7 +602,7 @@ int ortho64(const OrthoLayout& L, int batch, int m, int n, const double* G, long
     const double* Gi = G + i * strideg;
     double* Oi = O + i * strideo;
     const int parts = square_parts(m, n);
-    hipLaunchKernelGGL(square_sum_kernel, dim3(parts, 1), dim3(256), 0, st, Gi, OZGEMM_F64, n, m, ldg, 0L, part);
+    OZ_TRY(launch_square_sum(OZGEMM_F64, Gi, n, m, ldg, 0, 1, parts, part, st));
     hipLaunchKernelGGL(prepare64_kernel, tiles, dim3(256), 0, st, Gi, n, m, ldg, part, parts, eps,
                        as_it_lies ? X : XT, as_it_lies ? XT : X);
     OZ_TRY(hipGetLastError());
@@ -506,9 +626,8 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
             const double* co, double eps, void* O, long ldo, long strideo, char* ws, hipStream_t st) {
   const bool tall = n > m;  // as it lies: n rows of m entries
   const int r = tall ? m : n;
-  uint16_t* Xr = (uint16_t*)(ws + L.Xr);
-  uint16_t* Xc = (uint16_t*)(ws + L.Xc);
-  uint16_t* Xc2 = (uint16_t*)(ws + L.Xc2);
+  uint16_t* X = (uint16_t*)(ws + L.X1);
+  uint16_t* other = (uint16_t*)(ws + L.X2);
   uint16_t* P = (uint16_t*)(ws + L.P);
   uint16_t* Q = (uint16_t*)(ws + L.Q);
   double* part = (double*)(ws + L.part);
@@ -518,65 +637,89 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
   double t = START;
   Scales sc;
   if (!scales_of(co, steps, 0, &t, &sc)) return OZGEMM_RANGE;
-  hipLaunchKernelGGL(square_sum_kernel, dim3(parts, batch), dim3(256), 0, st, G, type, n, m, ldg, strideg, part);
-  Prepare pr{G, type, n, m, ldg, strideg, part, parts, eps, sc.X, tall ? Xc : Xr, tall ? Xr : Xc,
-             tall ? L.cp : L.rp, tall ? L.rp : L.cp};
-  hipLaunchKernelGGL(prepare_kernel, dim3(pr.cols_pad / 64, pr.rows_pad / 64, batch), dim3(256), 0, st, pr);
+  OZ_TRY(launch_square_sum(type, G, n, m, ldg, strideg, batch, parts, part, st));
+  const Prepare pr{G, n, m, ldg, strideg, part, parts, eps, sc.X, X, tall ? L.cp : L.rp, tall ? L.rp : L.cp};
+  const dim3 blocks((unsigned)((xp / 8 + 256 * PREPARE_RUNS - 1) / (256 * PREPARE_RUNS)), batch);
+  if (type == OZGEMM_F32)
+    hipLaunchKernelGGL(prepare_kernel<OZGEMM_F32>, blocks, dim3(256), 0, st, pr);
+  else if (type == OZGEMM_BF16)
+    hipLaunchKernelGGL(prepare_kernel<OZGEMM_BF16>, blocks, dim3(256), 0, st, pr);
+  else
+    hipLaunchKernelGGL(prepare_kernel<OZGEMM_F16>, blocks, dim3(256), 0, st, pr);
   OZ_TRY(hipGetLastError());
-  auto launch = [&](const Step& p) {
-    return L.tile == 64 ? launch_step_t<64, 2, 2>(p, batch, st) : launch_step_t<128, 2, 2>(p, batch, st);
+  int which = 0;
+  auto launch = [&](const Step& p, bool aks, bool bks, bool sym) {
+    const char* ev = getenv("OZT");
+    int tile = ev ? ev[which % 3] : (p.m % 128 || p.n % 128) ? 'c' : 'b';
+    ++which;
+    if (nprod == 3) switch (tile) {
+      case 'b': return launch_step_t<128, 2, 2, 2, true>(p, aks, bks, sym, st);
+      case 'd': return launch_step_t<128, 2, 4, 2, true>(p, aks, bks, sym, st);
+      case 'c': return launch_step_t<64, 2, 2, 2, true>(p, aks, bks, sym, st);
+      default: return launch_step_t<64, 2, 2, 4, true>(p, aks, bks, sym, st);
+    }
+    switch (tile) {
+      case 'a': return launch_step_t<256, 2, 4, 2, false>(p, aks, bks, sym, st);
+      case 'b': return launch_step_t<128, 2, 2, 2, false>(p, aks, bks, sym, st);
+      case 'D': return launch_step_t<128, 2, 4, 4, false>(p, aks, bks, sym, st);
+      case 'd': return launch_step_t<128, 2, 4, 2, false>(p, aks, bks, sym, st);
+      case 'c': return launch_step_t<64, 2, 2, 2, false>(p, aks, bks, sym, st);
+      default: return launch_step_t<64, 2, 2, 4, false>(p, aks, bks, sym, st);
+    }
   };
   t = START;
   for (int k = 0; k < steps; ++k) {
     if (!scales_of(co, steps, k, &t, &sc)) return OZGEMM_RANGE;
     const double a = co[3 * k], b = co[3 * k + 1], c = co[3 * k + 2];
+    const int x_ld = tall ? L.rp : L.cp;
     Step p{};
-    p.nprod = nprod;
-    // P = X X^T
-    p.A = p.B = Xr;
+    p.batch = batch;
+    // P = X X^T along the c entries: next to each other in a wide X, a row apart in a tall one
+    p.A = p.B = X;
     p.a_batch = p.b_batch = 2 * xp;
     p.a_plane = p.b_plane = xp;
+    p.a_ld = p.b_ld = x_ld;
     p.m = p.n = L.rp;
     p.k = L.cp;
-    p.symmetric = 1;
     p.alpha = (float)(sc.P / (sc.X * sc.X));
-    p.N = p.T = P;
+    p.N = P;
     p.s_batch = 2 * pp;
     p.s_plane = pp;
-    p.n_lo = p.t_lo = lo;
-    OZ_TRY(launch(p));
+    p.n_lo = lo;
+    OZ_TRY(launch(p, tall, tall, true));
     // Q = b P + c P^2
     p.A = p.B = P;
     p.a_batch = p.b_batch = 2 * pp;
     p.a_plane = p.b_plane = pp;
+    p.a_ld = p.b_ld = L.rp;
     p.k = L.rp;
     p.alpha = (float)(c * sc.Q / (sc.P * sc.P));
     p.beta = (float)(b * sc.Q / sc.P);
     p.S = P;
     p.s_lo = lo;
-    p.N = p.T = Q;
-    OZ_TRY(launch(p));
-    // X <- a X + Q X: tall results lie c x r (rows of X^T against Q), wide ones r x c
-    p.A = tall ? Q : Xc;
-    p.B = tall ? Xc : Q;
+    p.N = Q;
+    OZ_TRY(launch(p, false, false, true));
+    // X <- a X + Q X along the r rows, the result as X lies: wide, its row j
+    // is row j of Q against X's columns; tall, row j of X against Q
+    p.A = tall ? Q : X;
+    p.B = tall ? X : Q;
     p.a_batch = tall ? 2 * pp : 2 * xp;
     p.a_plane = tall ? pp : xp;
+    p.a_ld = tall ? L.rp : x_ld;
     p.b_batch = tall ? 2 * xp : 2 * pp;
     p.b_plane = tall ? xp : pp;
+    p.b_ld = tall ? x_ld : L.rp;
     p.m = tall ? L.rp : L.cp;
     p.n = tall ? L.cp : L.rp;
-    p.symmetric = 0;
     const double next = k + 1 < steps ? sc.next : 1.0;  // the result itself is on no grid
     p.alpha = (float)(next / (sc.Q * sc.X));
     p.beta = (float)(a * next / sc.X);
-    p.S = tall ? Xc : Xr;
+    p.S = X;
     p.s_lo = 1;
-    p.N = tall ? Xc2 : Xr;
-    p.T = tall ? Xr : Xc2;
+    p.N = other;
     p.s_batch = 2 * xp;
     p.s_plane = xp;
     p.n_lo = 1;
-    p.t_lo = lo;
     if (k + 1 == steps) {
       p.O = O;
       p.otype = type;
@@ -585,10 +728,10 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
       p.om = m;
       p.on = n;
     }
-    OZ_TRY(launch(p));
-    uint16_t* swap = Xc;
-    Xc = Xc2;
-    Xc2 = swap;
+    OZ_TRY(launch(p, !tall, false, false));
+    uint16_t* swap = X;
+    X = other;
+    other = swap;
   }
   return OZGEMM_OK;
 }
@@ -658,8 +801,7 @@ int ozgemm_orthogonalize(int type, int batch, int m, int n, const void* G, int l
   if (steps == 0) {
     const int parts = square_parts(m, n);
     double* part = (double*)(ws + L.part);
-    hipLaunchKernelGGL(square_sum_kernel, dim3(parts, batch), dim3(256), 0, st, G, type, n, m, (long)ldg,
-                       (long)strideg, part);
+    OZ_TRY(launch_square_sum(type, G, n, m, ldg, (long)strideg, batch, parts, part, st));
     const long total = (long)m * n;
     hipLaunchKernelGGL(normalise_kernel, dim3((unsigned)((total + 255) / 256), batch), dim3(256), 0, st, G, type, n, m,
                        (long)ldg, (long)strideg, part, parts, eps, O, (long)ldo, (long)strideo);

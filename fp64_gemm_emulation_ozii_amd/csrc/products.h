@@ -30,7 +30,7 @@ struct Operand16 {
 struct Grouped16 {
   Operand16 A, B;
   int bf16;   // the slices' type: 1 bfloat16, 0 half
-  int nprod;  // 1, or 3 for two slices each
+  int f32;    // two half slices each
   int m, n, q, groups;
   const int32_t* offsets;
   void* C;

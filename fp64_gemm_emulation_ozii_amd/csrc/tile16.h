@@ -5,7 +5,7 @@
 //
 // An operand lies "K-contiguous" (row i at i ld, its entries next to each
 // other) or "K-strided" (entry (i, k) at k ld + i).  K slices of 64 entries
-// go from HBM straight into LDS (16 bytes per lane) through two buffers, in
+// go from HBM straight into LDS (16 bytes per lane) through NB buffers, in
 // the operand's own order; a K-strided tile is transposed on its way from
 // LDS into registers (ds_read_b64_tr_b16: 16 lanes read 4 x 16 entries and
 // each receives a column of 4).  The loads carry a range check: what lies
@@ -13,9 +13,10 @@
 // dimension of a K-contiguous row are sent past the end, so ragged edges
 // cost no branch and never meet their neighbours' values.
 //
-// An operand may come as two slices (hi + lo, see slices.hip); three slice
-// products lo hi, hi lo, hi hi (smallest first) are then walked as one long
-// K loop into the same accumulators.
+// An operand may come as two slices (hi + lo, see slices.hip).  A K slice then
+// holds both of both operands, and every step forms the three products lo hi,
+// hi lo, hi hi into the same accumulators: three MFMAs per pair of tiles for
+// four tiles loaded, where walking the products one after the other loads six.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -62,24 +63,43 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
-// This wave's LDS reads are done and its loads into LDS have landed; then
-// every wave's.
+// This wave's LDS reads are done and all but its last AHEAD loads into LDS
+// have landed; then every wave's.
+template <int AHEAD>
 __device__ __forceinline__ void slice_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-  wait_loads<0>();
+  wait_loads<AHEAD>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-template <class T, int BM, int BN, int WM, int WN, bool AKS, bool BKS>
+// Block b of `total` tiles, each XCD (b mod 8) taking a contiguous eighth.
+__device__ __forceinline__ int xcd_order(int b, int total) {
+  const int x = b & 7, per = total >> 3, rest = total & 7;
+  return x * per + min(x, rest) + (b >> 3);
+}
+
+// Inside its run an XCD walks `major` panels GROUP at a time against all of
+// `minor`, so the blocks running together share both operands' panels in L2.
+template <int GROUP>
+__device__ __forceinline__ void panel_order(int w, int major, int minor, int& a, int& b) {
+  const int first = w / (GROUP * minor) * GROUP;
+  const int in = w % (GROUP * minor);
+  const int g = min(GROUP, major - first);
+  a = first + in % g;
+  b = in / g;
+}
+
+template <class T, int BM, int BN, int WM, int WN, bool AKS, bool BKS, int NB = 2, bool PAIR = false>
 struct Tile16 {
   static constexpr int NW = WM * WN, WAVES_N = WN;
   static constexpr int THREADS = NW * 64;
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-  static constexpr int A_BYTES = BM * BK16 * 2, B_BYTES = BN * BK16 * 2;
-  static constexpr int BUF = A_BYTES + B_BYTES;
-  static constexpr int SMEM = 2 * BUF;
+  static constexpr int PLANES = PAIR ? 2 : 1;
+  static constexpr int A_BYTES = BM * BK16 * 2, B_BYTES = BN * BK16 * 2;  // of one slice of the operand
+  static constexpr int BUF = PLANES * (A_BYTES + B_BYTES);
+  static constexpr int SMEM = NB * BUF;
   static constexpr int A_LOADS = A_BYTES / 1024 / NW, B_LOADS = B_BYTES / 1024 / NW;
   static_assert(A_LOADS * NW * 1024 == A_BYTES && B_LOADS * NW * 1024 == B_BYTES, "whole wave loads");
   static_assert(FM * WM * 16 == BM && FN * WN * 16 == BN, "whole matrix-core tiles");
@@ -103,7 +123,8 @@ struct Tile16 {
   template <int ROWS, bool KS, int LOADS>
   struct Loader {
     const char* p;   // the slice to load: its base,
-    int records;     // the bytes that may be read from there
+    int records;     // the bytes that may be read from there,
+    long plane;      // the bytes from there to the low slice
     int ld;
     int off[2];      // lane's byte offset in an even and an odd load (K-contiguous)
     int kin[2];      // lane's first k within the slice
@@ -113,6 +134,7 @@ struct Tile16 {
 
     __device__ __forceinline__ void init(const Source16& s, int lane_, int wave_) {
       ld = s.ld;
+      plane = s.plane * 2;
       last = s.last;
       rows = min(s.rows, ROWS);
       lane = lane_;
@@ -150,9 +172,9 @@ struct Tile16 {
     // Past the last slice every load brings zeros.
     __device__ __forceinline__ void stop() { records = 0; }
 
-    __device__ __forceinline__ void load1(int li, char* lds) const {
+    __device__ __forceinline__ void load1(int li, int low, char* lds) const {
       const __amdgpu_buffer_rsrc_t rsrc =
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, records, 0x00020000);
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p + low * plane), 0, records, 0x00020000);
       const int blk = wave * LOADS + li;
       int voff;
       if (KS) {
@@ -193,22 +215,40 @@ struct Tile16 {
     }
   }
 
-  // The whole product of one tile; nprod is 1, or 3 for operands in two slices.
+  // MFMA slots of a step: per A fragment i its products with every B fragment,
+  // the pair's three kinds one after the other, smallest first.
+  static constexpr int KINDS = PAIR ? 3 : 1;
+  static constexpr int SLOTS = KINDS * FM * FN;
+  static constexpr int NF = PLANES * (FM + FN);  // fragments of a step: B's (high, low), then A's (high, low of each i)
+  static constexpr int LPW = PLANES * (A_LOADS + B_LOADS);
+
+  // the slot after which fragment f of the next step is read: A's right after their last use
+  static constexpr int read_slot(int f) {
+    if (f < PLANES * FN) return f * (SLOTS / (PLANES * FN)) + (SLOTS / (PLANES * FN) > 1);
+    const int i = (f - PLANES * FN) / PLANES, low = (f - PLANES * FN) % PLANES;
+    return (i * KINDS + (low ? 1 : KINDS)) * FN - 1;
+  }
+  static constexpr int load_slot(int li) { return li * SLOTS / LPW + (SLOTS > LPW); }
+
+  // The whole product of one tile.
   //
   // Order of a slice t (two steps of 32 k): the MFMAs of a step run in fixed
   // slots, and after each slot go the LDS reads of the next step's fragments
-  // (an A fragment right after its last use) and, in the second step, the
-  // loads of slice t + 2.  One barrier per slice, a quarter into the second
-  // step, whose MFMAs cover the latency of the last reads of buffer t mod 2;
-  // this wave's loads of slice t + 1, issued a whole slice earlier, have
-  // landed by then.  Reads of buffer t + 1 and loads into buffer t follow it.
-  static constexpr int BAR = FM * FN / 4 - 1;
-  // slot r of FM FN pressed into those after the barrier
-  static constexpr int after_barrier(int r) { return BAR + 1 + r * (FM * FN - BAR - 1) / (FM * FN); }
+  // and, in the second step, the loads of slice t + NB into the buffer of
+  // slice t.  One barrier per slice, a quarter into the second step, whose
+  // MFMAs cover the latency of the last reads of slice t; this wave's loads of
+  // slice t + 1, issued NB - 1 slices earlier, have landed by then (loads
+  // return in order; those of NB - 2 slices stay in flight).  Reads of slice
+  // t + 1 and the loads follow it.  Two buffers are enough where a slice takes
+  // longer than a load (256 x 256 tiles, or two 128 x 128 blocks on a compute
+  // unit); a lone small tile's slice is over long before, and it keeps more
+  // slices in flight.
+  static constexpr int BAR = SLOTS / 4 - 1;
+  // slot r pressed into those after the barrier
+  static constexpr int after_barrier(int r) { return BAR + 1 + r * (SLOTS - BAR - 1) / SLOTS; }
 
   static __device__ __forceinline__ void run(v4f (&acc)[FM][FN], char* smem, const Source16& A, const Source16& B,
-                                             int q, int nprod) {
-    constexpr int SLOTS = FM * FN, LPW = A_LOADS + B_LOADS;
+                                             int q) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -221,88 +261,82 @@ struct Tile16 {
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    const int nk = (q + BK16 - 1) / BK16;
-    const int total = nk * nprod;
+    const int total = (q + BK16 - 1) / BK16;
     if (total == 0) return;
-    // The slices in the order they are loaded: `left` entries of the inner
-    // dimension remain of product u.
-    int u = 0, left = q;
-    auto planes = [&]() {
-      la.start(A.base + (nprod == 3 && u == 0 ? A.plane : 0), q);
-      lb.start(B.base + (nprod == 3 && u == 1 ? B.plane : 0), q);
-    };
+    int left = q;  // entries of the inner dimension from the slice to load on
+    la.start(A.base, left);
+    lb.start(B.base, left);
     auto advance = [&]() {
       left -= BK16;
       la.next(left);
       lb.next(left);
       if (left <= 0) {
-        if (++u < nprod) {
-          left = q;
-          planes();
-        } else {
-          la.stop();
-          lb.stop();
-        }
+        la.stop();
+        lb.stop();
       }
     };
-    planes();
+    // a buffer: A's high (and low) tile, then B's
     auto load1 = [&](int buf, int li) {
       char* d = smem + buf * BUF;
-      if (li < A_LOADS)
-        la.load1(li, d);
+      if (li < PLANES * A_LOADS)
+        la.load1(li % A_LOADS, li / A_LOADS, d + li / A_LOADS * A_BYTES);
       else
-        lb.load1(li - A_LOADS, d + A_BYTES);
+        lb.load1((li - PLANES * A_LOADS) % B_LOADS, (li - PLANES * A_LOADS) / B_LOADS,
+                 d + PLANES * A_BYTES + (li - PLANES * A_LOADS) / B_LOADS * B_BYTES);
     };
-    // fragment f of step ks in buffer buf: f < FN are B's, the rest A's
     auto read1 = [&](int buf, int ks, int f) -> v8s {
       const char* As = smem + buf * BUF;
-      if (f < FN) return fragment<BN, BKS>(As + A_BYTES, lane, wn * (BN / WN) + f * 16, ks);
-      return fragment<BM, AKS>(As, lane, wm * (BM / WM) + (f - FN) * 16, ks);
+      if (f < PLANES * FN)
+        return fragment<BN, BKS>(As + PLANES * A_BYTES + f / FN * B_BYTES, lane, wn * (BN / WN) + f % FN * 16, ks);
+      const int i = (f - PLANES * FN) / PLANES, low = (f - PLANES * FN) % PLANES;
+      return fragment<BM, AKS>(As + low * A_BYTES, lane, wm * (BM / WM) + i * 16, ks);
     };
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int li = 0; li < LPW; ++li) load1(b, li);
       advance();
     }
-    wait_loads<LPW>();  // slice 0 (loads return in order)
+    wait_loads<(NB - 1) * LPW>();  // slice 0
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    v8s cur[FM + FN], nxt[FM + FN];
+    v8s cur[NF], nxt[NF];
 #pragma unroll
-    for (int f = 0; f < FM + FN; ++f) cur[f] = read1(0, 0, f);
+    for (int f = 0; f < NF; ++f) cur[f] = read1(0, 0, f);
     __builtin_amdgcn_s_waitcnt(0xc07f);
 
+    int buf = 0;
     for (int t = 0; t < total; ++t) {
+      const int following = buf + 1 == NB ? 0 : buf + 1;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const int rbuf = ks ? (t + 1) & 1 : t & 1;  // (past the end: zeros, not used)
+        const int rbuf = ks ? following : buf;  // (past the end: zeros, not used)
 #pragma unroll
         for (int r = 0; r < SLOTS; ++r) {
-          const int i = r / FN, j = r % FN;
-          acc[i][j] = T::mfma(cur[FN + i], cur[j], acc[i][j]);
+          const int i = r / (KINDS * FN), kind = r / FN % KINDS, j = r % FN;
+          const int fa = PLANES * FN + i * PLANES + (PAIR && kind == 0), fb = j + (PAIR && kind == 1 ? FN : 0);
+          acc[i][j] = T::mfma(cur[fa], cur[fb], acc[i][j]);
           __builtin_amdgcn_sched_barrier(0);
           if (ks && r == BAR) {
-            slice_barrier();
+            slice_barrier<(NB - 2) * LPW>();
             __builtin_amdgcn_sched_barrier(0);
           }
 #pragma unroll
-          for (int f = 0; f < FM + FN; ++f) {
-            const int slot = f < FN ? f * (SLOTS / FN) + 1 : (f - FN) * FN + FN - 1;
-            if ((ks ? after_barrier(slot) : slot) == r) nxt[f] = read1(rbuf, 1 - ks, f);
-          }
+          for (int f = 0; f < NF; ++f)
+            if ((ks ? after_barrier(read_slot(f)) : read_slot(f)) == r) nxt[f] = read1(rbuf, 1 - ks, f);
           if (ks) {
 #pragma unroll
             for (int li = 0; li < LPW; ++li)
-              if (after_barrier(li * SLOTS / LPW + (SLOTS > LPW)) == r) load1(t & 1, li);
+              if (after_barrier(load_slot(li)) == r) load1(buf, li);
             if (r == SLOTS - 1) advance();
           }
           __builtin_amdgcn_sched_barrier(0);
         }
         if (ks) __builtin_amdgcn_s_waitcnt(0xc07f);
 #pragma unroll
-        for (int f = 0; f < FM + FN; ++f) cur[f] = nxt[f];
+        for (int f = 0; f < NF; ++f) cur[f] = nxt[f];
       }
+      buf = following;
     }
   }
 };
