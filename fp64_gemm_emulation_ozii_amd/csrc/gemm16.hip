@@ -41,96 +41,172 @@ struct Target {
 // Each wavefront passes its accumulators 16 columns at a time through a piece
 // of LDS of its own and writes runs of 8 rows: 16 or 32 bytes per lane, a
 // column's runs next to each other.  (From the accumulators themselves a lane
-// would write 8-byte pieces of 16 different columns.)
+// would write 8-byte pieces of 16 different columns.)  The caller has seen to
+// it that nobody uses the pieces.
 template <class Tile>
-__device__ __forceinline__ void store_tile(const v4f (&acc)[Tile::FM][Tile::FN], char* smem, const Target& t) {
-  constexpr int WTM = Tile::FM * 16, PITCH = WTM + 4, RUNS = WTM / 8;
-  static_assert(Tile::NW * 16 * PITCH * 4 <= Tile::SMEM, "staging fits the operand buffers");
-  slice_barrier<0>();  // every wave has read its last operands
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  float* stage = reinterpret_cast<float*>(smem) + wave * 16 * PITCH;
-  const int mw = t.m0 + wave / Tile::WAVES_N * WTM, nw = t.n0 + wave % Tile::WAVES_N * (Tile::FN * 16);
-  const int size = t.ctype == OZGEMM_F32 ? 4 : 2;
-  const bool wide = (t.ldc & 7) == 0 && ((uintptr_t)t.C & 15) == 0;
-#pragma unroll
-  for (int j = 0; j < Tile::FN; ++j) {
-#pragma unroll
-    for (int i = 0; i < Tile::FM; ++i)
-      *reinterpret_cast<v4f*>(stage + (lane & 15) * PITCH + i * 16 + 4 * (lane >> 4)) = acc[i][j];
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // the wave's own writes; no other wave uses this piece
-    asm volatile("" ::: "memory");
-#pragma unroll 1
-    for (int at = lane; at < 16 * RUNS; at += 64) {
-      const int c = at / RUNS, r = at % RUNS * 8;
-      const int col = nw + j * 16 + c, row = mw + r;
-      if (col >= t.n_end || row >= t.m) continue;
-      float v[8];
-      *reinterpret_cast<v4f*>(v) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r);
-      *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r + 4);
-      if (t.ea != nullptr) {
-        const int eb = t.eb[col];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = unscale(v[k], t.ea[min(row + k, t.m - 1)], eb);
-      }
-      char* out = (char*)t.C + ((long)col * t.ldc + row) * size;
-      const bool whole = wide && row + 8 <= t.m;
-      if (t.ctype == OZGEMM_F32) {
-        if (whole) {
-          *reinterpret_cast<v4f*>(out) = v4f{v[0], v[1], v[2], v[3]};
-          *reinterpret_cast<v4f*>(out + 16) = v4f{v[4], v[5], v[6], v[7]};
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (row + k < t.m) reinterpret_cast<float*>(out)[k] = v[k];
-        }
-      } else {
-        v8s h;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = (short)round16(v[k], t.ctype);
-        if (whole) {
-          *reinterpret_cast<v8s*>(out) = h;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (row + k < t.m) reinterpret_cast<short*>(out)[k] = h[k];
-        }
-      }
-    }
-    __builtin_amdgcn_s_waitcnt(0xc07f);
-    asm volatile("" ::: "memory");
+struct Store {
+  static constexpr int WTM = Tile::FM * 16, PITCH = WTM + 4, RUNS = WTM / 8, CH = 16 * RUNS / 64;
+  static constexpr int BYTES = Tile::NW * 16 * PITCH * 4;
+  static_assert(16 * RUNS % 64 == 0, "whole wavefronts of runs");
+
+  // Whether every lane stores every run of a tile, as 16 bytes (16-bit types only).
+  static __device__ __forceinline__ bool whole(const Target& t, int bm, int bn) {
+    return t.ctype != OZGEMM_F32 && aligned(t) && t.m0 + bm <= t.m && t.n0 + bn <= t.n_end;
   }
+  static constexpr int STORES = Tile::FN * CH;  // per wavefront then
+  static __device__ __forceinline__ bool aligned(const Target& t) {
+    return (t.ldc & 7) == 0 && ((uintptr_t)t.C & 15) == 0;
+  }
+
+  static __device__ __forceinline__ void run(const v4f (&acc)[Tile::FM][Tile::FN], char* smem, const Target& t) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float* stage = reinterpret_cast<float*>(smem) + wave * 16 * PITCH;
+    const int mw = t.m0 + Tile::wave_m(wave) * WTM, nw = t.n0 + Tile::wave_n(wave) * (Tile::FN * 16);
+    const int size = t.ctype == OZGEMM_F32 ? 4 : 2;
+    const bool wide = aligned(t);
+#pragma unroll
+    for (int j = 0; j < Tile::FN; ++j) {
+#pragma unroll
+      for (int i = 0; i < Tile::FM; ++i)
+        *reinterpret_cast<v4f*>(stage + (lane & 15) * PITCH + i * 16 + 4 * (lane >> 4)) = acc[i][j];
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // the wave's own writes; no other wave uses this piece
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int ch = 0; ch < CH; ++ch) {
+        const int at = ch * 64 + lane, c = at / RUNS, r = at % RUNS * 8;
+        const int col = nw + j * 16 + c, row = mw + r;
+        if (col >= t.n_end || row >= t.m) continue;
+        float v[8];
+        *reinterpret_cast<v4f*>(v) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r);
+        *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r + 4);
+        if (t.ea != nullptr) {
+          const int eb = t.eb[col];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = unscale(v[k], t.ea[min(row + k, t.m - 1)], eb);
+        }
+        char* out = (char*)t.C + ((long)col * t.ldc + row) * size;
+        const bool all = wide && row + 8 <= t.m;
+        if (t.ctype == OZGEMM_F32) {
+          if (all) {
+            *reinterpret_cast<v4f*>(out) = v4f{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<v4f*>(out + 16) = v4f{v[4], v[5], v[6], v[7]};
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (row + k < t.m) reinterpret_cast<float*>(out)[k] = v[k];
+          }
+        } else {
+          v8s h;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[k] = (short)round16(v[k], t.ctype);
+          if (all) {
+            *reinterpret_cast<v8s*>(out) = h;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (row + k < t.m) reinterpret_cast<short*>(out)[k] = h[k];
+          }
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+      asm volatile("" ::: "memory");
+    }
+  }
+};
+
+// How `total` tiles are shared out over gridDim.x = 3 units blocks, one per
+// compute unit at a time.  The first `units` blocks walk whole rounds of
+// tiles; a round before the last, the next `units` blocks take one tile each
+// as units become free (tiles at the end of a group are cheaper than others);
+// what then remains is less than a round, and where it is no more than half
+// of one, its tiles are cut into quarters for the last blocks, or else taken
+// whole.
+struct Share {
+  int rounds;    // of the first blocks
+  int first;     // tile of this block, -1: none
+  int quarter;   // -1: the whole tile
+};
+
+__device__ __forceinline__ Share share_of(int total, int units, int block) {
+  const int rounds = max(total / units - 1, 0);
+  const int kept = rounds * units;
+  if (block < units) return Share{rounds, rounds > 0 ? block : -1, -1};
+  block -= units;
+  const int left = total - kept;  // less than two rounds
+  if (block < units) return Share{0, block < left ? kept + block : -1, -1};
+  block -= units;
+  const int rest = left - units;
+  if (rest <= 0) return Share{0, -1, -1};
+  if (rest * 2 <= units) return Share{0, block < rest * 4 ? kept + units + block / 4 : -1, block % 4};
+  return Share{0, block < rest ? kept + units + block : -1, -1};
 }
 
-template <class T, int BM, int BN, int WM, int WN, bool AKS, bool PAIR>
-__global__ __launch_bounds__(WM* WN * 64) void grouped_n_kernel(Grouped16 g) {
-  using Tile = Tile16<T, BM, BN, WM, WN, AKS, false, 2, PAIR>;
-  __shared__ __attribute__((aligned(1024))) char smem[Tile::SMEM];
-  const int tiles_m = (g.m + BM - 1) / BM;
-  const int tiles_n = count_group_tiles(g.offsets, g.groups, g.n, BN);
-  const long total = (long)tiles_m * tiles_n;
-  if (blockIdx.x >= total) return;
-  int nj, mi;
-  panel_order<4>(xcd_order(blockIdx.x, (int)total), tiles_n, tiles_m, nj, mi);
-  const GroupTile gt = find_group_tile(g.offsets, g.groups, g.n, BN, nj);
-  if (gt.group < 0) return;
-  const int m0 = mi * BM, n0 = gt.begin;
+// A block's tiles.  The next tile's first slice lands in buffer 0 while this
+// one's results go out through the LDS behind it, and its products begin
+// before they are written.
+template <class T, int BT, int NB_SMALL, bool AKS, bool PAIR>
+__global__ __launch_bounds__(512) void grouped_n_kernel(Grouped16 g) {
+  using Tile = Tile16<T, BT, BT, 2, 4, AKS, false, 2, PAIR>;
+  using Out = Store<Tile>;
+  using Small = Tile16<T, BT / 2, BT / 2, 2, 4, AKS, false, NB_SMALL, PAIR>;
+  constexpr int STAGE = Tile::BUF;
+  constexpr int SMEM = STAGE + (Tile::BUF > Out::BYTES ? Tile::BUF : Out::BYTES);
+  static_assert(Small::SMEM <= SMEM && Store<Small>::BYTES <= SMEM, "quarter tiles use the same LDS");
+  __shared__ __attribute__((aligned(1024))) char smem[SMEM];
+  const int tiles_m = (g.m + BT - 1) / BT;
+  const GroupIndex index(g.offsets, g.groups, g.n, BT);
+  const int total = tiles_m * index.total, units = gridDim.x / 3;
+  const Share share = share_of(total, units, blockIdx.x);
+  if (share.first < 0) return;
   Source16 A, B;
-  A.ld = (int)g.A.ld;
-  A.plane = g.A.plane;
-  A.base = g.A.p + gt.group * g.A.batch + (AKS ? (long)m0 : (long)m0 * g.A.ld);
-  A.rows = g.m - m0;
-  A.last = (int)g.A.last - (AKS ? m0 : 0);
-  B.ld = (int)g.B.ld;
-  B.plane = g.B.plane;
-  B.base = g.B.p + (long)n0 * g.B.ld;
-  B.rows = g.n - n0;
-  B.last = (int)g.B.last;
+  Target to;
+  auto place = [&](int L, int quarter, int side) {
+    int nj, mi;
+    panel_order<4>(xcd_order(L, total), index.total, tiles_m, nj, mi);
+    const GroupTile gt = index.find(nj);
+    const int m0 = mi * BT + (quarter & 1) * side, n0 = gt.begin + (quarter >> 1) * side;
+    A = Source16{g.A.p + gt.group * g.A.batch + (AKS ? (long)m0 : (long)m0 * g.A.ld), g.A.plane, (int)g.A.ld,
+                 g.m - m0, (int)g.A.last - (AKS ? m0 : 0)};
+    B = Source16{g.B.p + (long)n0 * g.B.ld, g.B.plane, (int)g.B.ld, gt.end - n0, (int)g.B.last};
+    to = Target{g.C, g.ctype, g.ldc, m0, g.m, n0, gt.end, g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr,
+                g.B.ex};
+  };
+  if (share.quarter >= 0) {
+    place(share.first, share.quarter, BT / 2);
+    if (to.m0 >= to.m || to.n0 >= to.n_end) return;
+    v4f acc[Small::FM][Small::FN];
+    Small::run(acc, smem, A, B, g.q);
+    slice_barrier<0>();
+    Store<Small>::run(acc, smem, to);
+    return;
+  }
+  typename Tile::Feed feed(smem);
+  place(share.first, 0, 0);
+  feed.begin(A, B, g.q);
+  feed.issue(0);
   v4f acc[Tile::FM][Tile::FN];
-  Tile::run(acc, smem, A, B, g.q);
-  store_tile<Tile>(acc, smem,
-                   Target{g.C, g.ctype, g.ldc, m0, g.m, n0, gt.end,
-                          g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr, g.B.ex});
+  bool whole = false;
+  for (int round = 1, L = share.first;; ++round) {
+    if (whole)
+      Tile::template resume<Out::STORES>(acc, feed, g.q, to.n_end - to.n0);
+    else
+      Tile::template resume<0>(acc, feed, g.q, to.n_end - to.n0);
+    const Target from = to;
+    slice_barrier<0>();  // every wave has read its last operands, and no load into LDS is in flight
+    const bool more = round < share.rounds;
+    if (more) {
+      L += units;
+      place(L, 0, 0);
+      feed.begin(A, B, g.q);
+      feed.issue(0);
+    }
+    Out::run(acc, smem + STAGE, from);
+    if (!more) break;
+    whole = Out::whole(from, BT, BT);
+    __builtin_amdgcn_s_barrier();  // every wave has read its staged results
+    asm volatile("" ::: "memory");
+  }
 }
 
 template <class T, int BM, int BN, int WM, int WN, bool KS, bool PAIR>
@@ -169,16 +245,20 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_k_kernel(Grouped16 g) {
   }
   v4f acc[Tile::FM][Tile::FN];
   Tile::run(acc, smem, A, B, inner);
+  slice_barrier<0>();  // every wave has read its last operands
   char* C = (char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2);
-  store_tile<Tile>(acc, smem,
+  static_assert(Store<Tile>::BYTES <= Tile::SMEM, "staging fits the operand buffers");
+  Store<Tile>::run(acc, smem,
                    Target{C, g.ctype, g.ldc, m0, g.m, q0, g.q, g.A.ex ? g.A.ex + e * g.A.ex_batch : nullptr,
                           g.B.ex ? g.B.ex + e * g.B.ex_batch : nullptr});
 }
 
-template <class T, int BT, bool AKS, bool PAIR>
+template <class T, int BT, int NB_SMALL, bool AKS, bool PAIR>
 hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
-  const long blocks = group_tiles_max(g.n, g.groups, BT) * ((g.m + BT - 1) / BT);
-  hipLaunchKernelGGL((grouped_n_kernel<T, BT, BT, 2, 4, AKS, PAIR>), dim3((unsigned)blocks), dim3(512), 0, st, g);
+  int cus = 0;
+  const hipError_t err = device_units(&cus);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL((grouped_n_kernel<T, BT, NB_SMALL, AKS, PAIR>), dim3(3 * cus), dim3(512), 0, st, g);
   return hipGetLastError();
 }
 
@@ -202,9 +282,9 @@ bool grouped_k_fits(const Grouped16& g) {
 
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
   if (g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
-  if (g.f32) return grouped_n<Half, 128, false, true>(g, st);
-  if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, true, false>(g, st) : grouped_n<Bfloat, 256, false, false>(g, st);
-  return g.A.ks ? grouped_n<Half, 256, true, false>(g, st) : grouped_n<Half, 256, false, false>(g, st);
+  if (g.f32) return grouped_n<Half, 128, 4, false, true>(g, st);
+  if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, 4, true, false>(g, st) : grouped_n<Bfloat, 256, 4, false, false>(g, st);
+  return g.A.ks ? grouped_n<Half, 256, 4, true, false>(g, st) : grouped_n<Half, 256, 4, false, false>(g, st);
 }
 
 hipError_t launch_grouped_k(const Grouped16& g, hipStream_t st) {

@@ -70,11 +70,6 @@ __device__ __forceinline__ int walk_groups(const int32_t* __restrict__ offsets, 
   return carry;
 }
 
-// Tiles of all groups.
-__device__ __forceinline__ int count_group_tiles(const int32_t* __restrict__ offsets, int groups, int n, int tile) {
-  return walk_groups(offsets, groups, n, tile, [](int, int, int, int) { return false; });
-}
-
 // The tile number idx in the order of the groups (called by whole
 // wavefronts; every lane gets the same answer).
 __device__ __forceinline__ GroupTile find_group_tile(const int32_t* __restrict__ offsets, int groups, int n, int tile,
@@ -111,5 +106,38 @@ __device__ __forceinline__ GroupTile group_at(const int32_t* __restrict__ offset
   });
   return t;
 }
+
+// The groups' tiles for a wavefront that looks up many: up to 64 groups are
+// walked once and kept, one per lane.
+struct GroupIndex {
+  const int32_t* offsets;
+  int groups, n, tile;
+  int lo, hi, upto;  // lane l: group l (groups <= 64)
+  int total;
+
+  __device__ __forceinline__ GroupIndex(const int32_t* o, int g, int nn, int t) : offsets(o), groups(g), n(nn), tile(t) {
+    total = __builtin_amdgcn_readfirstlane(walk_groups(offsets, groups, n, tile, [&](int, int l, int h, int u) {
+      lo = l;
+      hi = h;
+      upto = u;
+      return false;
+    }));
+  }
+
+  __device__ __forceinline__ GroupTile find(int idx) const {
+    if (groups > 64) return find_group_tile(offsets, groups, n, tile, idx);
+    GroupTile t{-1, 0, 0, 0, 0};
+    const unsigned long long over = __ballot(upto > idx);
+    if (over == 0) return t;
+    const int l = __ffsll(over) - 1;
+    t.group = l;
+    t.end = __builtin_amdgcn_readlane(hi, l);
+    const int begin = __builtin_amdgcn_readlane(lo, l);
+    t.first = __builtin_amdgcn_readlane(upto, l) - (t.end - begin + tile - 1) / tile;
+    t.tile = idx - t.first;
+    t.begin = begin + t.tile * tile;
+    return t;
+  }
+};
 
 }  // namespace oz

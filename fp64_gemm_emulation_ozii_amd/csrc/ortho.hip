@@ -302,7 +302,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* stage = reinterpret_cast<float*>(smem) + wave * 16 * PITCH;
-  const int mw = m0 + wave / WN * WTM, nw = n0 + wave % WN * (Tile::FN * 16);
+  const int mw = m0 + Tile::wave_m(wave) * WTM, nw = n0 + Tile::wave_n(wave) * (Tile::FN * 16);
   const uint16_t* S = p.S ? p.S + b * p.s_batch : nullptr;
   uint16_t* N = p.N + b * p.s_batch;
   const bool mirror = SYM && mi != nj;  // a diagonal tile holds both halves itself

@@ -69,6 +69,9 @@ hipError_t dgemm_region_table(char* region, int s, hipStream_t st);  // once bef
 int dgemm_region(char* region, int m, int n, int q, const double* A, int lda, const double* B, int ldb, double* C,
                  int ldc, int s, hipStream_t st);
 
+// Compute units of the current device.
+hipError_t device_units(int* cus);
+
 // Keep the name of a HIP error for ozgemm_strerror and return OZGEMM_HIP_ERROR.
 int record_hip_error(hipError_t err);
 

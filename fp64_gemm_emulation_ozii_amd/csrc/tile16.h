@@ -104,6 +104,13 @@ struct Tile16 {
   static_assert(A_LOADS * NW * 1024 == A_BYTES && B_LOADS * NW * 1024 == B_BYTES, "whole wave loads");
   static_assert(FM * WM * 16 == BM && FN * WN * 16 == BN, "whole matrix-core tiles");
 
+  // Which part of the tile a wavefront computes.  Wavefronts w and w + 4 share a
+  // SIMD; the columns' halves are dealt so that each SIMD has both, and a tile
+  // of which only the first half exists takes half the time (see resume).
+  static constexpr int HALF = WN > 1 ? WN / 2 : 1;
+  static __device__ __forceinline__ int wave_m(int wave) { return wave / HALF % WM; }
+  static __device__ __forceinline__ int wave_n(int wave) { return wave % HALF + wave / (HALF * WM) * HALF; }
+
   // K-contiguous rows of 128 bytes: 16-byte chunk c of row r sits at chunk
   // c ^ swz(r), so that the 16 rows of an operand read fall in different
   // 16-byte bank slots (as in the int8 product).
@@ -247,43 +254,71 @@ struct Tile16 {
   // slot r pressed into those after the barrier
   static constexpr int after_barrier(int r) { return BAR + 1 + r * (SLOTS - BAR - 1) / SLOTS; }
 
-  static __device__ __forceinline__ void run(v4f (&acc)[FM][FN], char* smem, const Source16& A, const Source16& B,
-                                             int q) {
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WN, wn = wave % WN;
+  // The loads of one tile's slices, in order.
+  struct Feed {
     Loader<BM, AKS, A_LOADS> la;
     Loader<BN, BKS, B_LOADS> lb;
-    la.init(A, lane, wave);
-    lb.init(B, lane, wave);
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    int left;  // entries of the inner dimension from the slice to load on
+    char* smem;
 
-    const int total = (q + BK16 - 1) / BK16;
-    if (total == 0) return;
-    int left = q;  // entries of the inner dimension from the slice to load on
-    la.start(A.base, left);
-    lb.start(B.base, left);
-    auto advance = [&]() {
-      left -= BK16;
-      la.next(left);
-      lb.next(left);
+    __device__ __forceinline__ Feed(char* lds) : smem(lds) {}
+
+    __device__ __forceinline__ void begin(const Source16& A, const Source16& B, int q) {
+      const int lane = threadIdx.x & 63;
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      la.init(A, lane, wave);
+      lb.init(B, lane, wave);
+      left = q;
+      la.start(A.base, left);
+      lb.start(B.base, left);
+      end();
+    }
+    __device__ __forceinline__ void end() {
       if (left <= 0) {
         la.stop();
         lb.stop();
       }
-    };
-    // a buffer: A's high (and low) tile, then B's
-    auto load1 = [&](int buf, int li) {
+    }
+    __device__ __forceinline__ void advance() {
+      left -= BK16;
+      la.next(left);
+      lb.next(left);
+      end();
+    }
+    // load li of a slice; a buffer holds A's high (and low) tile, then B's
+    __device__ __forceinline__ void load1(int buf, int li) const {
       char* d = smem + buf * BUF;
       if (li < PLANES * A_LOADS)
         la.load1(li % A_LOADS, li / A_LOADS, d + li / A_LOADS * A_BYTES);
       else
         lb.load1((li - PLANES * A_LOADS) % B_LOADS, (li - PLANES * A_LOADS) / B_LOADS,
                  d + PLANES * A_BYTES + (li - PLANES * A_LOADS) / B_LOADS * B_BYTES);
-    };
+    }
+    __device__ __forceinline__ void issue(int buf) {
+#pragma unroll
+      for (int li = 0; li < LPW; ++li) load1(buf, li);
+      advance();
+    }
+  };
+
+  static __device__ __forceinline__ void run(v4f (&acc)[FM][FN], char* smem, const Source16& A, const Source16& B,
+                                             int q) {
+    Feed feed(smem);
+    feed.begin(A, B, q);
+    feed.issue(0);
+    resume<0>(acc, feed, q, BN);
+  }
+
+  // The product of the tile whose slice 0 has been issued; LATER more memory
+  // operations may have followed it.  A wavefront whose columns all lie past
+  // the first `cols` only loads.
+  template <int LATER>
+  static __device__ __forceinline__ void resume(v4f (&acc)[FM][FN], Feed& feed, int q, int cols) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave_m(wave), wn = wave_n(wave);
+    const char* smem = feed.smem;
+    const int total = (q + BK16 - 1) / BK16;
     auto read1 = [&](int buf, int ks, int f) -> v8s {
       const char* As = smem + buf * BUF;
       if (f < PLANES * FN)
@@ -292,14 +327,23 @@ struct Tile16 {
       return fragment<BM, AKS>(As + low * A_BYTES, lane, wm * (BM / WM) + i * 16, ks);
     };
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    for (int b = 1; b < NB; ++b) feed.issue(b);
 #pragma unroll
-      for (int li = 0; li < LPW; ++li) load1(b, li);
-      advance();
-    }
-    wait_loads<(NB - 1) * LPW>();  // slice 0
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    wait_loads<(NB - 1) * LPW + LATER>();  // slice 0 (loads and stores leave the counter in order)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    if (wn * (BN / WN) >= cols) {
+      int buf = 0;
+      for (int t = 0; t < total; ++t) {
+        slice_barrier<(NB - 2) * LPW>();
+        feed.issue(buf);
+        buf = buf + 1 == NB ? 0 : buf + 1;
+      }
+      return;
+    }
     v8s cur[NF], nxt[NF];
 #pragma unroll
     for (int f = 0; f < NF; ++f) cur[f] = read1(0, 0, f);
@@ -327,8 +371,8 @@ struct Tile16 {
           if (ks) {
 #pragma unroll
             for (int li = 0; li < LPW; ++li)
-              if (after_barrier(load_slot(li)) == r) load1(buf, li);
-            if (r == SLOTS - 1) advance();
+              if (after_barrier(load_slot(li)) == r) feed.load1(buf, li);
+            if (r == SLOTS - 1) feed.advance();
           }
           __builtin_amdgcn_sched_barrier(0);
         }
