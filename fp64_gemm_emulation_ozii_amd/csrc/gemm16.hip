@@ -249,7 +249,7 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_k_kernel(Grouped16 g) {
   char* C = (char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2);
   static_assert(Store<Tile>::BYTES <= Tile::SMEM, "staging fits the operand buffers");
   Store<Tile>::run(acc, smem,
-                   Target{C, g.ctype, g.ldc, m0, g.m, q0, g.q, g.A.ex ? g.A.ex + e * g.A.ex_batch : nullptr,
+                   Target{C, g.ctype, g.ldc, m0, g.m, q0, g.q, g.A.ex && len > 0 ? g.A.ex + e * g.A.ex_batch : nullptr,
                           g.B.ex ? g.B.ex + e * g.B.ex_batch : nullptr});
 }
 

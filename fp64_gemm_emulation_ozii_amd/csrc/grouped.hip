@@ -37,6 +37,7 @@ struct Room {
   long ld;        // entries per row
   size_t plane;   // entries per slice
   size_t at, ex;  // offsets of the slices and of the exponents
+  size_t part;    // of the partial maxima of K-strided F32 entries
 };
 
 size_t take(size_t& total, size_t bytes) {
@@ -45,12 +46,15 @@ size_t take(size_t& total, size_t bytes) {
   return at;
 }
 
-Room room(int type, bool used, size_t rows, size_t k, size_t exponents, size_t& total) {
-  Room r{used, (long)up(k, 64), 0, 0, 0};
+Room room(int type, bool used, size_t rows, size_t k, size_t exponents, size_t part, size_t& total) {
+  Room r{used, (long)up(k, 64), 0, 0, 0, 0};
   if (!used) return r;
   r.plane = rows * (size_t)r.ld;
   r.at = take(total, r.plane * 2 * (type == OZGEMM_F32 ? 2 : 1));
-  if (type == OZGEMM_F32) r.ex = take(total, exponents * 4);
+  if (type == OZGEMM_F32) {
+    r.ex = take(total, exponents * 4);
+    r.part = take(total, part);
+  }
   return r;
 }
 
@@ -66,8 +70,9 @@ Rooms gemm_rooms(int type, int groups, int m, int n, int q, int transa, const vo
   const bool a_in_place = !f32 && aligned16(A, lda, stridea) && (transa ? q : m) % 8 == 0;
   const bool b_in_place = !f32 && aligned16(B, ldb, 0) && q % 8 == 0;
   const bool any = m > 0 && n > 0 && q > 0 && groups > 0;
-  r.A = room(type, any && !a_in_place, (size_t)groups * m, q, (size_t)groups * m, r.total);
-  r.B = room(type, any && !b_in_place, n, q, n, r.total);
+  r.A = room(type, any && !a_in_place, (size_t)groups * m, q, (size_t)groups * m,
+             transa ? 0 : slice_part_bytes(m, q, groups, false), r.total);
+  r.B = room(type, any && !b_in_place, n, q, n, 0, r.total);
   return r;
 }
 
@@ -77,8 +82,8 @@ Rooms outer_rooms(int type, int groups, int m, int q, int n, const void* A, int 
   const bool any = m > 0 && n > 0 && q > 0 && groups > 0;
   // every group's columns begin at a multiple of 64
   const size_t k = (size_t)n + 63 * (size_t)std::min(groups, n);
-  r.A = room(type, any && !in_place, m, k, (size_t)groups * m, r.total);
-  r.B = room(type, any && !in_place, q, k, (size_t)groups * q, r.total);
+  r.A = room(type, any && !in_place, m, k, (size_t)groups * m, slice_part_bytes(m, n, groups, true), r.total);
+  r.B = room(type, any && !in_place, q, k, (size_t)groups * q, slice_part_bytes(q, n, groups, true), r.total);
   return r;
 }
 
@@ -170,7 +175,8 @@ int ozgemm_grouped_gemm(int type, int ctype, int groups, int m, int n, int q, in
     if (transa)
       OZ_TRY(launch_slice_rows(type, A, lda, (long)stridea, groups, m, q, d, r.A.ld, (long)r.A.plane, ex, st));
     else
-      OZ_TRY(launch_slice_cols(type, A, lda, (long)stridea, groups, m, q, d, r.A.ld, (long)r.A.plane, ex, st));
+      OZ_TRY(launch_slice_cols(type, A, lda, (long)stridea, groups, m, q, d, r.A.ld, (long)r.A.plane, ex,
+                               (uint32_t*)(ws + r.A.part), st));
   }
   if (r.B.used) {
     g.B = sliced(type, r.B, ws, 0, 0);
@@ -237,9 +243,9 @@ int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n, c
     g.A = sliced(type, r.A, ws, 0, m);
     g.B = sliced(type, r.B, ws, 0, q);
     OZ_TRY(launch_slice_groups(type, A, lda, m, n, offsets, groups, (uint16_t*)(ws + r.A.at), r.A.ld,
-                               (long)r.A.plane, (int32_t*)(ws + r.A.ex), st));
+                               (long)r.A.plane, (int32_t*)(ws + r.A.ex), (uint32_t*)(ws + r.A.part), st));
     OZ_TRY(launch_slice_groups(type, B, ldb, q, n, offsets, groups, (uint16_t*)(ws + r.B.at), r.B.ld,
-                               (long)r.B.plane, (int32_t*)(ws + r.B.ex), st));
+                               (long)r.B.plane, (int32_t*)(ws + r.B.ex), (uint32_t*)(ws + r.B.part), st));
   }
   OZ_TRY(launch_grouped_k(g, st));
   return OZGEMM_OK;

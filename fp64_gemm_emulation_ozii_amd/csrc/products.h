@@ -53,13 +53,17 @@ hipError_t launch_grouped_k(const Grouped16& g, hipStream_t st);
 // rows x K, element (r, k) at src[r ld + k]; `batches` of them, `sbatch` apart
 hipError_t launch_slice_rows(int type, const void* src, long ld, long sbatch, int batches, int rows, int K,
                              uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st);
-// element (r, k) at src[k ld + r], `batches` of them, `sbatch` apart
+// element (r, k) at src[k ld + r], `batches` of them, `sbatch` apart; part:
+// slice_part_bytes of scratch (F32)
 hipError_t launch_slice_cols(int type, const void* src, long ld, long sbatch, int batches, int rows, int K,
-                             uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st);
+                             uint16_t* dst, long dld, long plane, int32_t* ex, uint32_t* part, hipStream_t st);
+size_t slice_part_bytes(int rows, long K, int groups, bool ragged);
 // element (r, k) at src[k ld + r], k in groups that begin at offsets[e]; group
-// e's rows begin at 64 x (its 64-tiles before); ex[e rows + r]
+// e's rows begin at 64 x (its 64-tiles before); ex[e rows + r], not written for
+// a group without k
 hipError_t launch_slice_groups(int type, const void* src, long ld, int rows, int n, const int32_t* offsets,
-                               int groups, uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st);
+                               int groups, uint16_t* dst, long dld, long plane, int32_t* ex, uint32_t* part,
+                               hipStream_t st);
 
 // ozgemm.hip: Scheme II products in a region of a caller's workspace
 // (conservative budget, no configuration; the region holds every product of

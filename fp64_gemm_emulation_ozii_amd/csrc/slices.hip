@@ -13,17 +13,15 @@
 // per row of A and column of B); as there, a row holding Inf or NaN gets
 // OZGEMM_EXP_NONFINITE and zero slices.
 //
-// The passes are bound by HBM: each entry is read once (the row maxima of
-// K-contiguous rows twice, the second time from L2) and each plane written
-// once.
+// The passes are bound by HBM: each plane is written once and each entry read
+// once (twice where its row is K-strided or longer than a wavefront's
+// registers hold: the maximum has to be known first).
 #include "groups.h"
 #include "products.h"
 
 namespace oz {
 
 namespace {
-
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 // frexp exponent of a float's |.| bit pattern; 0 for zero, the flag for Inf and NaN
 __device__ __forceinline__ int exponent32(uint32_t b) {
@@ -33,73 +31,118 @@ __device__ __forceinline__ int exponent32(uint32_t b) {
   return biased > 0 ? biased - 126 : (31 - __clz((int)b)) - 148;
 }
 
-// bits of one entry, widened to 32 (16-bit types travel as they are)
+// Four entries next to each other as 32-bit patterns (16-bit types travel as
+// they are), zeros past `left`.
 template <int TYPE>
-__device__ __forceinline__ uint32_t load_bits(const void* src, long at) {
-  return TYPE == OZGEMM_F32 ? ((const uint32_t*)src)[at] : ((const uint16_t*)src)[at];
+__device__ __forceinline__ void load4(const void* src, long at, int left, bool wide, uint32_t (&v)[4]) {
+  if (TYPE == OZGEMM_F32) {
+    const uint32_t* p = (const uint32_t*)src + at;
+    if (wide && left >= 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0;
+  } else {
+    const uint16_t* p = (const uint16_t*)src + at;
+    if (wide && left >= 4) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      v[0] = x.x & 0xffffu, v[1] = x.x >> 16, v[2] = x.y & 0xffffu, v[3] = x.y >> 16;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0;
+  }
 }
 
+// Whether every run of four that begins at a multiple of four of a row lies aligned.
 template <int TYPE>
-__device__ __forceinline__ void slices_of(uint32_t bits, int e, uint16_t& hi, uint16_t& lo) {
-  if (TYPE != OZGEMM_F32) {
-    hi = (uint16_t)bits;
-    lo = 0;
-    return;
-  }
-  if (e == OZGEMM_EXP_NONFINITE) {
-    hi = lo = 0;
-    return;
-  }
+__device__ __forceinline__ bool wide_runs(const void* src, long base, long ld) {
+  return ((uintptr_t)src & (TYPE == OZGEMM_F32 ? 15 : 7)) == 0 && (base & 3) == 0 && (ld & 3) == 0;
+}
+
+// hi in the low half, lo in the high one (16-bit types: the entry itself)
+template <int TYPE>
+__device__ __forceinline__ uint32_t slices_of(uint32_t bits, int e) {
+  if (TYPE != OZGEMM_F32) return bits;
+  if (e == OZGEMM_EXP_NONFINITE) return 0;
   const float y = __builtin_ldexpf(__builtin_bit_cast(float, bits), 15 - e);
   const _Float16 h = (_Float16)y;
-  hi = __builtin_bit_cast(uint16_t, h);
-  lo = __builtin_bit_cast(uint16_t, (_Float16)(y - (float)h));
+  return __builtin_bit_cast(uint16_t, h) |
+         ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)(y - (float)h)) << 16);
 }
 
-// One block per row: its maximum, then its slices.
+// The high halves and the low halves of four slices as two words each.
+__device__ __forceinline__ uint2 lows(const uint32_t (&s)[4]) {
+  return uint2{(s[0] & 0xffffu) | (s[1] << 16), (s[2] & 0xffffu) | (s[3] << 16)};
+}
+__device__ __forceinline__ uint2 highs(const uint32_t (&s)[4]) {
+  return uint2{(s[0] >> 16) | (s[1] & 0xffff0000u), (s[2] >> 16) | (s[3] & 0xffff0000u)};
+}
+
 template <int TYPE>
+__device__ __forceinline__ void put4(uint16_t* out, long plane, uint32_t (&v)[4], int e) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = slices_of<TYPE>(v[i], e);
+  *reinterpret_cast<uint2*>(out) = lows(v);
+  if (TYPE == OZGEMM_F32) *reinterpret_cast<uint2*>(out + plane) = highs(v);
+}
+
+// K-contiguous rows, a wavefront each: RUNS runs of four entries per lane are
+// kept in registers between the row's maximum and its slices, so a row of up
+// to 256 RUNS entries is read once; longer rows are read twice.
+template <int TYPE, int RUNS>
 __global__ __launch_bounds__(256) void slice_rows_kernel(const void* __restrict__ src, long ld, long sbatch, int rows,
-                                                         int K, uint16_t* __restrict__ dst, long dld, long plane,
-                                                         int32_t* __restrict__ ex) {
-  const long row = blockIdx.x;
+                                                         long total, int K, uint16_t* __restrict__ dst, long dld,
+                                                         long plane, int32_t* __restrict__ ex) {
+  const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= total) return;
   const long from = row / rows * sbatch + row % rows * ld;
+  const bool wide = wide_runs<TYPE>(src, sbatch, ld);
   uint16_t* out = dst + row * dld;
   const int Kp = (K + 63) / 64 * 64;
-  int e = 0;
-  if (TYPE == OZGEMM_F32) {
-    uint32_t mx = 0;
-    for (int k = threadIdx.x; k < K; k += 256) mx = max(mx, load_bits<TYPE>(src, from + k) & 0x7fffffffu);
-    __shared__ uint32_t part[4];
+  uint32_t v[RUNS][4];
+  uint32_t mx = 0;
+  const bool once = Kp <= 256 * RUNS;
+  for (int k0 = 0; k0 < Kp; k0 += 256 * RUNS) {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = mx;
-    __syncthreads();
-    e = exponent32(max(max(part[0], part[1]), max(part[2], part[3])));
-    if (threadIdx.x == 0) ex[row] = e;
+    for (int i = 0; i < RUNS; ++i) load4<TYPE>(src, from + k0 + i * 256 + lane * 4, K - k0 - i * 256 - lane * 4, wide, v[i]);
+    if (TYPE != OZGEMM_F32) {
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i)
+        if (k0 + i * 256 + lane * 4 < Kp) put4<TYPE>(out + k0 + i * 256 + lane * 4, plane, v[i], 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx = max(mx, v[i][j] & 0x7fffffffu);
+    }
   }
-  for (int k = threadIdx.x * 2; k < Kp; k += 512) {
-    uint16_t h0 = 0, l0 = 0, h1 = 0, l1 = 0;
-    if (k < K) slices_of<TYPE>(load_bits<TYPE>(src, from + k), e, h0, l0);
-    if (k + 1 < K) slices_of<TYPE>(load_bits<TYPE>(src, from + k + 1), e, h1, l1);
-    *reinterpret_cast<uint32_t*>(out + k) = h0 | ((uint32_t)h1 << 16);
-    if (TYPE == OZGEMM_F32) *reinterpret_cast<uint32_t*>(out + plane + k) = l0 | ((uint32_t)l1 << 16);
+  if (TYPE != OZGEMM_F32) return;
+#pragma unroll
+  for (int d = 32; d; d >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, d));
+  const int e = exponent32(mx);
+  if (lane == 0) ex[row] = e;
+  for (int k0 = 0; k0 < Kp; k0 += 256 * RUNS) {
+    if (!once) {
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) load4<TYPE>(src, from + k0 + i * 256 + lane * 4, K - k0 - i * 256 - lane * 4, wide, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i)
+      if (k0 + i * 256 + lane * 4 < Kp) put4<TYPE>(out + k0 + i * 256 + lane * 4, plane, v[i], e);
   }
 }
 
-__global__ __launch_bounds__(256) void fill_exponents_kernel(int32_t* __restrict__ ex, long n) {
-  const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) ex[i] = 0;
-}
-
-// The columns' maxima bits into ex (as unsigned integers; zero before), one
-// block per 64 rows r and CHUNK k.  With offsets, the k of group e; else
-// batch e's.
-constexpr int CHUNK = 256;
-
+// Tiles of TILE k: with offsets, of the ragged groups; else of `groups`
+// matrices of K each.
 struct KRange {
   int group;
   int k0, k1;   // within the source
   long dst_k;   // where k0 lands in a destination row
+  int tile;     // the tile's place in its group
 };
 
 template <int TILE>
@@ -107,115 +150,171 @@ __device__ __forceinline__ KRange k_range(const int32_t* offsets, int groups, in
   if (offsets == nullptr) {
     const int per = (K + TILE - 1) / TILE;
     const int b = idx / per, t = idx % per;
-    return KRange{b, t * TILE, min(K, (t + 1) * TILE), (long)t * TILE};
+    return KRange{b, t * TILE, min(K, (t + 1) * TILE), (long)t * TILE, t};
   }
   const GroupTile g = find_group_tile(offsets, groups, K, TILE, idx);
-  return KRange{g.group, g.begin, min(g.end, g.begin + TILE), (long)idx * TILE};
+  return KRange{g.group, g.begin, min(g.end, g.begin + TILE), (long)idx * TILE, g.tile};
 }
+
+// Bits of the largest |entry| of every column r of a tile of CHUNK k, one
+// block per 256 columns: part[tile][r].
+constexpr int CHUNK = 256;
 
 __global__ __launch_bounds__(256) void column_max_kernel(const float* __restrict__ src, long ld, long sbatch,
                                                          int rows, int K, const int32_t* __restrict__ offsets,
-                                                         int groups, uint32_t* __restrict__ ex) {
+                                                         int groups, uint32_t* __restrict__ part) {
   const KRange g = k_range<CHUNK>(offsets, groups, K, blockIdx.x);
   if (g.group < 0) return;
-  const int r = blockIdx.y * 64 + (threadIdx.x & 63);
-  const uint32_t* p = (const uint32_t*)src + (offsets ? 0 : g.group * sbatch);
-  uint32_t mx = 0;
-  if (r < rows)
-    for (int k = g.k0 + (threadIdx.x >> 6); k < g.k1; k += 4) mx = max(mx, p[(long)k * ld + r] & 0x7fffffffu);
-  __shared__ uint32_t part[4][64];
-  part[threadIdx.x >> 6][threadIdx.x & 63] = mx;
-  __syncthreads();
-  if (threadIdx.x < 64 && r < rows) {
-    mx = max(max(part[0][threadIdx.x], part[1][threadIdx.x]), max(part[2][threadIdx.x], part[3][threadIdx.x]));
-    if (mx) atomicMax(ex + (long)g.group * rows + r, mx);  // a maximum: the order does not matter
+  const int lane = threadIdx.x & 63, r = blockIdx.y * 256 + lane * 4;
+  const long base = offsets ? 0 : g.group * sbatch;
+  const bool wide = wide_runs<OZGEMM_F32>(src, base, ld);
+  uint32_t mx[4] = {0, 0, 0, 0};
+  if (r < rows) {
+    // eight loads in flight; a k past the end reads the last one again
+    for (int k = g.k0 + (threadIdx.x >> 6); k < g.k1; k += 32) {
+      uint32_t v[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load4<OZGEMM_F32>(src, base + (long)min(k + 4 * i, g.k1 - 1) * ld + r, rows - r, wide, v[i]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = max(mx[j], v[i][j] & 0x7fffffffu);
+    }
   }
+  __shared__ uint32_t s[4][256];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s[threadIdx.x >> 6][lane * 4 + j] = mx[j];
+  __syncthreads();
+  const int c = blockIdx.y * 256 + threadIdx.x;
+  if (c < rows)
+    part[(long)blockIdx.x * rows + c] = max(max(s[0][threadIdx.x], s[1][threadIdx.x]), max(s[2][threadIdx.x], s[3][threadIdx.x]));
 }
 
-__global__ __launch_bounds__(256) void exponents_kernel(int32_t* __restrict__ ex, long n) {
-  const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) ex[i] = exponent32((uint32_t)ex[i]);
-}
-
-// A 64 x 64 tile of K-strided entries, transposed through LDS.
+// A 64 x 64 tile of K-strided entries, cut into slices and transposed through
+// LDS.  The columns' exponents come from the partial maxima of the group's
+// chunks; the group's first tile writes them down.
 template <int TYPE>
 __global__ __launch_bounds__(256) void slice_cols_kernel(const void* __restrict__ src, long ld, long sbatch, int rows,
                                                          int K, const int32_t* __restrict__ offsets, int groups,
                                                          uint16_t* __restrict__ dst, long dld, long plane,
-                                                         const int32_t* __restrict__ ex) {
+                                                         int32_t* __restrict__ ex, const uint32_t* __restrict__ part) {
   const KRange g = k_range<64>(offsets, groups, K, blockIdx.x);
   if (g.group < 0) return;
   __shared__ uint32_t tile[64][65];
+  __shared__ uint32_t most[4][64];
   const int r0 = blockIdx.y * 64;
   const long from = offsets ? 0 : g.group * sbatch;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int k = i >> 6, r = i & 63;
-    tile[k][r] = g.k0 + k < g.k1 && r0 + r < rows ? load_bits<TYPE>(src, from + (long)(g.k0 + k) * ld + r0 + r) : 0;
+  const bool wide = wide_runs<TYPE>(src, from, ld);
+  const int rr = (threadIdx.x & 15) * 4, kk = threadIdx.x >> 4;
+  uint32_t v[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = g.k0 + kk + 16 * i;
+    load4<TYPE>(src, from + (long)k * ld + r0 + rr, k < g.k1 ? rows - r0 - rr : 0, wide, v[i]);
   }
+  if (TYPE == OZGEMM_F32) {
+    int first, count;
+    if (offsets) {
+      const GroupTile c = group_at(offsets, groups, K, CHUNK, g.group);
+      first = c.first;
+      count = (c.end - c.begin + CHUNK - 1) / CHUNK;
+    } else {
+      count = (K + CHUNK - 1) / CHUNK;
+      first = g.group * count;
+    }
+    const int r = threadIdx.x & 63;
+    uint32_t mx = 0;
+    if (r0 + r < rows)
+      for (int c = threadIdx.x >> 6; c < count; c += 4) mx = max(mx, part[(long)(first + c) * rows + r0 + r]);
+    most[threadIdx.x >> 6][r] = mx;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      const int e = exponent32(max(max(most[0][r], most[1][r]), max(most[2][r], most[3][r])));
+      most[0][r] = (uint32_t)e;
+      if (g.tile == 0 && r0 + r < rows) ex[(long)g.group * rows + r0 + r] = e;
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      tile[kk + 16 * i][rr + j] = slices_of<TYPE>(v[i][j], TYPE == OZGEMM_F32 ? (int)most[0][rr + j] : 0);
   __syncthreads();
   uint16_t* base = dst + (offsets ? 0 : (long)g.group * rows * dld) + g.dst_k;
-  for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-    const int r = i >> 5, k = (i & 31) * 2;
-    if (r0 + r < rows) {
-      const int e = TYPE == OZGEMM_F32 ? ex[(long)g.group * rows + r0 + r] : 0;
-      uint16_t h0, l0, h1, l1;
-      slices_of<TYPE>(tile[k][r], e, h0, l0);
-      slices_of<TYPE>(tile[k + 1][r], e, h1, l1);
-      uint16_t* out = base + (long)(r0 + r) * dld + k;
-      *reinterpret_cast<uint32_t*>(out) = h0 | ((uint32_t)h1 << 16);
-      if (TYPE == OZGEMM_F32) *reinterpret_cast<uint32_t*>(out + plane) = l0 | ((uint32_t)l1 << 16);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int i = half * 256 + threadIdx.x, r = i >> 3, k = (i & 7) * 8;
+    if (r0 + r >= rows) continue;
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = tile[k + j][r];
+      b[j] = tile[k + 4 + j][r];
+    }
+    uint16_t* out = base + (long)(r0 + r) * dld + k;
+    const uint2 la = lows(a), lb = lows(b);
+    *reinterpret_cast<uint4*>(out) = uint4{la.x, la.y, lb.x, lb.y};
+    if (TYPE == OZGEMM_F32) {
+      const uint2 ha = highs(a), hb = highs(b);
+      *reinterpret_cast<uint4*>(out + plane) = uint4{ha.x, ha.y, hb.x, hb.y};
     }
   }
 }
 
+long k_tiles(const int32_t* offsets, long K, long groups, long tile) {
+  return offsets ? group_tiles_max(K, groups, tile) : (K + tile - 1) / tile * groups;
+}
+
 hipError_t slice_cols(int type, const void* src, long ld, long sbatch, int rows, int K, const int32_t* offsets,
-                      int groups, uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st) {
+                      int groups, uint16_t* dst, long dld, long plane, int32_t* ex, uint32_t* part, hipStream_t st) {
   if (rows < 1 || K < 1 || groups < 1) return hipSuccess;
-  const unsigned rt = (unsigned)((rows + 63) / 64);
-  const auto tiles = [&](long tile) {
-    return offsets ? group_tiles_max(K, groups, tile) : (K + tile - 1) / tile * groups;
-  };
-  if (tiles(64) > 0x7fffffffL || rt > 65535) return hipErrorInvalidValue;
+  const dim3 tiles((unsigned)k_tiles(offsets, K, groups, 64), (unsigned)((rows + 63) / 64));
   if (type == OZGEMM_F32) {
-    const long n = (long)groups * rows;
-    const dim3 g1((unsigned)((n + 255) / 256));
-    hipLaunchKernelGGL(fill_exponents_kernel, g1, dim3(256), 0, st, ex, n);
-    hipLaunchKernelGGL(column_max_kernel, dim3((unsigned)tiles(CHUNK), rt), dim3(256), 0, st, (const float*)src, ld,
-                       sbatch, rows, K, offsets, groups, (uint32_t*)ex);
-    hipLaunchKernelGGL(exponents_kernel, g1, dim3(256), 0, st, ex, n);
-    hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F32>, dim3((unsigned)tiles(64), rt), dim3(256), 0, st, src, ld,
-                       sbatch, rows, K, offsets, groups, dst, dld, plane, ex);
+    hipLaunchKernelGGL(column_max_kernel, dim3((unsigned)k_tiles(offsets, K, groups, CHUNK), (unsigned)((rows + 255) / 256)),
+                       dim3(256), 0, st, (const float*)src, ld, sbatch, rows, K, offsets, groups, part);
+    hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F32>, tiles, dim3(256), 0, st, src, ld, sbatch, rows, K, offsets,
+                       groups, dst, dld, plane, ex, part);
   } else {
-    hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F16>, dim3((unsigned)tiles(64), rt), dim3(256), 0, st, src, ld,
-                       sbatch, rows, K, offsets, groups, dst, dld, plane, ex);
+    hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F16>, tiles, dim3(256), 0, st, src, ld, sbatch, rows, K, offsets,
+                       groups, dst, dld, plane, ex, part);
   }
+  return hipGetLastError();
+}
+
+template <int TYPE, int RUNS>
+hipError_t slice_rows(const void* src, long ld, long sbatch, int rows, long total, int K, uint16_t* dst, long dld,
+                      long plane, int32_t* ex, hipStream_t st) {
+  hipLaunchKernelGGL((slice_rows_kernel<TYPE, RUNS>), dim3((unsigned)((total + 3) / 4)), dim3(256), 0, st, src, ld,
+                     sbatch, rows, total, K, dst, dld, plane, ex);
   return hipGetLastError();
 }
 
 }  // namespace
 
+size_t slice_part_bytes(int rows, long K, int groups, bool ragged) {
+  return (size_t)k_tiles(ragged ? (const int32_t*)1 : nullptr, K, groups, CHUNK) * rows * 4;
+}
+
 hipError_t launch_slice_rows(int type, const void* src, long ld, long sbatch, int batches, int rows, int K,
                              uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st) {
   if (rows < 1 || batches < 1 || K < 1) return hipSuccess;
   const long n = (long)rows * batches;
-  if (n > 0x7fffffffL) return hipErrorInvalidValue;
-  if (type == OZGEMM_F32)
-    hipLaunchKernelGGL(slice_rows_kernel<OZGEMM_F32>, dim3((unsigned)n), dim3(256), 0, st, src, ld, sbatch, rows, K,
-                       dst, dld, plane, ex);
-  else
-    hipLaunchKernelGGL(slice_rows_kernel<OZGEMM_F16>, dim3((unsigned)n), dim3(256), 0, st, src, ld, sbatch, rows, K,
-                       dst, dld, plane, ex);
-  return hipGetLastError();
+  if (type != OZGEMM_F32) return slice_rows<OZGEMM_F16, 4>(src, ld, sbatch, rows, n, K, dst, dld, plane, ex, st);
+  if (K <= 1024) return slice_rows<OZGEMM_F32, 4>(src, ld, sbatch, rows, n, K, dst, dld, plane, ex, st);
+  if (K <= 2048) return slice_rows<OZGEMM_F32, 8>(src, ld, sbatch, rows, n, K, dst, dld, plane, ex, st);
+  return slice_rows<OZGEMM_F32, 16>(src, ld, sbatch, rows, n, K, dst, dld, plane, ex, st);
 }
 
 hipError_t launch_slice_cols(int type, const void* src, long ld, long sbatch, int batches, int rows, int K,
-                             uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st) {
-  return slice_cols(type, src, ld, sbatch, rows, K, nullptr, batches, dst, dld, plane, ex, st);
+                             uint16_t* dst, long dld, long plane, int32_t* ex, uint32_t* part, hipStream_t st) {
+  return slice_cols(type, src, ld, sbatch, rows, K, nullptr, batches, dst, dld, plane, ex, part, st);
 }
 
 hipError_t launch_slice_groups(int type, const void* src, long ld, int rows, int n, const int32_t* offsets,
-                               int groups, uint16_t* dst, long dld, long plane, int32_t* ex, hipStream_t st) {
-  return slice_cols(type, src, ld, 0, rows, n, offsets, groups, dst, dld, plane, ex, st);
+                               int groups, uint16_t* dst, long dld, long plane, int32_t* ex, uint32_t* part,
+                               hipStream_t st) {
+  return slice_cols(type, src, ld, 0, rows, n, offsets, groups, dst, dld, plane, ex, part, st);
 }
 
 }  // namespace oz
