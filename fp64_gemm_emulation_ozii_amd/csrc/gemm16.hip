@@ -142,130 +142,131 @@ __device__ __forceinline__ Share share_of(int total, int units, int block) {
   return Share{0, block < rest ? kept + units + block : -1, -1};
 }
 
+// A tile to compute: its operands, its inner dimension and where it goes.
+struct Job {
+  Source16 A, B;
+  int inner;
+  Target to;
+};
+
 // A block's tiles.  The next tile's first slice lands in buffer 0 while this
 // one's results go out through the LDS behind it, and its products begin
-// before they are written.
-template <class T, int BT, int NB_SMALL, bool AKS, bool PAIR>
-__global__ __launch_bounds__(512) void grouped_n_kernel(Grouped16 g) {
-  using Tile = Tile16<T, BT, BT, 2, 4, AKS, false, 2, PAIR>;
+// before they are written.  place(L, dm, dn) gives the job of tile L from
+// (dm, dn) in it on.
+template <class Tile, class Small>
+struct Walk {
   using Out = Store<Tile>;
-  using Small = Tile16<T, BT / 2, BT / 2, 2, 4, AKS, false, NB_SMALL, PAIR>;
-  constexpr int STAGE = Tile::BUF;
-  constexpr int SMEM = STAGE + (Tile::BUF > Out::BYTES ? Tile::BUF : Out::BYTES);
+  static constexpr int STAGE = Tile::BUF;
+  static constexpr int SMEM = STAGE + (Tile::BUF > Out::BYTES ? Tile::BUF : Out::BYTES);
   static_assert(Small::SMEM <= SMEM && Store<Small>::BYTES <= SMEM, "quarter tiles use the same LDS");
-  __shared__ __attribute__((aligned(1024))) char smem[SMEM];
+
+  template <class Place>
+  static __device__ __forceinline__ void run(char* smem, int total, Place place) {
+    constexpr int BT = Tile::ROWS_M;
+    static_assert(BT == Tile::ROWS_N && BT == 2 * Small::ROWS_M && BT == 2 * Small::ROWS_N, "square tiles and quarters");
+    const int units = gridDim.x / 3;
+    const Share share = share_of(total, units, blockIdx.x);
+    if (share.first < 0) return;
+    if (share.quarter >= 0) {
+      const Job job = place(share.first, (share.quarter & 1) * (BT / 2), (share.quarter >> 1) * (BT / 2));
+      if (job.to.m0 >= job.to.m || job.to.n0 >= job.to.n_end) return;
+      v4f acc[Small::FM][Small::FN];
+      Small::run(acc, smem, job.A, job.B, job.inner);
+      slice_barrier<0>();
+      Store<Small>::run(acc, smem, job.to);
+      return;
+    }
+    typename Tile::Feed feed(smem);
+    Job job = place(share.first, 0, 0);
+    feed.begin(job.A, job.B, job.inner);
+    feed.issue(0);
+    v4f acc[Tile::FM][Tile::FN];
+    bool whole = false;
+    for (int round = 1, L = share.first;; ++round) {
+      if (whole)
+        Tile::template resume<Out::STORES>(acc, feed, job.inner, job.to.n_end - job.to.n0);
+      else
+        Tile::template resume<0>(acc, feed, job.inner, job.to.n_end - job.to.n0);
+      const Target from = job.to;
+      slice_barrier<0>();  // every wave has read its last operands, and no load into LDS is in flight
+      const bool more = round < share.rounds;
+      if (more) {
+        L += units;
+        job = place(L, 0, 0);
+        feed.begin(job.A, job.B, job.inner);
+        feed.issue(0);
+      }
+      Out::run(acc, smem + STAGE, from);
+      if (!more) break;
+      whole = Out::whole(from, BT, BT);
+      __builtin_amdgcn_s_barrier();  // every wave has read its staged results
+      asm volatile("" ::: "memory");
+    }
+  }
+};
+
+template <class T, int BT, bool AKS, bool PAIR>
+__global__ __launch_bounds__(512) void grouped_n_kernel(Grouped16 g) {
+  using Tiles = Walk<Tile16<T, BT, BT, 2, 4, AKS, false, 2, PAIR>, Tile16<T, BT / 2, BT / 2, 2, 4, AKS, false, 4, PAIR>>;
+  __shared__ __attribute__((aligned(1024))) char smem[Tiles::SMEM];
   const int tiles_m = (g.m + BT - 1) / BT;
   const GroupIndex index(g.offsets, g.groups, g.n, BT);
-  const int total = tiles_m * index.total, units = gridDim.x / 3;
-  const Share share = share_of(total, units, blockIdx.x);
-  if (share.first < 0) return;
-  Source16 A, B;
-  Target to;
-  auto place = [&](int L, int quarter, int side) {
+  const int total = tiles_m * index.total;
+  Tiles::run(smem, total, [&](int L, int dm, int dn) {
     int nj, mi;
     panel_order<4>(xcd_order(L, total), index.total, tiles_m, nj, mi);
     const GroupTile gt = index.find(nj);
-    const int m0 = mi * BT + (quarter & 1) * side, n0 = gt.begin + (quarter >> 1) * side;
-    A = Source16{g.A.p + gt.group * g.A.batch + (AKS ? (long)m0 : (long)m0 * g.A.ld), g.A.plane, (int)g.A.ld,
-                 g.m - m0, (int)g.A.last - (AKS ? m0 : 0)};
-    B = Source16{g.B.p + (long)n0 * g.B.ld, g.B.plane, (int)g.B.ld, gt.end - n0, (int)g.B.last};
-    to = Target{g.C, g.ctype, g.ldc, m0, g.m, n0, gt.end, g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr,
-                g.B.ex};
-  };
-  if (share.quarter >= 0) {
-    place(share.first, share.quarter, BT / 2);
-    if (to.m0 >= to.m || to.n0 >= to.n_end) return;
-    v4f acc[Small::FM][Small::FN];
-    Small::run(acc, smem, A, B, g.q);
-    slice_barrier<0>();
-    Store<Small>::run(acc, smem, to);
-    return;
-  }
-  typename Tile::Feed feed(smem);
-  place(share.first, 0, 0);
-  feed.begin(A, B, g.q);
-  feed.issue(0);
-  v4f acc[Tile::FM][Tile::FN];
-  bool whole = false;
-  for (int round = 1, L = share.first;; ++round) {
-    if (whole)
-      Tile::template resume<Out::STORES>(acc, feed, g.q, to.n_end - to.n0);
-    else
-      Tile::template resume<0>(acc, feed, g.q, to.n_end - to.n0);
-    const Target from = to;
-    slice_barrier<0>();  // every wave has read its last operands, and no load into LDS is in flight
-    const bool more = round < share.rounds;
-    if (more) {
-      L += units;
-      place(L, 0, 0);
-      feed.begin(A, B, g.q);
-      feed.issue(0);
-    }
-    Out::run(acc, smem + STAGE, from);
-    if (!more) break;
-    whole = Out::whole(from, BT, BT);
-    __builtin_amdgcn_s_barrier();  // every wave has read its staged results
-    asm volatile("" ::: "memory");
-  }
+    const int m0 = mi * BT + dm, n0 = gt.begin + dn;
+    return Job{Source16{g.A.p + gt.group * g.A.batch + (AKS ? (long)m0 : (long)m0 * g.A.ld), g.A.plane, (int)g.A.ld,
+                        g.m - m0, (int)g.A.last - (AKS ? m0 : 0)},
+               Source16{g.B.p + (long)n0 * g.B.ld, g.B.plane, (int)g.B.ld, gt.end - n0, (int)g.B.last}, g.q,
+               Target{g.C, g.ctype, g.ldc, m0, g.m, n0, gt.end,
+                      g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr, g.B.ex}};
+  });
 }
 
-template <class T, int BM, int BN, int WM, int WN, bool KS, bool PAIR>
-__global__ __launch_bounds__(WM* WN * 64) void grouped_k_kernel(Grouped16 g) {
-  using Tile = Tile16<T, BM, BN, WM, WN, KS, KS, 2, PAIR>;
-  __shared__ __attribute__((aligned(1024))) char smem[Tile::SMEM];
-  const int tiles_m = (g.m + BM - 1) / BM, tiles_q = (g.q + BN - 1) / BN;
-  const int per = tiles_m * tiles_q;
-  const int w = xcd_order(blockIdx.x, per * g.groups);
-  int mi, qj;
-  panel_order<4>(w % per, tiles_m, tiles_q, mi, qj);
-  const int e = w / per;
-  const GroupTile gt = group_at(g.offsets, g.groups, g.n, BK16, e);
-  const int len = gt.end - gt.begin;
-  const int m0 = mi * BM, q0 = qj * BN;
-  Source16 A, B;
-  A.ld = (int)g.A.ld;
-  A.plane = g.A.plane;
-  B.ld = (int)g.B.ld;
-  B.plane = g.B.plane;
-  A.rows = g.m - m0;
-  B.rows = g.q - q0;
-  int inner = len;
-  if (KS) {
-    A.base = g.A.p + gt.begin * g.A.ld + m0;
-    A.last = (int)g.A.last - m0;
-    B.base = g.B.p + gt.begin * g.B.ld + q0;
-    B.last = (int)g.B.last - q0;
-  } else {  // padded planes: the group's rows begin at 64 x its tiles before
-    const int k0 = gt.first * BK16;
-    inner = (len + BK16 - 1) / BK16 * BK16;
-    A.base = g.A.p + (long)m0 * g.A.ld + k0;
-    A.last = (int)g.A.last - k0;
-    B.base = g.B.p + (long)q0 * g.B.ld + k0;
-    B.last = (int)g.B.last - k0;
-  }
-  v4f acc[Tile::FM][Tile::FN];
-  Tile::run(acc, smem, A, B, inner);
-  slice_barrier<0>();  // every wave has read its last operands
-  char* C = (char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2);
-  static_assert(Store<Tile>::BYTES <= Tile::SMEM, "staging fits the operand buffers");
-  Store<Tile>::run(acc, smem,
-                   Target{C, g.ctype, g.ldc, m0, g.m, q0, g.q, g.A.ex && len > 0 ? g.A.ex + e * g.A.ex_batch : nullptr,
-                          g.B.ex ? g.B.ex + e * g.B.ex_batch : nullptr});
+template <class T, int BT, bool KS, bool PAIR>
+__global__ __launch_bounds__(512) void grouped_k_kernel(Grouped16 g) {
+  using Tiles = Walk<Tile16<T, BT, BT, 2, 4, KS, KS, 2, PAIR>, Tile16<T, BT / 2, BT / 2, 2, 4, KS, KS, 4, PAIR>>;
+  __shared__ __attribute__((aligned(1024))) char smem[Tiles::SMEM];
+  const int tiles_m = (g.m + BT - 1) / BT, tiles_q = (g.q + BT - 1) / BT;
+  const int per = tiles_m * tiles_q, total = per * g.groups;
+  const GroupIndex index(g.offsets, g.groups, g.n, BK16);
+  Tiles::run(smem, total, [&](int L, int dm, int dn) {
+    // Every XCD takes an eighth of each group's tiles: the groups' lengths
+    // differ, and an XCD with whole groups of its own waited for the longest.
+    const int x = L & 7, i = L >> 3, eighth = per >> 3;
+    const int e = per % 8 == 0 ? i / eighth : L / per;
+    int mi, qj;
+    panel_order<4>(per % 8 == 0 ? x * eighth + i % eighth : L % per, tiles_m, tiles_q, mi, qj);
+    const GroupTile gt = index.at(e);
+    const int len = gt.end - gt.begin, m0 = mi * BT + dm, q0 = qj * BT + dn;
+    // K-strided: the group's columns; else padded planes, where they begin at 64 x its tiles before
+    const int k0 = KS ? gt.begin : gt.first * BK16;
+    const long a_at = KS ? k0 * g.A.ld + m0 : m0 * g.A.ld + k0, b_at = KS ? k0 * g.B.ld + q0 : q0 * g.B.ld + k0;
+    return Job{Source16{g.A.p + a_at, g.A.plane, (int)g.A.ld, g.m - m0, (int)g.A.last - (KS ? m0 : k0)},
+               Source16{g.B.p + b_at, g.B.plane, (int)g.B.ld, g.q - q0, (int)g.B.last - (KS ? q0 : k0)},
+               KS ? len : (len + BK16 - 1) / BK16 * BK16,
+               Target{(char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2), g.ctype, g.ldc, m0, g.m, q0,
+                      g.q, g.A.ex ? g.A.ex + e * g.A.ex_batch : nullptr, g.B.ex ? g.B.ex + e * g.B.ex_batch : nullptr}};
+  });
 }
 
-template <class T, int BT, int NB_SMALL, bool AKS, bool PAIR>
+template <class T, int BT, bool AKS, bool PAIR>
 hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
   int cus = 0;
   const hipError_t err = device_units(&cus);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((grouped_n_kernel<T, BT, NB_SMALL, AKS, PAIR>), dim3(3 * cus), dim3(512), 0, st, g);
+  hipLaunchKernelGGL((grouped_n_kernel<T, BT, AKS, PAIR>), dim3(3 * cus), dim3(512), 0, st, g);
   return hipGetLastError();
 }
 
 template <class T, int BT, bool KS, bool PAIR>
 hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
-  const long blocks = (long)((g.m + BT - 1) / BT) * ((g.q + BT - 1) / BT) * g.groups;
-  hipLaunchKernelGGL((grouped_k_kernel<T, BT, BT, 2, 4, KS, PAIR>), dim3((unsigned)blocks), dim3(512), 0, st, g);
+  int cus = 0;
+  const hipError_t err = device_units(&cus);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL((grouped_k_kernel<T, BT, KS, PAIR>), dim3(3 * cus), dim3(512), 0, st, g);
   return hipGetLastError();
 }
 
@@ -282,9 +283,9 @@ bool grouped_k_fits(const Grouped16& g) {
 
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
   if (g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
-  if (g.f32) return grouped_n<Half, 128, 4, false, true>(g, st);
-  if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, 4, true, false>(g, st) : grouped_n<Bfloat, 256, 4, false, false>(g, st);
-  return g.A.ks ? grouped_n<Half, 256, 4, true, false>(g, st) : grouped_n<Half, 256, 4, false, false>(g, st);
+  if (g.f32) return grouped_n<Half, 128, false, true>(g, st);
+  if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, true, false>(g, st) : grouped_n<Bfloat, 256, false, false>(g, st);
+  return g.A.ks ? grouped_n<Half, 256, true, false>(g, st) : grouped_n<Half, 256, false, false>(g, st);
 }
 
 hipError_t launch_grouped_k(const Grouped16& g, hipStream_t st) {

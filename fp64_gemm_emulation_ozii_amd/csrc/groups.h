@@ -138,6 +138,16 @@ struct GroupIndex {
     t.begin = begin + t.tile * tile;
     return t;
   }
+
+  // Group e's boundaries and the tiles of the groups before it.
+  __device__ __forceinline__ GroupTile at(int e) const {
+    if (groups > 64) return group_at(offsets, groups, n, tile, e);
+    GroupTile t{e, 0, 0, 0, 0};
+    t.begin = __builtin_amdgcn_readlane(lo, e);
+    t.end = __builtin_amdgcn_readlane(hi, e);
+    t.first = __builtin_amdgcn_readlane(upto, e) - (t.end - t.begin + tile - 1) / tile;
+    return t;
+  }
 };
 
 }  // namespace oz

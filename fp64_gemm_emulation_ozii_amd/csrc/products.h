@@ -59,8 +59,7 @@ hipError_t launch_slice_cols(int type, const void* src, long ld, long sbatch, in
                              uint16_t* dst, long dld, long plane, int32_t* ex, uint32_t* part, hipStream_t st);
 size_t slice_part_bytes(int rows, long K, int groups, bool ragged);
 // element (r, k) at src[k ld + r], k in groups that begin at offsets[e]; group
-// e's rows begin at 64 x (its 64-tiles before); ex[e rows + r], not written for
-// a group without k
+// e's rows begin at 64 x (its 64-tiles before); ex[e rows + r]
 hipError_t launch_slice_groups(int type, const void* src, long ld, int rows, int n, const int32_t* offsets,
                                int groups, uint16_t* dst, long dld, long plane, int32_t* ex, uint32_t* part,
                                hipStream_t st);

@@ -158,7 +158,7 @@ __device__ __forceinline__ KRange k_range(const int32_t* offsets, int groups, in
 
 // Bits of the largest |entry| of every column r of a tile of CHUNK k, one
 // block per 256 columns: part[tile][r].
-constexpr int CHUNK = 256;
+constexpr int CHUNK = 64;
 
 __global__ __launch_bounds__(256) void column_max_kernel(const float* __restrict__ src, long ld, long sbatch,
                                                          int rows, int K, const int32_t* __restrict__ offsets,
@@ -190,18 +190,44 @@ __global__ __launch_bounds__(256) void column_max_kernel(const float* __restrict
     part[(long)blockIdx.x * rows + c] = max(max(s[0][threadIdx.x], s[1][threadIdx.x]), max(s[2][threadIdx.x], s[3][threadIdx.x]));
 }
 
+// The exponents of 64 columns of one group from its chunks' maxima.
+__global__ __launch_bounds__(256) void column_exponents_kernel(const uint32_t* __restrict__ part, int rows, int K,
+                                                               const int32_t* __restrict__ offsets, int groups,
+                                                               int32_t* __restrict__ ex) {
+  const int e = blockIdx.x, lane = threadIdx.x & 63, r = blockIdx.y * 64 + lane;
+  int count = (K + CHUNK - 1) / CHUNK, first = e * count;
+  if (offsets) {
+    const GroupTile g = group_at(offsets, groups, K, CHUNK, e);
+    first = g.first;
+    count = (g.end - g.begin + CHUNK - 1) / CHUNK;
+  }
+  uint32_t mx = 0;
+  if (r < rows) {
+    for (int c = threadIdx.x >> 6; c < count; c += 32) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = part[(long)(first + min(c + 4 * i, count - 1)) * rows + r];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = max(mx, v[i]);
+    }
+  }
+  __shared__ uint32_t s[4][64];
+  s[threadIdx.x >> 6][lane] = mx;
+  __syncthreads();
+  if (threadIdx.x < 64 && r < rows) ex[(long)e * rows + r] = exponent32(max(max(s[0][lane], s[1][lane]), max(s[2][lane], s[3][lane])));
+}
+
 // A 64 x 64 tile of K-strided entries, cut into slices and transposed through
-// LDS.  The columns' exponents come from the partial maxima of the group's
-// chunks; the group's first tile writes them down.
+// LDS.
 template <int TYPE>
 __global__ __launch_bounds__(256) void slice_cols_kernel(const void* __restrict__ src, long ld, long sbatch, int rows,
                                                          int K, const int32_t* __restrict__ offsets, int groups,
                                                          uint16_t* __restrict__ dst, long dld, long plane,
-                                                         int32_t* __restrict__ ex, const uint32_t* __restrict__ part) {
+                                                         const int32_t* __restrict__ ex) {
   const KRange g = k_range<64>(offsets, groups, K, blockIdx.x);
   if (g.group < 0) return;
   __shared__ uint32_t tile[64][65];
-  __shared__ uint32_t most[4][64];
+  __shared__ int32_t es[64];
   const int r0 = blockIdx.y * 64;
   const long from = offsets ? 0 : g.group * sbatch;
   const bool wide = wide_runs<TYPE>(src, from, ld);
@@ -213,33 +239,14 @@ __global__ __launch_bounds__(256) void slice_cols_kernel(const void* __restrict_
     load4<TYPE>(src, from + (long)k * ld + r0 + rr, k < g.k1 ? rows - r0 - rr : 0, wide, v[i]);
   }
   if (TYPE == OZGEMM_F32) {
-    int first, count;
-    if (offsets) {
-      const GroupTile c = group_at(offsets, groups, K, CHUNK, g.group);
-      first = c.first;
-      count = (c.end - c.begin + CHUNK - 1) / CHUNK;
-    } else {
-      count = (K + CHUNK - 1) / CHUNK;
-      first = g.group * count;
-    }
-    const int r = threadIdx.x & 63;
-    uint32_t mx = 0;
-    if (r0 + r < rows)
-      for (int c = threadIdx.x >> 6; c < count; c += 4) mx = max(mx, part[(long)(first + c) * rows + r0 + r]);
-    most[threadIdx.x >> 6][r] = mx;
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      const int e = exponent32(max(max(most[0][r], most[1][r]), max(most[2][r], most[3][r])));
-      most[0][r] = (uint32_t)e;
-      if (g.tile == 0 && r0 + r < rows) ex[(long)g.group * rows + r0 + r] = e;
-    }
+    if (threadIdx.x < 64) es[threadIdx.x] = r0 + (int)threadIdx.x < rows ? ex[(long)g.group * rows + r0 + threadIdx.x] : 0;
     __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      tile[kk + 16 * i][rr + j] = slices_of<TYPE>(v[i][j], TYPE == OZGEMM_F32 ? (int)most[0][rr + j] : 0);
+      tile[kk + 16 * i][rr + j] = slices_of<TYPE>(v[i][j], TYPE == OZGEMM_F32 ? es[rr + j] : 0);
   __syncthreads();
   uint16_t* base = dst + (offsets ? 0 : (long)g.group * rows * dld) + g.dst_k;
 #pragma unroll
@@ -273,11 +280,13 @@ hipError_t slice_cols(int type, const void* src, long ld, long sbatch, int rows,
   if (type == OZGEMM_F32) {
     hipLaunchKernelGGL(column_max_kernel, dim3((unsigned)k_tiles(offsets, K, groups, CHUNK), (unsigned)((rows + 255) / 256)),
                        dim3(256), 0, st, (const float*)src, ld, sbatch, rows, K, offsets, groups, part);
+    hipLaunchKernelGGL(column_exponents_kernel, dim3(groups, (unsigned)((rows + 63) / 64)), dim3(256), 0, st, part,
+                       rows, K, offsets, groups, ex);
     hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F32>, tiles, dim3(256), 0, st, src, ld, sbatch, rows, K, offsets,
-                       groups, dst, dld, plane, ex, part);
+                       groups, dst, dld, plane, ex);
   } else {
     hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F16>, tiles, dim3(256), 0, st, src, ld, sbatch, rows, K, offsets,
-                       groups, dst, dld, plane, ex, part);
+                       groups, dst, dld, plane, ex);
   }
   return hipGetLastError();
 }

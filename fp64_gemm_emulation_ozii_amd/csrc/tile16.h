@@ -93,7 +93,7 @@ __device__ __forceinline__ void panel_order(int w, int major, int minor, int& a,
 
 template <class T, int BM, int BN, int WM, int WN, bool AKS, bool BKS, int NB = 2, bool PAIR = false>
 struct Tile16 {
-  static constexpr int NW = WM * WN, WAVES_N = WN;
+  static constexpr int NW = WM * WN, ROWS_M = BM, ROWS_N = BN;
   static constexpr int THREADS = NW * 64;
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   static constexpr int PLANES = PAIR ? 2 : 1;
