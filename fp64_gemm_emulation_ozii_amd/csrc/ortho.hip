@@ -20,7 +20,6 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
-#include <cstdlib>
 
 #include "products.h"
 #include "tile16.h"
@@ -267,25 +266,10 @@ struct Step {
   int om, on;         // the result's own size
 };
 
-template <int BT, int WM, int WN, int NB, bool PAIR, bool AKS, bool BKS, bool SYM>
-__global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
-  using Tile = Tile16<Half, BT, BT, WM, WN, AKS, BKS, NB, PAIR>;
-  __shared__ __attribute__((aligned(1024))) char smem[Tile::SMEM];
-  const int tm = p.m / BT, tn = p.n / BT;
-  const int per = SYM ? tm * (tm + 1) / 2 : tm * tn;
-  const int w = xcd_order(blockIdx.x, per * p.batch);
-  const long b = w / per;
-  const int t = w % per;
-  int mi, nj;
-  if (SYM) {  // tiles (mi, nj), nj <= mi, by rows of the triangle
-    mi = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
-    while ((mi + 1) * (mi + 2) / 2 <= t) ++mi;
-    while (mi * (mi + 1) / 2 > t) --mi;
-    nj = t - mi * (mi + 1) / 2;
-  } else {
-    panel_order<4>(t, tm, tn, mi, nj);
-  }
-  const int m0 = mi * BT, n0 = nj * BT;
+// The tile with corner (m0, n0) of matrix b; sizes are multiples of 64, and
+// what lies past them arrives as zero and is not written.
+template <class Tile, bool AKS, bool BKS, bool SYM>
+__device__ __forceinline__ void step_tile(const Step& p, char* smem, long b, int m0, int n0) {
   const Source16 A{p.A + b * p.a_batch + (AKS ? (long)m0 : (long)m0 * p.a_ld), p.a_plane, p.a_ld, p.m - m0,
                    AKS ? p.m - m0 : p.k};
   const Source16 B{p.B + b * p.b_batch + (BKS ? (long)n0 : (long)n0 * p.b_ld), p.b_plane, p.b_ld, p.n - n0,
@@ -305,16 +289,19 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
   const int mw = m0 + Tile::wave_m(wave) * WTM, nw = n0 + Tile::wave_n(wave) * (Tile::FN * 16);
   const uint16_t* S = p.S ? p.S + b * p.s_batch : nullptr;
   uint16_t* N = p.N + b * p.s_batch;
-  const bool mirror = SYM && mi != nj;  // a diagonal tile holds both halves itself
+  const bool mirror = SYM && m0 != n0;  // a diagonal tile holds both halves itself
   auto offset = [&](int j, int ch) {
     const int at = ch * 64 + lane;
     return (long)(nw + j * 16 + at / RUNS) * p.m + mw + at % RUNS * 8;
   };
+  // (a run of 8 rows and 16 columns lie inside or outside as a whole)
+  auto inside = [&](int j, int ch) { return nw + j * 16 < p.n && mw + (ch * 64 + lane) % RUNS * 8 < p.m; };
   v8s sh[2][CH] = {}, sl[2][CH] = {};
   auto fetch = [&](int j) {
     if (S == nullptr) return;
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
+      if (!inside(j, ch)) continue;
       const long off = offset(j, ch);
       sh[j & 1][ch] = *reinterpret_cast<const v8s*>(S + off);
       if (p.s_lo) sl[j & 1][ch] = *reinterpret_cast<const v8s*>(S + p.s_plane + off);
@@ -333,6 +320,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
       const int at = ch * 64 + lane, c = at / RUNS, r = at % RUNS * 8;
+      if (!inside(j, ch)) continue;
       float v[8];
       *reinterpret_cast<v4f*>(v) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r);
       *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r + 4);
@@ -371,6 +359,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
 #pragma unroll
       for (int ch = 0; ch < (WTM * 2 + 63) / 64; ++ch) {
         const int at = ch * 64 + lane, r = at >> 1, c = (at & 1) * 8;
+        if (r >= WTM || mw + r >= p.m || nw + j * 16 >= p.n) continue;
         v8s h, l;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -388,20 +377,85 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p) {
   }
 }
 
-template <int BT, int WM, int WN, int NB, bool PAIR>
-hipError_t launch_step_t(const Step& p, bool aks, bool bks, bool sym, hipStream_t st) {
-  const long tm = p.m / BT, tn = p.n / BT;
-  const dim3 grid((unsigned)((sym ? tm * (tm + 1) / 2 : tm * tn) * p.batch)), block(WM * WN * 64);
+// One block per tile; the tiles past `whole` (a last round of them that would
+// leave most compute units idle) are cut into quarters.
+template <int BT, int WM, int WN, int NB, bool PAIR, bool QUARTERS, bool AKS, bool BKS, bool SYM>
+__global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p, int whole) {
+  using Tile = Tile16<Half, BT, BT, WM, WN, AKS, BKS, NB, PAIR>;
+  using Small = Tile16<Half, QUARTERS ? BT / 2 : BT, QUARTERS ? BT / 2 : BT, WM, WN, AKS, BKS, 4, PAIR>;
+  constexpr int SMEM = QUARTERS && Small::SMEM > Tile::SMEM ? Small::SMEM : Tile::SMEM;
+  __shared__ __attribute__((aligned(1024))) char smem[SMEM];
+  const int tm = (p.m + BT - 1) / BT, tn = (p.n + BT - 1) / BT;
+  const int per = SYM ? tm * (tm + 1) / 2 : tm * tn, total = per * p.batch;
+  int L = blockIdx.x, quarter = -1;
+  if (QUARTERS && L >= whole) {
+    quarter = (L - whole) % 4;
+    L = whole + (L - whole) / 4;
+  }
+  const int w = xcd_order(L, total);
+  const long b = w / per;
+  const int t = w % per;
+  int mi, nj;
+  if (SYM) {
+    triangle_order<4>(t, tm, mi, nj);
+  } else {
+    panel_order<4>(t, tm, tn, mi, nj);
+  }
+  int m0 = mi * BT, n0 = nj * BT;
+  if (QUARTERS && quarter >= 0) {
+    m0 += (quarter & 1) * (BT / 2);
+    n0 += (quarter >> 1) * (BT / 2);
+    if (m0 >= p.m || n0 >= p.n || (SYM && m0 < n0)) return;
+    step_tile<Small, AKS, BKS, SYM>(p, smem, b, m0, n0);
+  } else {
+    step_tile<Tile, AKS, BKS, SYM>(p, smem, b, m0, n0);
+  }
+}
+
+template <int BT, int WM, int WN, int NB, bool PAIR, bool QUARTERS>
+hipError_t launch_step_t(const Step& p, bool aks, bool sym, int units, hipStream_t st) {
+  const long tm = (p.m + BT - 1) / BT, tn = (p.n + BT - 1) / BT;
+  const long tiles = (sym ? tm * (tm + 1) / 2 : tm * tn) * p.batch, rest = tiles % units;
+  const int whole = (int)(QUARTERS && rest * 2 <= units ? tiles - rest : tiles);
+  const dim3 grid((unsigned)(whole + 4 * (tiles - whole))), block(WM * WN * 64);
   if (sym && aks)
-    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, true, true, true>), grid, block, 0, st, p);
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, QUARTERS, true, true, true>), grid, block, 0, st, p, whole);
   else if (sym)
-    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, false, false, true>), grid, block, 0, st, p);
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, QUARTERS, false, false, true>), grid, block, 0, st, p, whole);
   else if (aks)
-    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, true, false, false>), grid, block, 0, st, p);
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, QUARTERS, true, false, false>), grid, block, 0, st, p, whole);
   else
-    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, false, false, false>), grid, block, 0, st, p);
-  (void)bks;
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, QUARTERS, false, false, false>), grid, block, 0, st, p, whole);
   return hipGetLastError();
+}
+
+// The tile size of a product of S K slices: the modelled time, in us, of its
+// rounds of one tile per compute unit (a quartered last round counts 0.4 per
+// `units` quarters).  A round takes S slices and a start and an end; measured
+// with every unit busy:
+//   one slice product   256 x 256  1.6 S + 9   128 x 128  0.7 S + 7   64 x 64  0.2 S + 2
+//   three               128 x 128  1.25 S + 8                         64 x 64  0.43 S + 3
+hipError_t launch_step(const Step& p, int nprod, bool aks, bool sym, hipStream_t st) {
+  int units = 0;
+  const hipError_t err = device_units(&units);
+  if (err != hipSuccess) return err;
+  const double S = p.k / BK16;
+  auto rounds = [&](int bt, bool quarters) {
+    const long tm = (p.m + bt - 1) / bt, tn = (p.n + bt - 1) / bt;
+    const long tiles = (sym ? tm * (tm + 1) / 2 : tm * tn) * p.batch, rest = tiles % units;
+    const double last = rest == 0 ? 0 : quarters && rest * 2 <= units ? 0.4 * ((4 * rest + units - 1) / units) : 1;
+    return (double)(tiles / units) + last;
+  };
+  if (nprod == 3) {
+    if (rounds(128, true) * (1.25 * S + 8) <= rounds(64, false) * (0.43 * S + 3))
+      return launch_step_t<128, 2, 4, 2, true, true>(p, aks, sym, units, st);
+    return launch_step_t<64, 2, 2, 2, true, false>(p, aks, sym, units, st);
+  }
+  const double t256 = rounds(256, true) * (1.6 * S + 9), t128 = rounds(128, true) * (0.7 * S + 7),
+               t64 = rounds(64, false) * (0.2 * S + 2);
+  if (t256 <= t128 && t256 <= t64) return launch_step_t<256, 2, 4, 2, false, true>(p, aks, sym, units, st);
+  if (t128 <= t64) return launch_step_t<128, 2, 4, 4, false, true>(p, aks, sym, units, st);
+  return launch_step_t<64, 2, 2, 4, false, false>(p, aks, sym, units, st);
 }
 
 // FP64: X and its transpose, Q = b P + c P2, X <- a X + Y both ways round
@@ -470,16 +524,8 @@ int square_parts(int m, int n) {
   return (int)(blocks < 1 ? 1 : blocks > SQUARE_PARTS ? SQUARE_PARTS : blocks);
 }
 
-// Tile size of the step products: the padded matrix is cut into whole tiles.
-int step_tile(int batch, int r, int c) {
-  (void)batch;
-  if (getenv("OZP")) return atoi(getenv("OZP"));
-  if (r <= 64 || c <= 64) return 64;
-  return 128;
-}
-
 struct OrthoLayout {
-  int tile, rp, cp;
+  int rp, cp;  // sizes padded to 64
   size_t part, X1, X2, P, Q, total;        // 16-bit slices
   size_t X, XT, Y, dgemm;                  // FP64
 };
@@ -503,9 +549,8 @@ OrthoLayout ortho_layout(int type, int batch, int m, int n, int s) {
     L.dgemm = take(dgemm_region_bytes(r, c, s));
     return L;
   }
-  L.tile = step_tile(batch, r, c);
-  L.rp = (int)up(r, L.tile);
-  L.cp = (int)up(c, L.tile);
+  L.rp = (int)up(r, 64);
+  L.cp = (int)up(c, 64);
   const size_t rc = (size_t)batch * 2 * L.rp * L.cp * 2, rr = (size_t)batch * 2 * L.rp * L.rp * 2;
   L.X1 = take(rc);
   L.X2 = take(rc);
@@ -647,26 +692,6 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
   else
     hipLaunchKernelGGL(prepare_kernel<OZGEMM_F16>, blocks, dim3(256), 0, st, pr);
   OZ_TRY(hipGetLastError());
-  int which = 0;
-  auto launch = [&](const Step& p, bool aks, bool bks, bool sym) {
-    const char* ev = getenv("OZT");
-    int tile = ev ? ev[which % 3] : (p.m % 128 || p.n % 128) ? 'c' : 'b';
-    ++which;
-    if (nprod == 3) switch (tile) {
-      case 'b': return launch_step_t<128, 2, 2, 2, true>(p, aks, bks, sym, st);
-      case 'd': return launch_step_t<128, 2, 4, 2, true>(p, aks, bks, sym, st);
-      case 'c': return launch_step_t<64, 2, 2, 2, true>(p, aks, bks, sym, st);
-      default: return launch_step_t<64, 2, 2, 4, true>(p, aks, bks, sym, st);
-    }
-    switch (tile) {
-      case 'a': return launch_step_t<256, 2, 4, 2, false>(p, aks, bks, sym, st);
-      case 'b': return launch_step_t<128, 2, 2, 2, false>(p, aks, bks, sym, st);
-      case 'D': return launch_step_t<128, 2, 4, 4, false>(p, aks, bks, sym, st);
-      case 'd': return launch_step_t<128, 2, 4, 2, false>(p, aks, bks, sym, st);
-      case 'c': return launch_step_t<64, 2, 2, 2, false>(p, aks, bks, sym, st);
-      default: return launch_step_t<64, 2, 2, 4, false>(p, aks, bks, sym, st);
-    }
-  };
   t = START;
   for (int k = 0; k < steps; ++k) {
     if (!scales_of(co, steps, k, &t, &sc)) return OZGEMM_RANGE;
@@ -686,7 +711,7 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
     p.s_batch = 2 * pp;
     p.s_plane = pp;
     p.n_lo = lo;
-    OZ_TRY(launch(p, tall, tall, true));
+    OZ_TRY(launch_step(p, nprod, tall, true, st));
     // Q = b P + c P^2
     p.A = p.B = P;
     p.a_batch = p.b_batch = 2 * pp;
@@ -698,7 +723,7 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
     p.S = P;
     p.s_lo = lo;
     p.N = Q;
-    OZ_TRY(launch(p, false, false, true));
+    OZ_TRY(launch_step(p, nprod, false, true, st));
     // X <- a X + Q X along the r rows, the result as X lies: wide, its row j
     // is row j of Q against X's columns; tall, row j of X against Q
     p.A = tall ? Q : X;
@@ -728,7 +753,7 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
       p.om = m;
       p.on = n;
     }
-    OZ_TRY(launch(p, !tall, false, false));
+    OZ_TRY(launch_step(p, nprod, !tall, false, st));
     uint16_t* swap = X;
     X = other;
     other = swap;

@@ -91,6 +91,36 @@ __device__ __forceinline__ void panel_order(int w, int major, int minor, int& a,
   b = in / g;
 }
 
+// Tiles (a, b), b <= a < size, of a symmetric result: GROUP rows of tiles at a
+// time, down each column of them, so that blocks running together share
+// panels as above (3 to 5% faster at 4096 rows than row after row of tiles).
+template <int GROUP>
+__device__ __forceinline__ void triangle_order(int w, int size, int& a, int& b) {
+  // GROUP i rows' worth of triangle come before row group i
+  int i = 0, rows = min(GROUP, size);
+  while (true) {
+    const int tiles = rows * GROUP * i + rows * (rows + 1) / 2;
+    if (w < tiles) break;
+    w -= tiles;
+    ++i;
+    rows = min(GROUP, size - GROUP * i);
+  }
+  const int first = GROUP * i;
+  if (w < rows * first) {
+    a = first + w % rows;
+    b = w / rows;
+    return;
+  }
+  w -= rows * first;
+  int c = 0;
+  while (w >= rows - c) {
+    w -= rows - c;
+    ++c;
+  }
+  a = first + c + w;
+  b = first + c;
+}
+
 template <class T, int BM, int BN, int WM, int WN, bool AKS, bool BKS, int NB = 2, bool PAIR = false>
 struct Tile16 {
   static constexpr int NW = WM * WN, ROWS_M = BM, ROWS_N = BN;
@@ -191,7 +221,7 @@ struct Tile16 {
         const int c = (lane % CPR) ^ (kswz<ROWS>(k) << 1);
         voff = (k * ld + c * 8) * 2;
       } else {
-        voff = base[blk & 1] + blk * 16 * ld;
+        voff = ((blk & 1) ? base[1] : base[0]) + blk * 16 * ld;
       }
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + blk * 1024), 16,
                                                voff, 0, 0, 0);
@@ -222,15 +252,22 @@ struct Tile16 {
     }
   }
 
-  // MFMA slots of a step: per A fragment i its products with every B fragment,
-  // the pair's three kinds one after the other, smallest first.
+  // MFMA slots of a step.  Long steps: per A fragment i its products with every
+  // B fragment, the pair's three kinds one after the other, smallest first.
+  // Short ones: all of one kind before the next, which keeps MFMAs into the
+  // same accumulator apart.
   static constexpr int KINDS = PAIR ? 3 : 1;
   static constexpr int SLOTS = KINDS * FM * FN;
+  static constexpr bool SHORT = SLOTS <= 24;
   static constexpr int NF = PLANES * (FM + FN);  // fragments of a step: B's (high, low), then A's (high, low of each i)
   static constexpr int LPW = PLANES * (A_LOADS + B_LOADS);
 
-  // the slot after which fragment f of the next step is read: A's right after their last use
+  // The slot after which fragment f of the next step is read.  Short steps
+  // read them all in their first half, whose latency the second half covers;
+  // in the long steps of a 256 x 256 tile each A fragment is read right after
+  // its last use, so that old and new can share registers.
   static constexpr int read_slot(int f) {
+    if (SHORT) return f * SLOTS / (2 * NF);
     if (f < PLANES * FN) return f * (SLOTS / (PLANES * FN)) + (SLOTS / (PLANES * FN) > 1);
     const int i = (f - PLANES * FN) / PLANES, low = (f - PLANES * FN) % PLANES;
     return (i * KINDS + (low ? 1 : KINDS)) * FN - 1;
@@ -357,7 +394,7 @@ struct Tile16 {
         const int rbuf = ks ? following : buf;  // (past the end: zeros, not used)
 #pragma unroll
         for (int r = 0; r < SLOTS; ++r) {
-          const int i = r / (KINDS * FN), kind = r / FN % KINDS, j = r % FN;
+          const int i = SHORT ? r / FN % FM : r / (KINDS * FN), kind = SHORT ? r / (FM * FN) : r / FN % KINDS, j = r % FN;
           const int fa = PLANES * FN + i * PLANES + (PAIR && kind == 0), fb = j + (PAIR && kind == 1 ? FN : 0);
           acc[i][j] = T::mfma(cur[fa], cur[fb], acc[i][j]);
           __builtin_amdgcn_sched_barrier(0);
