@@ -252,6 +252,103 @@ __global__ __launch_bounds__(512) void grouped_k_kernel(Grouped16 g) {
   });
 }
 
+// Groups of a few columns: bound by reading the weights once.  A block takes
+// ROWS rows of a group's weights and up to 64 of its columns; its four
+// wavefronts share the inner dimension, 32 DEPTH entries of it at a time,
+// whose loads are all in flight before the first product, straight from HBM
+// into the MFMA's operand layout (16 rows x 64 bytes per load; the two halves
+// of a 128-byte line are loaded one after the other).  The columns, which the
+// L2 serves, come the same way.  The wavefronts' sums meet in LDS.
+template <class T, int MR, int DEPTH>
+__global__ __launch_bounds__(256, 2) void few_columns_kernel(Grouped16 g) {
+  constexpr int ROWS = 16 * MR, COLS = 64, CF = COLS / 16;
+  __shared__ float sums[4][CF][16][ROWS + 4];
+  const GroupIndex index(g.offsets, g.groups, g.n, COLS);
+  const int tiles_m = (g.m + ROWS - 1) / ROWS;
+  if ((int)blockIdx.x >= tiles_m * index.total) return;
+  const int nj = blockIdx.x / tiles_m, m0 = blockIdx.x % tiles_m * ROWS;
+  const GroupTile gt = index.find(nj);
+  const int n0 = gt.begin, cols = min(gt.end - n0, COLS), frags = (cols + 15) / 16;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int kl = wave * 32 * DEPTH + (lane >> 4) * 8;  // this lane's first k in a chunk
+  // rows past the end read the last one again (their sums are not stored)
+  const uint16_t* a[MR];
+#pragma unroll
+  for (int i = 0; i < MR; ++i)
+    a[i] = g.A.p + gt.group * g.A.batch + (long)min(m0 + i * 16 + (lane & 15), g.m - 1) * g.A.ld + kl;
+  const uint16_t* b[CF];
+#pragma unroll
+  for (int c = 0; c < CF; ++c) b[c] = g.B.p + (long)(n0 + min(c * 16 + (lane & 15), cols - 1)) * g.B.ld + kl;
+  v4f acc[MR][CF] = {};
+  const v8s zero = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int k0 = 0; k0 < g.q; k0 += 4 * 32 * DEPTH) {
+    v8s av[DEPTH][MR];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+#pragma unroll
+      for (int i = 0; i < MR; ++i)
+        av[d][i] = kl + k0 + d * 32 < g.q ? *reinterpret_cast<const v8s*>(a[i] + k0 + d * 32) : zero;
+#pragma unroll
+    for (int c = 0; c < CF; ++c) {
+      if (c >= frags) break;
+      v8s bv[DEPTH];
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d)
+        bv[d] = kl + k0 + d * 32 < g.q ? *reinterpret_cast<const v8s*>(b[c] + k0 + d * 32) : zero;
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d)
+#pragma unroll
+        for (int i = 0; i < MR; ++i) acc[i][c] = T::mfma(av[d][i], bv[d], acc[i][c]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CF; ++c)
+#pragma unroll
+    for (int i = 0; i < MR; ++i)
+      if (c < frags) *reinterpret_cast<v4f*>(&sums[wave][c][lane & 15][i * 16 + 4 * (lane >> 4)]) = acc[i][c];
+  __syncthreads();
+  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
+  for (int at = threadIdx.x; at < frags * 16 * (ROWS / 4); at += 256) {
+    const int r = at % (ROWS / 4) * 4, c = at / (ROWS / 4), row = m0 + r;
+    if (c >= cols || row >= g.m) continue;
+    v4f v = *reinterpret_cast<const v4f*>(&sums[0][c >> 4][c & 15][r]);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const v4f*>(&sums[w][c >> 4][c & 15][r]);
+    const long to = (long)(n0 + c) * g.ldc + row;
+    if (g.ctype == OZGEMM_F32) {
+      float* out = (float*)g.C + to;
+      if (wide && row + 4 <= g.m) {
+        *reinterpret_cast<v4f*>(out) = v;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (row + k < g.m) out[k] = v[k];
+      }
+    } else {
+      v4s h;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = (short)round16(v[k], g.ctype);
+      short* out = (short*)g.C + to;
+      if (wide && row + 4 <= g.m) {
+        *reinterpret_cast<v4s*>(out) = h;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (row + k < g.m) out[k] = h[k];
+      }
+    }
+  }
+}
+
+template <class T>
+hipError_t few_columns(const Grouped16& g, hipStream_t st) {
+  const long tiles = group_tiles_max(g.n, g.groups, 64);
+  constexpr int MR = 1, DEPTH = 16;
+  hipLaunchKernelGGL((few_columns_kernel<T, MR, DEPTH>), dim3((unsigned)(tiles * ((g.m + 16 * MR - 1) / (16 * MR)))),
+                     dim3(256), 0, st, g);
+  return hipGetLastError();
+}
+
 template <class T, int BT, bool AKS, bool PAIR>
 hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
   int cus = 0;
@@ -274,7 +371,7 @@ hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
 
 // counted with the smallest tiles any variant uses
 bool grouped_n_fits(const Grouped16& g) {
-  return group_tiles_max(g.n, g.groups, 64) * ((g.m + 63) / 64) <= 0x7fffffffL;
+  return group_tiles_max(g.n, g.groups, 64) * ((g.m + 15) / 16) <= 0x7fffffffL;
 }
 
 bool grouped_k_fits(const Grouped16& g) {
@@ -284,6 +381,7 @@ bool grouped_k_fits(const Grouped16& g) {
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
   if (g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
   if (g.f32) return grouped_n<Half, 128, false, true>(g, st);
+  if (!g.A.ks && (g.n <= 64 || g.n <= 32L * g.groups)) return g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
   if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, true, false>(g, st) : grouped_n<Bfloat, 256, false, false>(g, st);
   return g.A.ks ? grouped_n<Half, 256, true, false>(g, st) : grouped_n<Half, 256, false, false>(g, st);
 }

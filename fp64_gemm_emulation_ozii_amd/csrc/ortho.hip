@@ -130,17 +130,16 @@ __global__ __launch_bounds__(256) void square_sum_kernel(const void* __restrict_
   __shared__ double s[4];
   const long base = blockIdx.y * batch;
   const bool wide = wide_rows(G, base, ld, TYPE == OZGEMM_F32 ? 4 : 2);
-  const int per = (cols + 2047) / 2048;
-  const long pieces = (long)rows * per;
+  const int per = (cols + 2047) / 2048, pieces = rows * per;
   // narrow rows: each wavefront takes a row of its own
   const bool narrow = cols <= 512;
   double sum = 0;
-  const long first = narrow ? (long)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  const long step = narrow ? (long)gridDim.x * 4 : gridDim.x;
+  const int first = narrow ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int step = narrow ? gridDim.x * 4 : gridDim.x;
   const int lane8 = (narrow ? (threadIdx.x & 63) : threadIdx.x) * 8;
-  for (long i = first; i < pieces; i += step) {
+  for (int i = first; i < pieces; i += step) {
     const long r = i / per;
-    const int c = (int)(i - r * per) * 2048 + lane8;
+    const int c = (i - (int)r * per) * 2048 + lane8;
     if (c >= cols) continue;
     if (TYPE == OZGEMM_F64) {
       const double* q = (const double*)G + base + r * ld + c;
@@ -189,7 +188,7 @@ __device__ __forceinline__ float joined(uint16_t hi, uint16_t lo) {
 }
 
 // G (rows x cols) scaled and cut into slices, zeros in the padding.
-constexpr int PREPARE_RUNS = 4;  // runs of 8 entries per thread
+constexpr int PREPARE_RUNS = 2;  // runs of 8 entries per thread
 
 struct Prepare {
   const void* G;
@@ -209,12 +208,12 @@ __global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
   const double f = inverse_norm(p.part, p.parts, b, p.eps, s) * p.scale;
   const long plane = (long)p.rows_pad * p.cols_pad, base = b * p.batch;
   const bool wide = wide_rows(p.G, base, p.ld, TYPE == OZGEMM_F32 ? 4 : 2);
-  const int per = p.cols_pad / 8;
+  const int per = p.cols_pad / 8, runs = (int)(plane / 8);
 #pragma unroll
   for (int i = 0; i < PREPARE_RUNS; ++i) {
-    const long at = ((long)blockIdx.x * PREPARE_RUNS + i) * 256 + threadIdx.x;
-    if (at * 8 >= plane) return;
-    const int r = (int)(at / per), c = (int)(at - (long)r * per) * 8;
+    const int at = (blockIdx.x * PREPARE_RUNS + i) * 256 + threadIdx.x;
+    if (at >= runs) return;
+    const int r = at / per, c = (at - r * per) * 8;
     float v[8];
     load8<TYPE>(p.G, base + r * p.ld + c, r < p.rows ? p.cols - c : 0, wide, v);
     v8s h, l;
@@ -226,7 +225,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
       h[e] = (short)hi;
       l[e] = (short)lo;
     }
-    uint16_t* out = p.X + b * 2 * plane + at * 8;
+    uint16_t* out = p.X + b * 2 * plane + (long)at * 8;
     *reinterpret_cast<v8s*>(out) = h;
     *reinterpret_cast<v8s*>(out + plane) = l;
   }
@@ -433,8 +432,11 @@ hipError_t launch_step_t(const Step& p, bool aks, bool sym, int units, hipStream
 // rounds of one tile per compute unit (a quartered last round counts 0.4 per
 // `units` quarters).  A round takes S slices and a start and an end; measured
 // with every unit busy:
-//   one slice product   256 x 256  1.6 S + 9   128 x 128  0.7 S + 7   64 x 64  0.2 S + 2
-//   three               128 x 128  1.25 S + 8                         64 x 64  0.43 S + 3
+//   one slice product   256 x 256  1.4 S + 9   128 x 128  0.6 S + 7   64 x 64  0.23 S + 3
+//   three               128 x 128  1.2 S + 8                          64 x 64  0.43 S + 3
+// (64 x 64 with three products: two blocks of four wavefronts on a unit; where
+// there is only one for each, eight wavefronts and four buffers, 0.53 S
+// against 0.74 S.)
 hipError_t launch_step(const Step& p, int nprod, bool aks, bool sym, hipStream_t st) {
   int units = 0;
   const hipError_t err = device_units(&units);
@@ -447,12 +449,13 @@ hipError_t launch_step(const Step& p, int nprod, bool aks, bool sym, hipStream_t
     return (double)(tiles / units) + last;
   };
   if (nprod == 3) {
-    if (rounds(128, true) * (1.25 * S + 8) <= rounds(64, false) * (0.43 * S + 3))
+    if (rounds(128, true) * (1.2 * S + 8) <= rounds(64, false) * (0.43 * S + 3))
       return launch_step_t<128, 2, 4, 2, true, true>(p, aks, sym, units, st);
+    if (rounds(64, false) <= 1) return launch_step_t<64, 2, 4, 4, true, false>(p, aks, sym, units, st);
     return launch_step_t<64, 2, 2, 2, true, false>(p, aks, sym, units, st);
   }
-  const double t256 = rounds(256, true) * (1.6 * S + 9), t128 = rounds(128, true) * (0.7 * S + 7),
-               t64 = rounds(64, false) * (0.2 * S + 2);
+  const double t256 = rounds(256, true) * (1.4 * S + 9), t128 = rounds(128, true) * (0.6 * S + 7),
+               t64 = rounds(64, false) * (0.23 * S + 3);
   if (t256 <= t128 && t256 <= t64) return launch_step_t<256, 2, 4, 2, false, true>(p, aks, sym, units, st);
   if (t128 <= t64) return launch_step_t<128, 2, 4, 4, false, true>(p, aks, sym, units, st);
   return launch_step_t<64, 2, 2, 4, false, false>(p, aks, sym, units, st);
@@ -518,10 +521,11 @@ __global__ __launch_bounds__(256) void update64_kernel(double* __restrict__ X, d
 
 constexpr int SQUARE_PARTS = 1024;
 
-// Blocks that sum one matrix's squares: 16 entries a thread, up to SQUARE_PARTS.
-int square_parts(int m, int n) {
-  const long blocks = ((long)m * n + 4095) / 4096;
-  return (int)(blocks < 1 ? 1 : blocks > SQUARE_PARTS ? SQUARE_PARTS : blocks);
+// Blocks that sum one matrix's squares: up to two pieces of a row per
+// wavefront (narrow rows) or block, SQUARE_PARTS at most.
+int square_parts(int m, int n) {  // n rows of m entries
+  const long pieces = m <= 512 ? (n + 7) / 8 : ((long)n * ((m + 2047) / 2048) + 1) / 2;
+  return (int)(pieces < 1 ? 1 : pieces > SQUARE_PARTS ? SQUARE_PARTS : pieces);
 }
 
 struct OrthoLayout {

@@ -287,7 +287,8 @@ struct Tile16 {
   // longer than a load (256 x 256 tiles, or two 128 x 128 blocks on a compute
   // unit); a lone small tile's slice is over long before, and it keeps more
   // slices in flight.
-  static constexpr int BAR = SLOTS / 4 - 1;
+  static constexpr int BAR = SLOTS >= 8 ? SLOTS / 4 - 1 : 0;
+  static_assert(SLOTS >= 2, "the loads and reads of the second step follow its barrier");
   // slot r pressed into those after the barrier
   static constexpr int after_barrier(int r) { return BAR + 1 + r * (SLOTS - BAR - 1) / SLOTS; }
 
