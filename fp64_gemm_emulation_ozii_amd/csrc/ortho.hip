@@ -137,20 +137,27 @@ __global__ __launch_bounds__(256) void square_sum_kernel(const void* __restrict_
   const int first = narrow ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   const int step = narrow ? gridDim.x * 4 : gridDim.x;
   const int lane8 = (narrow ? (threadIdx.x & 63) : threadIdx.x) * 8;
-  for (int i = first; i < pieces; i += step) {
-    const long r = i / per;
-    const int c = (i - (int)r * per) * 2048 + lane8;
-    if (c >= cols) continue;
-    if (TYPE == OZGEMM_F64) {
-      const double* q = (const double*)G + base + r * ld + c;
+  constexpr int AHEAD = TYPE == OZGEMM_F64 ? 1 : 4;  // pieces in flight
+  for (int i0 = first; i0 < pieces; i0 += step * AHEAD) {
+    float v[AHEAD][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < cols) sum = __builtin_fma(q[e], q[e], sum);
-    } else {
-      float v[8];
-      load8<TYPE>(G, base + r * ld + c, cols - c, wide, v);
+    for (int u = 0; u < AHEAD; ++u) {
+      const int i = i0 + u * step, r = i / per, c = (i - r * per) * 2048 + lane8;
+      const int left = i < pieces ? cols - c : 0;
+      if (TYPE == OZGEMM_F64) {
+        const double* q = (const double*)G + base + r * ld + c;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)v[e], (double)v[e], sum);
+        for (int e = 0; e < 8; ++e)
+          if (e < left) sum = __builtin_fma(q[e], q[e], sum);
+      } else {
+        load8<TYPE>(G, base + r * ld + c, left, wide, v[u]);
+      }
+    }
+    if (TYPE != OZGEMM_F64) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)v[u][e], (double)v[u][e], sum);
     }
   }
   sum = block_sum(sum, s);
@@ -188,7 +195,7 @@ __device__ __forceinline__ float joined(uint16_t hi, uint16_t lo) {
 }
 
 // G (rows x cols) scaled and cut into slices, zeros in the padding.
-constexpr int PREPARE_RUNS = 2;  // runs of 8 entries per thread
+constexpr int PREPARE_RUNS = 4;  // runs of 8 entries per thread, at most
 
 struct Prepare {
   const void* G;
@@ -199,6 +206,7 @@ struct Prepare {
   double eps, scale;
   uint16_t* X;   // [batch][2][rows_pad][cols_pad]
   int rows_pad, cols_pad;
+  int each;      // runs per thread: fewer where the blocks would not fill the card
 };
 
 template <int TYPE>
@@ -211,8 +219,8 @@ __global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
   const int per = p.cols_pad / 8, runs = (int)(plane / 8);
 #pragma unroll
   for (int i = 0; i < PREPARE_RUNS; ++i) {
-    const int at = (blockIdx.x * PREPARE_RUNS + i) * 256 + threadIdx.x;
-    if (at >= runs) return;
+    const int at = (blockIdx.x * p.each + i) * 256 + threadIdx.x;
+    if (i >= p.each || at >= runs) return;
     const int r = at / per, c = (at - r * per) * 8;
     float v[8];
     load8<TYPE>(p.G, base + r * p.ld + c, r < p.rows ? p.cols - c : 0, wide, v);
@@ -519,7 +527,7 @@ __global__ __launch_bounds__(256) void update64_kernel(double* __restrict__ X, d
 // Host side
 // ---------------------------------------------------------------------------
 
-constexpr int SQUARE_PARTS = 1024;
+constexpr int SQUARE_PARTS = 256;
 
 // Blocks that sum one matrix's squares: up to two pieces of a row per
 // wavefront (narrow rows) or block, SQUARE_PARTS at most.
@@ -687,8 +695,9 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
   Scales sc;
   if (!scales_of(co, steps, 0, &t, &sc)) return OZGEMM_RANGE;
   OZ_TRY(launch_square_sum(type, G, n, m, ldg, strideg, batch, parts, part, st));
-  const Prepare pr{G, n, m, ldg, strideg, part, parts, eps, sc.X, X, tall ? L.cp : L.rp, tall ? L.rp : L.cp};
-  const dim3 blocks((unsigned)((xp / 8 + 256 * PREPARE_RUNS - 1) / (256 * PREPARE_RUNS)), batch);
+  const Prepare pr{G, n, m, ldg, strideg, part, parts, eps, sc.X, X, tall ? L.cp : L.rp, tall ? L.rp : L.cp,
+                   xp / 8 * batch < 4096L * 256 ? 1 : PREPARE_RUNS};
+  const dim3 blocks((unsigned)((xp / 8 + 256 * pr.each - 1) / (256 * pr.each)), batch);
   if (type == OZGEMM_F32)
     hipLaunchKernelGGL(prepare_kernel<OZGEMM_F32>, blocks, dim3(256), 0, st, pr);
   else if (type == OZGEMM_BF16)

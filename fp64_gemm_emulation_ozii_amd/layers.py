@@ -6,6 +6,8 @@ Work goes on the current stream of the tensors' device.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import ozgemm as L
@@ -24,6 +26,15 @@ def _no_grad(*tensors) -> None:
     if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
         raise RuntimeError("this call is not recorded by autograd: make it under torch.no_grad() and take the "
                            "gradients from grouped_linear_grads")
+
+
+def _on_device(device):
+    """A context in which `device`, a GPU, is the current one."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}: these products run on the GPU only")
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _rows(t, what: str):
@@ -103,7 +114,7 @@ def grouped_linear(X, W, offsets, out=None, out_dtype=None):
     Y = _target(out, (n, m), (X.dtype, torch.float32) if out is not None else (out_dtype or X.dtype,), X, "out")
     if Y.dtype not in (X.dtype, torch.float32):
         raise TypeError(f"grouped_linear: results are {X.dtype} or float32, not {Y.dtype}")
-    with torch.cuda.device(X.device):
+    with _on_device(X.device):
         X, ldb = _rows(X, "X")
         W, transa, lda, stridea = _weights(W)
         L.ozgemm_grouped_gemm(t, _TYPES[Y.dtype], g, m, n, q, transa, W, lda, stridea, X, ldb, offsets, Y, _ld(Y))
@@ -132,7 +143,7 @@ def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
     dW = _target(dW, (g, m, q), (X.dtype, torch.float32) if dW is not None else (dw_dtype or X.dtype,), X, "dW")
     if dW.dtype not in (X.dtype, torch.float32):
         raise TypeError(f"grouped_linear_grads: dW is {X.dtype} or float32, not {dW.dtype}")
-    with torch.cuda.device(X.device):
+    with _on_device(X.device):
         X, ldx = _rows(X, "X")
         dY, ldy = _rows(dY, "dY")
         W, transa, lda, stridea = _weights(W)
@@ -177,7 +188,7 @@ def orthogonalize(G, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7, out=None
                          f"{out.dtype} on {out.device}")
     if G.numel() == 0:
         return out
-    with torch.cuda.device(G.device):
+    with _on_device(G.device):
         g = _matrices(G)
         o = _matrices(out)
         if o is None:

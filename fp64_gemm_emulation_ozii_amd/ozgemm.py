@@ -369,6 +369,11 @@ def ozgemm_phase_calls():
 # products over ragged groups (raw C-ABI signatures; column-major)
 # --------------------------------------------------------------------------
 
+# the workspace's argument number: what a call returns that needs one and has none
+_GEMM_NO_WORKSPACE = -16
+_OUTER_NO_WORKSPACE = -15
+
+
 def _room(workspace, nbytes: int, device):
     """(tensor kept alive, pointer, bytes) of a call's workspace: the given
     one, or one from torch's allocator on the current stream (which hands it
@@ -389,12 +394,19 @@ def ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, A, lda, s
 
 def ozgemm_grouped_gemm(type, ctype, groups, m, n, q, transa, A, lda, stridea, B, ldb, offsets, C, ldc,
                         workspace=None, stream=None, check: bool = True) -> int:
-    """With ``workspace=None`` the bytes the call needs come from torch's
-    allocator; a given workspace (a device tensor) stays the caller's."""
-    need = ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, A, lda, stridea, B, ldb)
-    keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"))
-    st = lib().ozgemm_grouped_gemm(type, ctype, groups, m, n, q, transa, _ptr(A), lda, stridea, _ptr(B), ldb,
-                                   _ptr(offsets), _ptr(C), ldc, ws, nbytes, _stream(stream))
+    """With ``workspace=None`` the bytes the call needs, if any, come from
+    torch's allocator; a given workspace (a device tensor) stays the
+    caller's."""
+    L, hs = lib(), _stream(stream)
+    ops = (type, ctype, groups, m, n, q, transa, _ptr(A), lda, stridea, _ptr(B), ldb, _ptr(offsets), _ptr(C), ldc)
+    st = _GEMM_NO_WORKSPACE if workspace is None else None
+    if workspace is None and type != OZGEMM_F32:  # 16-bit operands are usually read in place
+        st = L.ozgemm_grouped_gemm(*ops, None, 0, hs)
+    if st is None or st == _GEMM_NO_WORKSPACE:
+        need = 0 if workspace is not None else ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, A,
+                                                                                  lda, stridea, B, ldb)
+        keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"))
+        st = L.ozgemm_grouped_gemm(*ops, ws, nbytes, hs)
     return _check(st, "ozgemm_grouped_gemm") if check else st
 
 
@@ -405,10 +417,16 @@ def ozgemm_grouped_outer_workspace_bytes(type, groups, m, q, n, A, lda, B, ldb) 
 def ozgemm_grouped_outer(type, ctype, groups, m, q, n, A, lda, B, ldb, offsets, C, ldc, stridec, workspace=None,
                          stream=None, check: bool = True) -> int:
     """Workspace as for :func:`ozgemm_grouped_gemm`."""
-    need = ozgemm_grouped_outer_workspace_bytes(type, groups, m, q, n, A, lda, B, ldb)
-    keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"))
-    st = lib().ozgemm_grouped_outer(type, ctype, groups, m, q, n, _ptr(A), lda, _ptr(B), ldb, _ptr(offsets),
-                                    _ptr(C), ldc, stridec, ws, nbytes, _stream(stream))
+    L, hs = lib(), _stream(stream)
+    ops = (type, ctype, groups, m, q, n, _ptr(A), lda, _ptr(B), ldb, _ptr(offsets), _ptr(C), ldc, stridec)
+    st = _OUTER_NO_WORKSPACE if workspace is None else None
+    if workspace is None and type != OZGEMM_F32:
+        st = L.ozgemm_grouped_outer(*ops, None, 0, hs)
+    if st is None or st == _OUTER_NO_WORKSPACE:
+        need = 0 if workspace is not None else ozgemm_grouped_outer_workspace_bytes(type, groups, m, q, n, A, lda, B,
+                                                                                   ldb)
+        keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"))
+        st = L.ozgemm_grouped_outer(*ops, ws, nbytes, hs)
     return _check(st, "ozgemm_grouped_outer") if check else st
 
 

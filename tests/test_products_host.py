@@ -148,3 +148,12 @@ def test_orthogonalize_workspace_bytes():
 def test_orthogonalize_python_refusals(how, error):
     with pytest.raises(error):
         oz.orthogonalize(**{"G": torch.zeros(8, 8), **how})
+
+
+def test_tensors_off_the_gpu_are_refused():
+    with pytest.raises(ValueError, match="GPU"):
+        oz.grouped_linear(**_args())
+    with pytest.raises(ValueError, match="GPU"):
+        oz.grouped_linear_grads(**_args(dY=torch.zeros(10, 4)))
+    with pytest.raises(ValueError, match="GPU"):
+        oz.orthogonalize(torch.zeros(8, 8))
