@@ -664,13 +664,14 @@ int ortho64(const OrthoLayout& L, int batch, int m, int n, const double* G, long
                        as_it_lies ? X : XT, as_it_lies ? XT : X);
     OZ_TRY(hipGetLastError());
     for (int k = 0; k < steps; ++k) {
-      int status = dgemm_region(region, r, r, c, X, r, XT, c, P, r, s, st);
-      if (!status) status = dgemm_region(region, r, r, r, P, r, P, r, Q, r, s, st);
+      // P = X X^T from X^T's columns against themselves; P and Q are their own transposes
+      int status = dgemm_region_tn(region, r, r, c, XT, c, XT, c, P, r, s, st);
+      if (!status) status = dgemm_region_tn(region, r, r, r, P, r, P, r, Q, r, s, st);
       if (status) return status;
       const long rr = (long)r * r;
       hipLaunchKernelGGL(combine64_kernel, dim3((unsigned)((rr + 255) / 256)), dim3(256), 0, st, Q, P, co[3 * k + 1],
                          co[3 * k + 2], rr);
-      if ((status = dgemm_region(region, r, c, r, Q, r, X, r, Y, r, s, st))) return status;
+      if ((status = dgemm_region_tn(region, r, c, r, Q, r, X, r, Y, r, s, st))) return status;
       hipLaunchKernelGGL(update64_kernel, xt, dim3(256), 0, st, X, XT, Y, co[3 * k], c, r,
                          k + 1 == steps ? Oi : nullptr, ldo, as_it_lies ? 0 : 1);
       OZ_TRY(hipGetLastError());

@@ -839,12 +839,52 @@ hipError_t dgemm_region_table(char* region, int s, hipStream_t st) {
   return hipGetLastError();
 }
 
-int dgemm_region(char* region, int m, int n, int q, const double* A, int lda, const double* B, int ldb, double* C,
-                 int ldc, int s, hipStream_t st) {
+namespace {
+
+// Exponents and residue planes of the columns of X (q x rows, one column per
+// row of the planes), conservative budget.
+int region_side(const double* X, int rows, int q, int ld, const ResidueConsts& rc, int32_t* ex, int8_t* planes,
+                int rows_pad, int q_pad, hipStream_t st) {
+  if (col_residue_fits(q)) {
+    OZ_CHECK(launch_col_residue(X, rows, q, ld, ex, rc, planes, rows_pad, q_pad, st));
+    return 0;
+  }
+  OZ_CHECK(launch_col_exp(X, q, rows, ld, ex, st));
+  OZ_CHECK(launch_residue(X, rows, q, ld, 1, ex, rc, planes, rows_pad, q_pad, nullptr, 0, 0, st));
+  return 0;
+}
+
+}  // namespace
+
+int dgemm_region_tn(char* region, int m, int n, int q, const double* A, int lda, const double* B, int ldb, double* C,
+                    int ldc, int s, hipStream_t st) {
   int mp, np, qp;
   dims(m, n, q, &mp, &np, &qp);
-  const Ctx x{region, make_layout(m, n, q, s), mp, st, OZGEMM_BOUND_CONSERVATIVE};
-  return run_dgemm(x, reinterpret_cast<const double*>(region), m, n, q, A, lda, B, ldb, C, ldc, s, nullptr);
+  const Layout lay = make_layout(m, n, q, s);
+  ResidueConsts rc;
+  GemmConsts gc;
+  CrtConsts cc;
+  make_consts(s, q, OZGEMM_BOUND_CONSERVATIVE, &rc, &gc, &cc);
+  cc.wtab = reinterpret_cast<const double*>(region);
+  int32_t* e = reinterpret_cast<int32_t*>(region + lay.e);
+  int32_t* f = reinterpret_cast<int32_t*>(region + lay.f);
+  int8_t* Ares = reinterpret_cast<int8_t*>(region + lay.ares);
+  int8_t* Bres = reinterpret_cast<int8_t*>(region + lay.bres);
+  uint8_t* rt = reinterpret_cast<uint8_t*>(region + lay.rt);
+  int status = region_side(A, m, q, lda, rc, e, Ares, mp, qp, st);
+  if (status) return status;
+  if (A == B && m == n && lda == ldb) {  // one operand against itself: its planes serve both sides
+    f = e;
+    Bres = Ares;
+  } else if ((status = region_side(B, n, q, ldb, rc, f, Bres, np, qp, st))) {
+    return status;
+  }
+  SplitChoice split{};
+  int cus = 0;
+  if ((status = product_split(lay, mp, np, qp, s, &split, &cus))) return status;
+  OZ_CHECK(launch_gemm(Ares, Bres, mp, np, qp, gc, nullptr, rt, split, rt, cus, st));
+  OZ_CHECK(launch_crt(rt, m, n, mp, np, e, f, cc, C, ldc, st));
+  return 0;
 }
 
 }  // namespace oz

@@ -69,8 +69,9 @@ hipError_t launch_slice_groups(int type, const void* src, long ld, int rows, int
 // an r x c matrix's iteration).
 size_t dgemm_region_bytes(int r, int c, int s);
 hipError_t dgemm_region_table(char* region, int s, hipStream_t st);  // once before the products of a call
-int dgemm_region(char* region, int m, int n, int q, const double* A, int lda, const double* B, int ldb, double* C,
-                 int ldc, int s, hipStream_t st);
+// C (m x n) = A^T B with A q x m and B q x n, q >= 1; A may be B.
+int dgemm_region_tn(char* region, int m, int n, int q, const double* A, int lda, const double* B, int ldb, double* C,
+                    int ldc, int s, hipStream_t st);
 
 // Compute units of the current device.
 hipError_t device_units(int* cus);
