@@ -49,11 +49,13 @@ struct Store {
   static constexpr int BYTES = Tile::NW * 16 * PITCH * 4;
   static_assert(16 * RUNS % 64 == 0, "whole wavefronts of runs");
 
-  // Whether every lane stores every run of a tile, as 16 bytes (16-bit types only).
-  static __device__ __forceinline__ bool whole(const Target& t, int bm, int bn) {
-    return t.ctype != OZGEMM_F32 && aligned(t) && t.m0 + bm <= t.m && t.n0 + bn <= t.n_end;
+  // 16-byte stores of every wavefront, in STORES, where every lane stores
+  // every run of a tile; 0 where some do not.
+  static __device__ __forceinline__ int stores(const Target& t, int bm, int bn) {
+    const bool all = aligned(t) && t.m0 + bm <= t.m && t.n0 + bn <= t.n_end;
+    return !all ? 0 : t.ctype == OZGEMM_F32 ? 2 : 1;
   }
-  static constexpr int STORES = Tile::FN * CH;  // per wavefront then
+  static constexpr int STORES = Tile::FN * CH;
   static __device__ __forceinline__ bool aligned(const Target& t) {
     return (t.ldc & 7) == 0 && ((uintptr_t)t.C & 15) == 0;
   }
@@ -65,8 +67,21 @@ struct Store {
     const int mw = t.m0 + Tile::wave_m(wave) * WTM, nw = t.n0 + Tile::wave_n(wave) * (Tile::FN * 16);
     const int size = t.ctype == OZGEMM_F32 ? 4 : 2;
     const bool wide = aligned(t);
+    // a lane's runs all begin at the same row
+    static_assert(64 % RUNS == 0, "a lane keeps its rows");
+    const int row = mw + lane % RUNS * 8;
+    int ea[8] = {};
+    if (t.ea != nullptr) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ea[k] = t.ea[min(row + k, t.m - 1)];
+    }
 #pragma unroll
     for (int j = 0; j < Tile::FN; ++j) {
+      int eb[CH] = {};
+      if (t.ea != nullptr) {
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) eb[ch] = t.eb[min(nw + j * 16 + (ch * 64 + lane) / RUNS, t.n_end - 1)];
+      }
 #pragma unroll
       for (int i = 0; i < Tile::FM; ++i)
         *reinterpret_cast<v4f*>(stage + (lane & 15) * PITCH + i * 16 + 4 * (lane >> 4)) = acc[i][j];
@@ -75,15 +90,14 @@ struct Store {
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
         const int at = ch * 64 + lane, c = at / RUNS, r = at % RUNS * 8;
-        const int col = nw + j * 16 + c, row = mw + r;
+        const int col = nw + j * 16 + c;
         if (col >= t.n_end || row >= t.m) continue;
         float v[8];
         *reinterpret_cast<v4f*>(v) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r);
         *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r + 4);
         if (t.ea != nullptr) {
-          const int eb = t.eb[col];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = unscale(v[k], t.ea[min(row + k, t.m - 1)], eb);
+          for (int k = 0; k < 8; ++k) v[k] = unscale(v[k], ea[k], eb[ch]);
         }
         char* out = (char*)t.C + ((long)col * t.ldc + row) * size;
         const bool all = wide && row + 8 <= t.m;
@@ -181,12 +195,9 @@ struct Walk {
     feed.begin(job.A, job.B, job.inner);
     feed.issue(0);
     v4f acc[Tile::FM][Tile::FN];
-    bool whole = false;
+    int later = 0;
     for (int round = 1, L = share.first;; ++round) {
-      if (whole)
-        Tile::template resume<Out::STORES>(acc, feed, job.inner, job.to.n_end - job.to.n0);
-      else
-        Tile::template resume<0>(acc, feed, job.inner, job.to.n_end - job.to.n0);
+      Tile::template resume<Out::STORES>(acc, feed, job.inner, job.to.n_end - job.to.n0, later);
       const Target from = job.to;
       slice_barrier<0>();  // every wave has read its last operands, and no load into LDS is in flight
       const bool more = round < share.rounds;
@@ -198,7 +209,7 @@ struct Walk {
       }
       Out::run(acc, smem + STAGE, from);
       if (!more) break;
-      whole = Out::whole(from, BT, BT);
+      later = Out::stores(from, BT, BT);
       __builtin_amdgcn_s_barrier();  // every wave has read its staged results
       asm volatile("" ::: "memory");
     }

@@ -344,14 +344,15 @@ struct Tile16 {
     Feed feed(smem);
     feed.begin(A, B, q);
     feed.issue(0);
-    resume<0>(acc, feed, q, BN);
+    resume(acc, feed, q, BN);
   }
 
-  // The product of the tile whose slice 0 has been issued; LATER more memory
-  // operations may have followed it.  A wavefront whose columns all lie past
-  // the first `cols` only loads.
-  template <int LATER>
-  static __device__ __forceinline__ void resume(v4f (&acc)[FM][FN], Feed& feed, int q, int cols) {
+  // The product of the tile whose slice 0 has been issued.  SOME or twice SOME
+  // more memory operations have followed it where `later` is 1 or 2; it may be
+  // 0 always.  A wavefront whose columns all lie past the first `cols` only
+  // loads.
+  template <int SOME = 0>
+  static __device__ __forceinline__ void resume(v4f (&acc)[FM][FN], Feed& feed, int q, int cols, int later = 0) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave_m(wave), wn = wave_n(wave);
@@ -370,7 +371,13 @@ struct Tile16 {
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    wait_loads<(NB - 1) * LPW + LATER>();  // slice 0 (loads and stores leave the counter in order)
+    // slice 0 (loads and stores leave the counter in order)
+    if (SOME > 0 && later == 2)
+      wait_loads<(NB - 1) * LPW + 2 * SOME>();
+    else if (SOME > 0 && later == 1)
+      wait_loads<(NB - 1) * LPW + SOME>();
+    else
+      wait_loads<(NB - 1) * LPW>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if (wn * (BN / WN) >= cols) {
