@@ -218,6 +218,7 @@ int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n, c
               overlap(C, cb, offsets, ((size_t)groups + 1) * 4)))
     return -12;
   const Rooms r = outer_rooms(type, groups, m, q, n, A, lda, B, ldb);
+  if (r.A.used && r.A.ld > LD16_MAX) return OZGEMM_RANGE;
   if (r.total > 0 && (workspace == nullptr || ((uintptr_t)workspace & (WS_ALIGN - 1)))) return -15;
   if (workspace_bytes < r.total) return OZGEMM_WORKSPACE_TOO_SMALL;
   if (!any) return OZGEMM_OK;

@@ -309,7 +309,6 @@ struct State {
   int bound = OZGEMM_BOUND_CONSERVATIVE;  // bit budget of Scheme II calls
   bool timing = false;
   std::vector<std::array<hipEvent_t, 5>> events;
-  std::string hip_err;
   int panels = 0;  // ozgemm_set_panels: 0 automatic, 1 off, P >= 2 forced
   // the panel pipeline's second stream and its events (created at the first
   // pipelined call, on the device current then)
@@ -353,8 +352,11 @@ constexpr size_t TIMING_MAX_CALLS = 4096;
 constexpr int OZ_MAX_ROWS = OZGEMM_MAX_ROWS;
 static_assert((OZ_MAX_ROWS + ROW_PAD - 1) / ROW_PAD * ROW_PAD / 32 <= 65535, "row tiles fit grid.y");
 
+// The last HIP error of this thread (calls that keep no state may run on several).
+thread_local const char* hip_err = "";
+
 int hip_fail(hipError_t err) {
-  g.hip_err = hipGetErrorString(err);
+  hip_err = hipGetErrorString(err);
   return OZGEMM_HIP_ERROR;
 }
 
@@ -932,6 +934,7 @@ int ozgemm_free(void) {
   ozgemm_timing(0);
   release_side();
   g = State{};
+  hip_err = "";
   return OZGEMM_OK;
 }
 
@@ -955,7 +958,7 @@ const char* ozgemm_strerror(int status) {
              "OS II-fast, int32 product planes asked for at q >= 2^17, or a size above the configured maximum)";
     case OZGEMM_WORKSPACE_TOO_SMALL: return "workspace smaller than ozgemm_workspace_bytes";
     case OZGEMM_HIP_ERROR:
-      msg = "HIP error: " + g.hip_err;
+      msg = std::string("HIP error: ") + hip_err;
       return msg.c_str();
     default: return "unknown status";
   }

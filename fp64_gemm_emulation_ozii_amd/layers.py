@@ -37,12 +37,20 @@ def _on_device(device):
     return torch.cuda.device(device)
 
 
+def _fits(*sizes) -> None:
+    if max(sizes) > L.OZGEMM_MAX_ROWS:
+        raise ValueError(f"sizes go up to {L.OZGEMM_MAX_ROWS}, got {max(sizes)}")
+
+
+_LD_MAX = 2 ** 31 - 1  # leading dimensions are C ints
+
+
 def _rows(t, what: str):
     """A 2-d tensor with its rows' entries next to each other, and their distance."""
     if t.dim() != 2:
         raise ValueError(f"{what} must have two dimensions, got {tuple(t.shape)}")
     n, q = t.shape
-    if (q > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < max(1, q)):
+    if (q > 1 and t.stride(1) != 1) or (n > 1 and not max(1, q) <= t.stride(0) <= _LD_MAX):
         t = t.contiguous()
     return t, max(1, q, t.stride(0) if n > 1 else 0)
 
@@ -55,9 +63,9 @@ def _weights(W):
     g, m, q = W.shape
     s0, s1, s2 = W.stride()
     s0 = s0 if g > 1 else 0
-    if (q <= 1 or s2 == 1) and (m <= 1 or s1 >= max(1, q)):
+    if (q <= 1 or s2 == 1) and (m <= 1 or max(1, q) <= s1 <= _LD_MAX):
         return W, 1, max(1, q, s1 if m > 1 else 0), s0
-    if (m <= 1 or s1 == 1) and (q <= 1 or s2 >= max(1, m)):
+    if (m <= 1 or s1 == 1) and (q <= 1 or max(1, m) <= s2 <= _LD_MAX):
         return W, 0, max(1, m, s2 if q > 1 else 0), s0
     W = W.contiguous()
     return W, 1, max(1, q), m * q
@@ -84,7 +92,7 @@ def _target(out, shape, dtypes, like, what: str):
         raise ValueError(f"{what} must be {tuple(shape)} of {dtypes[0]} on {like.device}, got {tuple(out.shape)} of "
                          f"{out.dtype} on {out.device}")
     s = out.stride()
-    if (out.shape[-1] > 1 and s[-1] != 1) or (out.shape[-2] > 1 and s[-2] < max(1, out.shape[-1])) or (
+    if (out.shape[-1] > 1 and s[-1] != 1) or (out.shape[-2] > 1 and not max(1, out.shape[-1]) <= s[-2] <= _LD_MAX) or (
             out.dim() == 3 and out.shape[0] > 1 and s[0] < max(1, out.shape[1]) * max(s[1], out.shape[2])):
         raise ValueError(f"{what} must have its rows' entries next to each other and its rows apart, strides {s}")
     return out
@@ -110,6 +118,7 @@ def grouped_linear(X, W, offsets, out=None, out_dtype=None):
         raise ValueError(f"X {tuple(X.shape)} and W {tuple(W.shape)} do not go together")
     g, m, q = W.shape
     n = X.shape[0]
+    _fits(n, m, q)
     offsets = _offsets(offsets, g, X.device)
     Y = _target(out, (n, m), (X.dtype, torch.float32) if out is not None else (out_dtype or X.dtype,), X, "out")
     if Y.dtype not in (X.dtype, torch.float32):
@@ -138,6 +147,7 @@ def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
         raise ValueError(f"dY {tuple(dY.shape)}, X {tuple(X.shape)} and W {tuple(W.shape)} do not go together")
     g, m, q = W.shape
     n = X.shape[0]
+    _fits(n, m, q)
     offsets = _offsets(offsets, g, X.device)
     dX = _target(dX, (n, q), (X.dtype,), X, "dX")
     dW = _target(dW, (g, m, q), (X.dtype, torch.float32) if dW is not None else (dw_dtype or X.dtype,), X, "dW")
@@ -181,6 +191,7 @@ def orthogonalize(G, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7, out=None
     if torch.is_grad_enabled() and G.requires_grad:
         raise RuntimeError("orthogonalize is not recorded by autograd: call it under torch.no_grad()")
     r, c = G.shape[-2:]
+    _fits(r, c)
     if out is None:
         out = torch.empty(G.shape, dtype=G.dtype, device=G.device)
     elif out.shape != G.shape or out.dtype != G.dtype or out.device != G.device:
@@ -205,7 +216,7 @@ def _matrices(t):
     with contiguous rows, all evenly apart; None if it is none."""
     r, c = t.shape[-2:]
     ld = max(1, c, t.stride(-2) if r > 1 else 0)
-    if (c > 1 and t.stride(-1) != 1) or (r > 1 and t.stride(-2) < c):
+    if (c > 1 and t.stride(-1) != 1) or (r > 1 and not c <= t.stride(-2) <= _LD_MAX):
         return None
     batch, step = 1, 0
     for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):

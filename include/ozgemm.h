@@ -490,7 +490,8 @@ size_t ozgemm_grouped_gemm_workspace_bytes(int type, int groups, int m, int n, i
  * C + e stridec (stridec >= ldc q where groups > 1).  An empty group gives
  * zeros.  Types, errors and workspace as above; 16-bit operands are read in
  * place where columns begin on 16-byte boundaries and m and q are multiples
- * of 8. */
+ * of 8.  Operands that pass through the workspace (there each group begins at
+ * a multiple of 64) need n + 63 min(groups, n) <= 2^21 (OZGEMM_RANGE). */
 int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n,
                          const void *A, int lda, const void *B, int ldb,
                          const int32_t *offsets, void *C, int ldc, long long stridec,
@@ -516,7 +517,8 @@ size_t ozgemm_grouped_outer_workspace_bytes(int type, int groups, int m, int q, 
  *           budget whatever ozgemm_set_bound says); not looked at otherwise
  * The states between the products keep 22 bits or more (F64: 53); BF16
  * products are formed from 11-bit operands, F16 and F32 ones as the grouped
- * products of F32 operands are.  steps = 0 gives the normalised G.  A matrix
+ * products of F32 operands are.  The norm is a sum of squares in FP64 (F64
+ * entries beyond 1e153 overflow it: zeros).  steps = 0 gives the normalised G.  A matrix
  * of zeros gives zeros where eps > 0 (NaN where it is 0); one that holds Inf
  * or NaN gives NaN throughout (steps > 0).
  * Errors: -i for argument i; OZGEMM_RANGE for m or n above OZGEMM_ORTHO_MAX,

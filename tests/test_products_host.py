@@ -48,6 +48,8 @@ def test_grouped_gemm_refusals(change, status):
     (dict(C=O + 4), -12), (dict(n=L.OZGEMM_MAX_ROWS + 1), L.OZGEMM_RANGE),
     (dict(type=L.OZGEMM_F32), -15), (dict(type=L.OZGEMM_F32, ws=WS, nbytes=1000), L.OZGEMM_WORKSPACE_TOO_SMALL),
     (dict(A=A + 2), -15), (dict(ldb=129), -15),
+    # 2^21 columns, each group's rounded up to 64: the rows of the slices would pass 32-bit offsets
+    (dict(type=L.OZGEMM_F32, n=2090000, groups=1000, C=P + (40 << 34)), L.OZGEMM_RANGE),
     (dict(m=0), 0), (dict(q=0), 0), (dict(groups=0), 0),
 ])
 def test_grouped_outer_refusals(change, status):
@@ -157,3 +159,11 @@ def test_tensors_off_the_gpu_are_refused():
         oz.grouped_linear_grads(**_args(dY=torch.zeros(10, 4)))
     with pytest.raises(ValueError, match="GPU"):
         oz.orthogonalize(torch.zeros(8, 8))
+
+
+def test_sizes_past_the_limits_are_refused():
+    wide = torch.zeros(1).expand(1, L.OZGEMM_MAX_ROWS + 1)
+    with pytest.raises(ValueError, match="sizes"):
+        oz.grouped_linear(wide, torch.zeros(1).expand(1, 4, L.OZGEMM_MAX_ROWS + 1), torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="sizes"):
+        oz.orthogonalize(wide)
