@@ -263,6 +263,33 @@ __global__ __launch_bounds__(512) void grouped_k_kernel(Grouped16 g) {
   });
 }
 
+// Four consecutive rows of a column of C, `wide` where they can be stored as one.
+__device__ __forceinline__ void store4(const Grouped16& g, long col, int row, bool wide, v4f v) {
+  const long to = col * g.ldc + row;
+  if (g.ctype == OZGEMM_F32) {
+    float* out = (float*)g.C + to;
+    if (wide && row + 4 <= g.m) {
+      *reinterpret_cast<v4f*>(out) = v;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row + k < g.m) out[k] = v[k];
+    }
+  } else {
+    v4s h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = (short)round16(v[k], g.ctype);
+    short* out = (short*)g.C + to;
+    if (wide && row + 4 <= g.m) {
+      *reinterpret_cast<v4s*>(out) = h;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row + k < g.m) out[k] = h[k];
+    }
+  }
+}
+
 // Groups of a few columns: bound by reading the weights once.  A block takes
 // ROWS rows of a group's weights and up to 64 of its columns; its four
 // wavefronts share the inner dimension, 32 DEPTH entries of it at a time,
@@ -325,38 +352,88 @@ __global__ __launch_bounds__(256, 2) void few_columns_kernel(Grouped16 g) {
     v4f v = *reinterpret_cast<const v4f*>(&sums[0][c >> 4][c & 15][r]);
 #pragma unroll
     for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const v4f*>(&sums[w][c >> 4][c & 15][r]);
-    const long to = (long)(n0 + c) * g.ldc + row;
-    if (g.ctype == OZGEMM_F32) {
-      float* out = (float*)g.C + to;
-      if (wide && row + 4 <= g.m) {
-        *reinterpret_cast<v4f*>(out) = v;
-      } else {
+    store4(g, n0 + c, row, wide, v);
+  }
+}
+
+// The same for weights that lie K-strided (m entries next to each other).  A
+// wavefront takes 128 rows: a lane reads 8 of them of one k (16 lanes: 256
+// bytes next to each other), of 8 k in turn, and transposes its 8 x 8 entries
+// in registers into eight MFMA operands, the u-th of which has rows m0 + 8 i + u,
+// i = 0..15.  Eight wavefronts share the inner dimension.
+template <class T, int DEPTH>
+__global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
+  constexpr int ROWS = 128, COLS = 32, CF = COLS / 16, WAVES = 8;
+  __shared__ float sums[WAVES][16][ROWS + 4];
+  const GroupIndex index(g.offsets, g.groups, g.n, COLS);
+  const int tiles_m = (g.m + ROWS - 1) / ROWS;
+  if ((int)blockIdx.x >= tiles_m * index.total) return;
+  const int nj = blockIdx.x / tiles_m, m0 = blockIdx.x % tiles_m * ROWS;
+  const GroupTile gt = index.find(nj);
+  const int n0 = gt.begin, cols = min(gt.end - n0, COLS), frags = (cols + 15) / 16;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int kl = wave * 32 * DEPTH + (lane >> 4) * 8;  // this lane's first k in a chunk
+  const long ld = g.A.ld;
+  // rows past the end read the last eight again (m is a multiple of 8; their sums are not stored)
+  const uint16_t* a = g.A.p + gt.group * g.A.batch + min(m0 + (lane & 15) * 8, g.m - 8);
+  const uint16_t* b[CF];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (row + k < g.m) out[k] = v[k];
-      }
-    } else {
-      v4s h;
+  for (int c = 0; c < CF; ++c) b[c] = g.B.p + (long)(n0 + min(c * 16 + (lane & 15), cols - 1)) * g.B.ld + kl;
+  v4f acc[CF][8] = {};
+  const v8s zero = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int k0 = 0; k0 < g.q; k0 += WAVES * 32 * DEPTH) {
+    v8s av[DEPTH][8], bv[DEPTH][CF];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = (short)round16(v[k], g.ctype);
-      short* out = (short*)g.C + to;
-      if (wide && row + 4 <= g.m) {
-        *reinterpret_cast<v4s*>(out) = h;
-      } else {
+    for (int d = 0; d < DEPTH; ++d) {
+      const int k = kl + k0 + d * 32;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (row + k < g.m) out[k] = h[k];
-      }
+      for (int t = 0; t < 8; ++t) av[d][t] = k + t < g.q ? *reinterpret_cast<const v8s*>(a + (k + t) * ld) : zero;
+#pragma unroll
+      for (int c = 0; c < CF; ++c)
+        bv[d][c] = c < frags && k < g.q ? *reinterpret_cast<const v8s*>(b[c] + k0 + d * 32) : zero;
     }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        v8s f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) f[t] = av[d][t][u];
+#pragma unroll
+        for (int c = 0; c < CF; ++c) acc[c][u] = T::mfma(f, bv[d][c], acc[c][u]);
+      }
+  }
+  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
+#pragma unroll
+  for (int c = 0; c < CF; ++c) {
+    if (c >= frags) break;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float* s = &sums[wave][lane & 15][(4 * (lane >> 4) + r) * 8];
+      *reinterpret_cast<v4f*>(s) = v4f{acc[c][0][r], acc[c][1][r], acc[c][2][r], acc[c][3][r]};
+      *reinterpret_cast<v4f*>(s + 4) = v4f{acc[c][4][r], acc[c][5][r], acc[c][6][r], acc[c][7][r]};
+    }
+    __syncthreads();
+    const int r = threadIdx.x % (ROWS / 4) * 4, col = threadIdx.x / (ROWS / 4);  // 32 x 16 = every thread one run
+    if (c * 16 + col < cols && m0 + r < g.m) {
+      v4f v = *reinterpret_cast<const v4f*>(&sums[0][col][r]);
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const v4f*>(&sums[w][col][r]);
+      store4(g, n0 + c * 16 + col, m0 + r, wide, v);
+    }
+    __syncthreads();
   }
 }
 
 template <class T>
 hipError_t few_columns(const Grouped16& g, hipStream_t st) {
-  const long tiles = group_tiles_max(g.n, g.groups, 64);
-  constexpr int MR = 1, DEPTH = 16;
-  hipLaunchKernelGGL((few_columns_kernel<T, MR, DEPTH>), dim3((unsigned)(tiles * ((g.m + 16 * MR - 1) / (16 * MR)))),
-                     dim3(256), 0, st, g);
+  if (g.A.ks) {
+    const long blocks = group_tiles_max(g.n, g.groups, 32) * ((g.m + 127) / 128);
+    hipLaunchKernelGGL((few_columns_ks_kernel<T, 2>), dim3((unsigned)blocks), dim3(512), 0, st, g);
+  } else {
+    const long blocks = group_tiles_max(g.n, g.groups, 64) * ((g.m + 15) / 16);
+    hipLaunchKernelGGL((few_columns_kernel<T, 1, 16>), dim3((unsigned)blocks), dim3(256), 0, st, g);
+  }
   return hipGetLastError();
 }
 
@@ -382,7 +459,7 @@ hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
 
 // counted with the smallest tiles any variant uses
 bool grouped_n_fits(const Grouped16& g) {
-  return group_tiles_max(g.n, g.groups, 64) * ((g.m + 15) / 16) <= 0x7fffffffL;
+  return group_tiles_max(g.n, g.groups, 32) * ((g.m + 15) / 16) <= 0x7fffffffL;
 }
 
 bool grouped_k_fits(const Grouped16& g) {
@@ -392,7 +469,7 @@ bool grouped_k_fits(const Grouped16& g) {
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
   if (g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
   if (g.f32) return grouped_n<Half, 128, false, true>(g, st);
-  if (!g.A.ks && (g.n <= 64 || g.n <= 32L * g.groups)) return g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
+  if (g.n <= 64 || g.n <= 32L * g.groups) return g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
   if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, true, false>(g, st) : grouped_n<Bfloat, 256, false, false>(g, st);
   return g.A.ks ? grouped_n<Half, 256, true, false>(g, st) : grouped_n<Half, 256, false, false>(g, st);
 }
