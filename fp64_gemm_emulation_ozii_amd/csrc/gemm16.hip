@@ -129,13 +129,15 @@ struct Store {
   }
 };
 
-// How `total` tiles are shared out over gridDim.x = 3 units blocks, one per
+// How `total` tiles are shared out over gridDim.x = 4 units blocks, one per
 // compute unit at a time.  The first `units` blocks walk whole rounds of
 // tiles; a round before the last, the next `units` blocks take one tile each
 // as units become free (tiles at the end of a group are cheaper than others);
 // what then remains is less than a round, and where it is no more than half
-// of one, its tiles are cut into quarters for the last blocks, or else taken
-// whole.
+// of one, its tiles are cut into quarters for the last 2 units blocks, or else
+// taken whole.
+constexpr int SHARES = 4;  // blocks of a launch, in units
+
 struct Share {
   int rounds;    // of the first blocks
   int first;     // tile of this block, -1: none
@@ -178,7 +180,7 @@ struct Walk {
   static __device__ __forceinline__ void run(char* smem, int total, Place place) {
     constexpr int BT = Tile::ROWS_M;
     static_assert(BT == Tile::ROWS_N && BT == 2 * Small::ROWS_M && BT == 2 * Small::ROWS_N, "square tiles and quarters");
-    const int units = gridDim.x / 3;
+    const int units = gridDim.x / SHARES;
     const Share share = share_of(total, units, blockIdx.x);
     if (share.first < 0) return;
     if (share.quarter >= 0) {
@@ -291,16 +293,16 @@ __device__ __forceinline__ void store4(const Grouped16& g, long col, int row, bo
 }
 
 // Groups of a few columns: bound by reading the weights once.  A block takes
-// ROWS rows of a group's weights and up to 64 of its columns; its four
+// 16 MR rows of a group's weights and up to 64 of its columns; its eight
 // wavefronts share the inner dimension, 32 DEPTH entries of it at a time,
 // whose loads are all in flight before the first product, straight from HBM
 // into the MFMA's operand layout (16 rows x 64 bytes per load; the two halves
 // of a 128-byte line are loaded one after the other).  The columns, which the
 // L2 serves, come the same way.  The wavefronts' sums meet in LDS.
 template <class T, int MR, int DEPTH>
-__global__ __launch_bounds__(256, 2) void few_columns_kernel(Grouped16 g) {
-  constexpr int ROWS = 16 * MR, COLS = 64, CF = COLS / 16;
-  __shared__ float sums[4][CF][16][ROWS + 4];
+__global__ __launch_bounds__(512, 2) void few_columns_kernel(Grouped16 g) {
+  constexpr int ROWS = 16 * MR, COLS = 64, CF = COLS / 16, WAVES = 8;
+  __shared__ float sums[WAVES][16][ROWS + 4];
   const GroupIndex index(g.offsets, g.groups, g.n, COLS);
   const int tiles_m = (g.m + ROWS - 1) / ROWS;
   if ((int)blockIdx.x >= tiles_m * index.total) return;
@@ -319,7 +321,7 @@ __global__ __launch_bounds__(256, 2) void few_columns_kernel(Grouped16 g) {
   for (int c = 0; c < CF; ++c) b[c] = g.B.p + (long)(n0 + min(c * 16 + (lane & 15), cols - 1)) * g.B.ld + kl;
   v4f acc[MR][CF] = {};
   const v8s zero = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int k0 = 0; k0 < g.q; k0 += 4 * 32 * DEPTH) {
+  for (int k0 = 0; k0 < g.q; k0 += WAVES * 32 * DEPTH) {
     v8s av[DEPTH][MR];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
@@ -339,20 +341,22 @@ __global__ __launch_bounds__(256, 2) void few_columns_kernel(Grouped16 g) {
         for (int i = 0; i < MR; ++i) acc[i][c] = T::mfma(av[d][i], bv[d], acc[i][c]);
     }
   }
+  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
 #pragma unroll
-  for (int c = 0; c < CF; ++c)
+  for (int c = 0; c < CF; ++c) {
+    if (c >= frags) break;
 #pragma unroll
     for (int i = 0; i < MR; ++i)
-      if (c < frags) *reinterpret_cast<v4f*>(&sums[wave][c][lane & 15][i * 16 + 4 * (lane >> 4)]) = acc[i][c];
-  __syncthreads();
-  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
-  for (int at = threadIdx.x; at < frags * 16 * (ROWS / 4); at += 256) {
-    const int r = at % (ROWS / 4) * 4, c = at / (ROWS / 4), row = m0 + r;
-    if (c >= cols || row >= g.m) continue;
-    v4f v = *reinterpret_cast<const v4f*>(&sums[0][c >> 4][c & 15][r]);
+      *reinterpret_cast<v4f*>(&sums[wave][lane & 15][i * 16 + 4 * (lane >> 4)]) = acc[i][c];
+    __syncthreads();
+    const int r = threadIdx.x % (ROWS / 4) * 4, col = threadIdx.x / (ROWS / 4);
+    if (col < 16 && c * 16 + col < cols && m0 + r < g.m) {
+      v4f v = *reinterpret_cast<const v4f*>(&sums[0][col][r]);
 #pragma unroll
-    for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const v4f*>(&sums[w][c >> 4][c & 15][r]);
-    store4(g, n0 + c, row, wide, v);
+      for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const v4f*>(&sums[w][col][r]);
+      store4(g, n0 + c * 16 + col, m0 + r, wide, v);
+    }
+    __syncthreads();
   }
 }
 
@@ -425,14 +429,31 @@ __global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
   }
 }
 
+// Whether the kernels above are the faster ones.  They read the weights at
+// the card's rate and the columns once for every 32 or 128 rows; the tiles
+// read both from L2 but need many tiles in flight for that rate.  Measured in
+// us, K-contiguous weights (few columns against tiles):
+//   32 experts of 4096 x 2048   8 rows each 111 / 135   24: 131 / 139   32: 147 / 141
+//   64 of 1024 x 2048           8:  60 / 71             24:  72 / 73    32:  76 / 74
+//   8 of 2048 x 2048            8:  17 / 33             48:  26 / 36    64:  44 / 37
+//   1 of 4096 x 4096            8:  15 / 56                             128: 27 / 63
+bool few(const Grouped16& g, int units) {
+  const long tiles = (long)g.groups * ((g.m + 255) / 256);
+  const long most = tiles * 16 <= units ? 128 : tiles * 4 <= units ? 48 : 24;
+  return g.n <= most * g.groups;
+}
+
 template <class T>
 hipError_t few_columns(const Grouped16& g, hipStream_t st) {
   if (g.A.ks) {
     const long blocks = group_tiles_max(g.n, g.groups, 32) * ((g.m + 127) / 128);
     hipLaunchKernelGGL((few_columns_ks_kernel<T, 2>), dim3((unsigned)blocks), dim3(512), 0, st, g);
   } else {
-    const long blocks = group_tiles_max(g.n, g.groups, 64) * ((g.m + 15) / 16);
-    hipLaunchKernelGGL((few_columns_kernel<T, 1, 16>), dim3((unsigned)blocks), dim3(256), 0, st, g);
+    // 32 experts of 4096 x 2048, 8 / 32 rows each: MR 2, DEPTH 4 takes 111 / 147 us,
+    // 4, 4: 125 / 148; 1, 8: 134 / 206; 2, 8 (fewer blocks on a unit): 146 / 197
+    constexpr int MR = 2, DEPTH = 4;
+    const long blocks = group_tiles_max(g.n, g.groups, 64) * ((g.m + 16 * MR - 1) / (16 * MR));
+    hipLaunchKernelGGL((few_columns_kernel<T, MR, DEPTH>), dim3((unsigned)blocks), dim3(512), 0, st, g);
   }
   return hipGetLastError();
 }
@@ -442,7 +463,7 @@ hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
   int cus = 0;
   const hipError_t err = device_units(&cus);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((grouped_n_kernel<T, BT, AKS, PAIR>), dim3(3 * cus), dim3(512), 0, st, g);
+  hipLaunchKernelGGL((grouped_n_kernel<T, BT, AKS, PAIR>), dim3(SHARES * cus), dim3(512), 0, st, g);
   return hipGetLastError();
 }
 
@@ -451,7 +472,7 @@ hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
   int cus = 0;
   const hipError_t err = device_units(&cus);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((grouped_k_kernel<T, BT, KS, PAIR>), dim3(3 * cus), dim3(512), 0, st, g);
+  hipLaunchKernelGGL((grouped_k_kernel<T, BT, KS, PAIR>), dim3(SHARES * cus), dim3(512), 0, st, g);
   return hipGetLastError();
 }
 
@@ -469,7 +490,10 @@ bool grouped_k_fits(const Grouped16& g) {
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
   if (g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
   if (g.f32) return grouped_n<Half, 128, false, true>(g, st);
-  if (g.n <= 64 || g.n <= 32L * g.groups) return g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
+  int units = 0;
+  const hipError_t err = device_units(&units);
+  if (err != hipSuccess) return err;
+  if (few(g, units)) return g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
   if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, true, false>(g, st) : grouped_n<Bfloat, 256, false, false>(g, st);
   return g.A.ks ? grouped_n<Half, 256, true, false>(g, st) : grouped_n<Half, 256, false, false>(g, st);
 }

@@ -312,3 +312,67 @@ def test_a_given_workspace():
         L.ozgemm_grouped_gemm(L.OZGEMM_F32, L.OZGEMM_F32, 2, 50, 93, 70, 1, W, 70, 3500, X, 70, off, Y, 50,
                               workspace=ws[:need - 1])
     assert e.value.status == L.OZGEMM_WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.parametrize("layout", ["mq", "qm"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("sizes, m, q", [
+    ([1], 8, 8), ([2, 0, 1], 136, 1024), ([16] * 9, 264, 2056), ([17, 0, 31, 33, 1], 520, 264), ([100, 20, 3], 72, 520),
+    ([24] * 40, 128, 96), ([1] * 130, 40, 48), ([65, 2], 1032, 4104), ([5], 2048, 1008)])
+def test_few_rows(sizes, m, q, dtype, layout):
+    # single tokens and small batches: the weights are streamed, K shared by the wavefronts of a block
+    X, W, dY, off = draw(sizes, m, q, TYPES[dtype], m + q, before=3, behind=2)
+    X[:3], X[-2:] = float("nan"), float("inf")
+    if layout == "qm":
+        W = W.transpose(1, 2).contiguous().transpose(1, 2)
+    for out_dtype in (None, torch.float32):
+        out = torch.full((X.shape[0], m), 5.0, device="cuda", dtype=out_dtype or X.dtype)
+        Y = oz.grouped_linear(X, W, off, out=out)
+        check_all(X, W, dY, off, Y, None, None)
+        assert (out[:3] == 5).all() and (out[-2:] == 5).all()
+    dX = torch.full(X.shape, 5.0, device="cuda", dtype=X.dtype)
+    _, dW = oz.grouped_linear_grads(dY, X, W, off, dX=dX)
+    check_all(X, W, dY, off, Y, dX, dW)
+
+
+# tiles of 256 x 256 (f32: 128 x 128) in whole rounds of 256 compute units and every kind of rest: none, a
+# few tiles and half a round (cut into quarters), more than half a round
+@pytest.mark.parametrize("dtype, sizes, m", [
+    ("bf16", [256] * 32, 4096), ("bf16", [256] * 33, 4096), ("bf16", [200, 256, 300] * 13, 4096),
+    ("f16", [128] * 70, 2304), ("f16", [300] * 25, 6400), ("bf16", [1024, 0, 7000, 30, 5000], 2560),
+    ("f32", [128] * 32, 2048), ("f32", [128] * 37, 2304), ("f32", [60, 300] * 12, 2432)])
+@pytest.mark.parametrize("layout", ["mq", "qm"])
+def test_every_tile_is_written(dtype, sizes, m, layout):
+    X, W, dY, off = draw(sizes, m, 72, TYPES[dtype], len(sizes) + m)
+    if layout == "qm":
+        W = W.transpose(1, 2).contiguous().transpose(1, 2)
+    Y = torch.full(dY.shape, float("nan"), device="cuda", dtype=X.dtype)
+    oz.grouped_linear(X, W, off, out=Y)
+    check_all(X, W, dY, off, Y, None, None)
+    # the gradients of a layer with the sides exchanged: many tiles for them too
+    Wt = W.transpose(1, 2)
+    dX = torch.full(dY.shape, float("nan"), device="cuda", dtype=X.dtype)
+    dW = torch.full(Wt.shape, float("nan"), device="cuda", dtype=X.dtype)
+    oz.grouped_linear_grads(X, dY, Wt, off, dX=dX, dW=dW)
+    assert torch.equal(dX, Y)
+    o = off.tolist()
+    for e in range(len(sizes)):
+        s = slice(o[e], o[e + 1])
+        C, P = X[s].double().T @ dY[s].double(), X[s].double().abs().T @ dY[s].double().abs()
+        big = (X[s].double().abs().amax(0)[:, None] * dY[s].double().abs().amax(0)[None]) if sizes[e] else 0.0
+        check(dW[e], C, bound(C, P, sizes[e], X.dtype, dW.dtype, big))
+
+
+@pytest.mark.parametrize("dtype, groups, m, q", [("bf16", 9, 2048, 2048), ("f16", 3, 2560, 4096), ("f32", 5, 1024, 1152),
+                                                 ("bf16", 70, 520, 264), ("f32", 70, 264, 392)])
+def test_every_tile_of_the_weights_gradient_is_written(dtype, groups, m, q):
+    sizes = [(37 * e) % 101 for e in range(groups)]
+    X, W, dY, off = draw(sizes, m, q, TYPES[dtype], groups)
+    dW = torch.full(W.shape, float("nan"), device="cuda", dtype=X.dtype)
+    oz.grouped_linear_grads(dY, X, W, off, dW=dW)
+    o = off.tolist()
+    for e in range(groups):
+        s = slice(o[e], o[e + 1])
+        C, P = dY[s].double().T @ X[s].double(), dY[s].double().abs().T @ X[s].double().abs()
+        big = (dY[s].double().abs().amax(0)[:, None] * X[s].double().abs().amax(0)[None]) if sizes[e] else 0.0
+        check(dW[e], C, bound(C, P, sizes[e], X.dtype, dW.dtype, big))
