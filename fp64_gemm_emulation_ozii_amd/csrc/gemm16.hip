@@ -8,6 +8,7 @@
 // up in the offsets (one wavefront-wide scan per 64 groups).
 #include "groups.h"
 #include "products.h"
+#include "share.h"
 #include "tile16.h"
 
 namespace oz {
@@ -128,35 +129,6 @@ struct Store {
     }
   }
 };
-
-// How `total` tiles are shared out over gridDim.x = 4 units blocks, one per
-// compute unit at a time.  The first `units` blocks walk whole rounds of
-// tiles; a round before the last, the next `units` blocks take one tile each
-// as units become free (tiles at the end of a group are cheaper than others);
-// what then remains is less than a round, and where it is no more than half
-// of one, its tiles are cut into quarters for the last 2 units blocks, or else
-// taken whole.
-constexpr int SHARES = 4;  // blocks of a launch, in units
-
-struct Share {
-  int rounds;    // of the first blocks
-  int first;     // tile of this block, -1: none
-  int quarter;   // -1: the whole tile
-};
-
-__device__ __forceinline__ Share share_of(int total, int units, int block) {
-  const int rounds = max(total / units - 1, 0);
-  const int kept = rounds * units;
-  if (block < units) return Share{rounds, rounds > 0 ? block : -1, -1};
-  block -= units;
-  const int left = total - kept;  // less than two rounds
-  if (block < units) return Share{0, block < left ? kept + block : -1, -1};
-  block -= units;
-  const int rest = left - units;
-  if (rest <= 0) return Share{0, -1, -1};
-  if (rest * 2 <= units) return Share{0, block < rest * 4 ? kept + units + block / 4 : -1, block % 4};
-  return Share{0, block < rest ? kept + units + block : -1, -1};
-}
 
 // A tile to compute: its operands, its inner dimension and where it goes.
 struct Job {
