@@ -6,6 +6,8 @@
 // J_e are the groups of groups.h, known on the device only: a launch has a
 // block for every tile the groups could need, and each block looks its tile
 // up in the offsets (one wavefront-wide scan per 64 groups).
+#include <algorithm>
+
 #include "groups.h"
 #include "products.h"
 #include "share.h"
@@ -26,6 +28,33 @@ __device__ __forceinline__ uint16_t round16(float x, int ctype) {
 __device__ __forceinline__ float unscale(float x, int ea, int eb) {
   if (ea == OZGEMM_EXP_NONFINITE || eb == OZGEMM_EXP_NONFINITE) return __builtin_nanf("");
   return __builtin_ldexpf(x, ea + eb - 30);
+}
+
+// Four consecutive rows of a column of C, `wide` where they can be stored as one.
+__device__ __forceinline__ void store4(const Grouped16& g, long col, int row, bool wide, v4f v) {
+  const long to = col * g.ldc + row;
+  if (g.ctype == OZGEMM_F32) {
+    float* out = (float*)g.C + to;
+    if (wide && row + 4 <= g.m) {
+      *reinterpret_cast<v4f*>(out) = v;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row + k < g.m) out[k] = v[k];
+    }
+  } else {
+    v4s h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = (short)round16(v[k], g.ctype);
+    short* out = (short*)g.C + to;
+    if (wide && row + 4 <= g.m) {
+      *reinterpret_cast<v4s*>(out) = h;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row + k < g.m) out[k] = h[k];
+    }
+  }
 }
 
 // Where a tile's accumulators go: rows [m0, m) x columns [n0, n_end) of C,
@@ -215,9 +244,11 @@ __global__ __launch_bounds__(512) void grouped_k_kernel(Grouped16 g) {
   using Tiles = Walk<Tile16<T, BT, BT, 2, 4, KS, KS, 2, PAIR>, Tile16<T, BT / 2, BT / 2, 2, 4, KS, KS, 4, PAIR>>;
   __shared__ __attribute__((aligned(1024))) char smem[Tiles::SMEM];
   const int tiles_m = (g.m + BT - 1) / BT, tiles_q = (g.q + BT - 1) / BT;
-  const int per = tiles_m * tiles_q, total = per * g.groups;
+  const int per = tiles_m * tiles_q, whole = per * g.groups, total = whole * g.parts;
   const GroupIndex index(g.offsets, g.groups, g.n, BK16);
   Tiles::run(smem, total, [&](int L, int dm, int dn) {
+    const int part = L / whole;
+    L -= part * whole;
     // Every XCD takes an eighth of each group's tiles: the groups' lengths
     // differ, and an XCD with whole groups of its own waited for the longest.
     const int x = L & 7, i = L >> 3, eighth = per >> 3;
@@ -225,43 +256,22 @@ __global__ __launch_bounds__(512) void grouped_k_kernel(Grouped16 g) {
     int mi, qj;
     panel_order<4>(per % 8 == 0 ? x * eighth + i % eighth : L % per, tiles_m, tiles_q, mi, qj);
     const GroupTile gt = index.at(e);
-    const int len = gt.end - gt.begin, m0 = mi * BT + dm, q0 = qj * BT + dn;
+    const int m0 = mi * BT + dm, q0 = qj * BT + dn;
+    // this part's columns: whole slices of the group's
+    const int slices = (gt.end - gt.begin + BK16 - 1) / BK16, each = (slices + g.parts - 1) / g.parts;
+    const int from = min(part * each, slices) * BK16, len = min(gt.end - gt.begin - from, each * BK16);
     // K-strided: the group's columns; else padded planes, where they begin at 64 x its tiles before
-    const int k0 = KS ? gt.begin : gt.first * BK16;
+    const int k0 = (KS ? gt.begin : gt.first * BK16) + from;
     const long a_at = KS ? k0 * g.A.ld + m0 : m0 * g.A.ld + k0, b_at = KS ? k0 * g.B.ld + q0 : q0 * g.B.ld + k0;
     return Job{Source16{g.A.p + a_at, g.A.plane, (int)g.A.ld, g.m - m0, (int)g.A.last - (KS ? m0 : k0)},
                Source16{g.B.p + b_at, g.B.plane, (int)g.B.ld, g.q - q0, (int)g.B.last - (KS ? q0 : k0)},
-               KS ? len : (len + BK16 - 1) / BK16 * BK16,
-               Target{(char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2), g.ctype, g.ldc, m0, g.m, q0,
-                      g.q, g.A.ex ? g.A.ex + e * g.A.ex_batch : nullptr, g.B.ex ? g.B.ex + e * g.B.ex_batch : nullptr}};
+               len <= 0 ? 0 : KS ? len : (len + BK16 - 1) / BK16 * BK16,
+               g.parts > 1 ? Target{g.partial + ((long)part * g.groups + e) * g.m * g.q, OZGEMM_F32, g.m, m0, g.m, q0,
+                                    g.q, nullptr, nullptr}
+                           : Target{(char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2), g.ctype,
+                                    g.ldc, m0, g.m, q0, g.q, g.A.ex ? g.A.ex + e * g.A.ex_batch : nullptr,
+                                    g.B.ex ? g.B.ex + e * g.B.ex_batch : nullptr}};
   });
-}
-
-// Four consecutive rows of a column of C, `wide` where they can be stored as one.
-__device__ __forceinline__ void store4(const Grouped16& g, long col, int row, bool wide, v4f v) {
-  const long to = col * g.ldc + row;
-  if (g.ctype == OZGEMM_F32) {
-    float* out = (float*)g.C + to;
-    if (wide && row + 4 <= g.m) {
-      *reinterpret_cast<v4f*>(out) = v;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (row + k < g.m) out[k] = v[k];
-    }
-  } else {
-    v4s h;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = (short)round16(v[k], g.ctype);
-    short* out = (short*)g.C + to;
-    if (wide && row + 4 <= g.m) {
-      *reinterpret_cast<v4s*>(out) = h;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (row + k < g.m) out[k] = h[k];
-    }
-  }
 }
 
 // Groups of a few columns: bound by reading the weights once.  A block takes
@@ -439,12 +449,38 @@ hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
   return hipGetLastError();
 }
 
+// The sum of the parts, in their order, into C.
+__global__ __launch_bounds__(256) void join_parts_kernel(Grouped16 g) {
+  const int runs = (g.m + 3) / 4;
+  const long at = (long)blockIdx.x * 256 + threadIdx.x;
+  if (at >= (long)runs * g.q * g.groups) return;
+  const int row = (int)(at % runs) * 4, col = (int)(at / runs % g.q);
+  const long e = at / runs / g.q;
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < g.parts; ++p) {
+    const float* from = g.partial + (((long)p * g.groups + e) * g.q + col) * g.m + row;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += row + k < g.m ? from[k] : 0.f;
+  }
+  if (g.A.ex != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = unscale(v[k], g.A.ex[e * g.A.ex_batch + min(row + k, g.m - 1)], g.B.ex[e * g.B.ex_batch + col]);
+  }
+  g.C = (char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2);
+  store4(g, col, row, (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0, v);
+}
+
 template <class T, int BT, bool KS, bool PAIR>
 hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
   int cus = 0;
   const hipError_t err = device_units(&cus);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL((grouped_k_kernel<T, BT, KS, PAIR>), dim3(SHARES * cus), dim3(512), 0, st, g);
+  if (g.parts > 1) {
+    const long threads = (long)((g.m + 3) / 4) * g.q * g.groups;
+    hipLaunchKernelGGL(join_parts_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, g);
+  }
   return hipGetLastError();
 }
 
@@ -453,6 +489,20 @@ hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
 // counted with the smallest tiles any variant uses
 bool grouped_n_fits(const Grouped16& g) {
   return group_tiles_max(g.n, g.groups, 32) * ((g.m + 15) / 16) <= 0x7fffffffL;
+}
+
+// The tiles run as quarters while they are no more than half the units
+// (256 on MI355X); below that, parts of at least four slices make up the rest.
+int outer_parts(bool f32, int groups, int m, int q, int n) {
+  const long tile = f32 ? 128 : 256;
+  const long tiles = ((m + tile - 1) / tile) * ((q + tile - 1) / tile) * groups;
+  const long slices = ((long)n / groups + BK16 - 1) / BK16;
+  const long parts = std::min({256 / (4 * tiles), slices / 4, 32L});
+  return (int)std::max(parts, 1L);
+}
+
+size_t outer_partial_bytes(int parts, int groups, int m, int q) {
+  return parts > 1 ? (size_t)parts * groups * m * q * 4 : 0;
 }
 
 bool grouped_k_fits(const Grouped16& g) {

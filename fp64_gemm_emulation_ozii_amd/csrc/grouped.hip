@@ -60,6 +60,8 @@ Room room(int type, bool used, size_t rows, size_t k, size_t exponents, size_t p
 
 struct Rooms {
   Room A, B;
+  int parts;       // of an outer product's columns
+  size_t partial;  // offset of their sums
   size_t total;
 };
 
@@ -84,6 +86,8 @@ Rooms outer_rooms(int type, int groups, int m, int q, int n, const void* A, int 
   const size_t k = (size_t)n + 63 * (size_t)std::min(groups, n);
   r.A = room(type, any && !in_place, m, k, (size_t)groups * m, slice_part_bytes(m, n, groups, true), r.total);
   r.B = room(type, any && !in_place, q, k, (size_t)groups * q, slice_part_bytes(q, n, groups, true), r.total);
+  r.parts = any ? outer_parts(type == OZGEMM_F32, groups, m, q, n) : 1;
+  r.partial = take(r.total, outer_partial_bytes(r.parts, groups, m, q));
   return r;
 }
 
@@ -237,6 +241,8 @@ int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n, c
   g.ctype = ctype;
   g.ldc = ldc;
   g.cbatch = (long)stridec;
+  g.parts = r.parts;
+  g.partial = (float*)(ws + r.partial);
   g.A = in_place(A, lda, 0, !g.f32, m);
   g.B = in_place(B, ldb, 0, !g.f32, q);
   if (!grouped_k_fits(g)) return OZGEMM_RANGE;

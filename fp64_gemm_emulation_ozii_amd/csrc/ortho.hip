@@ -22,6 +22,7 @@
 #include <cmath>
 
 #include "products.h"
+#include "step64.h"
 #include "tile16.h"
 
 namespace oz {
@@ -469,6 +470,100 @@ hipError_t launch_step(const Step& p, int nprod, bool aks, bool sym, hipStream_t
   return launch_step_t<64, 2, 2, 4, false, false>(p, aks, sym, units, st);
 }
 
+// P = X X^T for few rows and long ones, along the c entries in `parts` parts:
+// every block sums 64 x 64 entries over its part of the slices, and the
+// parts' sums meet in FP32.  (All of P: at these sizes the time is a block's
+// slices, not the operations.)
+struct Parts {
+  const uint16_t* X;
+  long x_batch, x_plane;
+  int x_ld, r, c, batch, parts;
+  float alpha;
+  float* partial;  // [parts][batch][r][r]
+  uint16_t* P;     // [batch][2][r][r]
+  int lo;
+};
+
+template <bool PAIR, bool KS>
+__global__ __launch_bounds__(256, 2) void gram_parts_kernel(Parts p) {
+  using Tile = Tile16<Half, 64, 64, 2, 2, KS, KS, PAIR ? 2 : 4, PAIR>;
+  __shared__ __attribute__((aligned(1024))) char smem[Tile::SMEM];
+  const int t = p.r / 64;
+  int w = blockIdx.x;
+  const int part = w % p.parts;
+  w /= p.parts;
+  const int nj = w % t, mi = w / t % t;
+  const long b = w / (t * t);
+  const int slices = p.c / BK16, each = (slices + p.parts - 1) / p.parts;
+  const int from = min(part * each, slices) * BK16, len = min(p.c - from, each * BK16);
+  const uint16_t* X = p.X + b * p.x_batch;
+  auto source = [&](int r0) {
+    return Source16{X + (KS ? (long)from * p.x_ld + r0 : (long)r0 * p.x_ld + from), p.x_plane, p.x_ld, p.r - r0,
+                    KS ? p.r - r0 : p.c - from};
+  };
+  v4f acc[Tile::FM][Tile::FN];
+  Tile::run(acc, smem, source(mi * 64), source(nj * 64), max(len, 0));
+  slice_barrier<0>();  // no load into LDS outlives the block
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float* out = p.partial + ((long)part * p.batch + b) * p.r * p.r;
+#pragma unroll
+  for (int j = 0; j < Tile::FN; ++j)
+#pragma unroll
+    for (int i = 0; i < Tile::FM; ++i)
+      *reinterpret_cast<v4f*>(out + (long)(nj * 64 + Tile::wave_n(wave) * 32 + j * 16 + (lane & 15)) * p.r + mi * 64 +
+                              Tile::wave_m(wave) * 32 + i * 16 + 4 * (lane >> 4)) = acc[i][j];
+}
+
+__global__ __launch_bounds__(256) void gram_join_kernel(Parts p) {
+  const long plane = (long)p.r * p.r, at = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
+  const long b = blockIdx.y;
+  if (at >= plane) return;
+  float v[8] = {};
+  for (int q = 0; q < p.parts; ++q) {
+    const float* from = p.partial + ((long)q * p.batch + b) * plane + at;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += from[e];
+  }
+  v8s h, l;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint16_t hi, lo;
+    split(v[e] * p.alpha, hi, lo);
+    h[e] = (short)hi;
+    l[e] = (short)lo;
+  }
+  uint16_t* out = p.P + b * 2 * plane + at;
+  *reinterpret_cast<v8s*>(out) = h;
+  if (p.lo) *reinterpret_cast<v8s*>(out + plane) = l;
+}
+
+hipError_t launch_gram_parts(const Parts& p, int nprod, bool ks, hipStream_t st) {
+  const dim3 grid((unsigned)((long)(p.r / 64) * (p.r / 64) * p.batch * p.parts));
+  if (nprod == 3) {
+    if (ks)
+      hipLaunchKernelGGL((gram_parts_kernel<true, true>), grid, dim3(256), 0, st, p);
+    else
+      hipLaunchKernelGGL((gram_parts_kernel<true, false>), grid, dim3(256), 0, st, p);
+  } else {
+    if (ks)
+      hipLaunchKernelGGL((gram_parts_kernel<false, true>), grid, dim3(256), 0, st, p);
+    else
+      hipLaunchKernelGGL((gram_parts_kernel<false, false>), grid, dim3(256), 0, st, p);
+  }
+  const long runs = ((long)p.r * p.r / 8 + 255) / 256;
+  hipLaunchKernelGGL(gram_join_kernel, dim3((unsigned)runs, p.batch), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
+// Parts of the c entries for a batch of r x c (padded): where the tiles leave
+// most of the card's 256 units idle and each walks many slices.
+int gram_parts(int batch, int r, int c) {
+  const long tiles = (long)(r / 64) * (r / 64) * batch, slices = c / BK16;
+  const long parts = tiles > 128 ? 1 : slices / 4 < 512 / tiles ? slices / 4 : 512 / tiles;
+  return slices < 12 || parts < 2 ? 1 : (int)(parts < 32 ? parts : 32);
+}
+
 // FP64: X and its transpose, Q = b P + c P2, X <- a X + Y both ways round
 __global__ __launch_bounds__(256) void prepare64_kernel(const double* __restrict__ G, int rows, int cols, long ld,
                                                         const double* __restrict__ part, int parts, double eps,
@@ -486,6 +581,19 @@ __global__ __launch_bounds__(256) void prepare64_kernel(const double* __restrict
     const int c = c0 + (i >> 6), r = r0 + (i & 63);
     if (r < rows && c < cols) XT[(long)c * rows + r] = tile[i & 63][i >> 6];
   }
+}
+
+// X_0 of a batch, as G lies, on the way through the FP64 matrix cores
+__global__ __launch_bounds__(256) void scale64_kernel(const double* __restrict__ G, int rows, int cols, long ld,
+                                                      long batch, const double* __restrict__ part, int parts,
+                                                      double eps, double* __restrict__ X) {
+  __shared__ double s[4];
+  const long b = blockIdx.y;
+  const double f = inverse_norm(part, parts, b, eps, s);
+  const long at = (long)blockIdx.x * 256 + threadIdx.x;
+  if (at >= (long)rows * cols) return;
+  const long r = at / cols, c = at - r * cols;
+  X[b * rows * cols + at] = G[b * batch + r * ld + c] * f;
 }
 
 __global__ __launch_bounds__(256) void combine64_kernel(double* __restrict__ Q, const double* __restrict__ P, double b,
@@ -538,9 +646,29 @@ int square_parts(int m, int n) {  // n rows of m entries
 
 struct OrthoLayout {
   int rp, cp;  // sizes padded to 64
+  int parts;   // of P = X X^T
+  size_t partial;
   size_t part, X1, X2, P, Q, total;        // 16-bit slices
+  bool direct;                             // FP64: by the FP64 matrix cores
   size_t X, XT, Y, dgemm;                  // FP64
 };
+
+// Whether an FP64 batch goes by the FP64 matrix cores (step64.h) or by Scheme
+// II products, from modelled times of a step in us.  A product of the former
+// takes 1.2 us for every 64 of its inner dimension and 6 besides, or its
+// operations (half of them for the symmetric results) at 30 TFLOPS.  Scheme II
+// takes the matrices one after the other, 38 us per product for its passes'
+// launches, s int8 products at 2.2 POP/s, and residues and results at 6 TB/s.
+// Measured, five steps, s = 14, matrix cores against Scheme II, in ms:
+//   512^2 0.29 / 0.64   520 x 3688 0.95 / 1.15   1024^2 0.91 / 0.90
+//   1024 x 4096 2.3 / 1.6   2048^2 4.5 / 2.9   15 of 40 x 315 0.15 / 7.4
+bool by_matrix_cores(int batch, int r, int c, int s) {
+  const double R = r, C = c, B = batch;
+  auto product = [&](double ops, double k) { return fmax(B * ops / 30e6, ceil(k / 64) * 1.2 + 6); };
+  const double direct = product(R * R * C, C) + product(R * R * R, R) + product(2 * R * R * C, R);
+  const double bytes = (16 + s) * (2 * R * C + 2 * R * R) + (8 + s) * (2 * R * R + R * C) + 32 * R * R + 32 * R * C;
+  return direct <= B * (3 * 38 + s * 2 * (2 * R * R * C + R * R * R) / 2.2e9 + bytes / 6e6);
+}
 
 OrthoLayout ortho_layout(int type, int batch, int m, int n, int s) {
   OrthoLayout L{};
@@ -553,6 +681,14 @@ OrthoLayout ortho_layout(int type, int batch, int m, int n, int s) {
   L.part = take((size_t)batch * SQUARE_PARTS * 8);
   if (type == OZGEMM_F64) {
     const size_t rc = (size_t)r * c * 8, rr = (size_t)r * r * 8;
+    L.direct = by_matrix_cores(batch, r, c, s);
+    if (L.direct) {
+      L.X = take(batch * rc);
+      L.Y = take(batch * rc);
+      L.P = take(batch * rr);
+      L.Q = take(batch * rr);
+      return L;
+    }
     L.X = take(rc);
     L.XT = take(rc);
     L.Y = take(rc);
@@ -568,6 +704,8 @@ OrthoLayout ortho_layout(int type, int batch, int m, int n, int s) {
   L.X2 = take(rc);
   L.P = take(rr);
   L.Q = take(rr);
+  L.parts = gram_parts(batch, L.rp, L.cp);
+  if (L.parts > 1) L.partial = take((size_t)L.parts * batch * L.rp * L.rp * 4);
   return L;
 }
 
@@ -680,6 +818,85 @@ int ortho64(const OrthoLayout& L, int batch, int m, int n, const double* G, long
   return OZGEMM_OK;
 }
 
+// The same by the FP64 matrix cores, the whole batch at once.  X stays as G
+// lies: n rows of m entries.
+int ortho64_direct(const OrthoLayout& L, int batch, int m, int n, const double* G, long ldg, long strideg, int steps,
+                   const double* co, double eps, double* O, long ldo, long strideo, char* ws, hipStream_t st) {
+  const bool tall = n > m;
+  const int r = tall ? m : n, c = tall ? n : m;
+  double* X = (double*)(ws + L.X);
+  double* other = (double*)(ws + L.Y);
+  double* P = (double*)(ws + L.P);
+  double* Q = (double*)(ws + L.Q);
+  double* part = (double*)(ws + L.part);
+  const int parts = square_parts(m, n);
+  const long xs = (long)m * n, ps = (long)r * r;
+  OZ_TRY(launch_square_sum(OZGEMM_F64, G, n, m, ldg, strideg, batch, parts, part, st));
+  hipLaunchKernelGGL(scale64_kernel, dim3((unsigned)((xs + 255) / 256), batch), dim3(256), 0, st, G, n, m, ldg, strideg,
+                     part, parts, eps, X);
+  OZ_TRY(hipGetLastError());
+  // X(r-index i, c-index k) at i x_r + k x_c
+  const long x_r = tall ? 1 : m, x_c = tall ? m : 1;
+  int units = 0;
+  OZ_TRY(device_units(&units));
+  auto launch = [&](const Step64& p, bool sym) { return launch_step64(p, sym, units, st); };
+  for (int k = 0; k < steps; ++k) {
+    const double a = co[3 * k], b = co[3 * k + 1], cc = co[3 * k + 2];
+    Step64 p{};
+    p.batch = batch;
+    p.A = p.B = X;  // P = X X^T
+    p.a_i = p.b_j = x_r;
+    p.a_k = p.b_k = x_c;
+    p.a_batch = p.b_batch = xs;
+    p.m = p.n = r;
+    p.k = c;
+    p.alpha = 1;
+    p.N = P;
+    p.n_ld = r;
+    p.n_batch = ps;
+    OZ_TRY(launch(p, true));
+    p.A = p.B = P;  // Q = b P + c P^2
+    p.a_i = p.b_j = r;
+    p.a_k = p.b_k = 1;
+    p.a_batch = p.b_batch = ps;
+    p.k = r;
+    p.alpha = cc;
+    p.beta = b;
+    p.S = P;
+    p.s_ld = r;
+    p.s_batch = ps;
+    p.N = Q;
+    OZ_TRY(launch(p, true));
+    // X <- a X + Q X, row j of the result as X lies: wide, row j of Q against
+    // X's columns; tall, row j of X against Q
+    p.A = tall ? Q : X;
+    p.a_i = tall ? r : x_c;
+    p.a_k = tall ? 1 : x_r;
+    p.a_batch = tall ? ps : xs;
+    p.B = tall ? X : Q;
+    p.b_j = tall ? x_c : r;
+    p.b_k = 1;
+    p.b_batch = tall ? xs : ps;
+    p.m = m;
+    p.n = n;
+    p.k = r;
+    p.alpha = 1;
+    p.beta = a;
+    p.S = X;
+    p.s_ld = m;
+    p.s_batch = xs;
+    const bool last = k + 1 == steps;
+    p.N = last ? O : other;
+    p.n_ld = last ? ldo : m;
+    p.n_batch = last ? strideo : xs;
+    OZ_TRY(launch(p, false));
+    double* swap = X;
+    X = other;
+    other = swap;
+  }
+  return OZGEMM_OK;
+}
+
 int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void* G, long ldg, long strideg, int steps,
             const double* co, double eps, void* O, long ldo, long strideo, char* ws, hipStream_t st) {
   const bool tall = n > m;  // as it lies: n rows of m entries
@@ -725,7 +942,11 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
     p.s_batch = 2 * pp;
     p.s_plane = pp;
     p.n_lo = lo;
-    OZ_TRY(launch_step(p, nprod, tall, true, st));
+    if (L.parts > 1)
+      OZ_TRY(launch_gram_parts(Parts{X, 2 * xp, xp, x_ld, L.rp, L.cp, batch, L.parts, p.alpha,
+                                     (float*)(ws + L.partial), P, lo}, nprod, tall, st));
+    else
+      OZ_TRY(launch_step(p, nprod, tall, true, st));
     // Q = b P + c P^2
     p.A = p.B = P;
     p.a_batch = p.b_batch = 2 * pp;
@@ -847,6 +1068,9 @@ int ozgemm_orthogonalize(int type, int batch, int m, int n, const void* G, int l
     OZ_TRY(hipGetLastError());
     return OZGEMM_OK;
   }
+  if (type == OZGEMM_F64 && L.direct)
+    return ortho64_direct(L, batch, m, n, (const double*)G, ldg, (long)strideg, steps, coeffs, eps, (double*)O, ldo,
+                          (long)strideo, ws, st);
   if (type == OZGEMM_F64)
     return ortho64(L, batch, m, n, (const double*)G, ldg, (long)strideg, steps, coeffs, eps, s, (double*)O, ldo,
                    (long)strideo, ws, st);

@@ -491,7 +491,9 @@ size_t ozgemm_grouped_gemm_workspace_bytes(int type, int groups, int m, int n, i
  * zeros.  Types, errors and workspace as above; 16-bit operands are read in
  * place where columns begin on 16-byte boundaries and m and q are multiples
  * of 8.  Operands that pass through the workspace (there each group begins at
- * a multiple of 64) need n + 63 min(groups, n) <= 2^21 (OZGEMM_RANGE). */
+ * a multiple of 64) need n + 63 min(groups, n) <= 2^21 (OZGEMM_RANGE).  Small
+ * results of many columns are summed in parts, in a fixed order, whose sums
+ * take room in the workspace too. */
 int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n,
                          const void *A, int lda, const void *B, int ldb,
                          const int32_t *offsets, void *C, int ldc, long long stridec,
@@ -514,7 +516,9 @@ size_t ozgemm_grouped_outer_workspace_bytes(int type, int groups, int m, int q, 
  *   coeffs  HOST array of 3 steps numbers a, b, c, read before the call
  *           returns; |.| < 1e6
  *   s       moduli of the Scheme II products of OZGEMM_F64 (conservative
- *           budget whatever ozgemm_set_bound says); not looked at otherwise
+ *           budget whatever ozgemm_set_bound says); not looked at otherwise.
+ *           Small F64 matrices, for which those would be slower, go by the
+ *           FP64 matrix cores (a rule on the sizes and s)
  * The states between the products keep 22 bits or more (F64: 53); BF16
  * products are formed from 11-bit operands, F16 and F32 ones as the grouped
  * products of F32 operands are.  The norm is a sum of squares in FP64 (F64

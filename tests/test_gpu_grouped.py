@@ -376,3 +376,16 @@ def test_every_tile_of_the_weights_gradient_is_written(dtype, groups, m, q):
         C, P = dY[s].double().T @ X[s].double(), dY[s].double().abs().T @ X[s].double().abs()
         big = (dY[s].double().abs().amax(0)[:, None] * X[s].double().abs().amax(0)[None]) if sizes[e] else 0.0
         check(dW[e], C, bound(C, P, sizes[e], X.dtype, dW.dtype, big))
+
+
+@pytest.mark.parametrize("dtype, sizes, m, q", [("bf16", [3000], 64, 96), ("f16", [1500, 0, 2600, 40], 40, 136),
+                                                ("f32", [5000, 3], 72, 130), ("bf16", [9000], 33, 257),
+                                                ("f32", [70, 2000, 0, 1100], 128, 64)])
+def test_weights_gradient_summed_in_parts(dtype, sizes, m, q):
+    X, W, dY, off = draw(sizes, m, q, TYPES[dtype], m * q, before=5, behind=7)
+    X[:5], dY[-7:] = float("nan"), float("nan")
+    for dw_dtype in (None, torch.float32):
+        Y = oz.grouped_linear(X, W, off)
+        dX, dW = oz.grouped_linear_grads(dY, X, W, off, dw_dtype=dw_dtype)
+        check_all(X, W, dY, off, Y, dX, dW)
+        assert torch.equal(dW, oz.grouped_linear_grads(dY, X, W, off, dw_dtype=dw_dtype)[1])

@@ -63,7 +63,8 @@ def draw(shape, dtype, seed):
 
 SHAPES = [(1, 1), (1, 7), (7, 1), (2, 2), (16, 16), (17, 33), (64, 64), (65, 64), (64, 200), (200, 63), (129, 128),
           (3, 1000), (1000, 3), (257, 300), (333, 1003), (1003, 333), (512, 512), (3, 100, 70), (2, 3, 40, 90),
-          (5, 130, 129), (1024, 640), (9, 700, 1100), (2, 2048, 1100), (1300, 4000)]
+          (5, 130, 129), (1024, 640), (9, 700, 1100), (2, 2048, 1100), (1300, 4000), (40, 3000), (2900, 130),
+          (4, 1700, 64), (2, 200, 1024)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))

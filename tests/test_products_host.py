@@ -135,7 +135,8 @@ def test_orthogonalize_workspace_bytes():
     w = L.ozgemm_orthogonalize_workspace_bytes
     assert w(L.OZGEMM_F32, 2, 100, 50, 0) == w(L.OZGEMM_F32, 2, 50, 100, 0) >= 2 * 12 * 100 * 50
     assert w(L.OZGEMM_BF16, 1, 16384, 16384, 0) > 1 << 32
-    assert w(L.OZGEMM_F64, 1, 512, 512, 14) >= 5 * 512 * 512 * 8 + L.ozgemm_workspace_bytes(512, 512, 512, 14)
+    assert w(L.OZGEMM_F64, 1, 2048, 2048, 14) >= 5 * 2048 ** 2 * 8 + L.ozgemm_workspace_bytes(2048, 2048, 2048, 14)
+    assert w(L.OZGEMM_F64, 3, 96, 200, 14) >= 3 * (2 * 96 * 200 + 2 * 96 * 96) * 8
     for bad in ((4, 1, 8, 8, 14), (L.OZGEMM_F32, 0, 8, 8, 14), (L.OZGEMM_F64, 1, 8, 8, 0), (L.OZGEMM_F64, 1, 8, 8, 21)):
         assert w(*bad) == 0
 
