@@ -17,7 +17,8 @@ def __getattr__(name):
     # torch is imported with the first use of a function that takes tensors
     if name in ("grouped_linear", "grouped_linear_grads", "orthogonalize"):
         from . import layers
-        return getattr(layers, name)
+        globals()[name] = getattr(layers, name)
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

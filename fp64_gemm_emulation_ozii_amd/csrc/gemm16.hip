@@ -225,18 +225,50 @@ __global__ __launch_bounds__(512) void grouped_n_kernel(Grouped16 g) {
   __shared__ __attribute__((aligned(1024))) char smem[Tiles::SMEM];
   const int tiles_m = (g.m + BT - 1) / BT;
   const GroupIndex index(g.offsets, g.groups, g.n, BT);
-  const int total = tiles_m * index.total;
+  const int whole = tiles_m * index.total, total = whole * g.parts;
+  // a part's inner dimension: whole slices
+  const int each = ((g.q + BK16 - 1) / BK16 + g.parts - 1) / g.parts * BK16;
   Tiles::run(smem, total, [&](int L, int dm, int dn) {
+    const int part = L / whole, k0 = min(part * each, g.q);
     int nj, mi;
-    panel_order<4>(xcd_order(L, total), index.total, tiles_m, nj, mi);
+    panel_order<4>(xcd_order(L - part * whole, whole), index.total, tiles_m, nj, mi);
     const GroupTile gt = index.find(nj);
     const int m0 = mi * BT + dm, n0 = gt.begin + dn;
-    return Job{Source16{g.A.p + gt.group * g.A.batch + (AKS ? (long)m0 : (long)m0 * g.A.ld), g.A.plane, (int)g.A.ld,
-                        g.m - m0, (int)g.A.last - (AKS ? m0 : 0)},
-               Source16{g.B.p + (long)n0 * g.B.ld, g.B.plane, (int)g.B.ld, gt.end - n0, (int)g.B.last}, g.q,
-               Target{g.C, g.ctype, g.ldc, m0, g.m, n0, gt.end,
-                      g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr, g.B.ex}};
+    const long a_at = AKS ? k0 * g.A.ld + m0 : m0 * g.A.ld + k0;
+    return Job{Source16{g.A.p + gt.group * g.A.batch + a_at, g.A.plane, (int)g.A.ld, g.m - m0,
+                        (int)g.A.last - (AKS ? m0 : k0)},
+               Source16{g.B.p + n0 * g.B.ld + k0, g.B.plane, (int)g.B.ld, gt.end - n0, (int)g.B.last - k0},
+               min(each, g.q - k0),
+               g.parts > 1 ? Target{g.partial + (long)part * g.n * g.m, OZGEMM_F32, g.m, m0, g.m, n0, gt.end, nullptr,
+                                    nullptr}
+                           : Target{g.C, g.ctype, g.ldc, m0, g.m, n0, gt.end,
+                                    g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr, g.B.ex}};
   });
+}
+
+// The sum of the parts, in their order, into the columns of the groups: a
+// block per 64 columns of a group and 64 rows.
+__global__ __launch_bounds__(256) void join_columns_kernel(Grouped16 g) {
+  const GroupIndex index(g.offsets, g.groups, g.n, 64);
+  if ((int)blockIdx.x >= index.total) return;
+  const GroupTile gt = index.find(blockIdx.x);
+  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
+  const int row = blockIdx.y * 64 + (threadIdx.x & 15) * 4;
+  if (row >= g.m) return;
+  const int32_t* ea = g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr;
+  for (int col = gt.begin + (threadIdx.x >> 4); col < min(gt.end, gt.begin + 64); col += 16) {
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < g.parts; ++p) {
+      const float* from = g.partial + ((long)p * g.n + col) * g.m + row;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += row + k < g.m ? from[k] : 0.f;
+    }
+    if (ea != nullptr) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = unscale(v[k], ea[min(row + k, g.m - 1)], g.B.ex[col]);
+    }
+    store4(g, col, row, wide, v);
+  }
 }
 
 template <class T, int BT, bool KS, bool PAIR>
@@ -419,10 +451,10 @@ __global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
 //   64 of 1024 x 2048           8:  60 / 71             24:  72 / 73    32:  76 / 74
 //   8 of 2048 x 2048            8:  17 / 33             48:  26 / 36    64:  44 / 37
 //   1 of 4096 x 4096            8:  15 / 56                             128: 27 / 63
-bool few(const Grouped16& g, int units) {
-  const long tiles = (long)g.groups * ((g.m + 255) / 256);
+bool few_columns_fit(int groups, int m, int n) {
+  const long tiles = (long)groups * ((m + 255) / 256), units = 256;
   const long most = tiles * 16 <= units ? 128 : tiles * 4 <= units ? 48 : 24;
-  return g.n <= most * g.groups;
+  return n <= most * groups;
 }
 
 template <class T>
@@ -446,6 +478,9 @@ hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
   const hipError_t err = device_units(&cus);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL((grouped_n_kernel<T, BT, AKS, PAIR>), dim3(SHARES * cus), dim3(512), 0, st, g);
+  if (g.parts > 1)
+    hipLaunchKernelGGL(join_columns_kernel, dim3((unsigned)group_tiles_max(g.n, g.groups, 64), (unsigned)((g.m + 63) / 64)),
+                       dim3(256), 0, st, g);
   return hipGetLastError();
 }
 
@@ -488,22 +523,32 @@ hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
 
 // counted with the smallest tiles any variant uses
 bool grouped_n_fits(const Grouped16& g) {
-  return group_tiles_max(g.n, g.groups, 32) * ((g.m + 15) / 16) <= 0x7fffffffL;
+  return group_tiles_max(g.n, g.groups, 32) * ((g.m + 15) / 16) <= 0x7fffffffL;  // (parts only where tiles are few)
 }
 
-// The tiles run as quarters while they are no more than half the units
-// (256 on MI355X); below that, parts of at least four slices make up the rest.
+// Parts of an inner dimension of `slices` slices for `tiles` tiles: those run
+// as quarters while they are no more than half the units (256 on MI355X);
+// below that, parts of at least four slices make up the rest.
+static int parts_for(long tiles, long slices) {
+  return (int)std::max(std::min({256 / (4 * tiles), slices / 4, 32L}), 1L);
+}
+
 int outer_parts(bool f32, int groups, int m, int q, int n) {
   const long tile = f32 ? 128 : 256;
-  const long tiles = ((m + tile - 1) / tile) * ((q + tile - 1) / tile) * groups;
-  const long slices = ((long)n / groups + BK16 - 1) / BK16;
-  const long parts = std::min({256 / (4 * tiles), slices / 4, 32L});
-  return (int)std::max(parts, 1L);
+  return parts_for(((m + tile - 1) / tile) * ((q + tile - 1) / tile) * groups, ((long)n / groups + BK16 - 1) / BK16);
 }
 
 size_t outer_partial_bytes(int parts, int groups, int m, int q) {
   return parts > 1 ? (size_t)parts * groups * m * q * 4 : 0;
 }
+
+int gemm_parts(bool f32, int groups, int m, int n, int q) {
+  if (!f32 && few_columns_fit(groups, m, n)) return 1;
+  const long tile = f32 ? 128 : 256;
+  return parts_for(group_tiles_max(n, groups, tile) * ((m + tile - 1) / tile), (q + BK16 - 1) / BK16);
+}
+
+size_t gemm_partial_bytes(int parts, int m, int n) { return parts > 1 ? (size_t)parts * m * n * 4 : 0; }
 
 bool grouped_k_fits(const Grouped16& g) {
   return (long)((g.m + 63) / 64) * ((g.q + 63) / 64) <= 0x7fffffffL / g.groups;
@@ -512,10 +557,7 @@ bool grouped_k_fits(const Grouped16& g) {
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
   if (g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
   if (g.f32) return grouped_n<Half, 128, false, true>(g, st);
-  int units = 0;
-  const hipError_t err = device_units(&units);
-  if (err != hipSuccess) return err;
-  if (few(g, units)) return g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
+  if (few_columns_fit(g.groups, g.m, g.n)) return g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
   if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, true, false>(g, st) : grouped_n<Bfloat, 256, false, false>(g, st);
   return g.A.ks ? grouped_n<Half, 256, true, false>(g, st) : grouped_n<Half, 256, false, false>(g, st);
 }

@@ -60,7 +60,7 @@ Room room(int type, bool used, size_t rows, size_t k, size_t exponents, size_t p
 
 struct Rooms {
   Room A, B;
-  int parts;       // of an outer product's columns
+  int parts;       // of the inner dimension
   size_t partial;  // offset of their sums
   size_t total;
 };
@@ -75,6 +75,8 @@ Rooms gemm_rooms(int type, int groups, int m, int n, int q, int transa, const vo
   r.A = room(type, any && !a_in_place, (size_t)groups * m, q, (size_t)groups * m,
              transa ? 0 : slice_part_bytes(m, q, groups, false), r.total);
   r.B = room(type, any && !b_in_place, n, q, n, 0, r.total);
+  r.parts = any ? gemm_parts(f32, groups, m, n, q) : 1;
+  r.partial = take(r.total, gemm_partial_bytes(r.parts, m, n));
   return r;
 }
 
@@ -168,6 +170,8 @@ int ozgemm_grouped_gemm(int type, int ctype, int groups, int m, int n, int q, in
   g.C = C;
   g.ctype = ctype;
   g.ldc = ldc;
+  g.parts = r.parts;
+  g.partial = (float*)(ws + r.partial);
   // (F32 operands stay here only where nothing is read: no inner dimension)
   g.A = in_place(A, lda, (long)stridea, transa == 0 && !g.f32, ar);
   g.B = in_place(B, ldb, 0, false, q);

@@ -809,11 +809,7 @@ int noalloc_scratch(char** out) {
 
 int record_hip_error(hipError_t err) { return hip_fail(err); }
 
-hipError_t device_units(int* cus) {
-  int dev = 0;
-  const hipError_t err = hipGetDevice(&dev);
-  return err != hipSuccess ? err : hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev);
-}
+hipError_t device_units(int* cus) { return device_cus(cus) == 0 ? hipSuccess : hipErrorInvalidDevice; }
 
 // Scheme II products inside a caller's region, for paths that are a sequence
 // of them (products.h).  The W_t limbs of one s travel as a kernel argument,

@@ -36,8 +36,8 @@ struct Grouped16 {
   void* C;
   int ctype;
   long ldc, cbatch;
-  int parts;       // outer products: parts of a group's columns, whose sums meet in `partial`
-  float* partial;  // [parts][groups][q][m]
+  int parts;       // of the inner dimension (outer products: of each group's columns)
+  float* partial;  // their sums: [parts][n][m] (outer products: [parts][groups][q][m])
 };
 
 // Whether the launches below have at most 2^31 - 1 tiles.
@@ -45,8 +45,10 @@ bool grouped_n_fits(const Grouped16& g);
 bool grouped_k_fits(const Grouped16& g);
 // C(:, J_e) = A_e B(:, J_e): B's rows are the n columns of the call.
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st);
-// Parts for an outer product of these sizes, and the room they take: where its
-// tiles are too few for the card and its columns many.
+// Parts for a product of these sizes, and the room they take: where its tiles
+// are too few for the card and its inner dimension is long.
+int gemm_parts(bool f32, int groups, int m, int n, int q);
+size_t gemm_partial_bytes(int parts, int m, int n);
 int outer_parts(bool f32, int groups, int m, int q, int n);
 size_t outer_partial_bytes(int parts, int groups, int m, int q);
 // C_e (m x q) = sum over j in J_e: A's and B's inner dimension is the n columns.

@@ -148,6 +148,9 @@ def _check(status: int, where: str) -> int:
 def _stream(stream):
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object: 5 us less per call
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

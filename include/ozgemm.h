@@ -468,7 +468,9 @@ int ozgemm_mfma_ceiling(int blocks, int steps, unsigned seed, unsigned *sink, vo
  * overlap A or B.  16-bit operands are read in place where rows begin on
  * 16-byte boundaries and K-contiguous ones (A with transa = 1, B) have q a
  * multiple of 8, K-strided ones (A with transa = 0) m a multiple of 8; others,
- * and F32 operands, pass through the workspace.
+ * and F32 operands, pass through the workspace.  Results too small to fill the
+ * card are summed in parts of a long inner dimension, in a fixed order, whose
+ * sums take room in the workspace too.
  * Errors: -i for argument i; OZGEMM_RANGE for m, n or q above
  * OZGEMM_MAX_ROWS, groups above OZGEMM_GROUPS_MAX or a grid of more than
  * 2^31 tiles; OZGEMM_WORKSPACE_TOO_SMALL. */

@@ -389,3 +389,20 @@ def test_weights_gradient_summed_in_parts(dtype, sizes, m, q):
         dX, dW = oz.grouped_linear_grads(dY, X, W, off, dw_dtype=dw_dtype)
         check_all(X, W, dY, off, Y, dX, dW)
         assert torch.equal(dW, oz.grouped_linear_grads(dY, X, W, off, dw_dtype=dw_dtype)[1])
+
+
+@pytest.mark.parametrize("layout", ["mq", "qm"])
+@pytest.mark.parametrize("dtype, sizes, m, q", [("bf16", [300, 0, 200], 96, 4096), ("f16", [700], 33, 1601),
+                                                ("f32", [100, 40], 72, 2000), ("f32", [1], 24, 4096),
+                                                ("f32", [0, 130, 61], 200, 1090), ("bf16", [999], 264, 2056)])
+def test_products_summed_in_parts(dtype, sizes, m, q, layout):
+    X, W, dY, off = draw(sizes, m, q, TYPES[dtype], m * q + 1, before=6, behind=4)
+    X[:6], X[-4:] = float("nan"), float("inf")
+    if layout == "qm":
+        W = W.transpose(1, 2).contiguous().transpose(1, 2)
+    for out_dtype in (X.dtype, torch.float32):
+        out = torch.full((X.shape[0], m), 5.0, device="cuda", dtype=out_dtype)
+        Y = oz.grouped_linear(X, W, off, out=out)
+        check_all(X, W, dY, off, Y, None, None)
+        assert (out[:6] == 5).all() and (out[-4:] == 5).all()
+        assert torch.equal(out, oz.grouped_linear(X, W, off, out=out.clone()))
