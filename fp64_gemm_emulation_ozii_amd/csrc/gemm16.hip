@@ -312,43 +312,78 @@ __global__ __launch_bounds__(512) void grouped_k_kernel(Grouped16 g) {
 // whose loads are all in flight before the first product, straight from HBM
 // into the MFMA's operand layout (16 rows x 64 bytes per load; the two halves
 // of a 128-byte line are loaded one after the other).  The columns, which the
-// L2 serves, come the same way.  The wavefronts' sums meet in LDS.
+// L2 serves, come the same way.  The wavefronts' sums meet in LDS.  Single
+// precision goes without slices: at so few columns its matrix-core rate is
+// enough, and cutting the weights would read and write them three times over.
+//
+// Where the tiles of a product leave units idle and its inner dimension is
+// long, blocks share that too, in parts whose sums join_columns_kernel adds.
+// Rows (K-strided weights: 16 x the entries in 16 bytes) and columns of a tile:
+constexpr int FEW_MR = 2, FEW_ROWS = 16 * FEW_MR, FEW_COLS = 64, FEW_KS_COLS = 32;
+
+struct FewTile {
+  bool any;       // this block has a tile
+  int tile, m0;   // of the columns; first row
+  int k0, k_end;  // its part of the inner dimension
+};
+
+template <int ROWS, int CHUNK>
+__device__ __forceinline__ FewTile few_tile(Grouped16& g, const GroupIndex& index) {
+  const int tiles_m = (g.m + ROWS - 1) / ROWS, whole = tiles_m * index.total;
+  FewTile t{};
+  const int part = whole > 0 ? (int)blockIdx.x / whole : g.parts;
+  t.any = part < g.parts;
+  const int L = whole > 0 ? (int)blockIdx.x % whole : 0;
+  t.tile = L / tiles_m;
+  t.m0 = L % tiles_m * ROWS;
+  const int chunks = (g.q + CHUNK - 1) / CHUNK, per = (chunks + g.parts - 1) / g.parts * CHUNK;
+  t.k0 = part * per;
+  t.k_end = min(t.k0 + per, g.q);
+  if (g.parts > 1) {  // (the sum of an empty part is stored too)
+    g.C = g.partial + (long)part * g.n * g.m;
+    g.ctype = OZGEMM_F32;
+    g.ldc = g.m;
+  }
+  return t;
+}
+
 template <class T, int MR, int DEPTH>
 __global__ __launch_bounds__(512, 2) void few_columns_kernel(Grouped16 g) {
-  constexpr int ROWS = 16 * MR, COLS = 64, CF = COLS / 16, WAVES = 8;
+  constexpr int ROWS = 16 * MR, COLS = FEW_COLS, CF = COLS / 16, WAVES = 8, STEP = 4 * T::LANE;
+  typedef typename T::Entry Entry;
   __shared__ float sums[WAVES][16][ROWS + 4];
   const GroupIndex index(g.offsets, g.groups, g.n, COLS);
-  const int tiles_m = (g.m + ROWS - 1) / ROWS;
-  if ((int)blockIdx.x >= tiles_m * index.total) return;
-  const int nj = blockIdx.x / tiles_m, m0 = blockIdx.x % tiles_m * ROWS;
-  const GroupTile gt = index.find(nj);
+  const FewTile t = few_tile<ROWS, WAVES * STEP * DEPTH>(g, index);
+  if (!t.any) return;
+  const int m0 = t.m0;
+  const GroupTile gt = index.find(t.tile);
   const int n0 = gt.begin, cols = min(gt.end - n0, COLS), frags = (cols + 15) / 16;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int kl = wave * 32 * DEPTH + (lane >> 4) * 8;  // this lane's first k in a chunk
+  const int kl = wave * STEP * DEPTH + (lane >> 4) * T::LANE;  // this lane's first k in a chunk
   // rows past the end read the last one again (their sums are not stored)
-  const uint16_t* a[MR];
+  const Entry* a[MR];
 #pragma unroll
   for (int i = 0; i < MR; ++i)
-    a[i] = g.A.p + gt.group * g.A.batch + (long)min(m0 + i * 16 + (lane & 15), g.m - 1) * g.A.ld + kl;
-  const uint16_t* b[CF];
+    a[i] = (const Entry*)g.A.p + gt.group * g.A.batch + (long)min(m0 + i * 16 + (lane & 15), g.m - 1) * g.A.ld + kl;
+  const Entry* b[CF];
 #pragma unroll
-  for (int c = 0; c < CF; ++c) b[c] = g.B.p + (long)(n0 + min(c * 16 + (lane & 15), cols - 1)) * g.B.ld + kl;
+  for (int c = 0; c < CF; ++c) b[c] = (const Entry*)g.B.p + (long)(n0 + min(c * 16 + (lane & 15), cols - 1)) * g.B.ld + kl;
   v4f acc[MR][CF] = {};
   const v8s zero = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int k0 = 0; k0 < g.q; k0 += WAVES * 32 * DEPTH) {
+  for (int k0 = t.k0; k0 < t.k_end; k0 += WAVES * STEP * DEPTH) {
     v8s av[DEPTH][MR];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
 #pragma unroll
       for (int i = 0; i < MR; ++i)
-        av[d][i] = kl + k0 + d * 32 < g.q ? *reinterpret_cast<const v8s*>(a[i] + k0 + d * 32) : zero;
+        av[d][i] = kl + k0 + d * STEP < g.q ? *reinterpret_cast<const v8s*>(a[i] + k0 + d * STEP) : zero;
 #pragma unroll
     for (int c = 0; c < CF; ++c) {
       if (c >= frags) break;
       v8s bv[DEPTH];
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d)
-        bv[d] = kl + k0 + d * 32 < g.q ? *reinterpret_cast<const v8s*>(b[c] + k0 + d * 32) : zero;
+        bv[d] = kl + k0 + d * STEP < g.q ? *reinterpret_cast<const v8s*>(b[c] + k0 + d * STEP) : zero;
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d)
 #pragma unroll
@@ -375,50 +410,54 @@ __global__ __launch_bounds__(512, 2) void few_columns_kernel(Grouped16 g) {
 }
 
 // The same for weights that lie K-strided (m entries next to each other).  A
-// wavefront takes 128 rows: a lane reads 8 of them of one k (16 lanes: 256
-// bytes next to each other), of 8 k in turn, and transposes its 8 x 8 entries
-// in registers into eight MFMA operands, the u-th of which has rows m0 + 8 i + u,
-// i = 0..15.  Eight wavefronts share the inner dimension.
+// wavefront takes 16 V rows, V the entries of 16 bytes: a lane reads V of them
+// of one k (16 lanes: 256 bytes next to each other), of V k in turn, and
+// transposes its V x V entries in registers into V MFMA operands, the u-th of
+// which has rows m0 + V i + u, i = 0..15.  Eight wavefronts share the inner
+// dimension.
 template <class T, int DEPTH>
 __global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
-  constexpr int ROWS = 128, COLS = 32, CF = COLS / 16, WAVES = 8;
+  constexpr int V = T::LANE, ROWS = 16 * V, COLS = FEW_KS_COLS, CF = COLS / 16, WAVES = 8, STEP = 4 * V;
+  typedef typename T::Entry Entry;
+  typedef Entry Run __attribute__((ext_vector_type(V)));
   __shared__ float sums[WAVES][16][ROWS + 4];
   const GroupIndex index(g.offsets, g.groups, g.n, COLS);
-  const int tiles_m = (g.m + ROWS - 1) / ROWS;
-  if ((int)blockIdx.x >= tiles_m * index.total) return;
-  const int nj = blockIdx.x / tiles_m, m0 = blockIdx.x % tiles_m * ROWS;
-  const GroupTile gt = index.find(nj);
+  const FewTile t = few_tile<ROWS, WAVES * STEP * DEPTH>(g, index);
+  if (!t.any) return;
+  const int m0 = t.m0;
+  const GroupTile gt = index.find(t.tile);
   const int n0 = gt.begin, cols = min(gt.end - n0, COLS), frags = (cols + 15) / 16;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int kl = wave * 32 * DEPTH + (lane >> 4) * 8;  // this lane's first k in a chunk
+  const int kl = wave * STEP * DEPTH + (lane >> 4) * V;  // this lane's first k in a chunk
   const long ld = g.A.ld;
-  // rows past the end read the last eight again (m is a multiple of 8; their sums are not stored)
-  const uint16_t* a = g.A.p + gt.group * g.A.batch + min(m0 + (lane & 15) * 8, g.m - 8);
-  const uint16_t* b[CF];
+  // rows past the end read the last V again (m is a multiple of V; their sums are not stored)
+  const Entry* a = (const Entry*)g.A.p + gt.group * g.A.batch + min(m0 + (lane & 15) * V, g.m - V);
+  const Entry* b[CF];
 #pragma unroll
-  for (int c = 0; c < CF; ++c) b[c] = g.B.p + (long)(n0 + min(c * 16 + (lane & 15), cols - 1)) * g.B.ld + kl;
-  v4f acc[CF][8] = {};
-  const v8s zero = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int k0 = 0; k0 < g.q; k0 += WAVES * 32 * DEPTH) {
-    v8s av[DEPTH][8], bv[DEPTH][CF];
+  for (int c = 0; c < CF; ++c) b[c] = (const Entry*)g.B.p + (long)(n0 + min(c * 16 + (lane & 15), cols - 1)) * g.B.ld + kl;
+  v4f acc[CF][V] = {};
+  const Run zero = {};
+  for (int k0 = t.k0; k0 < t.k_end; k0 += WAVES * STEP * DEPTH) {
+    Run av[DEPTH][V], bv[DEPTH][CF];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      const int k = kl + k0 + d * 32;
+      const int k = kl + k0 + d * STEP;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) av[d][t] = k + t < g.q ? *reinterpret_cast<const v8s*>(a + (k + t) * ld) : zero;
+      for (int i = 0; i < V; ++i) av[d][i] = k + i < g.q ? *reinterpret_cast<const Run*>(a + (k + i) * ld) : zero;
 #pragma unroll
       for (int c = 0; c < CF; ++c)
-        bv[d][c] = c < frags && k < g.q ? *reinterpret_cast<const v8s*>(b[c] + k0 + d * 32) : zero;
+        bv[d][c] = c < frags && k < g.q ? *reinterpret_cast<const Run*>(b[c] + k0 + d * STEP) : zero;
     }
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        v8s f;
+      for (int u = 0; u < V; ++u) {
+        Run f;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) f[t] = av[d][t][u];
+        for (int i = 0; i < V; ++i) f[i] = av[d][i][u];
 #pragma unroll
-        for (int c = 0; c < CF; ++c) acc[c][u] = T::mfma(f, bv[d][c], acc[c][u]);
+        for (int c = 0; c < CF; ++c)
+          acc[c][u] = T::mfma(__builtin_bit_cast(v8s, f), __builtin_bit_cast(v8s, bv[d][c]), acc[c][u]);
       }
   }
   const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
@@ -426,14 +465,14 @@ __global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
   for (int c = 0; c < CF; ++c) {
     if (c >= frags) break;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float* s = &sums[wave][lane & 15][(4 * (lane >> 4) + r) * 8];
-      *reinterpret_cast<v4f*>(s) = v4f{acc[c][0][r], acc[c][1][r], acc[c][2][r], acc[c][3][r]};
-      *reinterpret_cast<v4f*>(s + 4) = v4f{acc[c][4][r], acc[c][5][r], acc[c][6][r], acc[c][7][r]};
-    }
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int u = 0; u < V; u += 4)
+        *reinterpret_cast<v4f*>(&sums[wave][lane & 15][(4 * (lane >> 4) + r) * V + u]) =
+            v4f{acc[c][u][r], acc[c][u + 1][r], acc[c][u + 2][r], acc[c][u + 3][r]};
     __syncthreads();
-    const int r = threadIdx.x % (ROWS / 4) * 4, col = threadIdx.x / (ROWS / 4);  // 32 x 16 = every thread one run
-    if (c * 16 + col < cols && m0 + r < g.m) {
+    const int r = threadIdx.x % (ROWS / 4) * 4, col = threadIdx.x / (ROWS / 4);
+    if (col < 16 && c * 16 + col < cols && m0 + r < g.m) {
       v4f v = *reinterpret_cast<const v4f*>(&sums[0][col][r]);
 #pragma unroll
       for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const v4f*>(&sums[w][col][r]);
@@ -443,33 +482,28 @@ __global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
   }
 }
 
-// Whether the kernels above are the faster ones.  They read the weights at
-// the card's rate and the columns once for every 32 or 128 rows; the tiles
-// read both from L2 but need many tiles in flight for that rate.  Measured in
-// us, K-contiguous weights (few columns against tiles):
-//   32 experts of 4096 x 2048   8 rows each 111 / 135   24: 131 / 139   32: 147 / 141
-//   64 of 1024 x 2048           8:  60 / 71             24:  72 / 73    32:  76 / 74
-//   8 of 2048 x 2048            8:  17 / 33             48:  26 / 36    64:  44 / 37
-//   1 of 4096 x 4096            8:  15 / 56                             128: 27 / 63
-bool few_columns_fit(int groups, int m, int n) {
-  const long tiles = (long)groups * ((m + 255) / 256), units = 256;
-  const long most = tiles * 16 <= units ? 128 : tiles * 4 <= units ? 48 : 24;
-  return n <= most * groups;
+hipError_t join_columns(const Grouped16& g, hipStream_t st) {
+  hipLaunchKernelGGL(join_columns_kernel, dim3((unsigned)group_tiles_max(g.n, g.groups, 64), (unsigned)((g.m + 63) / 64)),
+                     dim3(256), 0, st, g);
+  return hipGetLastError();
 }
 
+long few_blocks(bool ks, int lane, int groups, int m, int n) {
+  const long rows = ks ? 16 * lane : FEW_ROWS;
+  return group_tiles_max(n, groups, ks ? FEW_KS_COLS : FEW_COLS) * ((m + rows - 1) / rows);
+}
+
+// 32 experts of 4096 x 2048 (16-bit), 8 / 32 rows each: MR 2, DEPTH 4 takes 111 / 147 us,
+// 4, 4: 125 / 148; 1, 8: 134 / 206; 2, 8 (fewer blocks on a unit): 146 / 197.
+// K-strided f32, 1 of 1024 x 2048, 128 rows: DEPTH 2 takes 26 us, 4: 30.
 template <class T>
 hipError_t few_columns(const Grouped16& g, hipStream_t st) {
-  if (g.A.ks) {
-    const long blocks = group_tiles_max(g.n, g.groups, 32) * ((g.m + 127) / 128);
-    hipLaunchKernelGGL((few_columns_ks_kernel<T, 2>), dim3((unsigned)blocks), dim3(512), 0, st, g);
-  } else {
-    // 32 experts of 4096 x 2048, 8 / 32 rows each: MR 2, DEPTH 4 takes 111 / 147 us,
-    // 4, 4: 125 / 148; 1, 8: 134 / 206; 2, 8 (fewer blocks on a unit): 146 / 197
-    constexpr int MR = 2, DEPTH = 4;
-    const long blocks = group_tiles_max(g.n, g.groups, 64) * ((g.m + 16 * MR - 1) / (16 * MR));
-    hipLaunchKernelGGL((few_columns_kernel<T, MR, DEPTH>), dim3((unsigned)blocks), dim3(512), 0, st, g);
-  }
-  return hipGetLastError();
+  const unsigned blocks = (unsigned)(few_blocks(g.A.ks, T::LANE, g.groups, g.m, g.n) * g.parts);
+  if (g.A.ks)
+    hipLaunchKernelGGL((few_columns_ks_kernel<T, 2>), dim3(blocks), dim3(512), 0, st, g);
+  else
+    hipLaunchKernelGGL((few_columns_kernel<T, FEW_MR, 4>), dim3(blocks), dim3(512), 0, st, g);
+  return g.parts > 1 ? join_columns(g, st) : hipGetLastError();
 }
 
 template <class T, int BT, bool AKS, bool PAIR>
@@ -478,10 +512,7 @@ hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
   const hipError_t err = device_units(&cus);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL((grouped_n_kernel<T, BT, AKS, PAIR>), dim3(SHARES * cus), dim3(512), 0, st, g);
-  if (g.parts > 1)
-    hipLaunchKernelGGL(join_columns_kernel, dim3((unsigned)group_tiles_max(g.n, g.groups, 64), (unsigned)((g.m + 63) / 64)),
-                       dim3(256), 0, st, g);
-  return hipGetLastError();
+  return g.parts > 1 ? join_columns(g, st) : hipGetLastError();
 }
 
 // The sum of the parts, in their order, into C.
@@ -521,6 +552,38 @@ hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
 
 }  // namespace
 
+// Whether the kernels for few columns are the faster ones: 0, or the parts in
+// which they take the inner dimension.
+//
+// Where their blocks are no more than the units, a call takes a block's time:
+// about 1 ns per entry of the inner dimension and (1 + columns / 16), twice
+// that in f32, so parts of 10 us are made while units are idle.  Beyond 50 us
+// the 16-bit tiles are faster; those of f32 are not, which wait for the slices.
+// Measured in us (few columns / tiles):
+//   16-bit   1 of 1024 x 2048, 128 rows 15 / 30;  x 8192, 32 rows 23 / 30;  x 32768, 32 rows 29 / 50,
+//            256 rows 86 / 76
+//   f32      1 of 1024 x 2048, 128 rows 26 / 45;  x 8192, 32 rows 28 / 69;  x 32768, 32 rows 47 / 216,
+//            256 rows 210 / 345
+// Where they are more, they read the weights at the card's rate and the columns
+// once for every 32 or 128 rows; the tiles read both from L2 but need many
+// tiles in flight for that rate, and in f32 cut the weights into slices first:
+//   16-bit  32 of 4096 x 2048   8 rows each 111 / 135   24: 131 / 139   32: 147 / 141
+//           64 of 1024 x 2048   8:  60 / 71             24:  72 / 73    32:  76 / 74
+//            8 of 2048 x 2048   8:  17 / 33             48:  26 / 36    64:  44 / 37
+//   f32     32 of 2048 x 2048   8: 127 / 345            48: 239 / 362   96: 416 / 377
+//            8 of 2048 x 2048   8:  35 / 88             48:  65 / 92    64: 109 / 93
+int few_columns_parts(bool f32, bool ks, int groups, int m, int n, int q) {
+  const long units = 256, blocks = few_blocks(ks, f32 ? 4 : 8, groups, m, n);
+  if (blocks <= units) {
+    const long frags = std::min<long>((((long)n + groups - 1) / groups + 15) / 16, (ks ? FEW_KS_COLS : FEW_COLS) / 16);
+    const long ns = (long)q * (1 + frags) * (f32 ? 2 : 1);
+    const long parts = std::max(std::min({ns / 10000, units / std::max(blocks, 1L), 32L}), 1L);
+    return f32 || ns / parts <= 50000 ? (int)parts : 0;
+  }
+  const long tiles = (long)groups * ((m + 255) / 256), most = f32 || tiles * 4 <= units ? 48 : 24;
+  return n <= most * groups ? 1 : 0;
+}
+
 // counted with the smallest tiles any variant uses
 bool grouped_n_fits(const Grouped16& g) {
   return group_tiles_max(g.n, g.groups, 32) * ((g.m + 15) / 16) <= 0x7fffffffL;  // (parts only where tiles are few)
@@ -543,7 +606,6 @@ size_t outer_partial_bytes(int parts, int groups, int m, int q) {
 }
 
 int gemm_parts(bool f32, int groups, int m, int n, int q) {
-  if (!f32 && few_columns_fit(groups, m, n)) return 1;
   const long tile = f32 ? 128 : 256;
   return parts_for(group_tiles_max(n, groups, tile) * ((m + tile - 1) / tile), (q + BK16 - 1) / BK16);
 }
@@ -555,9 +617,9 @@ bool grouped_k_fits(const Grouped16& g) {
 }
 
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
+  if (g.few) return g.f32 ? few_columns<Single>(g, st) : g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
   if (g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
   if (g.f32) return grouped_n<Half, 128, false, true>(g, st);
-  if (few_columns_fit(g.groups, g.m, g.n)) return g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
   if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, true, false>(g, st) : grouped_n<Bfloat, 256, false, false>(g, st);
   return g.A.ks ? grouped_n<Half, 256, true, false>(g, st) : grouped_n<Half, 256, false, false>(g, st);
 }

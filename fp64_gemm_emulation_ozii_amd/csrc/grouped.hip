@@ -14,8 +14,9 @@ constexpr size_t WS_ALIGN = 256;
 
 bool known_type(int type) { return type == OZGEMM_F32 || type == OZGEMM_BF16 || type == OZGEMM_F16; }
 
-bool aligned16(const void* p, long ld, long batch) {
-  return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && batch % 8 == 0 && ld <= LD16_MAX;
+// `run`: entries in 16 bytes
+bool aligned16(const void* p, long ld, long batch, int run = 8) {
+  return ((uintptr_t)p & 15) == 0 && ld % run == 0 && batch % run == 0 && ld <= LD16_MAX;
 }
 
 // Bytes from the first entry of `batches` rows x cols column-major matrices
@@ -60,6 +61,7 @@ Room room(int type, bool used, size_t rows, size_t k, size_t exponents, size_t p
 
 struct Rooms {
   Room A, B;
+  int few;         // the kernels for few columns take it (0: no)
   int parts;       // of the inner dimension
   size_t partial;  // offset of their sums
   size_t total;
@@ -69,13 +71,17 @@ Rooms gemm_rooms(int type, int groups, int m, int n, int q, int transa, const vo
                  const void* B, int ldb) {
   const bool f32 = type == OZGEMM_F32;
   Rooms r{};
-  const bool a_in_place = !f32 && aligned16(A, lda, stridea) && (transa ? q : m) % 8 == 0;
-  const bool b_in_place = !f32 && aligned16(B, ldb, 0) && q % 8 == 0;
+  const int run = f32 ? 4 : 8;
+  const bool a_fits = aligned16(A, lda, stridea, run) && (transa ? q : m) % run == 0;
+  const bool b_fits = aligned16(B, ldb, 0, run) && q % run == 0;
+  if (m > 0 && n > 0 && groups > 0 && (!f32 || (a_fits && b_fits)))
+    r.few = few_columns_parts(f32, a_fits && transa == 0, groups, m, n, q);
+  const bool a_in_place = a_fits && (!f32 || r.few), b_in_place = b_fits && (!f32 || r.few);
   const bool any = m > 0 && n > 0 && q > 0 && groups > 0;
   r.A = room(type, any && !a_in_place, (size_t)groups * m, q, (size_t)groups * m,
              transa ? 0 : slice_part_bytes(m, q, groups, false), r.total);
   r.B = room(type, any && !b_in_place, n, q, n, 0, r.total);
-  r.parts = any ? gemm_parts(f32, groups, m, n, q) : 1;
+  r.parts = !any ? 1 : r.few ? r.few : gemm_parts(f32, groups, m, n, q);
   r.partial = take(r.total, gemm_partial_bytes(r.parts, m, n));
   return r;
 }
@@ -170,10 +176,11 @@ int ozgemm_grouped_gemm(int type, int ctype, int groups, int m, int n, int q, in
   g.C = C;
   g.ctype = ctype;
   g.ldc = ldc;
+  g.few = r.few > 0;
   g.parts = r.parts;
   g.partial = (float*)(ws + r.partial);
-  // (F32 operands stay here only where nothing is read: no inner dimension)
-  g.A = in_place(A, lda, (long)stridea, transa == 0 && !g.f32, ar);
+  // (F32 operands stay here for few columns, or where nothing is read)
+  g.A = in_place(A, lda, (long)stridea, transa == 0 && (g.few || !g.f32), ar);
   g.B = in_place(B, ldb, 0, false, q);
   if (!grouped_n_fits(g)) return OZGEMM_RANGE;
   if (r.A.used) {

@@ -30,7 +30,8 @@ struct Operand16 {
 struct Grouped16 {
   Operand16 A, B;
   int bf16;   // the slices' type: 1 bfloat16, 0 half
-  int f32;    // two half slices each
+  int f32;    // two half slices each (few columns: as they are)
+  bool few;   // by the kernels for few columns
   int m, n, q, groups;
   const int32_t* offsets;
   void* C;
@@ -45,6 +46,9 @@ bool grouped_n_fits(const Grouped16& g);
 bool grouped_k_fits(const Grouped16& g);
 // C(:, J_e) = A_e B(:, J_e): B's rows are the n columns of the call.
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st);
+// Whether a product of these sizes goes by the kernels for few columns: 0, or
+// the parts of its inner dimension.  They read F32 operands as they lie.
+int few_columns_parts(bool f32, bool a_strided, int groups, int m, int n, int q);
 // Parts for a product of these sizes, and the room they take: where its tiles
 // are too few for the card and its inner dimension is long.
 int gemm_parts(bool f32, int groups, int m, int n, int q);

@@ -31,14 +31,32 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
 struct Half {
+  static constexpr int LANE = 8;  // k per lane of an operand
+  typedef uint16_t Entry;
   static __device__ __forceinline__ v4f mfma(v8s a, v8s b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
   }
 };
 struct Bfloat {
+  static constexpr int LANE = 8;
+  typedef uint16_t Entry;
   static __device__ __forceinline__ v4f mfma(v8s a, v8s b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0,
                                                    0);
+  }
+};
+
+// Single precision as it is: lane l of an operand holds k = 4 (l / 16) .. + 3,
+// one of which goes into each of four products (both operands alike, so the
+// sum is over the same k whatever their order).
+struct Single {
+  static constexpr int LANE = 4;
+  typedef float Entry;
+  static __device__ __forceinline__ v4f mfma(v8s a, v8s b, v4f c) {
+    const v4f x = __builtin_bit_cast(v4f, a), y = __builtin_bit_cast(v4f, b);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[t], y[t], c, 0, 0, 0);
+    return c;
   }
 };
 

@@ -175,30 +175,35 @@ def test_neighbouring_rows_and_groups_do_not_meet():
 
 
 def test_infinities():
-    # 16-bit types follow the usual rules; in f32 a row with an infinity makes its results NaN
-    X = torch.ones(4, 64, device="cuda")
-    W = torch.ones(1, 8, 64, device="cuda")
-    X[1, 3] = float("inf")
-    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
-    for dtype in (torch.bfloat16, torch.float16):
-        Y = oz.grouped_linear(X.to(dtype), W.to(dtype), off)
-        assert torch.isinf(Y[1]).all() and (Y[[0, 2, 3]] == 64).all()
-    Y = oz.grouped_linear(X, W, off)
-    assert torch.isnan(Y[1]).all() and (Y[[0, 2, 3]] == 64).all()
+    # the usual rules, but for f32 in slices: there a row with an infinity makes its results NaN
+    for n, q in ((4, 64), (300, 64), (4, 66), (20000, 128)):
+        X = torch.ones(n, q, device="cuda")
+        W = torch.ones(1, 8, q, device="cuda")
+        X[1, 3] = float("inf")
+        off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        for dtype in (torch.bfloat16, torch.float16, torch.float32):
+            Y = oz.grouped_linear(X.to(dtype), W.to(dtype), off)
+            if dtype == torch.float32 and (q % 4 or n > 10000):
+                assert torch.isnan(Y[1]).all()
+            else:
+                assert torch.isinf(Y[1]).all()
+            assert (Y[2:] == q).all() and (Y[0] == q).all()
 
 
 def test_f32_range():
-    # rows far apart in size, subnormal rows and the largest: the grids follow each row
-    g = torch.Generator(device="cuda").manual_seed(2)
-    X = torch.randn(6, 96, generator=g, device="cuda")
-    X *= torch.tensor([1e-40, 1e-30, 1.0, 1e30, 3e37, 0.0], device="cuda")[:, None]
-    W = torch.randn(1, 24, 96, generator=g, device="cuda") * 0.1
-    W[0, 0] *= 1e-25
-    off = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
-    Y = oz.grouped_linear(X, W, off)
-    C, P = X.double() @ W[0].double().T, X.double().abs() @ W[0].double().abs().T
-    big = X.double().abs().amax(1)[:, None] * W[0].double().abs().amax(1)[None]
-    check(Y, C, bound(C, P, 96, torch.float32, torch.float32, big))
+    # rows far apart in size, subnormal rows and the largest; q: as they lie, and in slices (whose grids follow each row)
+    for n, q in ((6, 96), (300, 96), (6, 98), (20000, 96)):
+        g = torch.Generator(device="cuda").manual_seed(2)
+        X = torch.randn(n, q, generator=g, device="cuda")
+        X[:6] *= torch.tensor([1e-40, 1e-30, 1.0, 1e30, 3e37, 0.0], device="cuda")[:, None]
+        W = torch.randn(1, 24, q, generator=g, device="cuda") * 0.1
+        W[0, 0] *= 1e-25
+        off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        Y = oz.grouped_linear(X, W, off)
+        C, P = X.double() @ W[0].double().T, X.double().abs() @ W[0].double().abs().T
+        big = X.double().abs().amax(1)[:, None] * W[0].double().abs().amax(1)[None]
+        # in FP32, q products and q sums each round by at most half the smallest number, 2^-150
+        check(Y, C, bound(C, P, q, torch.float32, torch.float32, big) + q * 2.0 ** -149)
 
 
 def test_strides():
@@ -315,7 +320,7 @@ def test_a_given_workspace():
 
 
 @pytest.mark.parametrize("layout", ["mq", "qm"])
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("sizes, m, q", [
     ([1], 8, 8), ([2, 0, 1], 136, 1024), ([16] * 9, 264, 2056), ([17, 0, 31, 33, 1], 520, 264), ([100, 20, 3], 72, 520),
     ([24] * 40, 128, 96), ([1] * 130, 40, 48), ([65, 2], 1032, 4104), ([5], 2048, 1008)])
@@ -405,4 +410,21 @@ def test_products_summed_in_parts(dtype, sizes, m, q, layout):
         Y = oz.grouped_linear(X, W, off, out=out)
         check_all(X, W, dY, off, Y, None, None)
         assert (out[:6] == 5).all() and (out[-4:] == 5).all()
+        assert torch.equal(out, oz.grouped_linear(X, W, off, out=out.clone()))
+
+
+@pytest.mark.parametrize("layout", ["mq", "qm"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("sizes, m, q", [([5, 0, 17], 40, 12288), ([1], 24, 32768), ([130, 66], 72, 8200),
+                                         ([0, 0, 200], 130, 8232), ([3], 1000, 16388)])
+def test_few_columns_summed_in_parts(dtype, sizes, m, q, layout):
+    X, W, dY, off = draw(sizes, m, q, TYPES[dtype], m * q + 2, before=3, behind=2)
+    X[:3], X[-2:] = float("nan"), float("inf")
+    if layout == "qm":
+        W = W.transpose(1, 2).contiguous().transpose(1, 2)
+    for out_dtype in (X.dtype, torch.float32):
+        out = torch.full((X.shape[0], m), 5.0, device="cuda", dtype=out_dtype)
+        Y = oz.grouped_linear(X, W, off, out=out)
+        check_all(X, W, dY, off, Y, None, None)
+        assert (out[:3] == 5).all() and (out[-2:] == 5).all()
         assert torch.equal(out, oz.grouped_linear(X, W, off, out=out.clone()))

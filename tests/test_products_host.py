@@ -31,8 +31,10 @@ def outer(type=L.OZGEMM_BF16, ctype=None, groups=4, m=64, q=128, n=100, A=A, lda
     (dict(m=L.OZGEMM_MAX_ROWS + 1, ldc=1 << 22), L.OZGEMM_RANGE), (dict(n=L.OZGEMM_MAX_ROWS + 1), L.OZGEMM_RANGE),
     (dict(q=L.OZGEMM_MAX_ROWS + 1, lda=1 << 22, ldb=1 << 22), L.OZGEMM_RANGE),
     (dict(groups=L.OZGEMM_GROUPS_MAX + 1), L.OZGEMM_RANGE),
-    (dict(type=L.OZGEMM_F32), -16), (dict(type=L.OZGEMM_F32, ws=WS + 16, nbytes=1 << 30), -16),
-    (dict(type=L.OZGEMM_F32, ws=WS, nbytes=1000), L.OZGEMM_WORKSPACE_TOO_SMALL),
+    (dict(type=L.OZGEMM_F32, n=100000), -16), (dict(type=L.OZGEMM_F32, n=100000, ws=WS + 16, nbytes=1 << 30), -16),
+    (dict(type=L.OZGEMM_F32, n=100000, ws=WS, nbytes=1000), L.OZGEMM_WORKSPACE_TOO_SMALL),
+    (dict(type=L.OZGEMM_F32, A=A + 4), -16), (dict(type=L.OZGEMM_F32, transa=0, n=100000), -16),
+    (dict(type=L.OZGEMM_F32, ldb=129), -16), (dict(type=L.OZGEMM_F32, q=126), -16),
     (dict(ldb=129), -16), (dict(A=A + 2), -16), (dict(B=B + 8), -16),
     (dict(m=0), 0), (dict(n=0), 0), (dict(groups=0), 0), (dict(m=0, A=None, B=None, off=None, C=None), 0),
 ])
@@ -61,11 +63,14 @@ def test_workspace_bytes():
     assert w(L.OZGEMM_BF16, 4, 64, 100, 128, 1, A, 128, 64 * 128, B, 128) == 0  # read in place
     assert w(L.OZGEMM_BF16, 4, 64, 100, 128, 1, A + 2, 128, 64 * 128, B, 128) >= 4 * 64 * 128 * 2
     assert w(L.OZGEMM_BF16, 4, 64, 100, 129, 1, A, 136, 64 * 136, B, 136) >= (4 * 64 + 100) * 192 * 2
-    assert w(L.OZGEMM_F32, 4, 64, 100, 128, 1, A, 128, 64 * 128, B, 128) >= (4 * 64 + 100) * (128 * 4 + 4)
+    assert w(L.OZGEMM_F32, 4, 64, 100000, 128, 1, A, 128, 64 * 128, B, 128) >= (4 * 64 + 100000) * (128 * 4 + 4)
+    assert w(L.OZGEMM_F32, 4, 64, 100, 128, 1, A, 128, 64 * 128, B, 128) == 0  # few columns are read as they lie
+    assert w(L.OZGEMM_F32, 4, 64, 100, 128, 0, A, 64, 64 * 128, B, 128) == 0
+    assert w(L.OZGEMM_F32, 4, 64, 100, 128, 0, A + 4, 64, 64 * 128, B, 128) >= (4 * 64 + 100) * (128 * 4 + 4)
     assert w(L.OZGEMM_F64, 4, 64, 100, 128, 1, A, 128, 64 * 128, B, 128) == 0
     assert w(L.OZGEMM_F32, 4, 64, 0, 128, 1, A, 128, 64 * 128, B, 128) == 0
     # sizes past 32 bits
-    assert w(L.OZGEMM_F32, 64, 1 << 15, 1, 1 << 15, 1, A, 1 << 15, 1 << 30, B, 1 << 15) >= 1 << 38
+    assert w(L.OZGEMM_F32, 64, 1 << 15, 1, 1 << 15, 1, A + 4, 1 << 15, 1 << 30, B, 1 << 15) >= 1 << 38
     o = L.ozgemm_grouped_outer_workspace_bytes
     assert o(L.OZGEMM_F16, 4, 64, 128, 100, A, 64, B, 128) == 0
     assert o(L.OZGEMM_F16, 4, 60, 128, 100, A, 64, B, 128) >= (60 + 128) * 100 * 2
