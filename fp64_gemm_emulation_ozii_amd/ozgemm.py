@@ -402,8 +402,8 @@ def ozgemm_grouped_gemm(type, ctype, groups, m, n, q, transa, A, lda, stridea, B
     caller's."""
     L, hs = lib(), _stream(stream)
     ops = (type, ctype, groups, m, n, q, transa, _ptr(A), lda, stridea, _ptr(B), ldb, _ptr(offsets), _ptr(C), ldc)
-    st = _GEMM_NO_WORKSPACE if workspace is None else None
-    if workspace is None and type != OZGEMM_F32:  # 16-bit operands are usually read in place
+    st = None
+    if workspace is None:  # operands are usually read in place
         st = L.ozgemm_grouped_gemm(*ops, None, 0, hs)
     if st is None or st == _GEMM_NO_WORKSPACE:
         need = 0 if workspace is not None else ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, A,
