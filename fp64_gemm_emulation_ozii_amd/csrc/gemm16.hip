@@ -268,17 +268,12 @@ __global__ __launch_bounds__(256) void join_columns_kernel(Grouped16 g) {
   const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
   const int row = blockIdx.y * 64 + (threadIdx.x & 15) * 4;
   if (row >= g.m) return;
-  const int32_t* ea = g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr;
   for (int col = gt.begin + (threadIdx.x >> 4); col < min(gt.end, gt.begin + 64); col += 16) {
     v4f v = {0.f, 0.f, 0.f, 0.f};
     for (int p = 0; p < g.parts; ++p) {
       const float* from = g.partial + ((long)p * g.n + col) * g.m + row;
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] += row + k < g.m ? from[k] : 0.f;
-    }
-    if (ea != nullptr) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = unscale(v[k], ea[min(row + k, g.m - 1)], g.B.ex[col]);
     }
     store4(g, col, row, wide, v);
   }
@@ -366,7 +361,78 @@ __device__ __forceinline__ FewTile few_tile(Grouped16& g, const GroupIndex& inde
   return t;
 }
 
-template <class T, int MR, int DEPTH>
+// N entries next to each other, of a row of `length` entries of which `left`
+// are left; zeros follow where those are fewer.  EDGE: they may be, and may
+// lie on no 16-byte boundary.  Then the row's last N entries are read and moved
+// down.  AROUND: 16-bit entries come as the 32-bit words around them (1 of
+// 1023 x 1023, 64 rows: 23 us with reads that begin in the middle of a word, 13
+// so; where lanes read next to each other, as in few_outer_kernel, the further
+// reads cost more than that: 46 us against 68 for 4096 rows).  load() issues
+// the reads, get() works on what they brought, after all that are to be in flight.
+template <class E, int N, bool EDGE, bool AROUND = EDGE && sizeof(E) == 2>
+struct Run {
+  static constexpr int WORDS = N * (int)sizeof(E) / 4;
+  typedef E Entries __attribute__((ext_vector_type(N)));
+  typedef uint32_t Words __attribute__((ext_vector_type(WORDS), may_alias));
+  typedef Words Loose __attribute__((aligned(AROUND ? 4 : sizeof(E))));
+  typedef uint32_t Word __attribute__((may_alias));
+  Words w;
+  uint32_t after;  // the word after them, where the entries begin in the middle of one
+
+  __device__ __forceinline__ void load(const E* p, int left, int length) {
+    w = Words{};
+    after = 0;
+    if (left <= 0) return;
+    if (!EDGE) {
+      w = *reinterpret_cast<const Words*>(p);
+    } else if (length >= N) {
+      p -= max(N - left, 0);
+      if (AROUND) {
+        const Word* from = reinterpret_cast<const Word*>((uintptr_t)p & ~(uintptr_t)3);
+        w = *reinterpret_cast<const Loose*>(from);
+        after = from[WORDS - 1 + (((uintptr_t)p >> 1) & 1)];
+      } else {
+        w = *reinterpret_cast<const Loose*>(p);
+      }
+    } else {
+      Entries r = {};
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < left) r[i] = p[i];
+      w = __builtin_bit_cast(Words, r);
+    }
+  }
+
+  __device__ __forceinline__ Entries get(const E* p, int left, int length) const {
+    Words v = w;
+    if (EDGE && left > 0 && length >= N) {
+      const int over = max(N - left, 0);
+      if (AROUND) {
+        const int half = ((uintptr_t)(p - over) & 2) * 8;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+          v[i] = __builtin_amdgcn_alignbit(i + 1 < WORDS ? v[i + 1 < WORDS ? i + 1 : i] : after, v[i], half);
+      }
+      if (__ballot(over > 0) != 0) {
+        const int words = over * (int)sizeof(E) / 4;
+        const int half = over * (int)sizeof(E) % 4 * 8;
+#pragma unroll
+        for (int by = 1; by < WORDS; by *= 2) {
+          if (words & by) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) v[i] = i + by < WORDS ? v[i + by < WORDS ? i + by : i] : 0;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+          v[i] = __builtin_amdgcn_alignbit(i + 1 < WORDS ? v[i + 1 < WORDS ? i + 1 : i] : 0, v[i], half);
+      }
+    }
+    return __builtin_bit_cast(Entries, v);
+  }
+};
+
+template <class T, int MR, int DEPTH, bool EDGE>
 __global__ __launch_bounds__(512, 2) void few_columns_kernel(Grouped16 g) {
   constexpr int ROWS = 16 * MR, COLS = FEW_COLS, CF = COLS / 16, WAVES = 8, STEP = 4 * T::LANE;
   typedef typename T::Entry Entry;
@@ -388,25 +454,28 @@ __global__ __launch_bounds__(512, 2) void few_columns_kernel(Grouped16 g) {
 #pragma unroll
   for (int c = 0; c < CF; ++c) b[c] = (const Entry*)g.B.p + (long)(n0 + min(c * 16 + (lane & 15), cols - 1)) * g.B.ld + kl;
   v4f acc[MR][CF] = {};
-  const v8s zero = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int k0 = t.k0; k0 < t.k_end; k0 += WAVES * STEP * DEPTH) {
-    v8s av[DEPTH][MR];
+    const int left = g.q - kl - k0;  // entries from this lane's first on
+    Run<Entry, T::LANE, EDGE> av[DEPTH][MR];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
 #pragma unroll
       for (int i = 0; i < MR; ++i)
-        av[d][i] = kl + k0 + d * STEP < g.q ? *reinterpret_cast<const v8s*>(a[i] + k0 + d * STEP) : zero;
+        av[d][i].load(a[i] + k0 + d * STEP, left - d * STEP, g.q);
 #pragma unroll
     for (int c = 0; c < CF; ++c) {
       if (c >= frags) break;
-      v8s bv[DEPTH];
+      Run<Entry, T::LANE, EDGE> bv[DEPTH];
 #pragma unroll
-      for (int d = 0; d < DEPTH; ++d)
-        bv[d] = kl + k0 + d * STEP < g.q ? *reinterpret_cast<const v8s*>(b[c] + k0 + d * STEP) : zero;
+      for (int d = 0; d < DEPTH; ++d) bv[d].load(b[c] + k0 + d * STEP, left - d * STEP, g.q);
 #pragma unroll
-      for (int d = 0; d < DEPTH; ++d)
+      for (int d = 0; d < DEPTH; ++d) {
+        const v8s fb = __builtin_bit_cast(v8s, bv[d].get(b[c] + k0 + d * STEP, left - d * STEP, g.q));
 #pragma unroll
-        for (int i = 0; i < MR; ++i) acc[i][c] = T::mfma(av[d][i], bv[d], acc[i][c]);
+        for (int i = 0; i < MR; ++i)
+          acc[i][c] = T::mfma(__builtin_bit_cast(v8s, av[d][i].get(a[i] + k0 + d * STEP, left - d * STEP, g.q)), fb,
+                              acc[i][c]);
+      }
     }
   }
   const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
@@ -434,11 +503,11 @@ __global__ __launch_bounds__(512, 2) void few_columns_kernel(Grouped16 g) {
 // transposes its V x V entries in registers into V MFMA operands, the u-th of
 // which has rows m0 + V i + u, i = 0..15.  Eight wavefronts share the inner
 // dimension.
-template <class T, int DEPTH>
+template <class T, int DEPTH, bool EDGE>
 __global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
   constexpr int V = T::LANE, ROWS = 16 * V, COLS = FEW_KS_COLS, CF = COLS / 16, WAVES = 8, STEP = 4 * V;
   typedef typename T::Entry Entry;
-  typedef Entry Run __attribute__((ext_vector_type(V)));
+  typedef Run<Entry, V, EDGE> Piece;
   __shared__ float sums[WAVES][16][ROWS + 4];
   const GroupIndex index(g.offsets, g.groups, g.n, COLS);
   const FewTile t = few_tile<ROWS, WAVES * STEP * DEPTH>(g, index);
@@ -449,35 +518,42 @@ __global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int kl = wave * STEP * DEPTH + (lane >> 4) * V;  // this lane's first k in a chunk
   const long ld = g.A.ld;
-  // rows past the end read the last V again (m is a multiple of V; their sums are not stored)
-  const Entry* a = (const Entry*)g.A.p + gt.group * g.A.batch + min(m0 + (lane & 15) * V, g.m - V);
+  // rows past the end read the last V again (EDGE: nothing); their sums are not stored
+  const int row = m0 + (lane & 15) * V, rows = EDGE ? g.m - row : V;
+  const Entry* a = (const Entry*)g.A.p + gt.group * g.A.batch + (EDGE ? row : min(row, g.m - V));
   const Entry* b[CF];
 #pragma unroll
   for (int c = 0; c < CF; ++c) b[c] = (const Entry*)g.B.p + (long)(n0 + min(c * 16 + (lane & 15), cols - 1)) * g.B.ld + kl;
   v4f acc[CF][V] = {};
-  const Run zero = {};
   for (int k0 = t.k0; k0 < t.k_end; k0 += WAVES * STEP * DEPTH) {
-    Run av[DEPTH][V], bv[DEPTH][CF];
+    Piece av[DEPTH][V], bv[DEPTH][CF];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
       const int k = kl + k0 + d * STEP;
 #pragma unroll
-      for (int i = 0; i < V; ++i) av[d][i] = k + i < g.q ? *reinterpret_cast<const Run*>(a + (k + i) * ld) : zero;
+      for (int i = 0; i < V; ++i) av[d][i].load(a + (k + i) * ld, k + i < g.q ? rows : 0, g.m);
 #pragma unroll
-      for (int c = 0; c < CF; ++c)
-        bv[d][c] = c < frags && k < g.q ? *reinterpret_cast<const Run*>(b[c] + k0 + d * STEP) : zero;
+      for (int c = 0; c < CF; ++c) bv[d][c].load(b[c] + k0 + d * STEP, c < frags ? g.q - k : 0, g.q);
     }
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
+    for (int d = 0; d < DEPTH; ++d) {
+      const int k = kl + k0 + d * STEP;
+      typename Piece::Entries at[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) at[i] = av[d][i].get(a + (k + i) * ld, k + i < g.q ? rows : 0, g.m);
+      v8s fb[CF];
+#pragma unroll
+      for (int c = 0; c < CF; ++c)
+        fb[c] = __builtin_bit_cast(v8s, bv[d][c].get(b[c] + k0 + d * STEP, c < frags ? g.q - k : 0, g.q));
 #pragma unroll
       for (int u = 0; u < V; ++u) {
-        Run f;
+        typename Piece::Entries f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = av[d][i][u];
+        for (int i = 0; i < V; ++i) f[i] = at[i][u];
 #pragma unroll
-        for (int c = 0; c < CF; ++c)
-          acc[c][u] = T::mfma(__builtin_bit_cast(v8s, f), __builtin_bit_cast(v8s, bv[d][c]), acc[c][u]);
+        for (int c = 0; c < CF; ++c) acc[c][u] = T::mfma(__builtin_bit_cast(v8s, f), fb[c], acc[c][u]);
       }
+    }
   }
   const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
 #pragma unroll
@@ -515,14 +591,19 @@ long few_blocks(bool ks, int lane, int groups, int m, int n) {
 // 32 experts of 4096 x 2048 (16-bit), 8 / 32 rows each: MR 2, DEPTH 4 takes 111 / 147 us,
 // 4, 4: 125 / 148; 1, 8: 134 / 206; 2, 8 (fewer blocks on a unit): 146 / 197.
 // K-strided f32, 1 of 1024 x 2048, 128 rows: DEPTH 2 takes 26 us, 4: 30.
-template <class T>
+template <class T, bool EDGE>
 hipError_t few_columns(const Grouped16& g, hipStream_t st) {
   const unsigned blocks = (unsigned)(few_blocks(g.A.ks, T::LANE, g.groups, g.m, g.n) * g.parts);
   if (g.A.ks)
-    hipLaunchKernelGGL((few_columns_ks_kernel<T, 2>), dim3(blocks), dim3(512), 0, st, g);
+    hipLaunchKernelGGL((few_columns_ks_kernel<T, 2, EDGE>), dim3(blocks), dim3(512), 0, st, g);
   else
-    hipLaunchKernelGGL((few_columns_kernel<T, FEW_MR, 4>), dim3(blocks), dim3(512), 0, st, g);
+    hipLaunchKernelGGL((few_columns_kernel<T, FEW_MR, 4, EDGE>), dim3(blocks), dim3(512), 0, st, g);
   return g.parts > 1 ? join_columns(g, st) : hipGetLastError();
+}
+
+template <class T>
+hipError_t few(const Grouped16& g, hipStream_t st) {
+  return g.edge ? few_columns<T, true>(g, st) : few_columns<T, false>(g, st);
 }
 
 template <class T, int BT, bool AKS, bool PAIR>
@@ -532,6 +613,91 @@ hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL((grouped_n_kernel<T, BT, AKS, PAIR>), dim3(SHARES * cus), dim3(512), 0, st, g);
   return g.parts > 1 ? join_columns(g, st) : hipGetLastError();
+}
+
+// Outer products too small for the tiles, or of operands that those would
+// have to be copied for: 64 x 64 entries of a group's result per block, the
+// eight wavefronts share the group's columns.  A lane reads runs of 4 entries
+// of LANE columns of both operands and transposes them in registers into four
+// MFMA operands each: the u-th has rows m0 + 4 i + u, i = 0..15.
+constexpr int FEW_OUTER = 64;
+
+template <class T, bool EDGE>
+__global__ __launch_bounds__(512, 2) void few_outer_kernel(Grouped16 g) {
+  constexpr int R = 4, V = T::LANE, WAVES = 8, STEP = 4 * V, CHUNK = WAVES * STEP;
+  typedef typename T::Entry Entry;
+  typedef Run<Entry, R, EDGE, false> Piece;
+  typedef Entry Operand __attribute__((ext_vector_type(V)));
+  __shared__ float sums[WAVES][16][FEW_OUTER + 4];
+  const int tiles_m = (g.m + FEW_OUTER - 1) / FEW_OUTER, tiles_q = (g.q + FEW_OUTER - 1) / FEW_OUTER;
+  const int per = tiles_m * tiles_q, whole = per * g.groups;
+  const int part = blockIdx.x / whole, e = blockIdx.x % whole / per, tile = blockIdx.x % per;
+  const int m0 = tile % tiles_m * FEW_OUTER, q0 = tile / tiles_m * FEW_OUTER;
+  const GroupTile gt = group_at(g.offsets, g.groups, g.n, CHUNK, e);
+  const int chunks = (gt.end - gt.begin + CHUNK - 1) / CHUNK, each = (chunks + g.parts - 1) / g.parts * CHUNK;
+  const int from = gt.begin + part * each, to = min(from + each, gt.end);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // rows past the end read the last ones again (EDGE: nothing); their sums are not stored
+  const int row = m0 + (lane & 15) * R, col = q0 + (lane & 15) * R;
+  const int rows = EDGE ? g.m - row : R, cols = EDGE ? g.q - col : R;
+  const Entry* a = (const Entry*)g.A.p + (EDGE ? row : min(row, g.m - R));
+  const Entry* b = (const Entry*)g.B.p + (EDGE ? col : min(col, g.q - R));
+  v4f acc[R][R] = {};
+  for (int k0 = from; k0 < to; k0 += CHUNK) {
+    const int k = k0 + wave * STEP + (lane >> 4) * V;
+    Piece ap[V], bp[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      ap[i].load(a + (long)(k + i) * g.A.ld, k + i < to ? rows : 0, g.m);
+      bp[i].load(b + (long)(k + i) * g.B.ld, k + i < to ? cols : 0, g.q);
+    }
+    typename Piece::Entries av[V], bv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      av[i] = ap[i].get(a + (long)(k + i) * g.A.ld, k + i < to ? rows : 0, g.m);
+      bv[i] = bp[i].get(b + (long)(k + i) * g.B.ld, k + i < to ? cols : 0, g.q);
+    }
+    v8s fb[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      Operand f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = bv[i][u];
+      fb[u] = __builtin_bit_cast(v8s, f);
+    }
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      Operand f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = av[i][u];
+#pragma unroll
+      for (int w = 0; w < R; ++w) acc[w][u] = T::mfma(__builtin_bit_cast(v8s, f), fb[w], acc[w][u]);
+    }
+  }
+  if (g.parts > 1) {  // (the sum of an empty part is stored too)
+    g.C = g.partial + ((long)part * g.groups + e) * g.m * g.q;
+    g.ctype = OZGEMM_F32;
+    g.ldc = g.m;
+  } else {
+    g.C = (char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2);
+  }
+  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
+#pragma unroll
+  for (int w = 0; w < R; ++w) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<v4f*>(&sums[wave][lane & 15][(4 * (lane >> 4) + r) * R]) =
+          v4f{acc[w][0][r], acc[w][1][r], acc[w][2][r], acc[w][3][r]};
+    __syncthreads();
+    const int r = threadIdx.x % (FEW_OUTER / 4) * 4, c = threadIdx.x / (FEW_OUTER / 4);
+    if (c < 16 && q0 + c * R + w < g.q && m0 + r < g.m) {
+      v4f v = *reinterpret_cast<const v4f*>(&sums[0][c][r]);
+#pragma unroll
+      for (int x = 1; x < WAVES; ++x) v += *reinterpret_cast<const v4f*>(&sums[x][c][r]);
+      store4(g, q0 + c * R + w, m0 + r, wide, v);
+    }
+    __syncthreads();
+  }
 }
 
 // The sum of the parts, in their order, into C.
@@ -556,50 +722,77 @@ __global__ __launch_bounds__(256) void join_parts_kernel(Grouped16 g) {
   store4(g, col, row, (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0, v);
 }
 
+hipError_t join_parts(const Grouped16& g, hipStream_t st) {
+  const long threads = (long)((g.m + 3) / 4) * g.q * g.groups;
+  hipLaunchKernelGGL(join_parts_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, g);
+  return hipGetLastError();
+}
+
+long few_outer_blocks(int groups, int m, int q) {
+  return (long)((m + FEW_OUTER - 1) / FEW_OUTER) * ((q + FEW_OUTER - 1) / FEW_OUTER) * groups;
+}
+
+template <class T>
+hipError_t few_outer(const Grouped16& g, hipStream_t st) {
+  const unsigned blocks = (unsigned)(few_outer_blocks(g.groups, g.m, g.q) * g.parts);
+  if (g.edge)
+    hipLaunchKernelGGL((few_outer_kernel<T, true>), dim3(blocks), dim3(512), 0, st, g);
+  else
+    hipLaunchKernelGGL((few_outer_kernel<T, false>), dim3(blocks), dim3(512), 0, st, g);
+  return g.parts > 1 ? join_parts(g, st) : hipGetLastError();
+}
+
 template <class T, int BT, bool KS, bool PAIR>
 hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
   int cus = 0;
   const hipError_t err = device_units(&cus);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL((grouped_k_kernel<T, BT, KS, PAIR>), dim3(SHARES * cus), dim3(512), 0, st, g);
-  if (g.parts > 1) {
-    const long threads = (long)((g.m + 3) / 4) * g.q * g.groups;
-    hipLaunchKernelGGL(join_parts_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, g);
-  }
-  return hipGetLastError();
+  return g.parts > 1 ? join_parts(g, st) : hipGetLastError();
 }
 
 }  // namespace
 
 // Whether the kernels for few columns are the faster ones: 0, or the parts in
-// which they take the inner dimension.
+// which they take the inner dimension.  The others cut F32 and copy operands
+// off the 16-byte grid (`edge`) first.  Measured in us (few columns / tiles),
+// calls from the host, which takes 12:
 //
 // Where their blocks are no more than the units, a call takes a block's time:
 // about 1 ns per entry of the inner dimension and (1 + columns / 16), twice
-// that in f32, so parts of 10 us are made while units are idle.  Beyond 50 us
-// the 16-bit tiles are faster; those of f32 are not, which wait for the slices.
-// Measured in us (few columns / tiles):
+// that in f32, half as much again K-strided (f32: twice) or off the grid; so
+// parts of 8 us are made while units are idle.  Beyond 50 us the 16-bit tiles
+// are faster, unless they have to wait for copies.
 //   16-bit   1 of 1024 x 2048, 128 rows 15 / 30;  x 8192, 32 rows 23 / 30;  x 32768, 32 rows 29 / 50,
-//            256 rows 86 / 76
+//            256 rows 86 / 76;  1 of 1023 x 1023, 64 rows 13 / 23;  1 of 2047 x 2047, 64 rows 21 / 27
 //   f32      1 of 1024 x 2048, 128 rows 26 / 45;  x 8192, 32 rows 28 / 69;  x 32768, 32 rows 47 / 216,
 //            256 rows 210 / 345
-// Where they are more, they read the weights at the card's rate and the columns
-// once for every 32 or 128 rows; the tiles read both from L2 but need many
-// tiles in flight for that rate, and in f32 cut the weights into slices first:
+// Where they are some times more, it takes that many rounds of blocks, each
+// with a fixed time besides, against the tiles' launches:
+//   16-bit   1 of 256 x 512, 4096 rows 13 / 26;  64 of 128 x 128, 32768 rows 27 / 15
+//   copied   1 of 255 x 511, 4096 rows 23 / 56;  2 of 1399 x 89, 4096 rows 86 / 31
+//   f32      8 of 256 x 256, 4096 rows 17 / 24;  64 of 128 x 128, 32768 rows 54 / 41
+// Where they are many and the columns few, they read the weights at the card's
+// rate and the columns once for every 32 or 128 rows; the tiles read both from
+// L2 but need many in flight for that rate:
 //   16-bit  32 of 4096 x 2048   8 rows each 111 / 135   24: 131 / 139   32: 147 / 141
 //           64 of 1024 x 2048   8:  60 / 71             24:  72 / 73    32:  76 / 74
 //            8 of 2048 x 2048   8:  17 / 33             48:  26 / 36    64:  44 / 37
 //   f32     32 of 2048 x 2048   8: 127 / 345            48: 239 / 362   96: 416 / 377
 //            8 of 2048 x 2048   8:  35 / 88             48:  65 / 92    64: 109 / 93
-int few_columns_parts(bool f32, bool ks, int groups, int m, int n, int q) {
+int few_columns_parts(bool f32, bool edge, bool ks, int groups, int m, int n, int q) {
+  const bool copies = f32 || edge;
   const long units = 256, blocks = few_blocks(ks, f32 ? 4 : 8, groups, m, n);
+  const long frags = std::min<long>((((long)n + groups - 1) / groups + 15) / 16, (ks ? FEW_KS_COLS : FEW_COLS) / 16);
+  const long ns = (long)q * (1 + frags) * (f32 ? 2 : 1);
   if (blocks <= units) {
-    const long frags = std::min<long>((((long)n + groups - 1) / groups + 15) / 16, (ks ? FEW_KS_COLS : FEW_COLS) / 16);
-    const long ns = (long)q * (1 + frags) * (f32 ? 2 : 1);
-    const long parts = std::max(std::min({ns / 10000, units / std::max(blocks, 1L), 32L}), 1L);
-    return f32 || ns / parts <= 50000 ? (int)parts : 0;
+    const double slower = (ks ? (f32 ? 2 : 1.5) : 1) * (edge ? 1.5 : 1);
+    const long parts = std::max(std::min({(long)(ns * slower / 8000), units / std::max(blocks, 1L), 32L}), 1L);
+    return copies || ns / parts <= 50000 ? (int)parts : 0;
   }
-  const long tiles = (long)groups * ((m + 255) / 256), most = f32 || tiles * 4 <= units ? 48 : 24;
+  const long fixed = ks ? (f32 ? 4500 : 6500) : f32 ? (edge ? 8500 : 5500) : edge ? 7000 : 2500;
+  if (fixed + ns * (edge && !f32 ? 2 : 1) <= (copies ? 35000 : 17000) * units / blocks) return 1;
+  const long tiles = (long)groups * ((m + 255) / 256), most = copies || tiles * 4 <= units ? 48 : 24;
   return n <= most * groups ? 1 : 0;
 }
 
@@ -620,13 +813,29 @@ int outer_parts(bool f32, int groups, int m, int q, int n) {
   return parts_for(((m + tile - 1) / tile) * ((q + tile - 1) / tile) * groups, ((long)n / groups + BK16 - 1) / BK16);
 }
 
+// Measured in us (the kernel for small outer products / tiles): its time is
+// that of its 64 x 64 tiles' columns, 2^20 of them 30 us in 16 bits, 45 to 75
+// off the 8-byte grid, 105 in f32, and 6 at least; the tiles take a launch of
+// each copy, exponent and sum in parts, 11 to 30 us with hardly any columns.
+//   16-bit   8 of 256 x 256, 4096 rows 7 / 20;  1 of 1024 x 1024, 4096 rows 30 / 38, 32768 162 / 156
+//   copied   8 of 255 x 255, 4096 rows 10 / 53;  1 of 1023 x 1023, 4096 rows 56 / 73, 32768 809 / 242
+//   f32      8 of 256 x 256, 4096 rows 15 / 50;  1 of 1024 x 1024, 4096 rows 106 / 107;
+//            4 of 1023 x 511, 4096 rows 60 / 77, 32768 493 / 394
+int few_outer_parts(bool f32, int groups, int m, int q, int n) {
+  const long blocks = few_outer_blocks(groups, m, q), each = std::max(((long)n + groups - 1) / groups, 1L);
+  if (blocks > (1L << 20) / each) return 0;
+  const long chunks = (each + (f32 ? 127 : 255)) / (f32 ? 128 : 256);
+  return (int)std::max(std::min({512 / blocks, chunks / 4, 32L}), 1L);
+}
+
 size_t outer_partial_bytes(int parts, int groups, int m, int q) {
   return parts > 1 ? (size_t)parts * groups * m * q * 4 : 0;
 }
 
+// (In f32 so few tiles are no more than 256 blocks of few_columns_kernel.)
 int gemm_parts(bool f32, int groups, int m, int n, int q) {
-  const long tile = f32 ? 128 : 256;
-  return parts_for(group_tiles_max(n, groups, tile) * ((m + tile - 1) / tile), (q + BK16 - 1) / BK16);
+  if (f32) return 1;
+  return parts_for(group_tiles_max(n, groups, 256) * ((m + 255) / 256), (q + BK16 - 1) / BK16);
 }
 
 size_t gemm_partial_bytes(int parts, int m, int n) { return parts > 1 ? (size_t)parts * m * n * 4 : 0; }
@@ -636,7 +845,7 @@ bool grouped_k_fits(const Grouped16& g) {
 }
 
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
-  if (g.few) return g.f32 ? few_columns<Single>(g, st) : g.bf16 ? few_columns<Bfloat>(g, st) : few_columns<Half>(g, st);
+  if (g.few) return g.f32 ? few<Single>(g, st) : g.bf16 ? few<Bfloat>(g, st) : few<Half>(g, st);
   if (g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
   if (g.f32) return grouped_n<Half, 128, false, true>(g, st);
   if (g.bf16) return g.A.ks ? grouped_n<Bfloat, 256, true, false>(g, st) : grouped_n<Bfloat, 256, false, false>(g, st);
@@ -644,6 +853,7 @@ hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st) {
 }
 
 hipError_t launch_grouped_k(const Grouped16& g, hipStream_t st) {
+  if (g.few) return g.f32 ? few_outer<Single>(g, st) : g.bf16 ? few_outer<Bfloat>(g, st) : few_outer<Half>(g, st);
   if (g.A.ks != g.B.ks || (g.f32 && g.A.ks)) return hipErrorInvalidValue;
   if (g.f32) return grouped_k<Half, 128, false, true>(g, st);
   if (g.bf16) return g.A.ks ? grouped_k<Bfloat, 256, true, false>(g, st) : grouped_k<Bfloat, 256, false, false>(g, st);

@@ -61,7 +61,8 @@ Room room(int type, bool used, size_t rows, size_t k, size_t exponents, size_t p
 
 struct Rooms {
   Room A, B;
-  int few;         // the kernels for few columns take it (0: no)
+  int few;         // the kernels for few columns or small outer products take it (0: no)
+  bool edge;       // operands off the 16-byte grid
   int parts;       // of the inner dimension
   size_t partial;  // offset of their sums
   size_t total;
@@ -74,9 +75,9 @@ Rooms gemm_rooms(int type, int groups, int m, int n, int q, int transa, const vo
   const int run = f32 ? 4 : 8;
   const bool a_fits = aligned16(A, lda, stridea, run) && (transa ? q : m) % run == 0;
   const bool b_fits = aligned16(B, ldb, 0, run) && q % run == 0;
-  if (m > 0 && n > 0 && groups > 0 && (!f32 || (a_fits && b_fits)))
-    r.few = few_columns_parts(f32, a_fits && transa == 0, groups, m, n, q);
-  const bool a_in_place = a_fits && (!f32 || r.few), b_in_place = b_fits && (!f32 || r.few);
+  r.edge = !a_fits || !b_fits;
+  if (m > 0 && n > 0 && groups > 0) r.few = few_columns_parts(f32, r.edge, transa == 0, groups, m, n, q);
+  const bool a_in_place = r.few || (a_fits && !f32), b_in_place = r.few || (b_fits && !f32);
   const bool any = m > 0 && n > 0 && q > 0 && groups > 0;
   r.A = room(type, any && !a_in_place, (size_t)groups * m, q, (size_t)groups * m,
              transa ? 0 : slice_part_bytes(m, q, groups, false), r.total);
@@ -88,13 +89,17 @@ Rooms gemm_rooms(int type, int groups, int m, int n, int q, int transa, const vo
 
 Rooms outer_rooms(int type, int groups, int m, int q, int n, const void* A, int lda, const void* B, int ldb) {
   Rooms r{};
-  const bool in_place = type != OZGEMM_F32 && aligned16(A, lda, 0) && aligned16(B, ldb, 0) && m % 8 == 0 && q % 8 == 0;
+  const bool f32 = type == OZGEMM_F32;
+  const int run = f32 ? 4 : 8;
+  r.edge = !aligned16(A, lda, 0, run) || !aligned16(B, ldb, 0, run) || m % run != 0 || q % run != 0;
+  if (m > 0 && q > 0 && groups > 0) r.few = few_outer_parts(f32, groups, m, q, n);
+  const bool in_place = r.few || (!f32 && !r.edge);
   const bool any = m > 0 && n > 0 && q > 0 && groups > 0;
   // every group's columns begin at a multiple of 64
   const size_t k = (size_t)n + 63 * (size_t)std::min(groups, n);
   r.A = room(type, any && !in_place, m, k, (size_t)groups * m, slice_part_bytes(m, n, groups, true), r.total);
   r.B = room(type, any && !in_place, q, k, (size_t)groups * q, slice_part_bytes(q, n, groups, true), r.total);
-  r.parts = any ? outer_parts(type == OZGEMM_F32, groups, m, q, n) : 1;
+  r.parts = !any ? 1 : r.few ? r.few : outer_parts(f32, groups, m, q, n);
   r.partial = take(r.total, outer_partial_bytes(r.parts, groups, m, q));
   return r;
 }
@@ -177,6 +182,7 @@ int ozgemm_grouped_gemm(int type, int ctype, int groups, int m, int n, int q, in
   g.ctype = ctype;
   g.ldc = ldc;
   g.few = r.few > 0;
+  g.edge = r.edge;
   g.parts = r.parts;
   g.partial = (float*)(ws + r.partial);
   // (F32 operands stay here for few columns, or where nothing is read)
@@ -254,8 +260,10 @@ int ozgemm_grouped_outer(int type, int ctype, int groups, int m, int q, int n, c
   g.cbatch = (long)stridec;
   g.parts = r.parts;
   g.partial = (float*)(ws + r.partial);
-  g.A = in_place(A, lda, 0, !g.f32, m);
-  g.B = in_place(B, ldb, 0, !g.f32, q);
+  g.few = r.few > 0;
+  g.edge = r.edge;
+  g.A = in_place(A, lda, 0, g.few || !g.f32, m);
+  g.B = in_place(B, ldb, 0, g.few || !g.f32, q);
   if (!grouped_k_fits(g)) return OZGEMM_RANGE;
   if (r.A.used) {  // then B's too
     g.A = sliced(type, r.A, ws, 0, m);

@@ -31,7 +31,8 @@ struct Grouped16 {
   Operand16 A, B;
   int bf16;   // the slices' type: 1 bfloat16, 0 half
   int f32;    // two half slices each (few columns: as they are)
-  bool few;   // by the kernels for few columns
+  bool few;   // by the kernels for few columns or small outer products
+  bool edge;  // which then must not take runs of 16 bytes for aligned or whole
   int m, n, q, groups;
   const int32_t* offsets;
   void* C;
@@ -47,14 +48,17 @@ bool grouped_k_fits(const Grouped16& g);
 // C(:, J_e) = A_e B(:, J_e): B's rows are the n columns of the call.
 hipError_t launch_grouped_n(const Grouped16& g, hipStream_t st);
 // Whether a product of these sizes goes by the kernels for few columns: 0, or
-// the parts of its inner dimension.  They read F32 operands as they lie.
-int few_columns_parts(bool f32, bool a_strided, int groups, int m, int n, int q);
+// the parts of its inner dimension.  They read any operands as they lie; the
+// others need slices of F32 and copies of those off the 16-byte grid (`edge`).
+int few_columns_parts(bool f32, bool edge, bool a_strided, int groups, int m, int n, int q);
 // Parts for a product of these sizes, and the room they take: where its tiles
 // are too few for the card and its inner dimension is long.
 int gemm_parts(bool f32, int groups, int m, int n, int q);
 size_t gemm_partial_bytes(int parts, int m, int n);
 int outer_parts(bool f32, int groups, int m, int q, int n);
 size_t outer_partial_bytes(int parts, int groups, int m, int q);
+// The same for the kernel for small outer products.
+int few_outer_parts(bool f32, int groups, int m, int q, int n);
 // C_e (m x q) = sum over j in J_e: A's and B's inner dimension is the n columns.
 hipError_t launch_grouped_k(const Grouped16& g, hipStream_t st);
 

@@ -438,9 +438,8 @@ int ozgemm_mfma_ceiling(int blocks, int steps, unsigned seed, unsigned *sink, vo
  * the slices hold an entry to 2^-23 and the products drop at most 2^-22 of a
  * term (2^-39 of the row's largest entry where that is more), under the
  * rounding of the FP32 sums.  A row that holds Inf or NaN makes the outputs
- * it touches NaN, as in ozgemm_dgemm.  (ozgemm_grouped_gemm multiplies in FP32
- * as they lie operands that are aligned to 16 bytes, where there are few
- * columns: there Inf and NaN follow the usual rules.)
+ * it touches NaN, as in ozgemm_dgemm.  Small F32 products of either kind are
+ * multiplied in FP32 as they lie, where Inf and NaN follow the usual rules.
  * (BF16 and F16 follow the usual rules for Inf and NaN.)  Results do not
  * depend on the order in which blocks run. */
 #define OZGEMM_F64  0

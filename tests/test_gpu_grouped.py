@@ -87,6 +87,10 @@ SHAPES = [
     ([3] * 70 + [0] * 60 + [5] * 5, 40, 72),   # more groups than a wavefront has lanes
     ([513], 777, 131),
     ([40, 1000, 8], 2, 3),
+    # past what the kernels for few columns and small outer products take
+    ([9000, 0, 1, 8001, 77], 777, 515),
+    ([97, 0, 130] * 40, 648, 712),
+    ([301, 2, 240] * 30, 649, 713),
 ]
 
 
@@ -114,10 +118,10 @@ def test_results_in_single_precision(dtype):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-def test_whole_numbers_are_exact(dtype):
-    # f32 entries of 13 bits need both slices; |sums| <= 600 x 4097 x 2 < 2^24
+@pytest.mark.parametrize("sizes, m, q", [([70, 0, 333, 13], 200, 600), ([500, 0, 700, 313], 1100, 601)])
+def test_whole_numbers_are_exact(sizes, m, q, dtype):
+    # f32 entries of 13 bits need both slices; |sums| <= 1100 x 4097 x 2 < 2^24
     g = torch.Generator(device="cuda").manual_seed(1)
-    sizes, m, q = [70, 0, 333, 13], 200, 600
     n = sum(sizes)
     off = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device="cuda")
     sign = torch.randint(0, 2, (n, q), generator=g, device="cuda") * 2 - 1
@@ -135,9 +139,10 @@ def test_whole_numbers_are_exact(dtype):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-def test_rows_of_no_group_are_left_alone(dtype):
-    X, W, dY, off = draw([20, 0, 45], 96, 80, TYPES[dtype], 5, before=7, behind=30)
-    Y = torch.full((X.shape[0], 96), 7.5, device="cuda", dtype=X.dtype)
+@pytest.mark.parametrize("sizes, m, q", [([20, 0, 45], 96, 80), ([4001, 0, 13050], 1037, 579)])
+def test_rows_of_no_group_are_left_alone(sizes, m, q, dtype):
+    X, W, dY, off = draw(sizes, m, q, TYPES[dtype], 5, before=7, behind=30)
+    Y = torch.full((X.shape[0], m), 7.5, device="cuda", dtype=X.dtype)
     dX = torch.full(X.shape, 7.5, device="cuda", dtype=X.dtype)
     oz.grouped_linear(X, W, off, out=Y)
     _, dW = oz.grouped_linear_grads(dY, X, W, off, dX=dX)
@@ -146,10 +151,11 @@ def test_rows_of_no_group_are_left_alone(dtype):
     check_all(X, W, dY, off, Y, dX, dW)
 
 
-def test_rows_of_no_group_are_not_read_into_results():
+@pytest.mark.parametrize("sizes, m, q", [([20, 1, 45], 96, 80), ([20, 1, 45], 95, 79), ([4001, 1, 13050], 1037, 579)])
+def test_rows_of_no_group_are_not_read_into_results(sizes, m, q):
     # what lies around the groups is NaN: no result may see it
     for dtype in TYPES.values():
-        X, W, dY, off = draw([20, 1, 45], 96, 80, dtype, 6, before=9, behind=31)
+        X, W, dY, off = draw(sizes, m, q, dtype, 6, before=9, behind=31)
         for t in (X, dY):
             t[:9] = float("nan")
             t[-31:] = float("nan")
@@ -175,15 +181,15 @@ def test_neighbouring_rows_and_groups_do_not_meet():
 
 
 def test_infinities():
-    # the usual rules, but for f32 in slices: there a row with an infinity makes its results NaN
-    for n, q in ((4, 64), (300, 64), (4, 66), (20000, 128)):
+    # the usual rules, but for f32 in slices (many rows): there a row with an infinity makes its results NaN
+    for n, q in ((4, 64), (300, 64), (4, 65), (200000, 128), (200000, 67)):
         X = torch.ones(n, q, device="cuda")
         W = torch.ones(1, 8, q, device="cuda")
         X[1, 3] = float("inf")
         off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
         for dtype in (torch.bfloat16, torch.float16, torch.float32):
             Y = oz.grouped_linear(X.to(dtype), W.to(dtype), off)
-            if dtype == torch.float32 and (q % 4 or n > 10000):
+            if dtype == torch.float32 and n > 100000:
                 assert torch.isnan(Y[1]).all()
             else:
                 assert torch.isinf(Y[1]).all()
@@ -191,8 +197,8 @@ def test_infinities():
 
 
 def test_f32_range():
-    # rows far apart in size, subnormal rows and the largest; q: as they lie, and in slices (whose grids follow each row)
-    for n, q in ((6, 96), (300, 96), (6, 98), (20000, 96)):
+    # rows far apart in size, subnormal rows and the largest; as they lie, and in slices (whose grids follow each row)
+    for n, q in ((6, 96), (300, 96), (6, 97), (200000, 96), (200000, 97)):
         g = torch.Generator(device="cuda").manual_seed(2)
         X = torch.randn(n, q, generator=g, device="cuda")
         X[:6] *= torch.tensor([1e-40, 1e-30, 1.0, 1e30, 3e37, 0.0], device="cuda")[:, None]
@@ -305,18 +311,42 @@ def test_gradients_against_differences():
 
 
 def test_a_given_workspace():
-    X, W, _, off = draw([33, 60], 50, 70, torch.float32, 16)
-    need = L.ozgemm_grouped_gemm_workspace_bytes(L.OZGEMM_F32, 2, 50, 93, 70, 1, W, 70, 3500, X, 70)
+    X, W, _, off = draw([33, 100000], 50, 70, torch.float32, 16)
+    sizes = (2, 50, 100033, 70, 1, W, 70, 3500, X, 70)
+    need = L.ozgemm_grouped_gemm_workspace_bytes(L.OZGEMM_F32, *sizes)
+    assert need > 0
     ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
-    Y = torch.empty(93, 50, device="cuda")
-    L.ozgemm_grouped_gemm(L.OZGEMM_F32, L.OZGEMM_F32, 2, 50, 93, 70, 1, W, 70, 3500, X, 70, off, Y, 50,
-                          workspace=ws[:need])
+    Y = torch.empty(100033, 50, device="cuda")
+    L.ozgemm_grouped_gemm(L.OZGEMM_F32, L.OZGEMM_F32, *sizes, off, Y, 50, workspace=ws[:need])
     assert torch.equal(Y, oz.grouped_linear(X, W, off))
     assert (ws[need:] == 0x5A).all()
     with pytest.raises(L.OzgemmError) as e:
-        L.ozgemm_grouped_gemm(L.OZGEMM_F32, L.OZGEMM_F32, 2, 50, 93, 70, 1, W, 70, 3500, X, 70, off, Y, 50,
-                              workspace=ws[:need - 1])
+        L.ozgemm_grouped_gemm(L.OZGEMM_F32, L.OZGEMM_F32, *sizes, off, Y, 50, workspace=ws[:need - 1])
     assert e.value.status == L.OZGEMM_WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("layout", ["mq", "qm"])
+@pytest.mark.parametrize("sizes, m, q", [([9, 0, 30], 37, 45), ([1], 8, 1025), ([70, 3], 130, 7), ([5, 40], 3, 66),
+                                         ([33, 1], 515, 264), ([600], 129, 131)])
+def test_rows_off_the_16_byte_grid(sizes, m, q, layout, dtype):
+    # every operand begins one entry into rows of its own length + 3; what lies between them is NaN
+    def inside(t):
+        wide = torch.full((*t.shape[:-1], t.shape[-1] + 3), float("nan"), device="cuda", dtype=t.dtype)
+        wide[..., 1:-2] = t
+        return wide[..., 1:-2]
+
+    X, W, dY, off = draw(sizes, m, q, TYPES[dtype], m + 2 * q)
+    if layout == "qm":
+        W = inside(W.transpose(1, 2)).transpose(1, 2)
+    else:
+        W = inside(W)
+    X, dY = inside(X), inside(dY)
+    Y, dX, dW = inside(dY.new_zeros(X.shape[0], m)), inside(torch.zeros_like(X)), torch.empty_like(W)
+    oz.grouped_linear(X, W, off, out=Y)
+    oz.grouped_linear_grads(dY, X, W, off, dX=dX)
+    _, dW = oz.grouped_linear_grads(dY, X, W, off)
+    check_all(X, W, dY, off, Y, dX, dW)
 
 
 @pytest.mark.parametrize("layout", ["mq", "qm"])
@@ -385,7 +415,9 @@ def test_every_tile_of_the_weights_gradient_is_written(dtype, groups, m, q):
 
 @pytest.mark.parametrize("dtype, sizes, m, q", [("bf16", [3000], 64, 96), ("f16", [1500, 0, 2600, 40], 40, 136),
                                                 ("f32", [5000, 3], 72, 130), ("bf16", [9000], 33, 257),
-                                                ("f32", [70, 2000, 0, 1100], 128, 64)])
+                                                ("f32", [70, 2000, 0, 1100], 128, 64),
+                                                ("bf16", [30000, 0, 9000], 512, 264), ("f32", [40000], 500, 260),
+                                                ("f16", [33000], 511, 257)])
 def test_weights_gradient_summed_in_parts(dtype, sizes, m, q):
     X, W, dY, off = draw(sizes, m, q, TYPES[dtype], m * q, before=5, behind=7)
     X[:5], dY[-7:] = float("nan"), float("nan")
@@ -399,7 +431,8 @@ def test_weights_gradient_summed_in_parts(dtype, sizes, m, q):
 @pytest.mark.parametrize("layout", ["mq", "qm"])
 @pytest.mark.parametrize("dtype, sizes, m, q", [("bf16", [300, 0, 200], 96, 4096), ("f16", [700], 33, 1601),
                                                 ("f32", [100, 40], 72, 2000), ("f32", [1], 24, 4096),
-                                                ("f32", [0, 130, 61], 200, 1090), ("bf16", [999], 264, 2056)])
+                                                ("f32", [0, 130, 61], 200, 1090), ("bf16", [999], 264, 2056),
+                                                ("bf16", [256], 2048, 32768), ("f16", [300, 212], 1030, 8190)])
 def test_products_summed_in_parts(dtype, sizes, m, q, layout):
     X, W, dY, off = draw(sizes, m, q, TYPES[dtype], m * q + 1, before=6, behind=4)
     X[:6], X[-4:] = float("nan"), float("inf")

@@ -33,13 +33,17 @@ def outer(type=L.OZGEMM_BF16, ctype=None, groups=4, m=64, q=128, n=100, A=A, lda
     (dict(groups=L.OZGEMM_GROUPS_MAX + 1), L.OZGEMM_RANGE),
     (dict(type=L.OZGEMM_F32, n=100000), -16), (dict(type=L.OZGEMM_F32, n=100000, ws=WS + 16, nbytes=1 << 30), -16),
     (dict(type=L.OZGEMM_F32, n=100000, ws=WS, nbytes=1000), L.OZGEMM_WORKSPACE_TOO_SMALL),
-    (dict(type=L.OZGEMM_F32, A=A + 4), -16), (dict(type=L.OZGEMM_F32, transa=0, n=100000), -16),
-    (dict(type=L.OZGEMM_F32, ldb=129), -16), (dict(type=L.OZGEMM_F32, q=126), -16),
-    (dict(ldb=129), -16), (dict(A=A + 2), -16), (dict(B=B + 8), -16),
+    (dict(type=L.OZGEMM_F32, A=A + 4, n=100000), -16), (dict(type=L.OZGEMM_F32, transa=0, n=100000), -16),
+    (dict(type=L.OZGEMM_F32, ldb=129, n=100000), -16), (dict(q=126, n=100000), -16),
+    (dict(ldb=129, n=100000), -16), (dict(A=A + 2, n=100000), -16), (dict(B=B + 8, n=100000), -16),
     (dict(m=0), 0), (dict(n=0), 0), (dict(groups=0), 0), (dict(m=0, A=None, B=None, off=None, C=None), 0),
 ])
 def test_grouped_gemm_refusals(change, status):
     assert gemm(**change) == status
+
+
+# too many entries for the kernel that reads any operands as they lie
+WIDE = dict(q=20000, n=10000, ldb=20000, stridec=64 * 20000)
 
 
 @pytest.mark.parametrize("change, status", [
@@ -48,8 +52,9 @@ def test_grouped_gemm_refusals(change, status):
     (dict(ldb=127), -10), (dict(off=None), -11), (dict(C=None), -12), (dict(ldc=63), -13),
     (dict(stridec=64 * 128 - 1), -14), (dict(stridec=-1, groups=1), -14), (dict(C=A), -12), (dict(C=B), -12),
     (dict(C=O + 4), -12), (dict(n=L.OZGEMM_MAX_ROWS + 1), L.OZGEMM_RANGE),
-    (dict(type=L.OZGEMM_F32), -15), (dict(type=L.OZGEMM_F32, ws=WS, nbytes=1000), L.OZGEMM_WORKSPACE_TOO_SMALL),
-    (dict(A=A + 2), -15), (dict(ldb=129), -15),
+    (dict(type=L.OZGEMM_F32, **WIDE), -15),
+    (dict(type=L.OZGEMM_F32, ws=WS, nbytes=1000, **WIDE), L.OZGEMM_WORKSPACE_TOO_SMALL),
+    (dict(WIDE, A=A + 2), -15), (dict(WIDE, ldb=20001), -15),
     # 2^21 columns, each group's rounded up to 64: the rows of the slices would pass 32-bit offsets
     (dict(type=L.OZGEMM_F32, n=2090000, groups=1000, C=P + (40 << 34)), L.OZGEMM_RANGE),
     (dict(m=0), 0), (dict(q=0), 0), (dict(groups=0), 0),
@@ -61,20 +66,21 @@ def test_grouped_outer_refusals(change, status):
 def test_workspace_bytes():
     w = L.ozgemm_grouped_gemm_workspace_bytes
     assert w(L.OZGEMM_BF16, 4, 64, 100, 128, 1, A, 128, 64 * 128, B, 128) == 0  # read in place
-    assert w(L.OZGEMM_BF16, 4, 64, 100, 128, 1, A + 2, 128, 64 * 128, B, 128) >= 4 * 64 * 128 * 2
-    assert w(L.OZGEMM_BF16, 4, 64, 100, 129, 1, A, 136, 64 * 136, B, 136) >= (4 * 64 + 100) * 192 * 2
+    assert w(L.OZGEMM_BF16, 4, 64, 100, 128, 1, A + 2, 128, 64 * 128, B, 128) == 0  # so are few columns wherever they lie
+    assert w(L.OZGEMM_BF16, 4, 64, 100000, 128, 1, A + 2, 128, 64 * 128, B, 128) >= 4 * 64 * 128 * 2
+    assert w(L.OZGEMM_BF16, 4, 64, 100000, 129, 1, A, 136, 64 * 136, B, 136) >= (4 * 64 + 100000) * 192 * 2
     assert w(L.OZGEMM_F32, 4, 64, 100000, 128, 1, A, 128, 64 * 128, B, 128) >= (4 * 64 + 100000) * (128 * 4 + 4)
-    assert w(L.OZGEMM_F32, 4, 64, 100, 128, 1, A, 128, 64 * 128, B, 128) == 0  # few columns are read as they lie
+    assert w(L.OZGEMM_F32, 4, 64, 100, 128, 1, A, 128, 64 * 128, B, 128) == 0
     assert w(L.OZGEMM_F32, 4, 64, 100, 128, 0, A, 64, 64 * 128, B, 128) == 0
-    assert w(L.OZGEMM_F32, 4, 64, 100, 128, 0, A + 4, 64, 64 * 128, B, 128) >= (4 * 64 + 100) * (128 * 4 + 4)
     assert w(L.OZGEMM_F64, 4, 64, 100, 128, 1, A, 128, 64 * 128, B, 128) == 0
     assert w(L.OZGEMM_F32, 4, 64, 0, 128, 1, A, 128, 64 * 128, B, 128) == 0
     # sizes past 32 bits
-    assert w(L.OZGEMM_F32, 64, 1 << 15, 1, 1 << 15, 1, A + 4, 1 << 15, 1 << 30, B, 1 << 15) >= 1 << 38
+    assert w(L.OZGEMM_F32, 64, 1 << 15, 1 << 15, 1 << 15, 1, A, 1 << 15, 1 << 30, B, 1 << 15) >= 1 << 38
     o = L.ozgemm_grouped_outer_workspace_bytes
     assert o(L.OZGEMM_F16, 4, 64, 128, 100, A, 64, B, 128) == 0
-    assert o(L.OZGEMM_F16, 4, 60, 128, 100, A, 64, B, 128) >= (60 + 128) * 100 * 2
-    assert o(L.OZGEMM_F32, 4, 64, 128, 100, A, 64, B, 128) >= (64 + 128) * 100 * 4
+    assert o(L.OZGEMM_F16, 4, 60, 128, 100, A, 64, B, 128) == 0
+    assert o(L.OZGEMM_F16, 4, 60, 20000, 10000, A, 64, B, 20000) >= (60 + 20000) * 10000 * 2
+    assert o(L.OZGEMM_F32, 4, 64, 20000, 10000, A, 64, B, 20000) >= (64 + 20000) * 10000 * 4
 
 
 def _args(**change):
