@@ -682,18 +682,22 @@ __global__ __launch_bounds__(512, 2) void few_outer_kernel(Grouped16 g) {
     g.C = (char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2);
   }
   const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
+  const int waves = max(min((to - from + STEP - 1) / STEP, WAVES), 1);  // the others had no columns
 #pragma unroll
   for (int w = 0; w < R; ++w) {
+    if (wave < waves) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      *reinterpret_cast<v4f*>(&sums[wave][lane & 15][(4 * (lane >> 4) + r) * R]) =
-          v4f{acc[w][0][r], acc[w][1][r], acc[w][2][r], acc[w][3][r]};
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<v4f*>(&sums[wave][lane & 15][(4 * (lane >> 4) + r) * R]) =
+            v4f{acc[w][0][r], acc[w][1][r], acc[w][2][r], acc[w][3][r]};
+    }
     __syncthreads();
     const int r = threadIdx.x % (FEW_OUTER / 4) * 4, c = threadIdx.x / (FEW_OUTER / 4);
     if (c < 16 && q0 + c * R + w < g.q && m0 + r < g.m) {
       v4f v = *reinterpret_cast<const v4f*>(&sums[0][c][r]);
 #pragma unroll
-      for (int x = 1; x < WAVES; ++x) v += *reinterpret_cast<const v4f*>(&sums[x][c][r]);
+      for (int x = 1; x < WAVES; ++x)
+        if (x < waves) v += *reinterpret_cast<const v4f*>(&sums[x][c][r]);
       store4(g, q0 + c * R + w, m0 + r, wide, v);
     }
     __syncthreads();
@@ -817,13 +821,14 @@ int outer_parts(bool f32, int groups, int m, int q, int n) {
 // that of its 64 x 64 tiles' columns, 2^20 of them 30 us in 16 bits, 45 to 75
 // off the 8-byte grid, 105 in f32, and 6 at least; the tiles take a launch of
 // each copy, exponent and sum in parts, 11 to 30 us with hardly any columns.
+// Its blocks take 4 us each at the least, to look up, to start and to add.
 //   16-bit   8 of 256 x 256, 4096 rows 7 / 20;  1 of 1024 x 1024, 4096 rows 30 / 38, 32768 162 / 156
 //   copied   8 of 255 x 255, 4096 rows 10 / 53;  1 of 1023 x 1023, 4096 rows 56 / 73, 32768 809 / 242
 //   f32      8 of 256 x 256, 4096 rows 15 / 50;  1 of 1024 x 1024, 4096 rows 106 / 107;
 //            4 of 1023 x 511, 4096 rows 60 / 77, 32768 493 / 394
-int few_outer_parts(bool f32, int groups, int m, int q, int n) {
+int few_outer_parts(bool f32, bool edge, int groups, int m, int q, int n) {
   const long blocks = few_outer_blocks(groups, m, q), each = std::max(((long)n + groups - 1) / groups, 1L);
-  if (blocks > (1L << 20) / each) return 0;
+  if (blocks > std::min((1L << 20) / each, f32 || edge ? 1536L : 1024L)) return 0;
   const long chunks = (each + (f32 ? 127 : 255)) / (f32 ? 128 : 256);
   return (int)std::max(std::min({512 / blocks, chunks / 4, 32L}), 1L);
 }

@@ -92,7 +92,7 @@ Rooms outer_rooms(int type, int groups, int m, int q, int n, const void* A, int 
   const bool f32 = type == OZGEMM_F32;
   const int run = f32 ? 4 : 8;
   r.edge = !aligned16(A, lda, 0, run) || !aligned16(B, ldb, 0, run) || m % run != 0 || q % run != 0;
-  if (m > 0 && q > 0 && groups > 0) r.few = few_outer_parts(f32, groups, m, q, n);
+  if (m > 0 && q > 0 && groups > 0) r.few = few_outer_parts(f32, r.edge, groups, m, q, n);
   const bool in_place = r.few || (!f32 && !r.edge);
   const bool any = m > 0 && n > 0 && q > 0 && groups > 0;
   // every group's columns begin at a multiple of 64

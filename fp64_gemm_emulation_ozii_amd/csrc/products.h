@@ -58,7 +58,7 @@ size_t gemm_partial_bytes(int parts, int m, int n);
 int outer_parts(bool f32, int groups, int m, int q, int n);
 size_t outer_partial_bytes(int parts, int groups, int m, int q);
 // The same for the kernel for small outer products.
-int few_outer_parts(bool f32, int groups, int m, int q, int n);
+int few_outer_parts(bool f32, bool edge, int groups, int m, int q, int n);
 // C_e (m x q) = sum over j in J_e: A's and B's inner dimension is the n columns.
 hipError_t launch_grouped_k(const Grouped16& g, hipStream_t st);
 
