@@ -32,13 +32,13 @@ __device__ __forceinline__ float unscale(float x, int ea, int eb) {
   return __builtin_ldexpf(x, ea + eb - 30);
 }
 
-// Four consecutive rows of a column of C, `wide` where they can be stored as one.
-__device__ __forceinline__ void store4(const Grouped16& g, long col, int row, bool wide, v4f v) {
+// Four consecutive rows of a column of C.
+__device__ __forceinline__ void store4(const Grouped16& g, long col, int row, v4f v) {
   const long to = col * g.ldc + row;
   if (g.ctype == OZGEMM_F32) {
     float* out = (float*)g.C + to;
-    if (wide && row + 4 <= g.m) {
-      *reinterpret_cast<v4f*>(out) = v;
+    if (row + 4 <= g.m) {
+      *reinterpret_cast<v4f_any*>(out) = v;
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -49,8 +49,8 @@ __device__ __forceinline__ void store4(const Grouped16& g, long col, int row, bo
 #pragma unroll
     for (int k = 0; k < 4; ++k) h[k] = (short)round16(v[k], g.ctype);
     short* out = (short*)g.C + to;
-    if (wide && row + 4 <= g.m) {
-      *reinterpret_cast<v4s*>(out) = h;
+    if (row + 4 <= g.m) {
+      *reinterpret_cast<v4s_any*>(out) = h;
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -84,13 +84,10 @@ struct Store {
   // 16-byte stores of every wavefront, in STORES, where every lane stores
   // every run of a tile; 0 where some do not.
   static __device__ __forceinline__ int stores(const Target& t, int bm, int bn) {
-    const bool all = aligned(t) && t.m0 + bm <= t.m && t.n0 + bn <= t.n_end;
+    const bool all = t.m0 + bm <= t.m && t.n0 + bn <= t.n_end;
     return !all ? 0 : t.ctype == OZGEMM_F32 ? 2 : 1;
   }
   static constexpr int STORES = Tile::FN * CH;
-  static __device__ __forceinline__ bool aligned(const Target& t) {
-    return (t.ldc & 7) == 0 && ((uintptr_t)t.C & 15) == 0;
-  }
 
   static __device__ __forceinline__ void run(const v4f (&acc)[Tile::FM][Tile::FN], char* smem, const Target& t) {
     const int lane = threadIdx.x & 63;
@@ -98,7 +95,6 @@ struct Store {
     float* stage = reinterpret_cast<float*>(smem) + wave * 16 * PITCH;
     const int mw = t.m0 + Tile::wave_m(wave) * WTM, nw = t.n0 + Tile::wave_n(wave) * (Tile::FN * 16);
     const int size = t.ctype == OZGEMM_F32 ? 4 : 2;
-    const bool wide = aligned(t);
     // a lane's runs all begin at the same row
     static_assert(64 % RUNS == 0, "a lane keeps its rows");
     const int row = mw + lane % RUNS * 8;
@@ -132,11 +128,11 @@ struct Store {
           for (int k = 0; k < 8; ++k) v[k] = unscale(v[k], ea[k], eb[ch]);
         }
         char* out = (char*)t.C + ((long)col * t.ldc + row) * size;
-        const bool all = wide && row + 8 <= t.m;
+        const bool all = row + 8 <= t.m;
         if (t.ctype == OZGEMM_F32) {
           if (all) {
-            *reinterpret_cast<v4f*>(out) = v4f{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<v4f*>(out + 16) = v4f{v[4], v[5], v[6], v[7]};
+            *reinterpret_cast<v4f_any*>(out) = v4f{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<v4f_any*>(out + 16) = v4f{v[4], v[5], v[6], v[7]};
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -147,7 +143,7 @@ struct Store {
 #pragma unroll
           for (int k = 0; k < 8; ++k) h[k] = (short)round16(v[k], t.ctype);
           if (all) {
-            *reinterpret_cast<v8s*>(out) = h;
+            *reinterpret_cast<v8s_any*>(out) = h;
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -265,7 +261,6 @@ __global__ __launch_bounds__(256) void join_columns_kernel(Grouped16 g) {
   const GroupIndex index(g.offsets, g.groups, g.n, 64);
   if ((int)blockIdx.x >= index.total) return;
   const GroupTile gt = index.find(blockIdx.x);
-  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
   const int row = blockIdx.y * 64 + (threadIdx.x & 15) * 4;
   if (row >= g.m) return;
   for (int col = gt.begin + (threadIdx.x >> 4); col < min(gt.end, gt.begin + 64); col += 16) {
@@ -275,7 +270,7 @@ __global__ __launch_bounds__(256) void join_columns_kernel(Grouped16 g) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] += row + k < g.m ? from[k] : 0.f;
     }
-    store4(g, col, row, wide, v);
+    store4(g, col, row, v);
   }
 }
 
@@ -478,7 +473,6 @@ __global__ __launch_bounds__(512, 2) void few_columns_kernel(Grouped16 g) {
       }
     }
   }
-  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
 #pragma unroll
   for (int c = 0; c < CF; ++c) {
     if (c >= frags) break;
@@ -491,7 +485,7 @@ __global__ __launch_bounds__(512, 2) void few_columns_kernel(Grouped16 g) {
       v4f v = *reinterpret_cast<const v4f*>(&sums[0][col][r]);
 #pragma unroll
       for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const v4f*>(&sums[w][col][r]);
-      store4(g, n0 + c * 16 + col, m0 + r, wide, v);
+      store4(g, n0 + c * 16 + col, m0 + r, v);
     }
     __syncthreads();
   }
@@ -555,7 +549,6 @@ __global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
       }
     }
   }
-  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
 #pragma unroll
   for (int c = 0; c < CF; ++c) {
     if (c >= frags) break;
@@ -571,7 +564,7 @@ __global__ __launch_bounds__(512, 2) void few_columns_ks_kernel(Grouped16 g) {
       v4f v = *reinterpret_cast<const v4f*>(&sums[0][col][r]);
 #pragma unroll
       for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const v4f*>(&sums[w][col][r]);
-      store4(g, n0 + c * 16 + col, m0 + r, wide, v);
+      store4(g, n0 + c * 16 + col, m0 + r, v);
     }
     __syncthreads();
   }
@@ -681,7 +674,6 @@ __global__ __launch_bounds__(512, 2) void few_outer_kernel(Grouped16 g) {
   } else {
     g.C = (char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2);
   }
-  const bool wide = (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0;
   const int waves = max(min((to - from + STEP - 1) / STEP, WAVES), 1);  // the others had no columns
 #pragma unroll
   for (int w = 0; w < R; ++w) {
@@ -698,7 +690,7 @@ __global__ __launch_bounds__(512, 2) void few_outer_kernel(Grouped16 g) {
 #pragma unroll
       for (int x = 1; x < WAVES; ++x)
         if (x < waves) v += *reinterpret_cast<const v4f*>(&sums[x][c][r]);
-      store4(g, q0 + c * R + w, m0 + r, wide, v);
+      store4(g, q0 + c * R + w, m0 + r, v);
     }
     __syncthreads();
   }
@@ -723,7 +715,7 @@ __global__ __launch_bounds__(256) void join_parts_kernel(Grouped16 g) {
       v[k] = unscale(v[k], g.A.ex[e * g.A.ex_batch + min(row + k, g.m - 1)], g.B.ex[e * g.B.ex_batch + col]);
   }
   g.C = (char*)g.C + (size_t)e * g.cbatch * (g.ctype == OZGEMM_F32 ? 4 : 2);
-  store4(g, col, row, (g.ldc & 3) == 0 && ((uintptr_t)g.C & 15) == 0, v);
+  store4(g, col, row, v);
 }
 
 hipError_t join_parts(const Grouped16& g, hipStream_t st) {

@@ -62,14 +62,14 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
   return ((part[0] + part[1]) + (part[2] + part[3]));
 }
 
-// Eight entries next to each other, as FP64 (16-byte loads where `wide`).
+// Eight entries next to each other.
 template <int TYPE>
-__device__ __forceinline__ void load8(const void* p, long at, int left, bool wide, float (&v)[8]) {
+__device__ __forceinline__ void load8(const void* p, long at, int left, float (&v)[8]) {
   if (TYPE == OZGEMM_F32) {
     const float* q = (const float*)p + at;
-    if (wide && left >= 8) {
-      *reinterpret_cast<v4f*>(v) = *reinterpret_cast<const v4f*>(q);
-      *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f*>(q + 4);
+    if (left >= 8) {
+      *reinterpret_cast<v4f*>(v) = *reinterpret_cast<const v4f_any*>(q);
+      *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f_any*>(q + 4);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = e < left ? q[e] : 0.f;
@@ -77,8 +77,8 @@ __device__ __forceinline__ void load8(const void* p, long at, int left, bool wid
   } else {
     const short* q = (const short*)p + at;
     v8s h = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (wide && left >= 8) {
-      h = *reinterpret_cast<const v8s*>(q);
+    if (left >= 8) {
+      h = *reinterpret_cast<const v8s_any*>(q);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -92,12 +92,12 @@ __device__ __forceinline__ void load8(const void* p, long at, int left, bool wid
 }
 
 template <class V>
-__device__ __forceinline__ void store8(void* p, int type, long at, int left, bool wide, const V (&v)[8]) {
+__device__ __forceinline__ void store8(void* p, int type, long at, int left, const V (&v)[8]) {
   if (type == OZGEMM_F32) {
     float* q = (float*)p + at;
-    if (wide && left >= 8) {
-      *reinterpret_cast<v4f*>(q) = v4f{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<v4f*>(q + 4) = v4f{v[4], v[5], v[6], v[7]};
+    if (left >= 8) {
+      *reinterpret_cast<v4f_any*>(q) = v4f{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<v4f_any*>(q + 4) = v4f{v[4], v[5], v[6], v[7]};
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -110,17 +110,13 @@ __device__ __forceinline__ void store8(void* p, int type, long at, int left, boo
   for (int e = 0; e < 8; ++e)
     h[e] = type == OZGEMM_BF16 ? __builtin_bit_cast(short, (__bf16)v[e]) : __builtin_bit_cast(short, (_Float16)v[e]);
   short* q = (short*)p + at;
-  if (wide && left >= 8) {
-    *reinterpret_cast<v8s*>(q) = h;
+  if (left >= 8) {
+    *reinterpret_cast<v8s_any*>(q) = h;
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (e < left) q[e] = h[e];
   }
-}
-
-__device__ __forceinline__ bool wide_rows(const void* G, long base, long ld, int size) {
-  return ((uintptr_t)G & 15) == 0 && base * size % 16 == 0 && ld * size % 16 == 0;
 }
 
 // Sums of squares in FP64 (no square of an FP32 value leaves its range):
@@ -131,7 +127,6 @@ __global__ __launch_bounds__(256) void square_sum_kernel(const void* __restrict_
                                                          long batch, double* __restrict__ part) {
   __shared__ double s[4];
   const long base = blockIdx.y * batch;
-  const bool wide = wide_rows(G, base, ld, TYPE == OZGEMM_F32 ? 4 : 2);
   const int per = (cols + 2047) / 2048, pieces = rows * per;
   // narrow rows: each wavefront takes a row of its own
   const bool narrow = cols <= 512;
@@ -152,7 +147,7 @@ __global__ __launch_bounds__(256) void square_sum_kernel(const void* __restrict_
         for (int e = 0; e < 8; ++e)
           if (e < left) sum = __builtin_fma(q[e], q[e], sum);
       } else {
-        load8<TYPE>(G, base + r * ld + c, left, wide, v[u]);
+        load8<TYPE>(G, base + r * ld + c, left, v[u]);
       }
     }
     if (TYPE != OZGEMM_F64) {
@@ -218,7 +213,6 @@ __global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
   const long b = blockIdx.y;
   const double f = inverse_norm(p.part, p.parts, b, p.eps, s) * p.scale;
   const long plane = (long)p.rows_pad * p.cols_pad, base = b * p.batch;
-  const bool wide = wide_rows(p.G, base, p.ld, TYPE == OZGEMM_F32 ? 4 : 2);
   const int per = p.cols_pad / 8, runs = (int)(plane / 8);
 #pragma unroll
   for (int i = 0; i < PREPARE_RUNS; ++i) {
@@ -226,7 +220,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
     if (i >= p.each || at >= runs) return;
     const int r = at / per, c = (at - r * per) * 8;
     float v[8];
-    load8<TYPE>(p.G, base + r * p.ld + c, r < p.rows ? p.cols - c : 0, wide, v);
+    load8<TYPE>(p.G, base + r * p.ld + c, r < p.rows ? p.cols - c : 0, v);
     v8s h, l;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -341,7 +335,7 @@ __device__ __forceinline__ void step_tile(const Step& p, char* smem, long b, int
         const int col = nw + j * 16 + c, row = mw + r;
         if (col < p.on) {
           const long to = b * p.batcho + (long)col * p.ldo + row;
-          store8(p.O, p.otype, to, p.om - row, wide_rows(p.O, to, 0, p.otype == OZGEMM_F32 ? 4 : 2), v);
+          store8(p.O, p.otype, to, p.om - row, v);
         }
         continue;
       }

@@ -20,6 +20,7 @@
 // K-strided, 8192 x 2048: 28 us for the slices and 14 + 5 for the exponents.
 #include "groups.h"
 #include "products.h"
+#include "tile16.h"
 
 namespace oz {
 
@@ -36,32 +37,28 @@ __device__ __forceinline__ int exponent32(uint32_t b) {
 // Four entries next to each other as 32-bit patterns (16-bit types travel as
 // they are), zeros past `left`.
 template <int TYPE>
-__device__ __forceinline__ void load4(const void* src, long at, int left, bool wide, uint32_t (&v)[4]) {
+__device__ __forceinline__ void load4(const void* src, long at, int left, uint32_t (&v)[4]) {
   if (TYPE == OZGEMM_F32) {
     const uint32_t* p = (const uint32_t*)src + at;
-    if (wide && left >= 4) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    if (left >= 4) {
+      const v4u x = *reinterpret_cast<const v4u_any*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = x[i];
       return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0;
   } else {
     const uint16_t* p = (const uint16_t*)src + at;
-    if (wide && left >= 4) {
-      const uint2 x = *reinterpret_cast<const uint2*>(p);
-      v[0] = x.x & 0xffffu, v[1] = x.x >> 16, v[2] = x.y & 0xffffu, v[3] = x.y >> 16;
+    if (left >= 4) {
+      const v4s x = *reinterpret_cast<const v4s_any*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = (uint16_t)x[i];
       return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0;
   }
-}
-
-// Whether every run of four that begins at a multiple of four of a row lies aligned.
-template <int TYPE>
-__device__ __forceinline__ bool wide_runs(const void* src, long base, long ld) {
-  return ((uintptr_t)src & (TYPE == OZGEMM_F32 ? 15 : 7)) == 0 && (base & 3) == 0 && (ld & 3) == 0;
 }
 
 // hi in the low half, lo in the high one (16-bit types: the entry itself)
@@ -102,7 +99,6 @@ __global__ __launch_bounds__(256) void slice_rows_kernel(const void* __restrict_
   const int lane = threadIdx.x & 63;
   if (row >= total) return;
   const long from = row / rows * sbatch + row % rows * ld;
-  const bool wide = wide_runs<TYPE>(src, sbatch, ld);
   uint16_t* out = dst + row * dld;
   const int Kp = (K + 63) / 64 * 64;
   uint32_t v[RUNS][4];
@@ -110,7 +106,7 @@ __global__ __launch_bounds__(256) void slice_rows_kernel(const void* __restrict_
   const bool once = Kp <= 256 * RUNS;
   for (int k0 = 0; k0 < Kp; k0 += 256 * RUNS) {
 #pragma unroll
-    for (int i = 0; i < RUNS; ++i) load4<TYPE>(src, from + k0 + i * 256 + lane * 4, K - k0 - i * 256 - lane * 4, wide, v[i]);
+    for (int i = 0; i < RUNS; ++i) load4<TYPE>(src, from + k0 + i * 256 + lane * 4, K - k0 - i * 256 - lane * 4, v[i]);
     if (TYPE != OZGEMM_F32) {
 #pragma unroll
       for (int i = 0; i < RUNS; ++i)
@@ -130,7 +126,7 @@ __global__ __launch_bounds__(256) void slice_rows_kernel(const void* __restrict_
   for (int k0 = 0; k0 < Kp; k0 += 256 * RUNS) {
     if (!once) {
 #pragma unroll
-      for (int i = 0; i < RUNS; ++i) load4<TYPE>(src, from + k0 + i * 256 + lane * 4, K - k0 - i * 256 - lane * 4, wide, v[i]);
+      for (int i = 0; i < RUNS; ++i) load4<TYPE>(src, from + k0 + i * 256 + lane * 4, K - k0 - i * 256 - lane * 4, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < RUNS; ++i)
@@ -169,14 +165,13 @@ __global__ __launch_bounds__(256) void column_max_kernel(const float* __restrict
   if (g.group < 0) return;
   const int lane = threadIdx.x & 63, r = blockIdx.y * 256 + lane * 4;
   const long base = offsets ? 0 : g.group * sbatch;
-  const bool wide = wide_runs<OZGEMM_F32>(src, base, ld);
   uint32_t mx[4] = {0, 0, 0, 0};
   if (r < rows) {
     // eight loads in flight; a k past the end reads the last one again
     for (int k = g.k0 + (threadIdx.x >> 6); k < g.k1; k += 32) {
       uint32_t v[8][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) load4<OZGEMM_F32>(src, base + (long)min(k + 4 * i, g.k1 - 1) * ld + r, rows - r, wide, v[i]);
+      for (int i = 0; i < 8; ++i) load4<OZGEMM_F32>(src, base + (long)min(k + 4 * i, g.k1 - 1) * ld + r, rows - r, v[i]);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -232,13 +227,12 @@ __global__ __launch_bounds__(256) void slice_cols_kernel(const void* __restrict_
   __shared__ int32_t es[64];
   const int r0 = blockIdx.y * 64;
   const long from = offsets ? 0 : g.group * sbatch;
-  const bool wide = wide_runs<TYPE>(src, from, ld);
   const int rr = (threadIdx.x & 15) * 4, kk = threadIdx.x >> 4;
   uint32_t v[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int k = g.k0 + kk + 16 * i;
-    load4<TYPE>(src, from + (long)k * ld + r0 + rr, k < g.k1 ? rows - r0 - rr : 0, wide, v[i]);
+    load4<TYPE>(src, from + (long)k * ld + r0 + rr, k < g.k1 ? rows - r0 - rr : 0, v[i]);
   }
   if (TYPE == OZGEMM_F32) {
     if (threadIdx.x < 64) es[threadIdx.x] = r0 + (int)threadIdx.x < rows ? ex[(long)g.group * rows + r0 + threadIdx.x] : 0;

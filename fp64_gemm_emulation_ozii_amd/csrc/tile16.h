@@ -37,6 +37,15 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
+// Runs of a caller's array that begin at any of its entries: the hardware reads
+// and writes them as one all the same (22720 rows of 1811 results in bf16: 79 us
+// entry by entry where they lie on no 16-byte boundary, 42 so; in f32 158 / 95).
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef v4u v4u_any __attribute__((aligned(4)));
+typedef v4f v4f_any __attribute__((aligned(4)));
+typedef v4s v4s_any __attribute__((aligned(2)));
+typedef v8s v8s_any __attribute__((aligned(2)));
+
 struct Half {
   static constexpr int LANE = 8;  // k per lane of an operand
   typedef uint16_t Entry;
