@@ -9,6 +9,7 @@
 // wavefront-wide scan per 64 groups).  Groups of few columns have kernels of
 // their own, which stream the weights (few_columns_kernel).
 #include <algorithm>
+#include <cmath>
 
 #include "groups.h"
 #include "products.h"
@@ -263,12 +264,17 @@ __global__ __launch_bounds__(256) void join_columns_kernel(Grouped16 g) {
   const GroupTile gt = index.find(blockIdx.x);
   const int row = blockIdx.y * 64 + (threadIdx.x & 15) * 4;
   if (row >= g.m) return;
+  const int32_t* ea = g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr;
   for (int col = gt.begin + (threadIdx.x >> 4); col < min(gt.end, gt.begin + 64); col += 16) {
     v4f v = {0.f, 0.f, 0.f, 0.f};
     for (int p = 0; p < g.parts; ++p) {
       const float* from = g.partial + ((long)p * g.n + col) * g.m + row;
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] += row + k < g.m ? from[k] : 0.f;
+    }
+    if (ea != nullptr) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = unscale(v[k], ea[min(row + k, g.m - 1)], g.B.ex[col]);
     }
     store4(g, col, row, v);
   }
@@ -797,16 +803,34 @@ bool grouped_n_fits(const Grouped16& g) {
   return group_tiles_max(g.n, g.groups, 32) * ((g.m + 15) / 16) <= 0x7fffffffL;  // (parts only where tiles are few)
 }
 
-// Parts of an inner dimension of `slices` slices for `tiles` tiles: those run
-// as quarters while they are no more than half the units (256 on MI355X);
-// below that, parts of at least four slices make up the rest.
-static int parts_for(long tiles, long slices) {
-  return (int)std::max(std::min({256 / (4 * tiles), slices / 4, 32L}), 1L);
+// Parts of an inner dimension of `slices` slices for `tiles` tiles whose result
+// has `entries` entries, from modelled times in us: rounds of whole tiles at
+// 1.4 per slice and 9 besides (f32: 1.2 and 8), a last one of quarters at 0.6
+// and 6 where it is at most half full (share.h; `lone_slice` where they are
+// fewer than the units), and the sums' way through memory at 4 TB/s and a
+// launch.  Measured in us, the rule before (as many parts as quarters had
+// units) / this: outer products of 32768 rows, bf16 1 of 2048 x 2048 555 / 247,
+// 1 of 1024 x 1024 157 / 96, f32 1 of 1024 x 1024 860 / 388 (slices: 230).
+static int parts_for(bool f32, long tiles, long slices, double entries, double lone_slice) {
+  const long units = 256;
+  auto time = [&](long parts) {
+    const long total = tiles * parts, rest = total % units;
+    const double k = ceil((double)slices / parts);
+    const double whole = f32 ? 1.2 * k + 8 : 1.4 * k + 9, quarter = (rest * 4 <= units ? lone_slice : 0.6) * k + 6;
+    const double last = rest == 0 ? 0 : rest * 2 <= units ? quarter * ((4 * rest + units - 1) / units) : whole;
+    return (total / units) * whole + last + (parts > 1 ? 8 + 2 * 4 * entries * parts / 4e6 : 0);
+  };
+  int best = 1;
+  double least = 0.95 * time(1);
+  for (int parts = 2; parts <= 32 && parts * tiles <= 2 * units && parts * 4 <= slices; ++parts)
+    if (time(parts) < least) least = time(best = parts);
+  return best;
 }
 
 int outer_parts(bool f32, int groups, int m, int q, int n) {
   const long tile = f32 ? 128 : 256;
-  return parts_for(((m + tile - 1) / tile) * ((q + tile - 1) / tile) * groups, ((long)n / groups + BK16 - 1) / BK16);
+  return parts_for(f32, ((m + tile - 1) / tile) * ((q + tile - 1) / tile) * groups,
+                   ((long)n / groups + BK16 - 1) / BK16, (double)groups * m * q, 0.6);
 }
 
 // Measured in us (the kernel for small outer products / tiles): its time is
@@ -829,10 +853,11 @@ size_t outer_partial_bytes(int parts, int groups, int m, int q) {
   return parts > 1 ? (size_t)parts * groups * m * q * 4 : 0;
 }
 
-// (In f32 so few tiles are no more than 256 blocks of few_columns_kernel.)
+// (512 rows with 2048 x 2048: 64 quarters take 44 us in one part, 34 in four.)
 int gemm_parts(bool f32, int groups, int m, int n, int q) {
-  if (f32) return 1;
-  return parts_for(group_tiles_max(n, groups, 256) * ((m + 255) / 256), (q + BK16 - 1) / BK16);
+  const long tile = f32 ? 128 : 256;
+  return parts_for(f32, group_tiles_max(n, groups, tile) * ((m + tile - 1) / tile), (q + BK16 - 1) / BK16,
+                   (double)m * n, 1.1);
 }
 
 size_t gemm_partial_bytes(int parts, int m, int n) { return parts > 1 ? (size_t)parts * m * n * 4 : 0; }

@@ -417,7 +417,8 @@ def test_every_tile_of_the_weights_gradient_is_written(dtype, groups, m, q):
                                                 ("f32", [5000, 3], 72, 130), ("bf16", [9000], 33, 257),
                                                 ("f32", [70, 2000, 0, 1100], 128, 64),
                                                 ("bf16", [30000, 0, 9000], 512, 264), ("f32", [40000], 500, 260),
-                                                ("f16", [33000], 511, 257)])
+                                                ("f16", [33000], 511, 257), ("bf16", [33000], 1536, 2048),
+                                                ("f32", [20, 33000], 1024, 1032)])
 def test_weights_gradient_summed_in_parts(dtype, sizes, m, q):
     X, W, dY, off = draw(sizes, m, q, TYPES[dtype], m * q, before=5, behind=7)
     X[:5], dY[-7:] = float("nan"), float("nan")
