@@ -785,6 +785,7 @@ hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
 int few_columns_parts(bool f32, bool edge, bool ks, int groups, int m, int n, int q) {
   const bool copies = f32 || edge;
   const long units = 256, blocks = few_blocks(ks, f32 ? 4 : 8, groups, m, n);
+  if (blocks >= 1L << 23) return 0;  // a launch has fewer than 2^32 threads
   const long frags = std::min<long>((((long)n + groups - 1) / groups + 15) / 16, (ks ? FEW_KS_COLS : FEW_COLS) / 16);
   const long ns = (long)q * (1 + frags) * (f32 ? 2 : 1);
   if (blocks <= units) {

@@ -462,3 +462,23 @@ def test_few_columns_summed_in_parts(dtype, sizes, m, q, layout):
         check_all(X, W, dY, off, Y, None, None)
         assert (out[:3] == 5).all() and (out[-2:] == 5).all()
         assert torch.equal(out, oz.grouped_linear(X, W, off, out=out.clone()))
+
+
+@pytest.mark.parametrize("dtype, sizes, m, q", [("f32", [5, 3], 40, 12288), ("bf16", [300, 212], 1030, 8190),
+                                                ("f32", [20000, 19000], 500, 260), ("f16", [33000, 8], 512, 257)])
+def test_parts_in_a_captured_graph(dtype, sizes, m, q):
+    X, W, dY, off = draw(sizes, m, q, TYPES[dtype], m + q + 3)
+    run = lambda: (oz.grouped_linear(X, W, off), *oz.grouped_linear_grads(dY, X, W, off))  # noqa: E731
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = run()
+    for k in range(3):
+        X.mul_(-1.25)
+        off[1] -= k
+        graph.replay()
+        eager = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(cap, eager))
+        check_all(X, W, dY, off, *cap)
