@@ -23,18 +23,21 @@ def _type_of(t, what: str, allowed=(torch.float32, torch.bfloat16, torch.float16
 
 
 def _no_grad(*tensors) -> None:
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
-        raise RuntimeError("this call is not recorded by autograd: make it under torch.no_grad() and take the "
-                           "gradients from grouped_linear_grads")
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t.requires_grad:
+                raise RuntimeError("this call is not recorded by autograd: make it under torch.no_grad() and take the "
+                                   "gradients from grouped_linear_grads")
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on_device(device):
     """A context in which `device`, a GPU, is the current one."""
     if device.type != "cuda":
         raise ValueError(f"the tensors are on {device}: these products run on the GPU only")
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _fits(*sizes) -> None:
@@ -87,7 +90,7 @@ def _same(a, b, what: str) -> None:
 def _target(out, shape, dtypes, like, what: str):
     """The tensor a result goes to: `out`, checked, or a new one."""
     if out is None:
-        return torch.empty(shape, dtype=dtypes[0], device=like.device)
+        return like.new_empty(shape, dtype=dtypes[0])
     if tuple(out.shape) != tuple(shape) or out.dtype not in dtypes or out.device != like.device:
         raise ValueError(f"{what} must be {tuple(shape)} of {dtypes[0]} on {like.device}, got {tuple(out.shape)} of "
                          f"{out.dtype} on {out.device}")

@@ -132,9 +132,7 @@ def lib():
 
 def _ptr(x):
     """Device pointer of a tensor, an int address, or None (NULL)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
@@ -147,14 +145,27 @@ def _check(status: int, where: str) -> int:
 
 def _stream(stream):
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object: 5 us less per call
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """torch's current stream (the first call looks up how to ask for it
+    without a Stream object, which takes 5 us less)."""
+    global _current_stream
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    known = torch.cuda.is_initialized
+
+    def ask() -> int:
+        if raw is not None and device is not None and known():
+            return raw(device())
+        return torch.cuda.current_stream().cuda_stream
+
+    _current_stream = ask
+    return ask()
 
 
 # --------------------------------------------------------------------------
@@ -405,6 +416,8 @@ def ozgemm_grouped_gemm(type, ctype, groups, m, n, q, transa, A, lda, stridea, B
     st = None
     if workspace is None:  # operands are usually read in place
         st = L.ozgemm_grouped_gemm(*ops, None, 0, hs)
+        if st == OZGEMM_OK:
+            return st
     if st is None or st == _GEMM_NO_WORKSPACE:
         need = 0 if workspace is not None else ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, A,
                                                                                   lda, stridea, B, ldb)
