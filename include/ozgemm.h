@@ -466,10 +466,12 @@ int ozgemm_mfma_ceiling(int blocks, int steps, unsigned seed, unsigned *sink, vo
  *   B       q x n, ldb >= max(1, q);  C  m x n, ldc >= max(1, m), type
  *           ctype: `type` itself or OZGEMM_F32
  * Columns of no group are left as they were.  q = 0 gives zeros.  C must not
- * overlap A or B.  16-bit operands are read in place where rows begin on
- * 16-byte boundaries and K-contiguous ones (A with transa = 1, B) have q a
- * multiple of 8, K-strided ones (A with transa = 0) m a multiple of 8; others,
- * and F32 operands, pass through the workspace.  Results too small to fill the
+ * overlap A or B.  Every array begins at a multiple of its entries' size.
+ * Products of few columns and small ones read their operands as they lie.
+ * Larger ones do so with 16-bit operands whose rows begin on 16-byte
+ * boundaries, K-contiguous ones (A with transa = 1, B) with q a multiple of 8,
+ * K-strided ones (A with transa = 0) with m a multiple of 8; others, and F32
+ * operands, then pass through the workspace.  Results too small to fill the
  * card are summed in parts of a long inner dimension, in a fixed order, whose
  * sums take room in the workspace too.
  * Errors: -i for argument i; OZGEMM_RANGE for m, n or q above
@@ -491,9 +493,9 @@ size_t ozgemm_grouped_gemm_workspace_bytes(int type, int groups, int m, int n, i
  * of a layer of experts for its weights.  A is m x n (lda >= max(1, m)), B
  * q x n (ldb >= max(1, q)), C_e m x q (ldc >= max(1, m)), beginning at
  * C + e stridec (stridec >= ldc q where groups > 1).  An empty group gives
- * zeros.  Types, errors and workspace as above; 16-bit operands are read in
- * place where columns begin on 16-byte boundaries and m and q are multiples
- * of 8.  Operands that pass through the workspace (there each group begins at
+ * zeros.  Types, errors and workspace as above; larger products read 16-bit
+ * operands in place where columns begin on 16-byte boundaries and m and q are
+ * multiples of 8.  Operands that pass through the workspace (there each group begins at
  * a multiple of 64) need n + 63 min(groups, n) <= 2^21 (OZGEMM_RANGE).  Small
  * results of many columns are summed in parts, in a fixed order, whose sums
  * take room in the workspace too. */
