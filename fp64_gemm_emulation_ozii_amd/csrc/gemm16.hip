@@ -266,12 +266,7 @@ __global__ __launch_bounds__(256) void join_columns_kernel(Grouped16 g) {
   if (row >= g.m) return;
   const int32_t* ea = g.A.ex ? g.A.ex + gt.group * g.A.ex_batch : nullptr;
   for (int col = gt.begin + (threadIdx.x >> 4); col < min(gt.end, gt.begin + 64); col += 16) {
-    v4f v = {0.f, 0.f, 0.f, 0.f};
-    for (int p = 0; p < g.parts; ++p) {
-      const float* from = g.partial + ((long)p * g.n + col) * g.m + row;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] += row + k < g.m ? from[k] : 0.f;
-    }
+    v4f v = sum_parts(g.partial + (long)col * g.m + row, (long)g.n * g.m, g.parts, g.m - row);
     if (ea != nullptr) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = unscale(v[k], ea[min(row + k, g.m - 1)], g.B.ex[col]);
@@ -712,12 +707,7 @@ __global__ __launch_bounds__(256) void join_parts_kernel(Grouped16 g) {
   if (at >= (long)runs * g.q * g.groups) return;
   const int row = (int)(at % runs) * 4, col = (int)(at / runs % g.q);
   const long e = at / runs / g.q;
-  v4f v = {0.f, 0.f, 0.f, 0.f};
-  for (int p = 0; p < g.parts; ++p) {
-    const float* from = g.partial + (((long)p * g.groups + e) * g.q + col) * g.m + row;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] += row + k < g.m ? from[k] : 0.f;
-  }
+  v4f v = sum_parts(g.partial + (e * g.q + col) * g.m + row, (long)g.groups * g.q * g.m, g.parts, g.m - row);
   if (g.A.ex != nullptr) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)

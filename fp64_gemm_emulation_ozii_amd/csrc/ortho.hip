@@ -474,7 +474,7 @@ hipError_t launch_step(const Step& p, int nprod, bool aks, bool sym, hipStream_t
 }
 
 // P = X X^T for few rows and long ones, along the c entries in `parts` parts
-// (five steps on one f32 matrix of 64 x 4096: 172 us in one part, 104 so):
+// (five steps on one f32 matrix of 64 x 4096: 172 us in one part, 93 so):
 // every block sums 64 x 64 entries over its part of the slices, and the
 // parts' sums meet in FP32.  (All of P: at these sizes the time is a block's
 // slices, not the operations.)
@@ -523,17 +523,14 @@ __global__ __launch_bounds__(256) void gram_join_kernel(Parts p) {
   const long plane = (long)p.r * p.r, at = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
   const long b = blockIdx.y;
   if (at >= plane) return;
-  float v[8] = {};
-  for (int q = 0; q < p.parts; ++q) {
-    const float* from = p.partial + ((long)q * p.batch + b) * plane + at;
+  v4f v[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += from[e];
-  }
+  for (int e = 0; e < 2; ++e) v[e] = sum_parts(p.partial + b * plane + at + 4 * e, p.batch * plane, p.parts, 4);
   v8s h, l;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     uint16_t hi, lo;
-    split(v[e] * p.alpha, hi, lo);
+    split(v[e / 4][e % 4] * p.alpha, hi, lo);
     h[e] = (short)hi;
     l[e] = (short)lo;
   }
