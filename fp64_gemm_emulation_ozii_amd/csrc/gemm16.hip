@@ -178,11 +178,10 @@ struct Walk {
   static_assert(Small::SMEM <= SMEM && Store<Small>::BYTES <= SMEM, "quarter tiles use the same LDS");
 
   template <class Place>
-  static __device__ __forceinline__ void run(char* smem, int total, Place place) {
+  static __device__ __forceinline__ void run(char* smem, int total, int units, int skip, Place place) {
     constexpr int BT = Tile::ROWS_M;
     static_assert(BT == Tile::ROWS_N && BT == 2 * Small::ROWS_M && BT == 2 * Small::ROWS_N, "square tiles and quarters");
-    const int units = gridDim.x / SHARES;
-    const Share share = share_of(total, units, blockIdx.x);
+    const Share share = share_of(total, units, blockIdx.x + skip);
     if (share.first < 0) return;
     if (share.quarter >= 0) {
       const Job job = place(share.first, (share.quarter & 1) * (BT / 2), (share.quarter >> 1) * (BT / 2));
@@ -238,7 +237,7 @@ __global__ __launch_bounds__(512) void grouped_n_kernel(Grouped16 g) {
   const int whole = tiles_m * index.total, total = whole * g.parts;
   // a part's inner dimension: whole slices
   const int each = ((g.q + BK16 - 1) / BK16 + g.parts - 1) / g.parts * BK16;
-  Tiles::run(smem, total, [&](int L, int dm, int dn) {
+  Tiles::run(smem, total, g.units, g.skip, [&](int L, int dm, int dn) {
     const int part = L / whole, k0 = min(part * each, g.q);
     int nj, mi;
     panel_order<4>(xcd_order(L - part * whole, whole), index.total, tiles_m, nj, mi);
@@ -285,7 +284,7 @@ __global__ __launch_bounds__(512) void grouped_k_kernel(Grouped16 g) {
   const int tiles_m = (g.m + BT - 1) / BT, tiles_q = (g.q + BT - 1) / BT;
   const int per = tiles_m * tiles_q, whole = per * g.groups, total = whole * g.parts;
   const GroupIndex index(g.offsets, g.groups, g.n, BK16);
-  Tiles::run(smem, total, [&](int L, int dm, int dn) {
+  Tiles::run(smem, total, g.units, g.skip, [&](int L, int dm, int dn) {
     const int part = L / whole;
     L -= part * whole;
     // Every XCD takes an eighth of each group's tiles: the groups' lengths
@@ -601,11 +600,11 @@ hipError_t few(const Grouped16& g, hipStream_t st) {
 }
 
 template <class T, int BT, bool AKS, bool PAIR>
-hipError_t grouped_n(const Grouped16& g, hipStream_t st) {
-  int cus = 0;
-  const hipError_t err = device_units(&cus);
+hipError_t grouped_n(Grouped16 g, hipStream_t st) {
+  const hipError_t err = device_units(&g.units);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((grouped_n_kernel<T, BT, AKS, PAIR>), dim3(SHARES * cus), dim3(512), 0, st, g);
+  g.skip = shares_without(group_tiles_max(g.n, g.groups, BT) * ((g.m + BT - 1) / BT) * g.parts, g.units);
+  hipLaunchKernelGGL((grouped_n_kernel<T, BT, AKS, PAIR>), dim3(SHARES * g.units - g.skip), dim3(512), 0, st, g);
   return g.parts > 1 ? join_columns(g, st) : hipGetLastError();
 }
 
@@ -738,11 +737,11 @@ hipError_t few_outer(const Grouped16& g, hipStream_t st) {
 }
 
 template <class T, int BT, bool KS, bool PAIR>
-hipError_t grouped_k(const Grouped16& g, hipStream_t st) {
-  int cus = 0;
-  const hipError_t err = device_units(&cus);
+hipError_t grouped_k(Grouped16 g, hipStream_t st) {
+  const hipError_t err = device_units(&g.units);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((grouped_k_kernel<T, BT, KS, PAIR>), dim3(SHARES * cus), dim3(512), 0, st, g);
+  g.skip = shares_without((long)((g.m + BT - 1) / BT) * ((g.q + BT - 1) / BT) * g.groups * g.parts, g.units);
+  hipLaunchKernelGGL((grouped_k_kernel<T, BT, KS, PAIR>), dim3(SHARES * g.units - g.skip), dim3(512), 0, st, g);
   return g.parts > 1 ? join_parts(g, st) : hipGetLastError();
 }
 
@@ -800,17 +799,16 @@ bool grouped_n_fits(const Grouped16& g) {
 // Parts of an inner dimension of `slices` slices for `tiles` tiles whose result
 // has `entries` entries, from modelled times in us: rounds of whole tiles at
 // 1.4 per slice and 9 besides (f32: 1.2 and 8), a last one of quarters at 0.6
-// and 6 where it is at most half full (share.h; `lone_slice` where they are
-// fewer than the units), and the sums' way through memory at 4 TB/s and a
-// launch.  Measured in us, the rule before (as many parts as quarters had
+// and 6 where it is at most half full (share.h), and the sums' way through
+// memory at 4 TB/s and a launch.  Measured in us, the rule before (as many parts as quarters had
 // units) / this: outer products of 32768 rows, bf16 1 of 2048 x 2048 555 / 247,
 // 1 of 1024 x 1024 157 / 96, f32 1 of 1024 x 1024 860 / 388 (slices: 230).
-static int parts_for(bool f32, long tiles, long slices, double entries, double lone_slice) {
+static int parts_for(bool f32, long tiles, long slices, double entries) {
   const long units = 256;
   auto time = [&](long parts) {
     const long total = tiles * parts, rest = total % units;
     const double k = ceil((double)slices / parts);
-    const double whole = f32 ? 1.2 * k + 8 : 1.4 * k + 9, quarter = (rest * 4 <= units ? lone_slice : 0.6) * k + 6;
+    const double whole = f32 ? 1.2 * k + 8 : 1.4 * k + 9, quarter = (f32 ? 0.55 : 0.6) * k + 6;
     const double last = rest == 0 ? 0 : rest * 2 <= units ? quarter * ((4 * rest + units - 1) / units) : whole;
     return (total / units) * whole + last + (parts > 1 ? 8 + 2 * 4 * entries * parts / 4e6 : 0);
   };
@@ -824,7 +822,7 @@ static int parts_for(bool f32, long tiles, long slices, double entries, double l
 int outer_parts(bool f32, int groups, int m, int q, int n) {
   const long tile = f32 ? 128 : 256;
   return parts_for(f32, ((m + tile - 1) / tile) * ((q + tile - 1) / tile) * groups,
-                   ((long)n / groups + BK16 - 1) / BK16, (double)groups * m * q, 0.6);
+                   ((long)n / groups + BK16 - 1) / BK16, (double)groups * m * q);
 }
 
 // Measured in us (the kernel for small outer products / tiles): its time is
@@ -847,11 +845,10 @@ size_t outer_partial_bytes(int parts, int groups, int m, int q) {
   return parts > 1 ? (size_t)parts * groups * m * q * 4 : 0;
 }
 
-// (512 rows with 2048 x 2048: 64 quarters take 44 us in one part, 34 in four.)
 int gemm_parts(bool f32, int groups, int m, int n, int q) {
   const long tile = f32 ? 128 : 256;
   return parts_for(f32, group_tiles_max(n, groups, tile) * ((m + tile - 1) / tile), (q + BK16 - 1) / BK16,
-                   (double)m * n, 1.1);
+                   (double)m * n);
 }
 
 size_t gemm_partial_bytes(int parts, int m, int n) { return parts > 1 ? (size_t)parts * m * n * 4 : 0; }

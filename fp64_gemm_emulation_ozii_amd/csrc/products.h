@@ -39,6 +39,7 @@ struct Grouped16 {
   int ctype;
   long ldc, cbatch;
   int parts;       // of the inner dimension (outer products: of each group's columns)
+  int units, skip;  // compute units; blocks left out of the launch (share.h)
   float* partial;  // their sums: [parts][n][m] (outer products: [parts][groups][q][m])
 };
 

@@ -18,7 +18,7 @@ namespace oz {
 
 // `total` tiles on `units` compute units, which run one block each at a time,
 // in SHARES units blocks.  The first `units` blocks walk whole rounds of
-// tiles; a round before the last, the next `units` blocks take one tile each
+// tiles; the last full round goes to the next `units` blocks, one tile each
 // as units become free (tiles at the end of a group are cheaper than others);
 // what then remains is less than a round, and where it is no more than half
 // of one, its tiles are cut into quarters for the last 2 units blocks, or else
@@ -37,12 +37,17 @@ __host__ __device__ __forceinline__ Share share_of(int total, int units, int blo
   if (block < units) return Share{rounds, rounds > 0 ? block : -1, -1};
   block -= units;
   const int left = total - kept;  // less than two rounds
-  if (block < units) return Share{1, block < left ? kept + block : -1, -1};
+  const int full = left >= units ? units : 0;
+  if (block < units) return Share{1, block < full ? kept + block : -1, -1};
   block -= units;
-  const int rest = left - units;
-  if (rest <= 0) return Share{0, -1, -1};
-  if (rest * 2 <= units) return Share{1, block < rest * 4 ? kept + units + block / 4 : -1, block % 4};
-  return Share{1, block < rest ? kept + units + block : -1, -1};
+  const int rest = left - full;
+  if (rest * 2 <= units) return Share{1, block < rest * 4 ? kept + full + block / 4 : -1, block % 4};
+  return Share{1, block < rest ? kept + full + block : -1, -1};
 }
+
+// Blocks that a launch of at most `most` tiles can leave out from the first
+// on: those without a share whatever the tiles are (a block without one still
+// waits for a unit and looks the tiles up: 2 us each).
+inline int shares_without(long most, int units) { return most < units ? 2 * units : most < 2L * units ? units : 0; }
 
 }  // namespace oz

@@ -15,6 +15,10 @@ int main(int argc, char** argv) {
     for (int block = 0; block < oz::SHARES * units; ++block) {
       const oz::Share s = oz::share_of(total, units, block);
       if (s.first < 0) continue;
+      if (block < oz::shares_without(total, units)) {
+        std::printf("units %d total %d block %d: left out, but has tile %d\n", units, total, block, s.first);
+        return 1;
+      }
       for (int r = 0; r < (s.quarter >= 0 ? 1 : s.rounds); ++r) {
         const long tile = s.first + (long)r * units;
         if (tile < 0 || tile >= total) {
