@@ -755,17 +755,17 @@ hipError_t grouped_k(Grouped16 g, hipStream_t st) {
 // Where their blocks are no more than the units, a call takes a block's time:
 // about 1 ns per entry of the inner dimension and (1 + columns / 16), twice
 // that in f32, half as much again K-strided (f32: twice) or off the grid; so
-// parts of 8 us are made while units are idle.  Beyond 50 us the 16-bit tiles
-// are faster, unless they have to wait for copies.
-//   16-bit   1 of 1024 x 2048, 128 rows 15 / 30;  x 8192, 32 rows 23 / 30;  x 32768, 32 rows 29 / 50,
-//            256 rows 86 / 76;  1 of 1023 x 1023, 64 rows 13 / 23;  1 of 2047 x 2047, 64 rows 21 / 27
-//   f32      1 of 1024 x 2048, 128 rows 26 / 45;  x 8192, 32 rows 28 / 69;  x 32768, 32 rows 47 / 216,
-//            256 rows 210 / 345
+// parts of 8 us are made while units are idle.  Beyond 15 us (two columns of
+// MFMA tiles: 40) the 16-bit tiles are faster, unless they wait for copies.
+//   16-bit   1 of 1024 x 2048, 128 rows 15 / 17;  x 8192, 32 rows 20 / 22;  x 32768, 32 rows 29 / 37,
+//            256 rows 76 / 45;  1 of 1023 x 1023, 64 rows 13 / 21;  1 of 2047 x 2047, 64 rows 21 / 31
+//   f32      1 of 1024 x 2048, 128 rows 26 / 32;  x 8192, 32 rows 23 / 69;  x 32768, 32 rows 47 / 216,
+//            256 rows 210 / 300
 // Where they are some times more, it takes that many rounds of blocks, each
 // with a fixed time besides, against the tiles' launches:
-//   16-bit   1 of 256 x 512, 4096 rows 13 / 26;  64 of 128 x 128, 32768 rows 27 / 15
-//   copied   1 of 255 x 511, 4096 rows 23 / 56;  2 of 1399 x 89, 4096 rows 86 / 31
-//   f32      8 of 256 x 256, 4096 rows 17 / 24;  64 of 128 x 128, 32768 rows 54 / 41
+//   16-bit   16 of 512 x 512, 4096 rows 20 / 12;  64 of 128 x 128, 32768 rows 27 / 15
+//   copied   1 of 255 x 511, 4096 rows 23 / 23;  2 of 1399 x 89, 4096 rows 86 / 31
+//   f32      8 of 256 x 256, 4096 rows 17 / 18;  64 of 128 x 128, 32768 rows 54 / 41
 // Where they are many and the columns few, they read the weights at the card's
 // rate and the columns once for every 32 or 128 rows; the tiles read both from
 // L2 but need many in flight for that rate:
@@ -783,11 +783,13 @@ int few_columns_parts(bool f32, bool edge, bool ks, int groups, int m, int n, in
   if (blocks <= units) {
     const double slower = (ks ? (f32 ? 2 : 1.5) : 1) * (edge ? 1.5 : 1);
     const long parts = std::max(std::min({(long)(ns * slower / 8000), units / std::max(blocks, 1L), 32L}), 1L);
-    return copies || ns / parts <= 50000 ? (int)parts : 0;
+    return copies || ns / parts <= (frags > 2 ? 15000 : 40000) ? (int)parts : 0;
   }
   const long fixed = ks ? (f32 ? 4500 : 6500) : f32 ? (edge ? 8500 : 5500) : edge ? 7000 : 2500;
-  if (fixed + ns * (edge && !f32 ? 2 : 1) <= (copies ? 35000 : 17000) * units / blocks) return 1;
-  const long tiles = (long)groups * ((m + 255) / 256), most = copies || tiles * 4 <= units ? 48 : 24;
+  const double slower = f32 ? (ks ? 1.5 : 1) : edge ? 2 : 1;
+  const long most_ns = !copies ? 17000 : !ks ? 24000 : f32 ? 42000 : 35000;
+  if (fixed + ns * slower <= (double)most_ns * units / blocks) return 1;
+  const long tiles = (long)groups * ((m + 255) / 256), most = copies || tiles * 4 <= units ? 48 : ks ? 16 : 24;
   return n <= most * groups ? 1 : 0;
 }
 
@@ -827,16 +829,15 @@ int outer_parts(bool f32, int groups, int m, int q, int n) {
 
 // Measured in us (the kernel for small outer products / tiles): its time is
 // that of its 64 x 64 tiles' columns, 2^20 of them 30 us in 16 bits, 45 to 75
-// off the 8-byte grid, 105 in f32, and 6 at least; the tiles take a launch of
-// each copy, exponent and sum in parts, 11 to 30 us with hardly any columns.
-// Its blocks take 4 us each at the least, to look up, to start and to add.
-//   16-bit   8 of 256 x 256, 4096 rows 7 / 20;  1 of 1024 x 1024, 4096 rows 30 / 38, 32768 162 / 156
-//   copied   8 of 255 x 255, 4096 rows 10 / 53;  1 of 1023 x 1023, 4096 rows 56 / 73, 32768 809 / 242
-//   f32      8 of 256 x 256, 4096 rows 15 / 50;  1 of 1024 x 1024, 4096 rows 106 / 107;
-//            4 of 1023 x 511, 4096 rows 60 / 77, 32768 493 / 394
+// off the 8-byte grid, 105 in f32, and 4 for each block on a unit, to look up,
+// to start and to add; the tiles take a launch of each copy, exponent and sum
+// in parts besides their own.
+//   16-bit   8 of 256 x 256, 4096 rows 7 / 9, 32768 25 / 21;  16 of 512 x 512, 4096 rows 18 / 10
+//   copied   8 of 255 x 255, 4096 rows 10 / 26;  1 of 1023 x 1023, 4096 rows 57 / 39
+//   f32      8 of 256 x 256, 4096 rows 15 / 40;  1 of 1024 x 1024, 4096 rows 104 / 77
 int few_outer_parts(bool f32, bool edge, int groups, int m, int q, int n) {
   const long blocks = few_outer_blocks(groups, m, q), each = std::max(((long)n + groups - 1) / groups, 1L);
-  if (blocks > std::min((1L << 20) / each, f32 || edge ? 1536L : 1024L)) return 0;
+  if (blocks > std::min((f32 || edge ? 1L << 19 : 1L << 18) / each, f32 ? 1536L : 512L)) return 0;
   const long chunks = (each + (f32 ? 127 : 255)) / (f32 ? 128 : 256);
   return (int)std::max(std::min({512 / blocks, chunks / 4, 32L}), 1L);
 }
