@@ -388,16 +388,27 @@ _GEMM_NO_WORKSPACE = -16
 _OUTER_NO_WORKSPACE = -15
 
 
-def _room(workspace, nbytes: int, device):
+def _room(workspace, nbytes: int, device, stream: int):
     """(tensor kept alive, pointer, bytes) of a call's workspace: the given
-    one, or one from torch's allocator on the current stream (which hands it
-    out again only to work queued after this call)."""
+    one, or one from torch's allocator.
+
+    The allocator hands a freed block out again to work of the stream that was
+    current when it was allocated, and only after what that stream has queued
+    by then.  So the block is taken while the stream that the call runs on is the
+    current one."""
     if workspace is not None:
         return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
     if nbytes == 0:
         return None, None, 0
     import torch
-    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream == _current_stream():
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif stream & 1:  # no address of a stream: torch could not tell it from its own ones
+        raise ValueError(f"a call on the stream {stream:#x} needs its workspace given")
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if stream else
+                               torch.cuda.default_stream(device)):
+            t = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return t, t.data_ptr(), nbytes
 
 
@@ -409,8 +420,9 @@ def ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, A, lda, s
 def ozgemm_grouped_gemm(type, ctype, groups, m, n, q, transa, A, lda, stridea, B, ldb, offsets, C, ldc,
                         workspace=None, stream=None, check: bool = True) -> int:
     """With ``workspace=None`` the bytes the call needs, if any, come from
-    torch's allocator; a given workspace (a device tensor) stays the
-    caller's."""
+    torch's allocator, on the stream that the call runs on (``stream``: a torch
+    stream or a handle; the current one by default); a given workspace (a device
+    tensor) stays the caller's."""
     L, hs = lib(), _stream(stream)
     ops = (type, ctype, groups, m, n, q, transa, _ptr(A), lda, stridea, _ptr(B), ldb, _ptr(offsets), _ptr(C), ldc)
     st = None
@@ -421,7 +433,7 @@ def ozgemm_grouped_gemm(type, ctype, groups, m, n, q, transa, A, lda, stridea, B
     if st is None or st == _GEMM_NO_WORKSPACE:
         need = 0 if workspace is not None else ozgemm_grouped_gemm_workspace_bytes(type, groups, m, n, q, transa, A,
                                                                                   lda, stridea, B, ldb)
-        keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"))
+        keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"), hs)
         st = L.ozgemm_grouped_gemm(*ops, ws, nbytes, hs)
     return _check(st, "ozgemm_grouped_gemm") if check else st
 
@@ -441,7 +453,7 @@ def ozgemm_grouped_outer(type, ctype, groups, m, q, n, A, lda, B, ldb, offsets, 
     if st is None or st == _OUTER_NO_WORKSPACE:
         need = 0 if workspace is not None else ozgemm_grouped_outer_workspace_bytes(type, groups, m, q, n, A, lda, B,
                                                                                    ldb)
-        keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"))
+        keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"), hs)
         st = L.ozgemm_grouped_outer(*ops, ws, nbytes, hs)
     return _check(st, "ozgemm_grouped_outer") if check else st
 
@@ -454,9 +466,10 @@ def ozgemm_orthogonalize(type, batch, m, n, G, ldg, strideg, steps, coeffs, eps,
                          stream=None, check: bool = True) -> int:
     """``coeffs``: 3 * steps host numbers.  Workspace as for
     :func:`ozgemm_grouped_gemm`."""
+    hs = _stream(stream)
     co = (ctypes.c_double * max(3 * steps, 1))(*coeffs) if coeffs is not None else None
     need = ozgemm_orthogonalize_workspace_bytes(type, batch, m, n, s)
-    keep, ws, nbytes = _room(workspace, need, getattr(G, "device", "cuda"))
+    keep, ws, nbytes = _room(workspace, need, getattr(G, "device", "cuda"), hs)
     st = lib().ozgemm_orthogonalize(type, batch, m, n, _ptr(G), ldg, strideg, steps, co, eps, s, _ptr(O), ldo,
-                                    strideo, ws, nbytes, _stream(stream))
+                                    strideo, ws, nbytes, hs)
     return _check(st, "ozgemm_orthogonalize") if check else st
