@@ -1,7 +1,8 @@
 """Products of expert layers and the orthogonalisation of their updates on
 torch tensors (row-major): the calls of :mod:`.ozgemm` with their shapes, strides and types taken from the tensors.
 
-Nothing here is recorded by autograd: the gradients are calls of their own.
+Nothing here is recorded by autograd: the gradients are calls of their own, and
+tensors that require a gradient or carry a tangent are refused.
 Work goes on the current stream of the tensors' device.
 """
 from __future__ import annotations
@@ -9,6 +10,7 @@ from __future__ import annotations
 import contextlib
 
 import torch
+from torch.autograd import forward_ad
 
 from . import ozgemm as L
 
@@ -22,12 +24,20 @@ def _type_of(t, what: str, allowed=(torch.float32, torch.bfloat16, torch.float16
     return _TYPES[t.dtype]
 
 
-def _no_grad(*tensors) -> None:
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t.requires_grad:
-                raise RuntimeError("this call is not recorded by autograd: make it under torch.no_grad() and take the "
-                                   "gradients from grouped_linear_grads")
+def _no_grad(what: str, *tensors, instead: str = "") -> None:
+    """Refuses tensors whose derivatives would get lost: those that autograd
+    records (unless it is switched off), and those with a tangent of its forward
+    mode (which torch.no_grad() does not switch off)."""
+    for t in tensors:
+        if t is None:
+            continue
+        if t.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError(f"{what} is not recorded by autograd: call it under torch.no_grad(){instead}")
+        if forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{what} has no forward-mode derivative: call it on the primal of a dual tensor")
+
+
+_INSTEAD = " and take the gradients from grouped_linear_grads"
 
 
 _HERE = contextlib.nullcontext()
@@ -115,7 +125,7 @@ def grouped_linear(X, W, offsets, out=None, out_dtype=None):
     without ``out`` they are not written.
     """
     _same(X, W, "X and W")
-    _no_grad(X, W)
+    _no_grad("grouped_linear", X, W, out, instead=_INSTEAD)
     t = _type_of(X, "grouped_linear")
     if X.dim() != 2 or W.dim() != 3 or X.shape[1] != W.shape[2]:
         raise ValueError(f"X {tuple(X.shape)} and W {tuple(W.shape)} do not go together")
@@ -144,7 +154,7 @@ def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
     _same(X, W, "X and W")
     _same(dY, X, "dY and X")
     t = _type_of(X, "grouped_linear_grads")
-    _no_grad(dY, X, W)
+    _no_grad("grouped_linear_grads", dY, X, W, dX, dW)
     if X.dim() != 2 or W.dim() != 3 or dY.dim() != 2 or X.shape[1] != W.shape[2] or (
             dY.shape != (X.shape[0], W.shape[1])):
         raise ValueError(f"dY {tuple(dY.shape)}, X {tuple(X.shape)} and W {tuple(W.shape)} do not go together")
@@ -191,8 +201,7 @@ def orthogonalize(G, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7, out=None
         co = []
     if len(co) != steps or any(len(c) != 3 for c in co):
         raise ValueError(f"coeffs must be one triple or {steps} of them")
-    if torch.is_grad_enabled() and G.requires_grad:
-        raise RuntimeError("orthogonalize is not recorded by autograd: call it under torch.no_grad()")
+    _no_grad("orthogonalize", G, out)
     r, c = G.shape[-2:]
     _fits(r, c)
     if out is None:
