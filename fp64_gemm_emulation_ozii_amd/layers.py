@@ -40,6 +40,15 @@ def _no_grad(what: str, *tensors, instead: str = "") -> None:
 _INSTEAD = " and take the gradients from grouped_linear_grads"
 
 
+def _written(*tensors) -> None:
+    """Tells autograd that these tensors of the caller's hold other values now: a
+    graph that had saved one refuses its backward pass, as after torch's own
+    in-place operations."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -139,6 +148,7 @@ def grouped_linear(X, W, offsets, out=None, out_dtype=None):
     with _on_device(X.device):
         X, ldb = _rows(X, "X")
         W, transa, lda, stridea = _weights(W)
+        _written(out)
         L.ozgemm_grouped_gemm(t, _TYPES[Y.dtype], g, m, n, q, transa, W, lda, stridea, X, ldb, offsets, Y, _ld(Y))
     return Y
 
@@ -162,6 +172,7 @@ def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
     n = X.shape[0]
     _fits(n, m, q)
     offsets = _offsets(offsets, g, X.device)
+    given = dX, dW
     dX = _target(dX, (n, q), (X.dtype,), X, "dX")
     dW = _target(dW, (g, m, q), (X.dtype, torch.float32) if dW is not None else (dw_dtype or X.dtype,), X, "dW")
     if dW.dtype not in (X.dtype, torch.float32):
@@ -170,6 +181,7 @@ def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
         X, ldx = _rows(X, "X")
         dY, ldy = _rows(dY, "dY")
         W, transa, lda, stridea = _weights(W)
+        _written(*given)
         L.ozgemm_grouped_gemm(t, t, g, q, n, m, 1 - transa, W, lda, stridea, dY, ldy, offsets, dX, _ld(dX))
         L.ozgemm_grouped_outer(t, _TYPES[dW.dtype], g, q, m, n, X, ldx, dY, ldy, offsets, dW, _ld(dW),
                                max(dW.stride(0) if g > 1 else 0, _ld(dW) * m))
@@ -204,6 +216,7 @@ def orthogonalize(G, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7, out=None
     _no_grad("orthogonalize", G, out)
     r, c = G.shape[-2:]
     _fits(r, c)
+    given = out
     if out is None:
         out = torch.empty(G.shape, dtype=G.dtype, device=G.device)
     elif out.shape != G.shape or out.dtype != G.dtype or out.device != G.device:
@@ -218,6 +231,7 @@ def orthogonalize(G, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7, out=None
             raise ValueError(f"out must be matrices of contiguous rows evenly apart, strides {out.stride()}")
         if g is None:
             g = _matrices(G.contiguous())
+        _written(given)
         L.ozgemm_orthogonalize(t, g[1], c, r, g[0], g[2], g[3], steps, [v for x in co for v in x], eps, s, o[0], o[2],
                                o[3])
     return out

@@ -48,3 +48,38 @@ def test_a_tensor_that_requires_a_gradient_is_refused(call, name, shape):
         call(**{name: t})
     with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
         call(**{name: t})
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    # the calls as far as the library's, which stand-ins take: tensors on the CPU get there
+    import contextlib
+
+    from fp64_gemm_emulation_ozii_amd import layers
+    called = []
+    monkeypatch.setattr(layers, "_on_device", lambda device: contextlib.nullcontext())
+    for name in ("ozgemm_grouped_gemm", "ozgemm_grouped_outer", "ozgemm_orthogonalize"):
+        monkeypatch.setattr(layers.L, name, lambda *a, name=name: called.append(name))
+    return called
+
+
+@pytest.mark.parametrize("call, name, shape", [a for a in ARGUMENTS if a[1] in ("out", "dX", "dW")])
+def test_a_graph_that_saved_a_result_learns_that_it_was_written(no_library, call, name, shape):
+    w = torch.ones(shape, requires_grad=True)
+    result = torch.ones(shape)
+    y = (w * result).sum()  # saves `result` for w's gradient
+    call(**{name: result})
+    assert no_library
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
+def test_in_place_and_in_inference_mode(no_library):
+    G = torch.zeros(6, 8)
+    before = G._version
+    assert ortho(G=G, out=G) is G and G._version > before
+    with torch.inference_mode():
+        linear()
+        grads()
+        ortho()
+    assert len(no_library) == 5
