@@ -72,6 +72,7 @@ def _rows(t, what: str):
     if t.dim() != 2:
         raise ValueError(f"{what} must have two dimensions, got {tuple(t.shape)}")
     n, q = t.shape
+    t = t.resolve_neg()
     if (q > 1 and t.stride(1) != 1) or (n > 1 and not max(1, q) <= t.stride(0) <= _LD_MAX):
         t = t.contiguous()
     return t, max(1, q, t.stride(0) if n > 1 else 0)
@@ -83,6 +84,7 @@ def _weights(W):
     if W.dim() != 3:
         raise ValueError(f"the weights must have three dimensions [groups, out, in], got {tuple(W.shape)}")
     g, m, q = W.shape
+    W = W.resolve_neg()
     s0, s1, s2 = W.stride()
     s0 = s0 if g > 1 else 0
     if (q <= 1 or s2 == 1) and (m <= 1 or max(1, q) <= s1 <= _LD_MAX):
@@ -110,6 +112,8 @@ def _target(out, shape, dtypes, like, what: str):
     """The tensor a result goes to: `out`, checked, or a new one."""
     if out is None:
         return like.new_empty(shape, dtype=dtypes[0])
+    if out.is_neg():
+        raise ValueError(f"{what} must not be a negated view")
     if tuple(out.shape) != tuple(shape) or out.dtype not in dtypes or out.device != like.device:
         raise ValueError(f"{what} must be {tuple(shape)} of {dtypes[0]} on {like.device}, got {tuple(out.shape)} of "
                          f"{out.dtype} on {out.device}")
@@ -219,12 +223,15 @@ def orthogonalize(G, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7, out=None
     given = out
     if out is None:
         out = torch.empty(G.shape, dtype=G.dtype, device=G.device)
+    elif out.is_neg():
+        raise ValueError("out must not be a negated view")
     elif out.shape != G.shape or out.dtype != G.dtype or out.device != G.device:
         raise ValueError(f"out must be {tuple(G.shape)} of {G.dtype} on {G.device}, got {tuple(out.shape)} of "
                          f"{out.dtype} on {out.device}")
     if G.numel() == 0:
         return out
     with _on_device(G.device):
+        G = G.resolve_neg()
         g = _matrices(G)
         o = _matrices(out)
         if o is None:
