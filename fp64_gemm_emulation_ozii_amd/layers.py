@@ -124,6 +124,14 @@ def _target(out, shape, dtypes, like, what: str):
     return out
 
 
+def _overlap(a, b) -> bool:
+    """Whether two tensors share memory between their first and last entries."""
+    def end(t):
+        return t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+    return a.numel() > 0 and b.numel() > 0 and a.data_ptr() < end(b) and b.data_ptr() < end(a)
+
+
 def _ld(t) -> int:
     return max(1, t.shape[-1], t.stride(-2) if t.shape[-2] > 1 else 0)
 
@@ -135,7 +143,8 @@ def grouped_linear(X, W, offsets, out=None, out_dtype=None):
     X is [n, q], W [g, m, q] (either inner dimension contiguous), offsets
     int32 [g + 1] on the device, Y [n, m] in X's type or float32
     (``out_dtype``).  Rows of no group are left as they were in ``out``;
-    without ``out`` they are not written.
+    without ``out`` they are not written.  ``out`` must not overlap X, W or the
+    offsets, each taken from its first entry to its last.
     """
     _same(X, W, "X and W")
     _no_grad("grouped_linear", X, W, out, instead=_INSTEAD)
@@ -163,7 +172,8 @@ def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
 
     dX is [n, q] in X's type (rows of no group as in ``out`` there), dW
     [g, m, q] in X's type or float32 (``dw_dtype``), zeros for a group
-    without rows.
+    without rows.  Neither may overlap dY, X, the offsets or the other, nor
+    dX the weights.
     """
     _same(X, W, "X and W")
     _same(dY, X, "dY and X")
@@ -185,6 +195,9 @@ def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
         X, ldx = _rows(X, "X")
         dY, ldy = _rows(dY, "dY")
         W, transa, lda, stridea = _weights(W)
+        # dX is written before X is read for dW; the calls themselves refuse the other overlaps
+        if given[0] is not None and (_overlap(dX, X) or _overlap(dX, dW)):
+            raise ValueError("dX must not overlap X or dW")
         _written(*given)
         L.ozgemm_grouped_gemm(t, t, g, q, n, m, 1 - transa, W, lda, stridea, dY, ldy, offsets, dX, _ld(dX))
         L.ozgemm_grouped_outer(t, _TYPES[dW.dtype], g, q, m, n, X, ldx, dY, ldy, offsets, dW, _ld(dW),

@@ -70,3 +70,18 @@ def test_results_do_not_go_to_negated_views(seen):
     with pytest.raises(ValueError, match="negated"):
         layers.orthogonalize(X, out=negated(5, 1))
     assert not seen
+
+
+def test_gradients_that_would_overwrite_what_is_still_read(seen):
+    off = torch.tensor([0, 2, 6], dtype=torch.int32)
+    X, W, dY = torch.randn(6, 3), torch.randn(2, 4, 3), torch.randn(6, 4)
+    both = torch.zeros(6 * 3 + 2 * 4 * 3)
+    for bad in (dict(dX=X), dict(dX=both[:18].view(6, 3), dW=both[17:41].view(2, 4, 3)),
+                dict(dX=both[20:38].view(6, 3), dW=both[:24].view(2, 4, 3))):
+        with pytest.raises(ValueError, match="overlap"):
+            layers.grouped_linear_grads(dY, X, W, off, **bad)
+        assert not seen
+    # next to each other, and over an X that is read from a copy
+    layers.grouped_linear_grads(dY, X, W, off, dX=both[:18].view(6, 3), dW=both[18:42].view(2, 4, 3))
+    wide = torch.zeros(3, 6)
+    layers.grouped_linear_grads(dY, wide.t(), W, off, dX=wide.view(6, 3))
