@@ -21,6 +21,7 @@
 
 #include <cmath>
 
+#include "pieces.h"
 #include "products.h"
 #include "step64.h"
 #include "tile16.h"
@@ -238,11 +239,11 @@ __global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
 
 __global__ __launch_bounds__(256) void normalise_kernel(const void* G, int type, int rows, int cols, long ld,
                                                         long batch, const double* __restrict__ part, int parts,
-                                                        double eps, void* O, long ldo, long batcho) {
+                                                        double eps, void* O, long ldo, long batcho, long first) {
   __shared__ double s[4];
   const long b = blockIdx.y;
   const double f = inverse_norm(part, parts, b, eps, s);
-  const long at = (long)blockIdx.x * 256 + threadIdx.x;
+  const long at = (first + blockIdx.x) * 256 + threadIdx.x;
   if (at >= (long)rows * cols) return;
   const long r = at / cols, c = at - r * cols;
   store_value(O, type, b * batcho + r * ldo + c, load_value(G, type, b * batch + r * ld + c) * f);
@@ -1064,8 +1065,10 @@ int ozgemm_orthogonalize(int type, int batch, int m, int n, const void* G, int l
     double* part = (double*)(ws + L.part);
     OZ_TRY(launch_square_sum(type, G, n, m, ldg, (long)strideg, batch, parts, part, st));
     const long total = (long)m * n;
-    hipLaunchKernelGGL(normalise_kernel, dim3((unsigned)((total + 255) / 256), batch), dim3(256), 0, st, G, type, n, m,
-                       (long)ldg, (long)strideg, part, parts, eps, O, (long)ldo, (long)strideo);
+    in_pieces((total + 255) / 256, [&](long first, unsigned count) {
+      hipLaunchKernelGGL(normalise_kernel, dim3(count, batch), dim3(256), 0, st, G, type, n, m, (long)ldg,
+                         (long)strideg, part, parts, eps, O, (long)ldo, (long)strideo, first);
+    });
     OZ_TRY(hipGetLastError());
     return OZGEMM_OK;
   }

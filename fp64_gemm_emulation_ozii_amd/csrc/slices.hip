@@ -19,6 +19,7 @@
 // 2048 (268 MB read, as much written) take 107 us, 5.0 TB/s; 8192 rows 28.6 us.
 // K-strided, 8192 x 2048: 28 us for the slices and 14 + 5 for the exponents.
 #include "groups.h"
+#include "pieces.h"
 #include "products.h"
 #include "tile16.h"
 
@@ -94,8 +95,8 @@ __device__ __forceinline__ void put4(uint16_t* out, long plane, uint32_t (&v)[4]
 template <int TYPE, int RUNS>
 __global__ __launch_bounds__(256) void slice_rows_kernel(const void* __restrict__ src, long ld, long sbatch, int rows,
                                                          long total, int K, uint16_t* __restrict__ dst, long dld,
-                                                         long plane, int32_t* __restrict__ ex) {
-  const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
+                                                         long plane, int32_t* __restrict__ ex, long first) {
+  const long row = (first + blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (row >= total) return;
   const long from = row / rows * sbatch + row % rows * ld;
@@ -144,14 +145,14 @@ struct KRange {
 };
 
 template <int TILE>
-__device__ __forceinline__ KRange k_range(const int32_t* offsets, int groups, int K, int idx) {
+__device__ __forceinline__ KRange k_range(const int32_t* offsets, int groups, int K, long idx) {
   if (offsets == nullptr) {
     const int per = (K + TILE - 1) / TILE;
-    const int b = idx / per, t = idx % per;
+    const int b = (int)(idx / per), t = (int)(idx % per);
     return KRange{b, t * TILE, min(K, (t + 1) * TILE), (long)t * TILE, t};
   }
-  const GroupTile g = find_group_tile(offsets, groups, K, TILE, idx);
-  return KRange{g.group, g.begin, min(g.end, g.begin + TILE), (long)idx * TILE, g.tile};
+  const GroupTile g = find_group_tile(offsets, groups, K, TILE, (int)idx);
+  return KRange{g.group, g.begin, min(g.end, g.begin + TILE), idx * TILE, g.tile};
 }
 
 // Bits of the largest |entry| of every column r of a tile of CHUNK k, one
@@ -160,8 +161,9 @@ constexpr int CHUNK = 64;
 
 __global__ __launch_bounds__(256) void column_max_kernel(const float* __restrict__ src, long ld, long sbatch,
                                                          int rows, int K, const int32_t* __restrict__ offsets,
-                                                         int groups, uint32_t* __restrict__ part) {
-  const KRange g = k_range<CHUNK>(offsets, groups, K, blockIdx.x);
+                                                         int groups, uint32_t* __restrict__ part, long first) {
+  const long idx = first + blockIdx.x;
+  const KRange g = k_range<CHUNK>(offsets, groups, K, idx);
   if (g.group < 0) return;
   const int lane = threadIdx.x & 63, r = blockIdx.y * 256 + lane * 4;
   const long base = offsets ? 0 : g.group * sbatch;
@@ -184,7 +186,7 @@ __global__ __launch_bounds__(256) void column_max_kernel(const float* __restrict
   __syncthreads();
   const int c = blockIdx.y * 256 + threadIdx.x;
   if (c < rows)
-    part[(long)blockIdx.x * rows + c] = max(max(s[0][threadIdx.x], s[1][threadIdx.x]), max(s[2][threadIdx.x], s[3][threadIdx.x]));
+    part[idx * rows + c] = max(max(s[0][threadIdx.x], s[1][threadIdx.x]), max(s[2][threadIdx.x], s[3][threadIdx.x]));
 }
 
 // The exponents of 64 columns of one group from its chunks' maxima.
@@ -220,8 +222,8 @@ template <int TYPE>
 __global__ __launch_bounds__(256) void slice_cols_kernel(const void* __restrict__ src, long ld, long sbatch, int rows,
                                                          int K, const int32_t* __restrict__ offsets, int groups,
                                                          uint16_t* __restrict__ dst, long dld, long plane,
-                                                         const int32_t* __restrict__ ex) {
-  const KRange g = k_range<64>(offsets, groups, K, blockIdx.x);
+                                                         const int32_t* __restrict__ ex, long first) {
+  const KRange g = k_range<64>(offsets, groups, K, first + blockIdx.x);
   if (g.group < 0) return;
   __shared__ uint32_t tile[64][65];
   __shared__ int32_t es[64];
@@ -272,26 +274,34 @@ long k_tiles(const int32_t* offsets, long K, long groups, long tile) {
 hipError_t slice_cols(int type, const void* src, long ld, long sbatch, int rows, int K, const int32_t* offsets,
                       int groups, uint16_t* dst, long dld, long plane, int32_t* ex, uint32_t* part, hipStream_t st) {
   if (rows < 1 || K < 1 || groups < 1) return hipSuccess;
-  const dim3 tiles((unsigned)k_tiles(offsets, K, groups, 64), (unsigned)((rows + 63) / 64));
+  const long tiles = k_tiles(offsets, K, groups, 64);
+  const unsigned row_tiles = (unsigned)((rows + 63) / 64);
   if (type == OZGEMM_F32) {
-    hipLaunchKernelGGL(column_max_kernel, dim3((unsigned)k_tiles(offsets, K, groups, CHUNK), (unsigned)((rows + 255) / 256)),
-                       dim3(256), 0, st, (const float*)src, ld, sbatch, rows, K, offsets, groups, part);
-    hipLaunchKernelGGL(column_exponents_kernel, dim3(groups, (unsigned)((rows + 63) / 64)), dim3(256), 0, st, part,
-                       rows, K, offsets, groups, ex);
-    hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F32>, tiles, dim3(256), 0, st, src, ld, sbatch, rows, K, offsets,
-                       groups, dst, dld, plane, ex);
-  } else {
-    hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F16>, tiles, dim3(256), 0, st, src, ld, sbatch, rows, K, offsets,
-                       groups, dst, dld, plane, ex);
+    in_pieces(k_tiles(offsets, K, groups, CHUNK), [&](long first, unsigned count) {
+      hipLaunchKernelGGL(column_max_kernel, dim3(count, (unsigned)((rows + 255) / 256)), dim3(256), 0, st,
+                         (const float*)src, ld, sbatch, rows, K, offsets, groups, part, first);
+    });
+    hipLaunchKernelGGL(column_exponents_kernel, dim3(groups, row_tiles), dim3(256), 0, st, part, rows, K, offsets,
+                       groups, ex);
   }
+  in_pieces(tiles, [&](long first, unsigned count) {
+    if (type == OZGEMM_F32)
+      hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F32>, dim3(count, row_tiles), dim3(256), 0, st, src, ld, sbatch, rows,
+                         K, offsets, groups, dst, dld, plane, ex, first);
+    else
+      hipLaunchKernelGGL(slice_cols_kernel<OZGEMM_F16>, dim3(count, row_tiles), dim3(256), 0, st, src, ld, sbatch, rows,
+                         K, offsets, groups, dst, dld, plane, ex, first);
+  });
   return hipGetLastError();
 }
 
 template <int TYPE, int RUNS>
 hipError_t slice_rows(const void* src, long ld, long sbatch, int rows, long total, int K, uint16_t* dst, long dld,
                       long plane, int32_t* ex, hipStream_t st) {
-  hipLaunchKernelGGL((slice_rows_kernel<TYPE, RUNS>), dim3((unsigned)((total + 3) / 4)), dim3(256), 0, st, src, ld,
-                     sbatch, rows, total, K, dst, dld, plane, ex);
+  in_pieces((total + 3) / 4, [&](long first, unsigned count) {
+    hipLaunchKernelGGL((slice_rows_kernel<TYPE, RUNS>), dim3(count), dim3(256), 0, st, src, ld, sbatch, rows, total, K,
+                       dst, dld, plane, ex, first);
+  });
   return hipGetLastError();
 }
 
