@@ -3,14 +3,17 @@
 // X with its r rows no more than its c columns (G or its transpose; the
 // iteration commutes with the transpose).
 //
-// Everything between G and the result stays in half-precision slices
-// (slices.hip): x S = hi + lo with a power of two S that the host derives
-// from a bound on the iterate's singular values, which keeps 22 bits or more
-// of every state whatever the type.  BF16 operands use one slice product
-// (hi hi: its operands are off by 2^-11, an eighth of the result's own
-// rounding; the term a X, through which small singular values grow 3.4 times
-// a step, uses both slices, so rounding is not amplified with them).  F16 and
-// F32 use three.  F64 runs the library's Scheme II products.
+// X stays in half-precision slices (slices.hip) between the products:
+// x 2^E = hi + lo with E from a bound on the singular values of each matrix's
+// own iterate (scales.h), to 2^-22 or better, or 2^-38 of that bound for entries
+// far below it, whatever the type and however small |G| is beside eps.  F16 and
+// F32, and BF16 of less than 256 rows, hold P and Q likewise and take three
+// slice products.  Larger BF16 holds them, and multiplies X, in the high slice
+// alone (one product of operands that are off by 2^-12, a sixteenth of the
+// result's own rounding; the term a X, through which small singular values grow
+// 3.4 times a step, uses both slices, so rounding is not amplified with them;
+// ortho_products has what it costs in accuracy).  F64 runs the library's Scheme
+// II products.
 //
 // X stays as G lies: wide (r rows of c entries next to each other) or tall (c
 // rows of r).  P = X X^T runs along the c entries, Q X along the r rows; the
@@ -23,6 +26,7 @@
 
 #include "pieces.h"
 #include "products.h"
+#include "scales.h"
 #include "step64.h"
 #include "tile16.h"
 
@@ -174,12 +178,15 @@ hipError_t launch_square_sum(int type, const void* G, int rows, int cols, long l
   return hipGetLastError();
 }
 
-// 1 / (|G_b|_F + eps) from the partial sums of matrix b, in every thread of the block.
-__device__ __forceinline__ double inverse_norm(const double* part, int parts, long b, double eps, double* s) {
+// |G_b|_F from the partial sums of matrix b, in every thread of the block.
+__device__ __forceinline__ double frobenius(const double* part, int parts, long b, double* s) {
   double v = 0;
   for (int i = threadIdx.x; i < parts; i += 256) v += part[b * parts + i];
-  v = block_sum(v, s);
-  return 1.0 / (sqrt(v) + eps);
+  return sqrt(block_sum(v, s));
+}
+
+__device__ __forceinline__ double inverse_norm(const double* part, int parts, long b, double eps, double* s) {
+  return 1.0 / (frobenius(part, parts, b, s) + eps);
 }
 
 __device__ __forceinline__ void split(float y, uint16_t& hi, uint16_t& lo) {
@@ -192,7 +199,16 @@ __device__ __forceinline__ float joined(uint16_t hi, uint16_t lo) {
   return (float)__builtin_bit_cast(_Float16, hi) + (float)__builtin_bit_cast(_Float16, lo);
 }
 
-// G (rows x cols) scaled and cut into slices, zeros in the padding.  Bound by
+// The factors of a matrix's products, which the kernels of every step read
+// from the workspace: [step][matrix].
+struct StepFactors {
+  Factors of;
+  int pad;
+};
+static_assert(sizeof(StepFactors) == 32, "two 16-byte words");
+
+// G (rows x cols) scaled and cut into slices, zeros in the padding; one more
+// block for each matrix works out the factors of its steps meanwhile.  Bound by
 // HBM: 4096 x 8192 in bf16 reads 67 MB and writes 134 in 52.8 us, 3.8 TB/s.
 constexpr int PREPARE_RUNS = 4;  // runs of 8 entries per thread, at most
 
@@ -202,17 +218,37 @@ struct Prepare {
   long ld, batch;
   const double* part;
   int parts;
-  double eps, scale;
+  double eps;
   uint16_t* X;   // [batch][2][rows_pad][cols_pad]
   int rows_pad, cols_pad;
   int each;      // runs per thread: fewer where the blocks would not fill the card
+  StepFactors* factors;
+  int steps, batches;
+  double co[3 * OZGEMM_ORTHO_STEPS_MAX];
 };
 
 template <int TYPE>
 __global__ __launch_bounds__(256) void prepare_kernel(Prepare p) {
   __shared__ double s[4];
   const long b = blockIdx.y;
-  const double f = inverse_norm(p.part, p.parts, b, p.eps, s) * p.scale;
+  const double norm = frobenius(p.part, p.parts, b, s), t0 = first_bound(norm, p.eps);
+  if (blockIdx.x == gridDim.x - 1) {
+    __shared__ Bends bends[OZGEMM_ORTHO_STEPS_MAX];
+    if ((int)threadIdx.x < p.steps) {
+      const double* co = p.co + 3 * threadIdx.x;
+      bends[threadIdx.x] = bends_of(co[0], co[1], co[2]);
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    double t = t0;
+    for (int k = 0; k < p.steps; ++k) {
+      const Bounds r = advance(bends[k], t);
+      p.factors[(long)k * p.batches + b].of = factors_of(bends[k], r);
+      t = r.next;
+    }
+    return;
+  }
+  const double f = 1.0 / (norm + p.eps) * ldexp(1.0, grid_exponent(t0));
   const long plane = (long)p.rows_pad * p.cols_pad, base = b * p.batch;
   const int per = p.cols_pad / 8, runs = (int)(plane / 8);
 #pragma unroll
@@ -260,8 +296,9 @@ struct Step {
   int a_ld, b_ld;
   int m, n, k;        // padded
   int batch;
-  float alpha, beta;
-  const uint16_t* S;  // like N; nullptr: beta = 0
+  const StepFactors* factors;  // of this step; v = f[which] D + g[which] S
+  int which;
+  const uint16_t* S;  // like N; nullptr: none
   uint16_t* N;
   long s_batch, s_plane;  // of S and N alike
   int s_lo, n_lo;         // whether the low slices are there
@@ -301,6 +338,9 @@ __device__ __forceinline__ void step_tile(const Step& p, char* smem, long b, int
   };
   // (a run of 8 rows and 16 columns lie inside or outside as a whole)
   auto inside = [&](int j, int ch) { return nw + j * 16 < p.n && mw + (ch * 64 + lane) % RUNS * 8 < p.m; };
+  const Factors& by = p.factors[b].of;
+  const float alpha = by.f[p.which], beta = by.g[p.which];
+  const int down = by.next;  // the result itself is on no grid
   v8s sh[2][CH] = {}, sl[2][CH] = {};
   auto fetch = [&](int j) {
     if (S == nullptr) return;
@@ -331,11 +371,13 @@ __device__ __forceinline__ void step_tile(const Step& p, char* smem, long b, int
       *reinterpret_cast<v4f*>(v + 4) = *reinterpret_cast<const v4f*>(stage + c * PITCH + r + 4);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        v[e] = __builtin_fmaf(p.beta, joined((uint16_t)sh[j & 1][ch][e], (uint16_t)sl[j & 1][ch][e]), v[e] * p.alpha);
+        v[e] = __builtin_fmaf(beta, joined((uint16_t)sh[j & 1][ch][e], (uint16_t)sl[j & 1][ch][e]), v[e] * alpha);
       if (!SYM && p.O != nullptr) {
         const int col = nw + j * 16 + c, row = mw + r;
         if (col < p.on) {
           const long to = b * p.batcho + (long)col * p.ldo + row;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], -down);
           store8(p.O, p.otype, to, p.om - row, v);
         }
         continue;
@@ -483,7 +525,7 @@ struct Parts {
   const uint16_t* X;
   long x_batch, x_plane;
   int x_ld, r, c, batch, parts;
-  float alpha;
+  const StepFactors* factors;
   float* partial;  // [parts][batch][r][r]
   uint16_t* P;     // [batch][2][r][r]
   int lo;
@@ -524,6 +566,7 @@ __global__ __launch_bounds__(256) void gram_join_kernel(Parts p) {
   const long plane = (long)p.r * p.r, at = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
   const long b = blockIdx.y;
   if (at >= plane) return;
+  const float alpha = p.factors[b].of.f[0];
   v4f v[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) v[e] = sum_parts(p.partial + b * plane + at + 4 * e, p.batch * plane, p.parts, 4);
@@ -531,7 +574,7 @@ __global__ __launch_bounds__(256) void gram_join_kernel(Parts p) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     uint16_t hi, lo;
-    split(v[e / 4][e % 4] * p.alpha, hi, lo);
+    split(v[e / 4][e % 4] * alpha, hi, lo);
     h[e] = (short)hi;
     l[e] = (short)lo;
   }
@@ -650,7 +693,7 @@ struct OrthoLayout {
   int rp, cp;  // sizes padded to 64
   int parts;   // of P = X X^T
   size_t partial;
-  size_t part, X1, X2, P, Q, total;        // 16-bit slices
+  size_t part, factors, X1, X2, P, Q, total;  // 16-bit slices
   bool direct;                             // FP64: by the FP64 matrix cores
   size_t X, XT, Y, dgemm;                  // FP64
 };
@@ -702,6 +745,7 @@ OrthoLayout ortho_layout(int type, int batch, int m, int n, int s) {
   L.rp = (int)up(r, 64);
   L.cp = (int)up(c, 64);
   const size_t rc = (size_t)batch * 2 * L.rp * L.cp * 2, rr = (size_t)batch * 2 * L.rp * L.rp * 2;
+  L.factors = take((size_t)batch * OZGEMM_ORTHO_STEPS_MAX * sizeof(StepFactors));
   L.X1 = take(rc);
   L.X2 = take(rc);
   L.P = take(rr);
@@ -717,69 +761,22 @@ OrthoLayout ortho_layout(int type, int batch, int m, int n, int s) {
 // call is bound by its launches, three cost little and leave the rounding alone.
 int ortho_products(int type, int r) { return type == OZGEMM_BF16 && r >= 256 ? 1 : 3; }
 
-// Largest |p| over [0, t] of p(x) = a x + b x^3 + c x^5: at t or where
-// a + 3 b y + 5 c y^2 = 0, y = x^2.
-double peak(double a, double b, double c, double t) {
-  auto p = [&](double x) { return fabs(x * (a + x * x * (b + x * x * c))); };
-  double top = p(t);
-  double roots[2] = {-1, -1};
-  if (c != 0) {
-    const double d = 9 * b * b - 20 * a * c;
-    if (d >= 0) {
-      roots[0] = (-3 * b + sqrt(d)) / (10 * c);
-      roots[1] = (-3 * b - sqrt(d)) / (10 * c);
-    }
-  } else if (b != 0) {
-    roots[0] = -a / (3 * b);
-  }
-  for (double y : roots)
-    if (y > 0 && y < t * t) top = fmax(top, p(sqrt(y)));
-  return top;
-}
-
-// Largest |b y + c y^2| over [0, u].
-double peak_q(double b, double c, double u) {
-  double top = fabs(u * (b + c * u));
-  if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < u) top = fmax(top, fabs(b * b / (4 * c)));
-  return top;
-}
-
-// Power of two S with bound S in [2^13, 2^14): an entry may pass the bound four
-// times over before it leaves half's range (65504).  The bounds hold for the
-// exact iteration; they carry no further margin, because the polynomials of
-// a schedule grow steeply past the interval they are made for and every bit
-// given away here is lost to the low slices.
-bool grid(double bound, double* S) {
-  if (!(bound < 1e18)) return false;
-  int e = 0;
-  frexp(fmax(bound, 1e-6), &e);
-  *S = ldexp(1.0, 14 - e);
-  return true;
-}
-
 #define OZ_TRY(expr)                                                   \
   do {                                                                 \
     const hipError_t oz_err_ = (expr);                                 \
     if (oz_err_ != hipSuccess) return record_hip_error(oz_err_);       \
   } while (0)
 
-struct Scales {
-  double X, P, Q, next;
-};
-
-// The grids of every step; false where the bound leaves a double's sensible range.
-bool scales_of(const double* co, int steps, int i, double* t, Scales* out) {
-  (void)steps;
-  const double a = co[3 * i], b = co[3 * i + 1], c = co[3 * i + 2];
-  const double u = *t * *t;
-  const double after = peak(a, b, c, *t) * (1 + 1.0 / 1024);
-  if (!grid(*t, &out->X) || !grid(u, &out->P) || !grid(peak_q(b, c, u), &out->Q) || !grid(after, &out->next))
-    return false;
-  *t = after;
+// Whether no bound of a schedule's states leaves a double's sensible range, from t_0 = 1 on.
+bool schedule_fits(const double* co, int steps) {
+  double t = 1;
+  for (int k = 0; k < steps; ++k) {
+    const Bounds r = advance(bends_of(co[3 * k], co[3 * k + 1], co[3 * k + 2]), t);
+    if (!in_range(r)) return false;
+    t = r.next;
+  }
   return true;
 }
-
-constexpr double START = 1.0;  // |X_0| <= 1
 
 int ortho64(const OrthoLayout& L, int batch, int m, int n, const double* G, long ldg, long strideg, int steps,
             const double* co, double eps, int s, double* O, long ldo, long strideo, char* ws, hipStream_t st) {
@@ -911,13 +908,12 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
   const long xp = (long)L.rp * L.cp, pp = (long)L.rp * L.rp;
   const int nprod = ortho_products(type, r), lo = nprod == 3;
   const int parts = square_parts(m, n);
-  double t = START;
-  Scales sc;
-  if (!scales_of(co, steps, 0, &t, &sc)) return OZGEMM_RANGE;
+  StepFactors* factors = (StepFactors*)(ws + L.factors);
   OZ_TRY(launch_square_sum(type, G, n, m, ldg, strideg, batch, parts, part, st));
-  const Prepare pr{G, n, m, ldg, strideg, part, parts, eps, sc.X, X, tall ? L.cp : L.rp, tall ? L.rp : L.cp,
-                   xp / 8 * batch < 4096L * 256 ? 1 : PREPARE_RUNS};
-  const dim3 blocks((unsigned)((xp / 8 + 256 * pr.each - 1) / (256 * pr.each)), batch);
+  Prepare pr{G, n, m, ldg, strideg, part, parts, eps, X, tall ? L.cp : L.rp, tall ? L.rp : L.cp,
+             xp / 8 * batch < 4096L * 256 ? 1 : PREPARE_RUNS, factors, steps, batch, {}};
+  for (int i = 0; i < 3 * steps; ++i) pr.co[i] = co[i];
+  const dim3 blocks((unsigned)((xp / 8 + 256 * pr.each - 1) / (256 * pr.each)) + 1, batch);
   if (type == OZGEMM_F32)
     hipLaunchKernelGGL(prepare_kernel<OZGEMM_F32>, blocks, dim3(256), 0, st, pr);
   else if (type == OZGEMM_BF16)
@@ -925,13 +921,11 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
   else
     hipLaunchKernelGGL(prepare_kernel<OZGEMM_F16>, blocks, dim3(256), 0, st, pr);
   OZ_TRY(hipGetLastError());
-  t = START;
   for (int k = 0; k < steps; ++k) {
-    if (!scales_of(co, steps, k, &t, &sc)) return OZGEMM_RANGE;
-    const double a = co[3 * k], b = co[3 * k + 1], c = co[3 * k + 2];
     const int x_ld = tall ? L.rp : L.cp;
     Step p{};
     p.batch = batch;
+    p.factors = factors + (long)k * batch;
     // P = X X^T along the c entries: next to each other in a wide X, a row apart in a tall one
     p.A = p.B = X;
     p.a_batch = p.b_batch = 2 * xp;
@@ -939,13 +933,13 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
     p.a_ld = p.b_ld = x_ld;
     p.m = p.n = L.rp;
     p.k = L.cp;
-    p.alpha = (float)(sc.P / (sc.X * sc.X));
+    p.which = 0;
     p.N = P;
     p.s_batch = 2 * pp;
     p.s_plane = pp;
     p.n_lo = lo;
     if (L.parts > 1)
-      OZ_TRY(launch_gram_parts(Parts{X, 2 * xp, xp, x_ld, L.rp, L.cp, batch, L.parts, p.alpha,
+      OZ_TRY(launch_gram_parts(Parts{X, 2 * xp, xp, x_ld, L.rp, L.cp, batch, L.parts, p.factors,
                                      (float*)(ws + L.partial), P, lo}, nprod, tall, st));
     else
       OZ_TRY(launch_step(p, nprod, tall, true, st));
@@ -955,8 +949,7 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
     p.a_plane = p.b_plane = pp;
     p.a_ld = p.b_ld = L.rp;
     p.k = L.rp;
-    p.alpha = (float)(c * sc.Q / (sc.P * sc.P));
-    p.beta = (float)(b * sc.Q / sc.P);
+    p.which = 1;
     p.S = P;
     p.s_lo = lo;
     p.N = Q;
@@ -973,9 +966,7 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
     p.b_ld = tall ? x_ld : L.rp;
     p.m = tall ? L.rp : L.cp;
     p.n = tall ? L.cp : L.rp;
-    const double next = k + 1 < steps ? sc.next : 1.0;  // the result itself is on no grid
-    p.alpha = (float)(next / (sc.Q * sc.X));
-    p.beta = (float)(a * next / sc.X);
+    p.which = 2;
     p.S = X;
     p.s_lo = 1;
     p.N = other;
@@ -1051,11 +1042,7 @@ int ozgemm_orthogonalize(int type, int batch, int m, int n, const void* G, int l
   }
   if (any && (workspace == nullptr || ((uintptr_t)workspace & 255))) return -15;
   if (!any) return OZGEMM_OK;
-  double t = START;
-  Scales sc;
-  if (type != OZGEMM_F64)
-    for (int k = 0; k < steps; ++k)
-      if (!scales_of(coeffs, steps, k, &t, &sc)) return OZGEMM_RANGE;
+  if (type != OZGEMM_F64 && !schedule_fits(coeffs, steps)) return OZGEMM_RANGE;
   const OrthoLayout L = ortho_layout(type, batch, m, n, s);
   if (workspace_bytes < L.total) return OZGEMM_WORKSPACE_TOO_SMALL;
   hipStream_t st = (hipStream_t)hip_stream;
