@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <array>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -366,19 +367,21 @@ int hip_fail(hipError_t err) {
     if (oz_err_ != hipSuccess) return hip_fail(oz_err_); \
   } while (0)
 
-// Compute units of the current device (queried once per device).
+// Compute units of the current device (queried once per device; calls that
+// keep no state may ask from several host threads).
 int device_cus(int* cus) {
   constexpr int MAX_DEVICES = 64;
-  static int cached[MAX_DEVICES] = {};
+  static std::atomic<int> cached[MAX_DEVICES] = {};
   int dev = 0;
   OZ_CHECK(hipGetDevice(&dev));
   if (dev < 0 || dev >= MAX_DEVICES) return hip_fail(hipErrorInvalidDevice);
-  if (cached[dev] == 0) {
-    int v = 0;
-    OZ_CHECK(hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev));
-    cached[dev] = std::max(v, 1);
+  int units = cached[dev].load(std::memory_order_relaxed);
+  if (units == 0) {
+    OZ_CHECK(hipDeviceGetAttribute(&units, hipDeviceAttributeMultiprocessorCount, dev));
+    units = std::max(units, 1);
+    cached[dev].store(units, std::memory_order_relaxed);
   }
-  *cus = cached[dev];
+  *cus = units;
   return 0;
 }
 
