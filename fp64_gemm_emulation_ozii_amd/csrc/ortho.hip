@@ -6,14 +6,13 @@
 // X stays in half-precision slices (slices.hip) between the products:
 // x 2^E = hi + lo with E from a bound on the singular values of each matrix's
 // own iterate (scales.h), to 2^-22 or better, or 2^-38 of that bound for entries
-// far below it, whatever the type and however small |G| is beside eps.  F16 and
-// F32, and BF16 of less than 256 rows, hold P and Q likewise and take three
-// slice products.  Larger BF16 holds them, and multiplies X, in the high slice
-// alone (one product of operands that are off by 2^-12, a sixteenth of the
-// result's own rounding; the term a X, through which small singular values grow
-// 3.4 times a step, uses both slices, so rounding is not amplified with them;
-// ortho_products has what it costs in accuracy).  F64 runs the library's Scheme
-// II products.
+// far below it, whatever the type and however small |G| is beside eps; P and Q
+// lie likewise.  BF16, F16 and F32 all take three slice products of every two
+// states.  (One product of the high slices alone, with P and Q in one slice, took
+// half the time for BF16, but its results were off by 1.25 times their rounding
+// on four layers of 1024 x 4096, by 2 after eight steps, and by 9 with schedules
+// whose terms cancel, on matrices of low rank: so nothing takes it.)  F64 runs
+// the library's Scheme II products.
 //
 // X stays as G lies: wide (r rows of c entries next to each other) or tall (c
 // rows of r).  P = X X^T runs along the c entries, Q X along the r rows; the
@@ -301,7 +300,6 @@ struct Step {
   const uint16_t* S;  // like N; nullptr: none
   uint16_t* N;
   long s_batch, s_plane;  // of S and N alike
-  int s_lo, n_lo;         // whether the low slices are there
   void* O;
   int otype;
   long ldo, batcho;
@@ -349,7 +347,7 @@ __device__ __forceinline__ void step_tile(const Step& p, char* smem, long b, int
       if (!inside(j, ch)) continue;
       const long off = offset(j, ch);
       sh[j & 1][ch] = *reinterpret_cast<const v8s*>(S + off);
-      if (p.s_lo) sl[j & 1][ch] = *reinterpret_cast<const v8s*>(S + p.s_plane + off);
+      sl[j & 1][ch] = *reinterpret_cast<const v8s*>(S + p.s_plane + off);
     }
   };
   fetch(0);
@@ -392,7 +390,7 @@ __device__ __forceinline__ void step_tile(const Step& p, char* smem, long b, int
       }
       const long off = offset(j, ch);
       *reinterpret_cast<v8s*>(N + off) = h;
-      if (p.n_lo) *reinterpret_cast<v8s*>(N + p.s_plane + off) = l;
+      *reinterpret_cast<v8s*>(N + p.s_plane + off) = l;
       // the rounded slices go back to the staging piece for the other side
       if (mirror) {
 #pragma unroll
@@ -416,7 +414,7 @@ __device__ __forceinline__ void step_tile(const Step& p, char* smem, long b, int
         }
         const long off = (long)(mw + r) * p.n + nw + j * 16 + c;
         *reinterpret_cast<v8s*>(N + off) = h;
-        if (p.n_lo) *reinterpret_cast<v8s*>(N + p.s_plane + off) = l;
+        *reinterpret_cast<v8s*>(N + p.s_plane + off) = l;
       }
       __builtin_amdgcn_s_waitcnt(0xc07f);
       asm volatile("" ::: "memory");
@@ -433,10 +431,10 @@ __device__ __forceinline__ void step_tile(const Step& p, char* smem, long b, int
 // by its 136 tiles on 256 units (180 us, 760 TFLOPS, at 2.3 GHz); Q X of four
 // 1024 x 4096 by its one round of tiles, whose loads and stores (200 MB) do
 // not overlap its products (46 us).
-template <int BT, int WM, int WN, int NB, bool PAIR, bool QUARTERS, bool AKS, bool BKS, bool SYM>
+template <int BT, int WM, int WN, int NB, bool QUARTERS, bool AKS, bool BKS, bool SYM>
 __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p, int whole) {
-  using Tile = Tile16<Half, BT, BT, WM, WN, AKS, BKS, NB, PAIR>;
-  using Small = Tile16<Half, QUARTERS ? BT / 2 : BT, QUARTERS ? BT / 2 : BT, WM, WN, AKS, BKS, 4, PAIR>;
+  using Tile = Tile16<Half, BT, BT, WM, WN, AKS, BKS, NB, true>;
+  using Small = Tile16<Half, QUARTERS ? BT / 2 : BT, QUARTERS ? BT / 2 : BT, WM, WN, AKS, BKS, 4, true>;
   constexpr int SMEM = QUARTERS && Small::SMEM > Tile::SMEM ? Small::SMEM : Tile::SMEM;
   __shared__ __attribute__((aligned(1024))) char smem[SMEM];
   const int tm = (p.m + BT - 1) / BT, tn = (p.n + BT - 1) / BT;
@@ -466,33 +464,30 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p, int whole)
   }
 }
 
-template <int BT, int WM, int WN, int NB, bool PAIR, bool QUARTERS>
+template <int BT, int WM, int WN, int NB, bool QUARTERS>
 hipError_t launch_step_t(const Step& p, bool aks, bool sym, int units, hipStream_t st) {
   const long tm = (p.m + BT - 1) / BT, tn = (p.n + BT - 1) / BT;
   const long tiles = (sym ? tm * (tm + 1) / 2 : tm * tn) * p.batch, rest = tiles % units;
   const int whole = (int)(QUARTERS && rest * 2 <= units ? tiles - rest : tiles);
   const dim3 grid((unsigned)(whole + 4 * (tiles - whole))), block(WM * WN * 64);
   if (sym && aks)
-    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, QUARTERS, true, true, true>), grid, block, 0, st, p, whole);
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, QUARTERS, true, true, true>), grid, block, 0, st, p, whole);
   else if (sym)
-    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, QUARTERS, false, false, true>), grid, block, 0, st, p, whole);
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, QUARTERS, false, false, true>), grid, block, 0, st, p, whole);
   else if (aks)
-    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, QUARTERS, true, false, false>), grid, block, 0, st, p, whole);
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, QUARTERS, true, false, false>), grid, block, 0, st, p, whole);
   else
-    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, PAIR, QUARTERS, false, false, false>), grid, block, 0, st, p, whole);
+    hipLaunchKernelGGL((step_kernel<BT, WM, WN, NB, QUARTERS, false, false, false>), grid, block, 0, st, p, whole);
   return hipGetLastError();
 }
 
 // The tile size of a product of S K slices: the modelled time, in us, of its
 // rounds of one tile per compute unit (a quartered last round counts 0.4 per
 // `units` quarters).  A round takes S slices and a start and an end; measured
-// with every unit busy:
-//   one slice product   256 x 256  1.4 S + 9   128 x 128  0.6 S + 7   64 x 64  0.23 S + 3
-//   three               128 x 128  1.2 S + 8                          64 x 64  0.43 S + 3
-// (64 x 64 with three products: two blocks of four wavefronts on a unit; where
-// there is only one for each, eight wavefronts and four buffers, 0.53 S
-// against 0.74 S.)
-hipError_t launch_step(const Step& p, int nprod, bool aks, bool sym, hipStream_t st) {
+// with every unit busy: 128 x 128  1.2 S + 8   64 x 64  0.43 S + 3
+// (64 x 64: two blocks of four wavefronts on a unit; where there is only one for
+// each, eight wavefronts and four buffers, 0.53 S against 0.74 S.)
+hipError_t launch_step(const Step& p, bool aks, bool sym, hipStream_t st) {
   int units = 0;
   const hipError_t err = device_units(&units);
   if (err != hipSuccess) return err;
@@ -503,17 +498,10 @@ hipError_t launch_step(const Step& p, int nprod, bool aks, bool sym, hipStream_t
     const double last = rest == 0 ? 0 : quarters && rest * 2 <= units ? 0.4 * ((4 * rest + units - 1) / units) : 1;
     return (double)(tiles / units) + last;
   };
-  if (nprod == 3) {
-    if (rounds(128, true) * (1.2 * S + 8) <= rounds(64, false) * (0.43 * S + 3))
-      return launch_step_t<128, 2, 4, 2, true, true>(p, aks, sym, units, st);
-    if (rounds(64, false) <= 1) return launch_step_t<64, 2, 4, 4, true, false>(p, aks, sym, units, st);
-    return launch_step_t<64, 2, 2, 2, true, false>(p, aks, sym, units, st);
-  }
-  const double t256 = rounds(256, true) * (1.4 * S + 9), t128 = rounds(128, true) * (0.6 * S + 7),
-               t64 = rounds(64, false) * (0.23 * S + 3);
-  if (t256 <= t128 && t256 <= t64) return launch_step_t<256, 2, 4, 2, false, true>(p, aks, sym, units, st);
-  if (t128 <= t64) return launch_step_t<128, 2, 4, 4, false, true>(p, aks, sym, units, st);
-  return launch_step_t<64, 2, 2, 4, false, false>(p, aks, sym, units, st);
+  if (rounds(128, true) * (1.2 * S + 8) <= rounds(64, false) * (0.43 * S + 3))
+    return launch_step_t<128, 2, 4, 2, true>(p, aks, sym, units, st);
+  if (rounds(64, false) <= 1) return launch_step_t<64, 2, 4, 4, false>(p, aks, sym, units, st);
+  return launch_step_t<64, 2, 2, 2, false>(p, aks, sym, units, st);
 }
 
 // P = X X^T for few rows and long ones, along the c entries in `parts` parts
@@ -528,12 +516,11 @@ struct Parts {
   const StepFactors* factors;
   float* partial;  // [parts][batch][r][r]
   uint16_t* P;     // [batch][2][r][r]
-  int lo;
 };
 
-template <bool PAIR, bool KS>
+template <bool KS>
 __global__ __launch_bounds__(256, 2) void gram_parts_kernel(Parts p) {
-  using Tile = Tile16<Half, 64, 64, 2, 2, KS, KS, PAIR ? 2 : 4, PAIR>;
+  using Tile = Tile16<Half, 64, 64, 2, 2, KS, KS, 2, true>;
   __shared__ __attribute__((aligned(1024))) char smem[Tile::SMEM];
   const int t = p.r / 64;
   int w = blockIdx.x;
@@ -580,22 +567,15 @@ __global__ __launch_bounds__(256) void gram_join_kernel(Parts p) {
   }
   uint16_t* out = p.P + b * 2 * plane + at;
   *reinterpret_cast<v8s*>(out) = h;
-  if (p.lo) *reinterpret_cast<v8s*>(out + plane) = l;
+  *reinterpret_cast<v8s*>(out + plane) = l;
 }
 
-hipError_t launch_gram_parts(const Parts& p, int nprod, bool ks, hipStream_t st) {
+hipError_t launch_gram_parts(const Parts& p, bool ks, hipStream_t st) {
   const dim3 grid((unsigned)((long)(p.r / 64) * (p.r / 64) * p.batch * p.parts));
-  if (nprod == 3) {
-    if (ks)
-      hipLaunchKernelGGL((gram_parts_kernel<true, true>), grid, dim3(256), 0, st, p);
-    else
-      hipLaunchKernelGGL((gram_parts_kernel<true, false>), grid, dim3(256), 0, st, p);
-  } else {
-    if (ks)
-      hipLaunchKernelGGL((gram_parts_kernel<false, true>), grid, dim3(256), 0, st, p);
-    else
-      hipLaunchKernelGGL((gram_parts_kernel<false, false>), grid, dim3(256), 0, st, p);
-  }
+  if (ks)
+    hipLaunchKernelGGL((gram_parts_kernel<true>), grid, dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((gram_parts_kernel<false>), grid, dim3(256), 0, st, p);
   const long runs = ((long)p.r * p.r / 8 + 255) / 256;
   hipLaunchKernelGGL(gram_join_kernel, dim3((unsigned)runs, p.batch), dim3(256), 0, st, p);
   return hipGetLastError();
@@ -755,12 +735,6 @@ OrthoLayout ortho_layout(int type, int batch, int m, int n, int s) {
   return L;
 }
 
-// Slice products of a step.  One is enough for BF16 results: at 1024 rows the
-// error is 1.2 to 1.35 times the rounding of the result alone.  It falls with
-// the smaller side r (1.1 at 2048, 1.6 at 64), and below 256 rows, where a
-// call is bound by its launches, three cost little and leave the rounding alone.
-int ortho_products(int type, int r) { return type == OZGEMM_BF16 && r >= 256 ? 1 : 3; }
-
 #define OZ_TRY(expr)                                                   \
   do {                                                                 \
     const hipError_t oz_err_ = (expr);                                 \
@@ -899,14 +873,12 @@ int ortho64_direct(const OrthoLayout& L, int batch, int m, int n, const double* 
 int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void* G, long ldg, long strideg, int steps,
             const double* co, double eps, void* O, long ldo, long strideo, char* ws, hipStream_t st) {
   const bool tall = n > m;  // as it lies: n rows of m entries
-  const int r = tall ? m : n;
   uint16_t* X = (uint16_t*)(ws + L.X1);
   uint16_t* other = (uint16_t*)(ws + L.X2);
   uint16_t* P = (uint16_t*)(ws + L.P);
   uint16_t* Q = (uint16_t*)(ws + L.Q);
   double* part = (double*)(ws + L.part);
   const long xp = (long)L.rp * L.cp, pp = (long)L.rp * L.rp;
-  const int nprod = ortho_products(type, r), lo = nprod == 3;
   const int parts = square_parts(m, n);
   StepFactors* factors = (StepFactors*)(ws + L.factors);
   OZ_TRY(launch_square_sum(type, G, n, m, ldg, strideg, batch, parts, part, st));
@@ -937,12 +909,11 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
     p.N = P;
     p.s_batch = 2 * pp;
     p.s_plane = pp;
-    p.n_lo = lo;
     if (L.parts > 1)
       OZ_TRY(launch_gram_parts(Parts{X, 2 * xp, xp, x_ld, L.rp, L.cp, batch, L.parts, p.factors,
-                                     (float*)(ws + L.partial), P, lo}, nprod, tall, st));
+                                     (float*)(ws + L.partial), P}, tall, st));
     else
-      OZ_TRY(launch_step(p, nprod, tall, true, st));
+      OZ_TRY(launch_step(p, tall, true, st));
     // Q = b P + c P^2
     p.A = p.B = P;
     p.a_batch = p.b_batch = 2 * pp;
@@ -951,9 +922,8 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
     p.k = L.rp;
     p.which = 1;
     p.S = P;
-    p.s_lo = lo;
     p.N = Q;
-    OZ_TRY(launch_step(p, nprod, false, true, st));
+    OZ_TRY(launch_step(p, false, true, st));
     // X <- a X + Q X along the r rows, the result as X lies: wide, its row j
     // is row j of Q against X's columns; tall, row j of X against Q
     p.A = tall ? Q : X;
@@ -968,11 +938,9 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
     p.n = tall ? L.cp : L.rp;
     p.which = 2;
     p.S = X;
-    p.s_lo = 1;
     p.N = other;
     p.s_batch = 2 * xp;
     p.s_plane = xp;
-    p.n_lo = 1;
     if (k + 1 == steps) {
       p.O = O;
       p.otype = type;
@@ -981,7 +949,7 @@ int ortho16(const OrthoLayout& L, int type, int batch, int m, int n, const void*
       p.om = m;
       p.on = n;
     }
-    OZ_TRY(launch_step(p, nprod, !tall, false, st));
+    OZ_TRY(launch_step(p, !tall, false, st));
     uint16_t* swap = X;
     X = other;
     other = swap;

@@ -527,11 +527,9 @@ size_t ozgemm_grouped_outer_workspace_bytes(int type, int groups, int m, int q, 
  * Between its products X is kept in two half-precision slices (F64: as it is)
  * on a power-of-two grid that follows each matrix's own |G|_F / (|G|_F + eps)
  * and the coefficients: an entry to 2^-22 of itself or 2^-38 of the bound on X's
- * singular values, whichever is more.  F16 and F32 keep P and Q = b P + c P^2
- * likewise, and their products are formed as the grouped products of F32
- * operands are; so are BF16's where min(m, n) < 256.  Larger BF16 matrices
- * keep P and Q, and multiply X, in one slice of 11 bits: the result is off by up
- * to 1.3 times its rounding to BF16 (the same matrix given as F32 is not).
+ * singular values, whichever is more; P and Q = b P + c P^2 likewise.  Their
+ * products are formed as the grouped products of F32 operands are, whatever the
+ * type, and the result is rounded to it once.
  * The norm is a sum of squares in FP64 (F64 entries beyond 1e153 overflow it:
  * zeros; those below 1e-162 count as none).  steps = 0 gives the normalised G.
  * A matrix of zeros gives zeros where eps > 0 (NaN where it is 0); one that holds Inf
