@@ -168,7 +168,7 @@ struct Job {
 // A block's tiles.  The next tile's first slice lands in buffer 0 while this
 // one's results go out through the LDS behind it, and its products begin
 // before they are written (16384 rows, 32 groups of 4096 x 2048: 357 us with a
-// block per tile, 326 so).  place(L, dm, dn) gives the job of tile L from
+// block per tile, 326 so, call after call; 330 to 430 in single calls).  place(L, dm, dn) gives the job of tile L from
 // (dm, dn) in it on.
 template <class Tile, class Small>
 struct Walk {
@@ -224,7 +224,7 @@ struct Walk {
 // is 256 rows of the weights by 256 columns of one group, of which the last of
 // a group is half empty on average: 512 rows a group run at 840 TFLOPS.  Tiles
 // are walked group by group, four panels of columns against all rows of the
-// weights at a time on an XCD, so that weights come from HBM about once (546 MB
+// weights at a time on an XCD, so that weights come from HBM about once (536 MB
 // read for 537 MB of weights and 67 MB of rows, most of which stay in L2).
 // F32 (PAIR) holds two slices of both operands and takes 128 x 128: 8192 rows,
 // 16 groups of 2048 x 2048 take 295 us, 233 TFLOPS of f32 or 700 of its slices.
@@ -747,6 +747,9 @@ hipError_t grouped_k(Grouped16 g, hipStream_t st) {
 
 }  // namespace
 
+// (256 units: the rules below also size workspaces, which a host without a GPU may
+// ask for, so they are written for the card and do not ask the device.)
+//
 // Whether the kernels for few columns are the faster ones: 0, or the parts in
 // which they take the inner dimension.  The others cut F32 and copy operands
 // off the 16-byte grid (`edge`) first.  Measured in us (few columns / tiles),

@@ -426,11 +426,11 @@ __device__ __forceinline__ void step_tile(const Step& p, char* smem, long b, int
 // leave most compute units idle) are cut into quarters.  (Blocks that walk
 // tiles, as the grouped products', gained nothing here: a matrix has few
 // rounds, and a step's epilogue reads and writes as much as its operands.)
-// Bound by the matrix cores where the tiles fill the card (Q X of 4096 x 8192:
-// 245 us, 1120 TFLOPS, 55% of the MFMA cycles at 1.94 GHz); X X^T of 4096 rows
-// by its 136 tiles on 256 units (180 us, 760 TFLOPS, at 2.3 GHz); Q X of four
-// 1024 x 4096 by its one round of tiles, whose loads and stores (200 MB) do
-// not overlap its products (46 us).
+// Bound by the matrix cores where the tiles fill the card (4096 x 8192: Q X 706 us,
+// 389 TFLOPS or 1170 of its slices, 63% of the MFMA cycles at the 1.74 GHz that
+// the power leaves; X X^T about 400 us, 1030 of its slices).  Q X of four 1024 x
+// 4096 takes 107 us (960 of its slices): four rounds of tiles whose loads and
+// stores (200 MB) do not overlap their products.
 template <int BT, int WM, int WN, int NB, bool QUARTERS, bool AKS, bool BKS, bool SYM>
 __global__ __launch_bounds__(WM* WN * 64, 2) void step_kernel(Step p, int whole) {
   using Tile = Tile16<Half, BT, BT, WM, WN, AKS, BKS, NB, true>;

@@ -145,6 +145,12 @@ def grouped_linear(X, W, offsets, out=None, out_dtype=None):
     (``out_dtype``).  Rows of no group are left as they were in ``out``;
     without ``out`` they are not written.  ``out`` must not overlap X, W or the
     offsets, each taken from its first entry to its last.
+
+    bfloat16 and float16 sums are float32, rounded once.  float32 products of few
+    rows and small ones are formed in float32; larger ones of two half-precision
+    slices per entry, which hold it to 2^-23 of itself or 2^-40 of the largest
+    entry of its row of X or W, and where a row with Inf or NaN gives NaN.  The
+    sizes and the alignment alone decide which.
     """
     _same(X, W, "X and W")
     _no_grad("grouped_linear", X, W, out, instead=_INSTEAD)
@@ -172,7 +178,8 @@ def grouped_linear_grads(dY, X, W, offsets, dX=None, dW=None, dw_dtype=None):
 
     dX is [n, q] in X's type (rows of no group as in ``out`` there), dW
     [g, m, q] in X's type or float32 (``dw_dtype``), zeros for a group
-    without rows.  Neither may overlap dY, X, the offsets or the other, nor
+    without rows.  Sums and float32 operands as in :func:`grouped_linear` (for dW
+    a "row" is a column of X or dY within a group).  Neither may overlap dY, X, the offsets or the other, nor
     dX the weights.
     """
     _same(X, W, "X and W")
@@ -214,7 +221,8 @@ def orthogonalize(G, steps: int = 5, coeffs=QUINTIC, eps: float = 1e-7, out=None
     ``X = G / (norm + eps)``, then ``X = a X + (b P + c P P) X`` with
     ``P = X X^T`` (of the smaller side).
 
-    G is float64, float32, bfloat16 or float16 and the result of its type;
+    G is float64, float32, bfloat16 or float16 and the result of its type, rounded
+    once (between the steps X is held to 22 bits, float64 to 53);
     ``coeffs`` is one triple (a, b, c) or one for each step.  ``out`` may be G
     itself.  ``s`` is the number of moduli of the float64 products.
     """

@@ -438,8 +438,12 @@ int ozgemm_mfma_ceiling(int blocks, int steps, unsigned seed, unsigned *sink, vo
  * the slices hold an entry to 2^-23 and the products drop at most 2^-22 of a
  * term (2^-39 of the row's largest entry where that is more), under the
  * rounding of the FP32 sums.  A row that holds Inf or NaN makes the outputs
- * it touches NaN, as in ozgemm_dgemm.  Small F32 products of either kind are
- * multiplied in FP32 as they lie, where Inf and NaN follow the usual rules.
+ * it touches NaN, as in ozgemm_dgemm.  F32 products of few columns and small
+ * ones are multiplied in FP32 as they lie instead: an entry is itself however
+ * far below its row's largest, and Inf and NaN follow the usual rules.  Which
+ * of the two a call takes depends on its sizes and on the alignment of its
+ * operands alone; slices always need a workspace, so a call for which
+ * ..._workspace_bytes gives 0 goes in FP32.
  * (BF16 and F16 follow the usual rules for Inf and NaN.)  Results do not
  * depend on the order in which blocks run. */
 #define OZGEMM_F64  0
@@ -454,7 +458,9 @@ int ozgemm_mfma_ceiling(int blocks, int steps, unsigned seed, unsigned *sink, vo
  * increasing order (equal neighbours make an empty group) within [0, n].
  * Columns before offsets[0] and from offsets[groups] on belong to no group.
  * Offsets out of order or out of range are read as the nearest ordered ones
- * (running maximum, cut to [0, n]): nothing outside the operands is touched. */
+ * (running maximum, cut to [0, n]): nothing outside the operands is touched
+ * (but for the other half of an aligned 4-byte word that begins or ends with
+ * an operand's first or last 16-bit entry, which is read and not used). */
 
 /* C(:, j) = op(A_e) B(:, j) for the columns j of every group e: the product
  * of a layer of experts (columns are tokens, sorted by expert), and, with
@@ -466,7 +472,8 @@ int ozgemm_mfma_ceiling(int blocks, int steps, unsigned seed, unsigned *sink, vo
  *   B       q x n, ldb >= max(1, q);  C  m x n, ldc >= max(1, m), type
  *           ctype: `type` itself or OZGEMM_F32
  * Columns of no group are left as they were.  q = 0 gives zeros.  C must not
- * overlap A or B.  Every array begins at a multiple of its entries' size.
+ * overlap A, B or the offsets, each from its first entry to its last (rows
+ * that interleave overlap).  Every array begins at a multiple of its entries' size.
  * Products of few columns and small ones read their operands as they lie.
  * Larger ones do so with 16-bit operands whose rows begin on 16-byte
  * boundaries, K-contiguous ones (A with transa = 1, B) with q a multiple of 8,
