@@ -58,6 +58,38 @@ def test_whole_numbers_that_need_the_low_slices_of_any_operand(wide):
         assert torch.equal(dW[e].double(), dY[s].double().T @ X[s].double())
 
 
+@pytest.mark.parametrize("layout", ["mq", "qm"])
+@pytest.mark.parametrize("dtype, sizes, m, q", [
+    ("bf16", [300, 0, 200], 96, 4096), ("f16", [700], 33, 1601), ("f32", [100, 40], 72, 2000),
+    ("bf16", [256], 2048, 32768), ("f16", [300, 212], 1030, 8190), ("f32", [5, 0, 17], 40, 12288),
+    ("f32", [3], 1000, 16388), ("bf16", [3], 1000, 16389), ("f32", [9000, 0, 777], 520, 1031),
+    ("bf16", [30000, 0, 9000], 512, 264), ("f32", [40000], 500, 260), ("f16", [33000], 511, 257),
+    ("f32", [20, 33000], 1024, 1032), ("bf16", [33000], 1536, 2048), ("f16", [70, 0, 5000, 300] * 8, 264, 520)])
+def test_whole_numbers_over_long_sums(dtype, sizes, m, q, layout):
+    # no entry may be lost where the tolerances of long sums would let one pass: what is exact in FP32 comes out exactly
+    t, g = TYPES[dtype], torch.Generator(device="cuda").manual_seed(m + q)
+    n = sum(sizes)
+    off = torch.tensor([0, *torch.tensor(sizes).cumsum(0).tolist()], dtype=torch.int32, device="cuda")
+
+    def sparse(*shape):  # -1, 0 or 1, one in sixteen not 0
+        k = torch.randint(0, 32, shape, generator=g, device="cuda", dtype=torch.int8)
+        return (k == 0).to(t) - (k == 1).to(t)
+
+    X = (torch.randint(0, 2, (n, q), generator=g, device="cuda") * 2 - 1).to(t) * (4097 if dtype == "f32" else 7)
+    W, dY = sparse(len(sizes), m, q), sparse(n, m)
+    if layout == "qm":
+        W = W.transpose(1, 2).contiguous().transpose(1, 2)
+    Y = oz.grouped_linear(X, W, off, out_dtype=torch.float32)
+    dX, dW = oz.grouped_linear_grads(dY, X, W, off, dw_dtype=torch.float32)
+    o = off.tolist()
+    for e in range(len(sizes)):
+        s = slice(o[e], o[e + 1])
+        x, w, y = X[s].double(), W[e].double().contiguous(), dY[s].double()
+        for got, a, b in ((Y[s], x, w.T.contiguous()), (dX[s], y, w), (dW[e], y.T.contiguous(), x)):
+            assert not a.numel() or (a.abs() @ b.abs()).max() < 2 ** 24  # of ones: every partial sum is exact
+            assert torch.equal(got, (a @ b).to(got.dtype))
+
+
 def test_calls_from_several_host_threads():
     jobs = []
     for k, dtype in enumerate((torch.bfloat16, torch.float32, torch.float16, torch.float32)):
