@@ -403,7 +403,7 @@ def _room(workspace, nbytes: int, device, stream: int):
     import torch
     if stream == _current_stream():
         t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif stream & 1:  # no address of a stream: torch could not tell it from its own ones
+    elif 0 < stream < 4096 or stream & 1:  # HIP's names for the legacy stream and a thread's own: no stream object's address
         raise ValueError(f"a call on the stream {stream:#x} needs its workspace given")
     else:
         with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if stream else

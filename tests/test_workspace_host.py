@@ -101,11 +101,12 @@ def test_the_workspace_belongs_to_the_stream_of_the_call(world, call, stream, ha
 
 
 @pytest.mark.parametrize("call", CALLS)
-def test_a_handle_that_is_no_stream_needs_a_workspace(world, call):
+@pytest.mark.parametrize("handle", [1, 2])  # hipStreamLegacy, hipStreamPerThread
+def test_a_handle_that_is_no_stream_needs_a_workspace(world, call, handle):
     taken, lib = world
     with pytest.raises(ValueError, match="workspace"):
-        call(stream=1)
+        call(stream=handle)
     assert not lib.calls and not taken
     given = torch.zeros(NEED, dtype=torch.uint8)
-    assert call(stream=1, workspace=given) == 0
-    assert lib.calls == [(1, given.data_ptr())]
+    assert call(stream=handle, workspace=given) == 0
+    assert lib.calls == [(handle, given.data_ptr())]
