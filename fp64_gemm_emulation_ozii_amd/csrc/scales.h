@@ -37,11 +37,12 @@ __host__ __device__ inline double odd_quintic(double a, double b, double c, doub
 
 __host__ __device__ inline Bends bends_of(double a, double b, double c) {
   Bends s{a, b, c, {0, 0}, {0, 0}, 0, 0};
-  if (c != 0) {  // a + 3 b y + 5 c y^2 = 0
+  if (c != 0) {  // a + 3 b y + 5 c y^2 = 0, without the difference that loses the small root where c is
     const double d = 9 * b * b - 20 * a * c;
     if (d >= 0) {
-      s.y[0] = (-3 * b + sqrt(d)) / (10 * c);
-      s.y[1] = (-3 * b - sqrt(d)) / (10 * c);
+      const double h = -0.5 * (3 * b + copysign(sqrt(d), b));
+      s.y[0] = h / (5 * c);
+      if (h != 0) s.y[1] = a / h;
     }
     s.yq = -b / (2 * c);
     s.topq = fabs(b * b / (4 * c));

@@ -88,3 +88,13 @@ def test_results_near_the_end_of_single_precision():
     want = plain(G, eps=1e10)
     assert want.abs().max() < 1e-32
     assert rel(oz.orthogonalize(G, eps=1e10), want) <= tolerance(G, want, eps=1e10)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("c", [1e-16, -1e-18, 1e-30])
+def test_a_quintic_that_is_next_to_a_cubic(c, dtype):
+    # a first step to singular values up to 3 ** 0.5, where the cubic's p is 0: its peak lies before
+    coeffs = [(3 ** 0.5, 0.0, 0.0), (1.5, -0.5, c), (1.0, 0.0, 0.0)]
+    G = draw((70, 90), TYPES[dtype], 14)
+    want = plain(G, 3, coeffs)
+    assert rel(oz.orthogonalize(G, steps=3, coeffs=coeffs), want) <= tolerance(G, want, steps=3, coeffs=coeffs)

@@ -86,3 +86,13 @@ def test_first_bound(driver):
     got = [v for v, in driver(rows, "first")]
     assert got[:3] == [1.0, 1e-3 / (1e-3 + 1e-7), 1e-20 / (1e-20 + 1e-7)]
     assert got[3:7] == [1.0] * 4 and got[7] == 2.0 ** -400 and got[8] == 1.0
+
+
+@pytest.mark.parametrize("c", [1e-9, -1e-9, 1e-14, 1e-16, -1e-16, 1e-18, -1e-30, 1e-300, 0.0])
+@pytest.mark.parametrize("a, b, t", [(1.5, -0.5, 3 ** 0.5), (1.5, -0.5, 1.5), (3.0, -1.0, 1.2), (0.0, -1.0, 1.0), (-2.0, 2.0, 1.0)])
+def test_peaks_next_to_a_cubic(driver, a, b, c, t):
+    # the quintic's term is next to nothing: its stationary points are the cubic's (and one far away)
+    (X, P, Q, nxt, *_rest), = driver([(a, b, c, t)])
+    x = np.linspace(0, t, 20001)
+    p = np.abs(x * (a + x * x * (b + x * x * c))).max()
+    assert p <= nxt * (1 + 1e-12) and nxt <= p * (1 + 1.0 / 1024) * (1 + 1e-6)
