@@ -148,7 +148,7 @@ def grouped_linear(X, W, offsets, out=None, out_dtype=None):
 
     bfloat16 and float16 sums are float32, rounded once.  float32 products of few
     rows and small ones are formed in float32; larger ones of two half-precision
-    slices per entry, which hold it to 2^-23 of itself or 2^-40 of the largest
+    slices per entry, which hold it to 2^-23 of itself or 2^-39 of the largest
     entry of its row of X or W, and where a row with Inf or NaN gives NaN.  The
     sizes and the alignment alone decide which.
     """
