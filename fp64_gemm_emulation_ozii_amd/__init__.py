@@ -3,23 +3,30 @@ on AMD MI355X.
 
 The computation lives in the HIP library ``libozgemm.so`` (C-ABI in
 ``include/ozgemm.h``); :mod:`.ozgemm` is its ctypes binding,
-:mod:`.synthetic` draws seeded inputs and :mod:`.layers` holds the products
-of expert layers and the orthogonalisation of updates on torch tensors.  Importing the package loads nothing; the
+:mod:`.synthetic` draws seeded inputs, :mod:`.layers` holds the products of
+expert layers, the clipping of gradients and the orthogonalisation of updates on
+torch tensors, and :mod:`.blocks` a layer in 8 bits.  Importing the package loads nothing; the
 library is opened on first use and its absence is an error.
 """
 from . import ozgemm  # noqa: F401
 from .ozgemm import OzgemmError  # noqa: F401
 
-__all__ = ["ozgemm", "OzgemmError", "dgemm_colmajor", "grouped_linear", "grouped_linear_grads", "orthogonalize"]
+_LAYERS = ("grouped_linear", "grouped_linear_grads", "orthogonalize", "gradient_norm", "clip_gradients")
+_BLOCKS = ("quantize_blocks", "scaled_linear", "scaled_linear_grads", "rms_norm", "rms_norm_quantized", "rms_norm_grads")
+
+__all__ = ["ozgemm", "OzgemmError", "dgemm_colmajor", *_LAYERS, *_BLOCKS]
 
 
 def __getattr__(name):
     # torch is imported with the first use of a function that takes tensors
-    if name in ("grouped_linear", "grouped_linear_grads", "orthogonalize"):
-        from . import layers
-        globals()[name] = getattr(layers, name)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    if name in _LAYERS:
+        from . import layers as module
+    elif name in _BLOCKS:
+        from . import blocks as module
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    globals()[name] = getattr(module, name)
+    return globals()[name]
 
 
 def dgemm_colmajor(A_cm, B_cm, m: int, n: int, q: int, s: int, C_cm=None):

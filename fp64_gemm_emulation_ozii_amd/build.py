@@ -20,7 +20,8 @@ OUT = os.path.join(PKG, "libozgemm.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["ozgemm.hip", "scale.hip", "residue.hip", "gemm_i8.hip", "crt.hip", "scheme1.hip", "accu.hip", "probe.hip",
-           "gemm16.hip", "slices.hip", "grouped.hip", "ortho.hip"]
+           "gemm16.hip", "slices.hip", "grouped.hip", "ortho.hip", "quantize.hip", "gemm8.hip", "scaled.hip", "norm.hip",
+           "clip.hip"]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

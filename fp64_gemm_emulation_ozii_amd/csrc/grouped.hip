@@ -19,19 +19,6 @@ bool aligned16(const void* p, long ld, long batch, int run = 8) {
   return ((uintptr_t)p & 15) == 0 && ld % run == 0 && batch % run == 0 && ld <= LD16_MAX;
 }
 
-// Bytes from the first entry of `batches` rows x cols column-major matrices
-// to the end of the last.
-size_t extent(int rows, long cols, long ld, long long batch, int batches, size_t size) {
-  if (rows < 1 || cols < 1 || batches < 1) return 0;
-  return ((size_t)(batches - 1) * (size_t)batch + (size_t)(cols - 1) * (size_t)ld + (size_t)rows) * size;
-}
-
-bool overlap(const void* a, size_t abytes, const void* b, size_t bbytes) {
-  const char* pa = (const char*)a;
-  const char* pb = (const char*)b;
-  return abytes && bbytes && pa < pb + bbytes && pb < pa + abytes;
-}
-
 // Room for one operand laid out in the workspace.
 struct Room {
   bool used;

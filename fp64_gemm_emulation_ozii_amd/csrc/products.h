@@ -10,10 +10,23 @@
 namespace oz {
 
 inline size_t elem_bytes(int type) {
-  return type == OZGEMM_F64 ? 8 : type == OZGEMM_F32 ? 4 : 2;
+  return type == OZGEMM_F64 ? 8 : type == OZGEMM_F32 ? 4 : type == OZGEMM_E4M3 || type == OZGEMM_E5M2 ? 1 : 2;
 }
 
 inline size_t up(size_t x, size_t r) { return (x + r - 1) / r * r; }
+
+// Bytes from the first entry of `batches` rows x cols column-major matrices
+// to the end of the last.
+inline size_t extent(int rows, long cols, long ld, long long batch, int batches, size_t size) {
+  if (rows < 1 || cols < 1 || batches < 1) return 0;
+  return ((size_t)(batches - 1) * (size_t)batch + (size_t)(cols - 1) * (size_t)ld + (size_t)rows) * size;
+}
+
+inline bool overlap(const void* a, size_t abytes, const void* b, size_t bbytes) {
+  const char* pa = (const char*)a;
+  const char* pb = (const char*)b;
+  return abytes && bbytes && pa < pb + bbytes && pb < pa + abytes;
+}
 
 // An operand of a 16-bit product as the kernels read it.
 struct Operand16 {

@@ -1,5 +1,5 @@
-"""Products of expert layers and the orthogonalisation of their updates on
-torch tensors (row-major): the calls of :mod:`.ozgemm` with their shapes, strides and types taken from the tensors.
+"""Products of expert layers, the clipping of their gradients and the
+orthogonalisation of their updates on torch tensors (row-major): the calls of :mod:`.ozgemm` with their shapes, strides and types taken from the tensors.
 
 Nothing here is recorded by autograd: the gradients are calls of their own, and
 tensors that require a gradient or carry a tangent are refused.
@@ -282,3 +282,108 @@ def _matrices(t):
             step = stride
         batch *= size
     return t, batch, ld, step
+
+
+def _dense(t) -> bool:
+    """Whether a tensor's entries are a run of memory, in any order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    step = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _gradients(grads, what: str):
+    if isinstance(grads, torch.Tensor):
+        grads = (grads,)
+    grads = list(grads)
+    if len(grads) > L.OZGEMM_ARRAYS_MAX:
+        raise ValueError(f"{what}: up to {L.OZGEMM_ARRAYS_MAX} tensors, got {len(grads)}")
+    for g in grads:
+        if g.layout != torch.strided:
+            raise TypeError(f"{what}: {g.layout} tensors are not supported")
+        if g.device != grads[0].device:
+            raise ValueError(f"{what}: tensors on {grads[0].device} and {g.device}")
+    _no_grad(what, *grads)
+    return grads, [_type_of(g, what, tuple(_TYPES)) for g in grads]
+
+
+def gradient_norm(grads):
+    """The norm over all entries of ``grads`` (a tensor or several, of float64,
+    float32, bfloat16 and float16 together): a float64 tensor of one value on
+    their device, summed in float64 in a fixed order.
+
+    Where a model's gradients are spread over processes, bring their norms
+    together (the root of the sum of squares) and hand the result to
+    :func:`clip_gradients`.
+    """
+    grads, types = _gradients(grads, "gradient_norm")
+    if not grads:
+        return torch.zeros((), dtype=torch.float64)
+    with _on_device(grads[0].device):
+        flat = [g if _dense(g) and not g.is_neg() else g.resolve_neg().contiguous() for g in grads]
+        norm = torch.empty((), dtype=torch.float64, device=grads[0].device)
+        L.ozgemm_gradient_norm(types, flat, [g.numel() for g in flat], norm)
+    return norm
+
+
+def clip_gradients(grads, max_norm: float, norm=None, eps: float = 1e-6, out=None):
+    """Multiplies ``grads`` by ``min(1, max_norm / (norm + eps))``, in place, and
+    returns the norm they had: ``norm``, a float64 tensor of one value on their
+    device, or their own (:func:`gradient_norm`).
+
+    The host waits for nothing.  Entries are multiplied in float32 (float64 ones
+    in float64) and rounded once; where the factor is 1 they stay as they are.  A norm of
+    Inf makes finite entries 0 and infinite ones NaN, one of NaN makes all of them NaN.
+    ``out``, tensors of the same shapes and types, receives the products instead.
+    No two of the tensors that are written may share memory.
+    """
+    grads, types = _gradients(grads, "clip_gradients")
+    if not max_norm >= 0 or not eps >= 0:
+        raise ValueError(f"max_norm and eps must not be negative, got {max_norm} and {eps}")
+    if out is not None:
+        out = [out] if isinstance(out, torch.Tensor) else list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"out must be {len(grads)} tensors, got {len(out)}")
+        for g, o in zip(grads, out):
+            if o.layout != torch.strided or o.shape != g.shape or o.dtype != g.dtype or o.device != g.device:
+                raise ValueError(f"out must be {tuple(g.shape)} of {g.dtype} on {g.device}, got {tuple(o.shape)} of "
+                                 f"{o.dtype} on {o.device}")
+        _no_grad("clip_gradients", *out)
+    if norm is not None and (norm.dtype != torch.float64 or norm.numel() != 1 or (
+            grads and norm.device != grads[0].device) or norm.is_neg()):
+        raise ValueError(f"norm must be one float64 value on the gradients' device, got {norm.numel()} of {norm.dtype} on "
+                         f"{norm.device}")
+    to = grads if out is None else out
+    for o in to:
+        if o.is_neg():
+            raise ValueError("what is written must not be a negated view")
+        if any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
+            raise ValueError("what is written must not be an expanded tensor")
+    if norm is not None:
+        _no_grad("clip_gradients", norm)
+    if not grads:
+        return gradient_norm(grads) if norm is None else norm
+    with _on_device(grads[0].device):
+        if norm is None:
+            norm = gradient_norm([g.detach() for g in grads])
+        # runs of memory, entry by entry alike on both sides; others by way of copies
+        here, there = [], []
+        for g, o in zip(grads, to):
+            if g is o:
+                g = o = g if _dense(g) else g.contiguous()
+            else:
+                alike = g.stride() == o.stride() and _dense(g) and not g.is_neg()
+                g = g if alike else g.resolve_neg().contiguous()
+                o = o if alike or o.is_contiguous() else torch.empty_like(g)
+            here.append(g)
+            there.append(o)
+        _written(*to)
+        L.ozgemm_clip_gradients(types, here, [g.numel() for g in here], there, norm, max_norm, eps)
+        for o, t in zip(to, there):
+            if o is not t:
+                o.copy_(t)
+    return norm

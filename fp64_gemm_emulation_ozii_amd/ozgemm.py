@@ -43,9 +43,13 @@ OZGEMM_F64 = 0
 OZGEMM_F32 = 1
 OZGEMM_BF16 = 2
 OZGEMM_F16 = 3
+OZGEMM_E4M3 = 4
+OZGEMM_E5M2 = 5
 OZGEMM_GROUPS_MAX = 65536
 OZGEMM_ORTHO_MAX = 65536
 OZGEMM_ORTHO_STEPS_MAX = 64
+OZGEMM_ARRAYS_MAX = 65536
+OZGEMM_ARRAY_MAX = 1 << 40
 
 #: every symbol the header declares
 EXPORTS = (
@@ -58,6 +62,9 @@ EXPORTS = (
     "ozgemm_dgemm_noalloc", "ozgemm_set_panels", "ozgemm_mfma_ceiling",
     "ozgemm_grouped_gemm", "ozgemm_grouped_gemm_workspace_bytes", "ozgemm_grouped_outer",
     "ozgemm_grouped_outer_workspace_bytes", "ozgemm_orthogonalize", "ozgemm_orthogonalize_workspace_bytes",
+    "ozgemm_quantize_blocks", "ozgemm_scaled_gemm", "ozgemm_scaled_gemm_workspace_bytes", "ozgemm_rms_norm",
+    "ozgemm_rms_norm_grads", "ozgemm_rms_norm_grads_workspace_bytes", "ozgemm_gradient_norm",
+    "ozgemm_gradient_norm_workspace_bytes", "ozgemm_clip_gradients",
 )
 
 _lib = None
@@ -121,6 +128,21 @@ def lib():
                                          ctypes.c_double, c_int, vp, c_int, ll, vp, c_size, vp]),
         "ozgemm_orthogonalize_workspace_bytes": (c_size, [c_int] * 5),
         "ozgemm_grouped_outer_workspace_bytes": (c_size, [c_int] * 5 + [vp, c_int, vp, c_int]),
+    })
+    f64 = ctypes.c_double
+    ints, lls, ptrs = ip, ctypes.POINTER(ll), ctypes.POINTER(vp)
+    sig.update({
+        "ozgemm_quantize_blocks": (c_int, [c_int] * 5 + [vp, c_int] + [vp, c_int, vp, ll, ll] * 2 + [vp]),
+        "ozgemm_scaled_gemm": (c_int, [c_int] * 6 + [vp, c_int, vp, c_int, ll, ll, vp, c_int, vp, ll, ll, vp, c_int, vp,
+                                       c_size, vp]),
+        "ozgemm_scaled_gemm_workspace_bytes": (c_size, [c_int] * 4 + [vp, c_int, vp, c_int]),
+        "ozgemm_rms_norm": (c_int, [c_int] * 5 + [vp, c_int, vp, c_int, vp, f64, vp, c_int, vp, c_int, vp, ll, ll, vp]),
+        "ozgemm_rms_norm_grads": (c_int, [c_int] * 4 + [vp, c_int, vp, c_int, vp, vp, c_int, f64, vp, c_int, vp, vp,
+                                          c_size, vp]),
+        "ozgemm_rms_norm_grads_workspace_bytes": (c_size, [c_int] * 3),
+        "ozgemm_gradient_norm": (c_int, [c_int, ints, ptrs, lls, vp, vp, c_size, vp]),
+        "ozgemm_gradient_norm_workspace_bytes": (c_size, [c_int, ints, lls]),
+        "ozgemm_clip_gradients": (c_int, [c_int, ints, ptrs, lls, ptrs, vp, f64, f64, vp]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -473,3 +495,90 @@ def ozgemm_orthogonalize(type, batch, m, n, G, ldg, strideg, steps, coeffs, eps,
     st = lib().ozgemm_orthogonalize(type, batch, m, n, _ptr(G), ldg, strideg, steps, co, eps, s, _ptr(O), ldo,
                                     strideo, ws, nbytes, hs)
     return _check(st, "ozgemm_orthogonalize") if check else st
+
+
+# --------------------------------------------------------------------------
+# a layer in 8 bits, and the clipping of gradients (raw C-ABI signatures)
+# --------------------------------------------------------------------------
+
+def ozgemm_quantize_blocks(type, qtype, rows, n, q, X, ldx, V, ldv, S, srow, sblock, Vt=None, ldvt=0, St=None, strow=0,
+                           stblock=0, stream=None, check: bool = True) -> int:
+    st = lib().ozgemm_quantize_blocks(type, qtype, rows, n, q, _ptr(X), ldx, _ptr(V), ldv, _ptr(S), srow, sblock,
+                                      _ptr(Vt), ldvt, _ptr(St), strow, stblock, _stream(stream))
+    return _check(st, "ozgemm_quantize_blocks") if check else st
+
+
+_SCALED_NO_WORKSPACE = -20
+
+
+def ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, A, lda, B, ldb) -> int:
+    return int(lib().ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, _ptr(A), lda, _ptr(B), ldb))
+
+
+def ozgemm_scaled_gemm(atype, btype, ctype, m, n, q, A, lda, SA, rows_a, sarow, sablock, B, ldb, SB, sbrow, sbblock, C,
+                       ldc, workspace=None, stream=None, check: bool = True) -> int:
+    """Workspace as for :func:`ozgemm_grouped_gemm`."""
+    L, hs = lib(), _stream(stream)
+    ops = (atype, btype, ctype, m, n, q, _ptr(A), lda, _ptr(SA), rows_a, sarow, sablock, _ptr(B), ldb, _ptr(SB), sbrow,
+           sbblock, _ptr(C), ldc)
+    st = _SCALED_NO_WORKSPACE
+    if workspace is None:  # operands are usually read in place
+        st = L.ozgemm_scaled_gemm(*ops, None, 0, hs)
+    if st == _SCALED_NO_WORKSPACE:
+        need = 0 if workspace is not None else ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, A, lda, B, ldb)
+        keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"), hs)
+        st = L.ozgemm_scaled_gemm(*ops, ws, nbytes, hs)
+    return _check(st, "ozgemm_scaled_gemm") if check else st
+
+
+def ozgemm_rms_norm(type, ytype, wtype, n, q, X, ldx, R, ldr, w, eps, H, ldh, Y, ldy, S=None, srow=0, sblock=0,
+                    stream=None, check: bool = True) -> int:
+    st = lib().ozgemm_rms_norm(type, ytype, wtype, n, q, _ptr(X), ldx, _ptr(R), ldr, _ptr(w), eps, _ptr(H), ldh,
+                               _ptr(Y), ldy, _ptr(S), srow, sblock, _stream(stream))
+    return _check(st, "ozgemm_rms_norm") if check else st
+
+
+def ozgemm_rms_norm_grads_workspace_bytes(n, q, dw) -> int:
+    return int(lib().ozgemm_rms_norm_grads_workspace_bytes(n, q, dw))
+
+
+def ozgemm_rms_norm_grads(type, wtype, n, q, dY, lddy, H, ldh, w, dH, lddh, eps, dX, lddx, dw, workspace=None,
+                          stream=None, check: bool = True) -> int:
+    """Workspace as for :func:`ozgemm_grouped_gemm`."""
+    hs = _stream(stream)
+    need = 0 if workspace is not None else ozgemm_rms_norm_grads_workspace_bytes(n, q, 1 if dw is not None else 0)
+    keep, ws, nbytes = _room(workspace, need, getattr(H, "device", "cuda"), hs)
+    st = lib().ozgemm_rms_norm_grads(type, wtype, n, q, _ptr(dY), lddy, _ptr(H), ldh, _ptr(w), _ptr(dH), lddh, eps,
+                                     _ptr(dX), lddx, _ptr(dw), ws, nbytes, hs)
+    return _check(st, "ozgemm_rms_norm_grads") if check else st
+
+
+def _arrays(types, sizes):
+    n = max(1, len(types))
+    return (ctypes.c_int * n)(*types), (ctypes.c_longlong * n)(*sizes)
+
+
+def _addresses(tensors):
+    return (ctypes.c_void_p * max(1, len(tensors)))(*[_ptr(t) for t in tensors])
+
+
+def ozgemm_gradient_norm_workspace_bytes(types, sizes) -> int:
+    return int(lib().ozgemm_gradient_norm_workspace_bytes(len(types), *_arrays(types, sizes)))
+
+
+def ozgemm_gradient_norm(types, arrays, sizes, norm, workspace=None, stream=None, check: bool = True) -> int:
+    """``types``, ``arrays`` (tensors or addresses) and ``sizes``: lists of one
+    length.  Workspace as for :func:`ozgemm_grouped_gemm`."""
+    hs = _stream(stream)
+    t, s = _arrays(types, sizes)
+    need = 0 if workspace is not None else int(lib().ozgemm_gradient_norm_workspace_bytes(len(types), t, s))
+    keep, ws, nbytes = _room(workspace, need, getattr(norm, "device", "cuda"), hs)
+    st = lib().ozgemm_gradient_norm(len(types), t, _addresses(arrays), s, _ptr(norm), ws, nbytes, hs)
+    return _check(st, "ozgemm_gradient_norm") if check else st
+
+
+def ozgemm_clip_gradients(types, arrays, sizes, out, norm, most, eps, stream=None, check: bool = True) -> int:
+    t, s = _arrays(types, sizes)
+    st = lib().ozgemm_clip_gradients(len(types), t, _addresses(arrays), s, _addresses(out), _ptr(norm), most, eps,
+                                     _stream(stream))
+    return _check(st, "ozgemm_clip_gradients") if check else st

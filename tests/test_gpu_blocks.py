@@ -1,0 +1,257 @@
+"""Blocks of 128 in 8 bits, their products and the products' gradients, against
+64 bits.
+
+Tolerances.  Blocks are exact: a power of two and one rounding.  A product's
+entry is a sum of q products in blocks of 128: 128 + 4 additions in a block,
+two roundings of its scaling and one addition per block, none off by more than
+2^-23 of the sum of the magnitudes so far (matrix cores may cut instead of
+round).  The 8-bit matrix cores drop what lies under 2^-13 of the largest of the
+products that they add at once, so at most that per product.  A result of 16 bits
+is then off by half a step."""
+import pytest
+import torch
+
+import fp64_gemm_emulation_ozii_amd as oz
+from blocks_util import EIGHT, blocks, same, spread, value
+
+pytestmark = pytest.mark.gpu
+
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+SIZES = [(1, 1), (1, 128), (3, 130), (128, 128), (129, 127), (200, 4), (64, 1000), (517, 261), (1, 4099), (1000, 16)]
+
+
+def normal(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def check_blocks(got, x, rows, dtype):
+    v, s = blocks(x, rows, dtype)
+    assert got[0].dtype == dtype and got[1].dtype == torch.float32
+    assert same(got[1], s)
+    assert same(got[0], v)
+
+
+@pytest.mark.parametrize("dtype", list(EIGHT), ids=str)
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("n, q", SIZES)
+def test_blocks_of_a_matrix_and_its_transpose(n, q, t, rows, dtype):
+    x = (normal(gen(n + q), n, q) * torch.exp(3 * normal(gen(q), n, 1))).to(TYPES[t])
+    V, S, Vt, St = oz.quantize_blocks(x, rows=rows, both=True, dtype=dtype)
+    check_blocks((V, S), x, rows, dtype)
+    check_blocks((Vt, St), x.t(), rows, dtype)
+    one = oz.quantize_blocks(x, rows=rows, dtype=dtype)
+    assert same(one[0], V) and same(one[1], S)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+def test_blocks_of_views(t):
+    base = normal(gen(3), 300, 400).to(TYPES[t])
+    for x in (base[7:250, 3:301], base.t(), base.t()[5:, 1:200], base[::2], base[:, ::3], base[:1], base[:, :1].t(),
+              base[5].expand(9, 400)):
+        V, S, Vt, St = oz.quantize_blocks(x, both=True)
+        check_blocks((V, S), x, 1, E4M3)
+        check_blocks((Vt, St), x.t(), 1, E4M3)
+
+
+@pytest.mark.parametrize("dtype", list(EIGHT), ids=str)
+@pytest.mark.parametrize("rows", [1, 128])
+def test_blocks_with_extreme_entries(rows, dtype):
+    top = EIGHT[dtype][0]
+    x = torch.zeros(260, 384, device="cuda")
+    x[0, :3] = torch.tensor([float("inf"), 1.0, -2.0])
+    x[1, 128:131] = torch.tensor([float("nan"), float("-inf"), 3e38])
+    x[2, 256:258] = torch.tensor([2.0 ** -149, -(2.0 ** -149)])  # below the least scale's grid: zeros
+    x[3, 0] = 2.0 ** -120
+    x[140, :4] = torch.tensor([top, -top, top * 2.0 ** -9, 0.5])  # exactly the largest
+    x[141, 130] = top * (1 + 2.0 ** -20)  # just above
+    x[142, 300:303] = torch.tensor([torch.finfo(torch.float32).max, 1.0, -0.0])
+    x[259, 380] = -1.0
+    V, S, Vt, St = oz.quantize_blocks(x, rows=rows, both=True, dtype=dtype)
+    check_blocks((V, S), x, rows, dtype)
+    check_blocks((Vt, St), x.t(), rows, dtype)
+
+
+def test_every_half_and_bfloat16_is_rounded_right():
+    for t in (torch.float16, torch.bfloat16):
+        x = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32).to(torch.int16).view(t).view(512, 128).cuda()
+        for dtype in EIGHT:
+            for rows in (1, 128):
+                check_blocks(oz.quantize_blocks(x, rows=rows, dtype=dtype), x, rows, dtype)
+
+
+# ---------------------------------------------------------------- products
+
+def aligned(v, dtype, pad=0.0):
+    """The values as 8-bit rows on 16-byte boundaries, `pad` behind them."""
+    n, q = v.shape
+    out = torch.full((n, -(-q // 16) * 16), pad, device=v.device).to(dtype)
+    out[:, :q] = v.to(dtype)
+    return out[:, :q]
+
+
+def tolerance(x, xs, w, ws, rows, out, wide):
+    a, b = value(x, xs, 1).abs(), value(w, ws, rows).abs()
+    q = x.shape[1]
+    sums = a @ b.T.contiguous()
+    tol = sums * (128 + 4 + 2 + -(-q // 128) + 8) * 2.0 ** -23
+    if not wide:  # per block: 128 products, each off by 2^-13 of the block's largest
+        for k in range(0, q, 128):
+            tol += a[:, k:k + 128].amax(1)[:, None] * b[:, k:k + 128].amax(1)[None] * 128 * 2.0 ** -13
+    return tol
+
+
+def check_product(got, x, xs, w, ws, rows, wide):
+    want = value(x, xs, 1) @ value(w, ws, rows).T.contiguous()
+    tol = tolerance(x, xs, w, ws, rows, got.dtype, wide)
+    half = 0.0 if got.dtype == torch.float32 else torch.finfo(got.dtype).eps / 2
+    tol = tol * (1 + half) + half * want.abs() + (2.0 ** -25 if got.dtype == torch.float16 else 0.0)
+    assert ((got.double() - want).abs() <= tol).all()
+
+
+PRODUCTS = [(1, 128, 16), (1, 4096, 1000), (5, 130, 33), (16, 1, 1), (17, 100, 129), (33, 257, 31), (64, 2048, 512),
+            (65, 128, 128), (100, 1531, 77), (128, 64, 300), (200, 8192, 130), (300, 16, 257), (512, 500, 4100),
+            (1001, 1531, 2049), (3000, 260, 3000)]
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("tx, tw", [(E4M3, E4M3), (E5M2, E4M3), (E4M3, E5M2), (E5M2, E5M2)], ids=str)
+@pytest.mark.parametrize("n, q, m", PRODUCTS)
+def test_whole_numbers_come_out_exactly(n, q, m, tx, tw, rows):
+    # entries of -1, 0 and 1 (one in eight not 0) under scales of 1, 2 and 4: every partial sum is a whole number below 2^24
+    g = gen(n + q + m)
+
+    def whole(a, b, t):
+        k = torch.randint(0, 16, (a, b), generator=g, device="cuda")
+        return aligned(((k == 0).float() - (k == 1).float()), t, float("nan"))
+
+    def scales(a, b):
+        return 2.0 ** torch.randint(0, 3, (a, b), generator=g, device="cuda").float()
+
+    nb = -(-q // 128)
+    x, w, xs, ws = whole(n, q, tx), whole(m, q, tw), scales(n, nb), scales(-(-m // rows), nb)
+    want = value(x, xs, 1) @ value(w, ws, rows).T.contiguous()
+    for t in TYPES.values():
+        assert torch.equal(oz.scaled_linear(x, xs, w, ws, out_dtype=t), want.to(t))
+    xs = xs.t().contiguous().t()
+    assert torch.equal(oz.scaled_linear(x, xs, w, ws, out_dtype=torch.float32).double(), want)
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("n, q, m", PRODUCTS)
+def test_products_of_any_scales(n, q, m, t, rows):
+    g = gen(n * 3 + q + m)
+    x, xs = oz.quantize_blocks(normal(g, n, q) * torch.exp(normal(g, n, 1)))
+    w, ws = oz.quantize_blocks(normal(g, m, q), rows=rows)
+    xs, ws = (s * (1 + torch.rand(s.shape, generator=g, device="cuda")) for s in (xs, ws))
+    got = oz.scaled_linear(x, xs, w, ws, out_dtype=TYPES[t])
+    check_product(got, x, xs, w, ws, rows, t == "f32" or n <= 64)
+    # the same from rows off the 16-byte grid, bit for bit
+    for a, b in ((x.clone().contiguous()[:, :], w), (x, odd_rows(w)), (odd_rows(x), odd_rows(w))):
+        assert torch.equal(oz.scaled_linear(a, xs, b, ws, out_dtype=TYPES[t]), got)
+
+
+def odd_rows(v):
+    out = torch.zeros((v.shape[0], v.shape[1] + 3), device="cuda").to(v.dtype)[:, 1:-2]
+    return out.copy_(v)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("n", [3, 300])
+def test_sums_of_gaussian_entries_keep_their_digits(n, t):
+    # the 8-bit matrix cores are off by 1.5e-5 of the sums' norm; twice that, and the result's own rounding
+    g = gen(5)
+    x, xs = oz.quantize_blocks(normal(g, n, 4096))
+    w, ws = oz.quantize_blocks(normal(g, 512, 4096), rows=128)
+    got = oz.scaled_linear(x, xs, w, ws, out_dtype=TYPES[t]).double()
+    want = value(x, xs, 1) @ value(w, ws, 128).T.contiguous()
+    off = ((got - want).norm() / want.norm()).item()
+    assert off <= (1e-6 if t == "f32" else 3e-5 + torch.finfo(TYPES[t]).eps / 2)
+
+
+@pytest.mark.parametrize("n, m", [(3, 40), (300, 200), (1000, 9000)])
+@pytest.mark.parametrize("t", list(TYPES))
+def test_nan_and_infinities_stay_in_their_rows(n, m, t):
+    q = 200
+    g = gen(7)
+    x, xs = oz.quantize_blocks(normal(g, n, q), dtype=E5M2)
+    w, ws = oz.quantize_blocks(normal(g, m, q), dtype=E5M2)
+    x, w = x.float(), w.float()
+    w[m - 1, 199] = float("nan")
+    x[n - 1, 3] = float("inf")
+    w[0, 3] = 0.0
+    got = oz.scaled_linear(aligned(x, E5M2), xs, aligned(w, E5M2), ws, out_dtype=TYPES[t])
+    want = value(x, xs, 1) @ value(w, ws, 1).T.contiguous()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.isfinite(), want.isfinite())
+    assert got[:, m - 1].isnan().all() and got[n - 1, 0].isnan() and got[0, 0].isfinite()
+
+
+def test_results_go_where_they_are_asked_to():
+    g = gen(9)
+    for n, m in ((7, 50), (300, 270)):
+        x, xs = oz.quantize_blocks(normal(g, n, 300))
+        w, ws = oz.quantize_blocks(normal(g, m, 300), rows=128)
+        want = oz.scaled_linear(x, xs, w, ws)
+        frame = torch.full((n + 2, m + 5), 7.0, device="cuda", dtype=torch.bfloat16)
+        out = frame[1:-1, 3:-2]
+        assert oz.scaled_linear(x, xs, w, ws, out=out) is out
+        assert torch.equal(out, want)
+        frame[1:-1, 3:-2] = 7.0
+        assert (frame == 7.0).all()
+
+
+def test_no_entries():
+    e = torch.empty(0, 0, device="cuda")
+    for n, q, m in ((0, 5, 3), (4, 0, 3), (100, 0, 3), (4, 5, 0)):
+        x, xs = oz.quantize_blocks(torch.ones(n, q, device="cuda"))
+        w, ws = oz.quantize_blocks(torch.ones(m, q, device="cuda"))
+        assert x.shape == (n, q) and xs.shape == (n, -(-q // 128))
+        got = oz.scaled_linear(x, xs, w, ws)
+        assert got.shape == (n, m) and (got == 0).all()
+    assert oz.quantize_blocks(e, both=True)[2].shape == (0, 0)
+
+
+@pytest.mark.parametrize("n, q, m", [(40, 300, 200), (1000, 513, 129), (129, 1000, 2000)])
+@pytest.mark.parametrize("t", list(TYPES))
+def test_gradients(n, q, m, t):
+    g = gen(n)
+    X, W = normal(g, n, q).to(TYPES[t]), normal(g, m, q).to(TYPES[t])
+    dY = (normal(g, n, m) * torch.exp(normal(g, n, 1))).to(TYPES[t])
+    _, _, Xt, xts = oz.quantize_blocks(X, both=True)
+    _, _, Wt, wts = oz.quantize_blocks(W, rows=128, both=True)
+    for dtype in EIGHT:
+        dX, dW = oz.scaled_linear_grads(dY, Xt, xts, Wt, wts, dw_dtype=torch.float32, dtype=dtype)
+        assert dX.dtype == dY.dtype and dX.shape == (n, q) and dW.shape == (m, q)
+        v, s = blocks(dY, 1, dtype)
+        check_product(dX, v, s, Wt, wts, 128, t == "f32" or n <= 64)
+        v, s = blocks(dY.t(), 1, dtype)
+        check_product(dW, v, s, Xt, xts, 1, True)
+
+
+def test_gradients_of_a_layer_against_differences():
+    # Y = X W^T is linear in both: a step along D changes sum(Y dY) by sum(dX D); whole numbers, exact in 8 bits
+    g = gen(21)
+    X, W, dY, D = (torch.randint(-2, 3, s, generator=g, device="cuda").float() for s in
+                   ((150, 200), (90, 200), (150, 90), (150, 200)))
+    w, ws, Wt, wts = oz.quantize_blocks(W, rows=128, both=True)
+    _, _, Xt, xts = oz.quantize_blocks(X, both=True)
+
+    def loss(X):
+        return (oz.scaled_linear(*oz.quantize_blocks(X), w, ws, out_dtype=torch.float32).double() * dY.double()).sum()
+
+    dX, dW = oz.scaled_linear_grads(dY, Xt, xts, Wt, wts)
+    assert (dX.double() * D).sum() == (loss(X + D) - loss(X - D)) / 2
+    assert torch.equal(dW.double(), dY.double().T.contiguous() @ X.double())
+    assert torch.equal(dX.double(), dY.double() @ W.double())
+
+
+def test_the_spread_of_scales_matches_the_products():
+    s = torch.arange(6.0).view(2, 3)
+    assert spread(s, 130, 300, 128)[129, 299] == 5 and spread(s, 130, 300, 128)[127, 128] == 1
