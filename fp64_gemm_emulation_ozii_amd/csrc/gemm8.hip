@@ -16,11 +16,16 @@
 #include "block8.h"
 #include "gemm8.h"
 #include "products.h"
-#include "store.h"
 #include "tile16.h"
 
 namespace oz {
 namespace {
+
+// x rounded to a 16-bit type, to nearest-even.
+__device__ __forceinline__ uint16_t round16(float x, int ctype) {
+  return ctype == OZGEMM_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)x)
+                              : __builtin_bit_cast(uint16_t, (_Float16)x);
+}
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
@@ -63,27 +68,34 @@ struct Frag<TYPE, true> {
   }
 };
 
-// A block's sums of 16 x 16 results: lane l has rows 4 (l / 16) .. + 3 of column l mod 16.
-template <int TA, int TB, bool WIDE>
-__device__ __forceinline__ v4f block_product(const Frag<TA, WIDE>& a, const Frag<TB, WIDE>& b) {
-  v4f d = {0.f, 0.f, 0.f, 0.f};
+// A block's sums of 16 x 16 results, of one fragment of A with G of B: lane l
+// has rows 4 (l / 16) .. + 3 of column l mod 16.
+template <int TA, int TB, bool WIDE, int G>
+__device__ __forceinline__ void block_products(v4f (&d)[G], const Frag<TA, WIDE>& a, const Frag<TB, WIDE>* b) {
+#pragma unroll
+  for (int u = 0; u < G; ++u) d[u] = v4f{0.f, 0.f, 0.f, 0.f};
   if constexpr (WIDE) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.h[t], b.h[t], d, 0, 0, 0);
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int u = 0; u < G; ++u) d[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.h[t], b[u].h[t], d[u], 0, 0, 0);
   } else {
-    // scales of 1 (a byte of 127) within the instruction
-    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.w, b.w, d, TA == OZGEMM_E5M2, TB == OZGEMM_E5M2, 0, 127, 0,
-                                                         127);
+#pragma unroll
+    for (int u = 0; u < G; ++u)  // (scales of 0 within the instruction: none)
+      d[u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.w, b[u].w, d[u], TA == OZGEMM_E5M2, TB == OZGEMM_E5M2,
+                                                              0, 0, 0, 0);
   }
-  return d;
 }
 
-// The bytes of a 16-byte piece at or past `left` as zeros.
-__device__ __forceinline__ v4u8 first_bytes(v4u8 v, int left) {
+__device__ __forceinline__ void pin(v4f& v) { asm volatile("" : "+v"(v)); }
+
+// A mask of the bytes of a 16-byte piece before `left`.
+__device__ __forceinline__ v4u8 first_bytes(int left) {
+  v4u8 v;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int bits = min(max(left - 4 * k, 0), 4) * 8;
-    v[k] = bits == 32 ? v[k] : v[k] & ((1u << bits) - 1u);
+    v[k] = bits == 32 ? ~0u : (1u << bits) - 1u;
   }
   return v;
 }
@@ -92,165 +104,382 @@ __device__ __forceinline__ v4u8 first_bytes(v4u8 v, int left) {
 // Tiles
 // ---------------------------------------------------------------------------
 
-// BM x BN results by WM x WN wavefronts.  Blocks of 128 entries go from HBM
-// straight into LDS through two buffers, 16 bytes per lane, range-checked (rows
-// past the end arrive as zeros, as do pieces past the inner dimension), with
-// their rows' scales beside them.
+// BM x BN results by WM x WN wavefronts, a block per compute unit that walks its
+// tiles.  Blocks of 128 entries ("slices") go from HBM straight into LDS through two
+// buffers, 16 bytes per lane, range-checked (rows past the end arrive as zeros, as do
+// pieces past the inner dimension), with their rows' scales beside them.
+//
+// Two wavefronts share a SIMD, and each alternates one product with the scaling
+// of the one before last: a wavefront alone takes 49 cycles for a product of 32 and its
+// four multiply-adds, two together 38 each.  So nothing may hold both up:
+// fragments are read from LDS a row of products ahead, those of B for the next slice
+// right after their last use, and one barrier per slice stands before its last row:
+// every wavefront has then read the slice, whose buffer the loads of the slice
+// after the next go to, and the next slice, asked for a slice's time ago, has landed.
+// The stream of slices runs on over the tiles' ends.
 template <int TA, int TB, bool WIDE, bool AROW, int BM, int BN, int WM, int WN>
 struct Tile8 {
   static constexpr int NW = WM * WN, THREADS = NW * 64;
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   static constexpr int ROWS = BM + BN;
-  static constexpr int SCALES = ROWS * 4, BUF = ROWS * 128 + SCALES;
-  static constexpr int LOADS = ROWS * 128 / 1024 / NW, A_LOADS = BM * 128 / 1024 / NW;
-  static constexpr int SLOADS = (ROWS + THREADS - 1) / THREADS;
-  static_assert(LOADS * NW * 1024 == ROWS * 128 && A_LOADS * NW * 1024 == BM * 128, "whole wave loads");
-  static_assert(ROWS % THREADS == 0 && BM % 64 == 0, "whole wave loads of scales");
-  static constexpr int wave_m(int wave) { return wave % WM; }
-  static constexpr int wave_n(int wave) { return wave / WM; }
+  static constexpr int BUF = ROWS * 128, SLOT = THREADS * 4;  // of a slice; of its scales
+  static constexpr int SMEM = 2 * (BUF + SLOT);
+  static constexpr int LA = BM * 128 / 1024 / NW, LB = BN * 128 / 1024 / NW, LOADS = LA + LB + 1;  // of a wavefront
+  static_assert(LA % 2 == 0 && LA * NW * 1024 == BM * 128, "whole wave loads, the first of an even number");
+  static_assert(LB % 2 == 0 && LB * NW * 1024 == BN * 128, "whole wave loads, the first of an even number");
+  static_assert(ROWS <= THREADS && BM % 64 == 0, "a scale and a row a thread");
+  static_assert(FM % 4 == 0, "fragments of A and their scales change places, and stores take two");
   static __device__ __forceinline__ int swz(int row) { return ((row >> 1) ^ (row << 2)) & 7; }
 
-  static __device__ __forceinline__ void run(v4f (&acc)[FM][FN], char* smem, const Scaled8& g, int m0, int n0, int k0,
-                                             int k_end) {
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave_m(wave), wn = wave_n(wave);
-    // this lane's pieces: row r of 8, piece c, in loads of even and odd number
-    int offa[2], offb[2], kin[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = lane >> 3, c = (lane & 7) ^ swz(e * 8 + r);
-      kin[e] = c * 16;
-      offa[e] = r * (int)g.A.ld + kin[e];
-      offb[e] = r * (int)g.B.ld + kin[e];
+  // A tile of the call: rows from m0 and n0 on, part `part`, entries k0 .. k_end.
+  struct Place {
+    int m0, n0, part, k0, k_end;
+  };
+  static __device__ __forceinline__ Place place(const Scaled8& g, int tile) {
+    const int tiles_m = (g.m + BM - 1) / BM, tiles_n = (g.n + BN - 1) / BN, whole = tiles_m * tiles_n;
+    Place p;
+    p.part = tile / whole;
+    int nj, mi;
+    panel_order<4>(xcd_order(tile - p.part * whole, whole), tiles_n, tiles_m, nj, mi);
+    p.m0 = __builtin_amdgcn_readfirstlane(mi * BM);
+    p.n0 = __builtin_amdgcn_readfirstlane(nj * BN);
+    p.part = __builtin_amdgcn_readfirstlane(p.part);
+    const int each = (((g.q + 127) >> 7) + g.parts - 1) / g.parts * 128;
+    p.k0 = __builtin_amdgcn_readfirstlane(p.part * each);
+    p.k_end = __builtin_amdgcn_readfirstlane(min(g.q, p.k0 + each));
+    return p;
+  }
+
+  // The loads of a block's slices, in order.
+  struct Feed {
+    const Scaled8& g;
+    char* smem;
+    int lane, wave, tile, tiles;
+    const uint8_t *pa, *pb;
+    const float* ps;
+    long sstep;
+    // This lane's row and piece of eight rows that begin at an even or an odd
+    // multiple of 8: bytes from their first row, entries (one past the end: the
+    // offset lies past it too).
+    int kin0, kin1, offa0, offa1, offb0, offb1;
+    int reca, recb;  // bytes from pa, pb to the end of the last row's last 16-byte piece
+    int left;        // entries from the slice to load on
+    int s;           // its number
+
+    __device__ __forceinline__ Feed(const Scaled8& g_, char* lds, int lane_, int wave_, int tiles_)
+        : g(g_), smem(lds), lane(lane_), wave(wave_), tile(blockIdx.x), tiles(tiles_), s(0) {
+      kin0 = ((lane & 7) ^ swz(lane >> 3)) * 16;
+      kin1 = ((lane & 7) ^ swz(8 + (lane >> 3))) * 16;
+      begin();
     }
-    const int rows_a = min(g.m - m0, BM), rows_b = min(g.n - n0, BN);
-    const uint8_t* pa = g.A.p + (long)m0 * g.A.ld + k0;
-    const uint8_t* pb = g.B.p + (long)n0 * g.B.ld + k0;
-    // bytes from there to the end of the last row's last 16-byte piece
-    const int len = (g.q + 15) / 16 * 16 - k0;
-    int reca = (rows_a - 1) * (int)g.A.ld + len, recb = (rows_b - 1) * (int)g.B.ld + len;
-    const float* ps[SLOADS];
-    long sstep[SLOADS];
-#pragma unroll
-    for (int u = 0; u < SLOADS; ++u) {
-      const int r = (u * NW + wave) * 64 + lane;
-      const bool a = (u * NW + wave) * 64 < BM;
-      const int row = a ? min(m0 + r, g.m - 1) >> g.A.shift : min(n0 + r - BM, g.n - 1);
-      const Operand8& o = a ? g.A : g.B;
-      sstep[u] = o.sblock;
-      ps[u] = o.s + row * o.srow + (k0 >> 7) * o.sblock;
+    __device__ __forceinline__ void begin() {
+      const Place p = place(g, tile);
+      pa = g.A.p + (long)p.m0 * g.A.ld + p.k0;
+      pb = g.B.p + (long)p.n0 * g.B.ld + p.k0;
+      const int len = (g.q + 15) / 16 * 16 - p.k0;
+      reca = (min(g.m - p.m0, BM) - 1) * (int)g.A.ld + len;
+      recb = (min(g.n - p.n0, BN) - 1) * (int)g.B.ld + len;
+      const int first = wave * 64;
+      const bool a = first < BM;
+      const int row = a ? min(p.m0 + first + lane, g.m - 1) >> g.A.shift : min(p.n0 + first + lane - BM, g.n - 1);
+      sstep = a ? g.A.sblock : g.B.sblock;
+      ps = (a ? g.A.s + row * g.A.srow : g.B.s + row * g.B.srow) + (p.k0 >> 7) * sstep;
+      left = p.k_end - p.k0;
+      edge();
+      uniform();
     }
-    int left = k_end - k0;  // from the block to load on
-    const int total = (left + 127) >> 7;
-    auto issue = [&](int buf) {
-      char* d = smem + buf * BUF;
-      const __amdgpu_buffer_rsrc_t ra =
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pa), 0, left > 0 ? reca : 0, 0x00020000);
-      const __amdgpu_buffer_rsrc_t rb =
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pb), 0, left > 0 ? recb : 0, 0x00020000);
-#pragma unroll
-      for (int li = 0; li < LOADS; ++li) {
-        const bool a = li < A_LOADS;
-        const int blk = a ? wave * A_LOADS + li : wave * (LOADS - A_LOADS) + li - A_LOADS;
-        const int e = blk & 1;
-        const int off = kin[e] < left ? (a ? offa[e] : offb[e]) : (int)0x80000000;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            a ? ra : rb, (__attribute__((address_space(3))) void*)(d + (a ? 0 : BM * 128) + blk * 1024), 16,
-            off + blk * 8 * (int)(a ? g.A.ld : g.B.ld), 0, 0, 0);
+    // What is the same in all lanes stays in scalar registers, as the loads need it.
+    __device__ __forceinline__ void uniform() {
+      pa = same(pa);
+      pb = same(pb);
+      reca = __builtin_amdgcn_readfirstlane(reca);
+      recb = __builtin_amdgcn_readfirstlane(recb);
+      left = __builtin_amdgcn_readfirstlane(left);
+      tile = __builtin_amdgcn_readfirstlane(tile);
+      s = __builtin_amdgcn_readfirstlane(s);
+    }
+    static __device__ __forceinline__ const uint8_t* same(const uint8_t* p) {
+      const uint64_t u = (uint64_t)p;
+      return (const uint8_t*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)u) |
+                              (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32);
+    }
+    __device__ __forceinline__ void edge() {
+      const int r = lane >> 3, a = r * (int)g.A.ld, b = r * (int)g.B.ld, past = (int)0x80000000;
+      offa0 = kin0 < left ? a + kin0 : past;
+      offa1 = kin1 < left ? a + kin1 : past;
+      offb0 = kin0 < left ? b + kin0 : past;
+      offb1 = kin1 < left ? b + kin1 : past;
+    }
+    // 8 rows of an operand, `at` from its first, to where they lie in the buffer
+    static __device__ __forceinline__ void rows8(const uint8_t* p, int records, int at, char* to) {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, records, 0x00020000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, at, 0, 0, 0);
+    }
+    // load li of the slice
+    __device__ __forceinline__ void load1(int li) const {
+      char* to = smem + (s & 1) * (BUF + SLOT);
+      if (li < LA) {
+        const int row0 = (wave * LA + li) * 8;
+        rows8(pa, reca, (li & 1 ? offa1 : offa0) + row0 * (int)g.A.ld, to + row0 * 128);
+      } else if (li < LA + LB) {
+        const int row0 = (wave * LB + li - LA) * 8;
+        rows8(pb, recb, ((li - LA) & 1 ? offb1 : offb0) + row0 * (int)g.B.ld, to + (BM + row0) * 128);
+      } else {
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)ps,
+                                         (__attribute__((address_space(3))) void*)(to + BUF + wave * 256), 4, 0, 0);
       }
-#pragma unroll
-      for (int u = 0; u < SLOADS; ++u) {
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)ps[u],
-            (__attribute__((address_space(3))) void*)(d + ROWS * 128 + (u * NW + wave) * 256), 4, 0, 0);
-        if (left > 128) ps[u] += sstep[u];
-      }
+    }
+    __device__ __forceinline__ void next() {
+      ++s;
       left -= 128;
-      pa += 128;
-      pb += 128;
-      reca -= 128;
-      recb -= 128;
+      if (left > 0) {
+        pa += 128;
+        pb += 128;
+        reca -= 128;
+        recb -= 128;
+        ps += sstep;
+        if (left < 128) edge();
+      } else {
+        tile += gridDim.x;
+        if (tile < tiles)
+          begin();
+        else  // past the end: the loads go on, of zeros, for the counter's sake
+          reca = recb = left = 0;
+      }
+      uniform();
+    }
+    __device__ __forceinline__ void all() {
+#pragma unroll
+      for (int li = 0; li < LOADS; ++li) load1(li);
+      next();
+    }
+  };
+
+  // The restrict-qualified argument gives the read an alias scope; without one
+  // the compiler takes it to depend on the loads into LDS in flight.
+  template <class V>
+  static __device__ __forceinline__ V read(const char* __restrict__ p) {
+    return *reinterpret_cast<const V*>(p);
+  }
+
+  // A slice has landed; of the last 16-byte piece of its rows `tail` bytes count, the others go.
+  static __device__ __forceinline__ void arrive(char* buf, int left, int tail) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (left > 128 || tail == 0) return;
+    const int r = threadIdx.x;
+    if (r < ROWS) {
+      v4u8* at = reinterpret_cast<v4u8*>(buf + r * 128 + (((left - 1) >> 4) ^ swz(r)) * 16);
+      *at &= first_bytes(tail);
+    }
+    __syncthreads();
+  }
+
+  static constexpr int STORES = FM * FN / 2;
+
+  static __device__ __forceinline__ void walk(const Scaled8& g, char* smem, int lane, int wave, int tiles) {
+    const int wm = wave % WM, wn = wave / WM;
+    Feed feed(g, smem, lane, wave, tiles);
+    // rows 16 apart lie alike
+    const int at0 = (lane & 15) * 128 + (((lane >> 4) ^ swz(lane & 15)) * 16), at1 = at0 ^ 64;
+    const int a_at = wm * (BM / WM) * 128, b_at = (BM + wn * (BN / WN)) * 128;
+    const int sa_at = BUF + (wm * (BM / WM) + (AROW ? 4 * (lane >> 4) : 0)) * 4;
+    const int sb_at = BUF + (BM + wn * (BN / WN) + (lane & 15)) * 4;
+    v4u8 ra[2][2], rb[FN][2];
+    v4f s4[4];
+    float xn[FN], fn = 0.f;
+    auto read_a = [&](const char* buf, int i) {
+      ra[i & 1][0] = read<v4u8>(buf + a_at + i % FM * 2048 + at0);
+      ra[i & 1][1] = read<v4u8>(buf + a_at + i % FM * 2048 + at1);
+      if (AROW) s4[i & 3] = read<v4f>(buf + sa_at + i % FM * 64);
     };
+    auto read_b = [&](const char* buf, int j) {
+      rb[j][0] = read<v4u8>(buf + b_at + j * 2048 + at0);
+      rb[j][1] = read<v4u8>(buf + b_at + j * 2048 + at1);
+      xn[j] = read<float>(buf + sb_at + j * 64);
+      if (!AROW && j == 0) fn = read<float>(buf + sa_at);
+    };
+
+    Place p = place(g, blockIdx.x);
+    feed.all();
+    feed.all();
+    wait_loads<LOADS>();
+    arrive(smem, p.k_end - p.k0, (p.k_end - p.k0) & 15);
+    read_a(smem, 0);
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int j = 0; j < FN; ++j) read_b(smem, j);
+
+    v4f acc[FM][FN];
+    int s = 0, stored = 0;
+    for (int tile = blockIdx.x; tile < tiles;) {
+      const int next_tile = tile + gridDim.x;
+      const Place then = next_tile < tiles ? place(g, next_tile) : p;
 #pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (total > 0) issue(0);
-    const int tail = (k_end - k0) & 15;  // bytes of the last piece of a row that count
-    for (int t = 0; t < total; ++t) {
-      char* buf = smem + (t & 1) * BUF;
-      slice_barrier<0>();  // block t has landed, and everybody has read block t - 1
-      if (t + 1 < total) issue((t + 1) & 1);
-      if (t + 1 == total && tail != 0) {
-        const int c = ((k_end - k0) & 127) >> 4;
-        for (int r = threadIdx.x; r < ROWS; r += THREADS) {
-          v4u8* at = reinterpret_cast<v4u8*>(buf + r * 128 + (c ^ swz(r)) * 16);
-          *at = first_bytes(*at, tail);
-        }
-        __syncthreads();
-      }
-      auto piece = [&](int row, int h) {
-        return *reinterpret_cast<const v4u8*>(buf + row * 128 + ((h * 4 + (lane >> 4)) ^ swz(row)) * 16);
-      };
-      const float* sa = reinterpret_cast<const float*>(buf + ROWS * 128);
-      const float* sb = sa + BM;
-      Frag<TB, WIDE> b[FN];
-      float xb[FN];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int row = wn * (BN / WN) + j * 16 + (lane & 15);
-        b[j].set(piece(BM + row, 0), piece(BM + row, 1));
-        xb[j] = sb[row];
-      }
-      if (!AROW) {
-        const float s = sa[wm * (BM / WM)];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) xb[j] *= s;
-      }
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int row = wm * (BM / WM) + i * 16;
-        Frag<TA, WIDE> a;
-        a.set(piece(row + (lane & 15), 0), piece(row + (lane & 15), 1));
-        v4f s4 = {1.f, 1.f, 1.f, 1.f};
-        if (AROW) s4 = *reinterpret_cast<const v4f*>(sa + row + 4 * (lane >> 4));
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          const v4f d = block_product<TA, TB, WIDE>(a, b[j]);
+          acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+          pin(acc[i][j]);  // (no copy of the loop for a first slice added to zeros)
+        }
+      for (int left = p.k_end - p.k0; left > 0; left -= 128, ++s) {
+        char* buf = smem + (s & 1) * (BUF + SLOT);
+        char* other = smem + (~s & 1) * (BUF + SLOT);
+        Frag<TB, WIDE> b[FN];
+        float xb[FN];
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[i][j][r] = __builtin_fmaf(d[r], AROW ? s4[r] * xb[j] : xb[j], acc[i][j][r]);
+        for (int j = 0; j < FN; ++j) xb[j] = AROW ? xn[j] : xn[j] * fn;
+        // One or (wide) two products a slot, DELAY slots ahead of their scaling.
+        // pin() keeps both where they stand: the compiler would put every
+        // product right before its use and wait for it there.
+        constexpr int G = WIDE ? 2 : 1, PER = FN / G, SLOTS = FM * PER, DELAY = WIDE ? 1 : 2;
+        static_assert(FN % G == 0, "whole slots");
+        v4f d[DELAY + 1][G];
+        Frag<TA, WIDE> a;
+#pragma unroll
+        for (int r = 0; r < SLOTS + DELAY; ++r) {
+          if (r < SLOTS) {
+            const int i = r / PER;
+            if (r % PER == 0) {
+              a.set(ra[i & 1][0], ra[i & 1][1]);
+              if (i < FM - 1) {
+                read_a(buf, i + 1);
+              } else {
+                __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wavefront has read the slice,
+                if (stored == STORES)                // and its loads of the next one have landed
+                  wait_loads<STORES>();
+                else
+                  wait_loads<0>();
+                const Place& q = left > 128 ? p : then;
+                const int whole = q.k_end - q.k0;
+                arrive(other, left > 128 ? left - 128 : whole, whole & 15);
+                read_a(other, FM);
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+              if (i == 0) b[r % PER * G + u].set(rb[r % PER * G + u][0], rb[r % PER * G + u][1]);
+            block_products<TA, TB, WIDE, G>(d[r % (DELAY + 1)], a, &b[r % PER * G]);
+#pragma unroll
+            for (int u = 0; u < G; ++u) pin(d[r % (DELAY + 1)][u]);
+            if (i == FM - 1) {
+#pragma unroll
+              for (int u = 0; u < G; ++u) read_b(other, r % PER * G + u);
+#pragma unroll
+              for (int li = 0; li < LOADS; ++li)
+                if (li * PER / LOADS == r % PER) feed.load1(li);
+            }
+          }
+          if (r >= DELAY) {
+            const int i = (r - DELAY) / PER;
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+              const int j = (r - DELAY) % PER * G + u;
+              v4f& from = d[(r - DELAY) % (DELAY + 1)][u];
+              pin(from);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                acc[i][j][k] = __builtin_fmaf(from[k], AROW ? s4[i & 3][k] * xb[j] : xb[j], acc[i][j][k]);
+              pin(acc[i][j]);
+            }
+          }
+        }
+        feed.next();
+        stored = __builtin_amdgcn_readfirstlane(0);
+        asm volatile("" : "+s"(stored));  // (no copy of the loop for the first slice)
+      }
+      stored = store(acc, g, p, lane, wm, wn);
+      stored = __builtin_amdgcn_readfirstlane(stored);
+      asm volatile("" : "+s"(stored));
+      tile = next_tile;
+      p = then;
+    }
+    wait_loads<0>();
+  }
+
+  // A tile's results, straight from the accumulators; how many stores every
+  // wavefront of it is sure to have made (STORES, or 0 at the edges).  In 16 bits two
+  // fragments' lanes swap halves, so that a lane writes 8 rows at once.
+  static __device__ __forceinline__ int store(const v4f (&acc)[FM][FN], const Scaled8& g, const Place& p, int lane,
+                                              int wm, int wn) {
+    const int col0 = p.n0 + wn * (BN / WN) + (lane & 15), row0 = p.m0 + wm * (BM / WM);
+    if (g.parts > 1 || g.ctype == OZGEMM_F32) {
+      float* out = g.parts > 1 ? g.partial + (long)p.part * g.n * g.m : (float*)g.C;
+      const long ld = g.parts > 1 ? g.m : g.ldc;
+      const int row = row0 + 4 * (lane >> 4);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        if (col0 + j * 16 < g.n) {
+          float* to = out + (col0 + j * 16) * ld + row;
+#pragma unroll
+          for (int i = 0; i < FM; ++i) {
+            if (row + i * 16 + 4 <= g.m) {
+              *reinterpret_cast<v4f_any*>(to + i * 16) = acc[i][j];
+            } else if (row + i * 16 < g.m) {
+              some(to + i * 16, __builtin_bit_cast(v4u8, acc[i][j]), 4 * (g.m - row - i * 16));
+            }
+          }
         }
       }
+      return 0;  // (twice as many as STORES)
+    }
+    const int row = row0 + ((lane >> 4) & 1) * 16 + 8 * (lane >> 5);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      uint16_t* to = (uint16_t*)g.C + (long)(col0 + j * 16) * g.ldc + row;
+#pragma unroll
+      for (int i = 0; i < FM; i += 2) {
+        uint32_t w[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            w[u][k] = round16(acc[i + u][j][2 * k], g.ctype) | (uint32_t)round16(acc[i + u][j][2 * k + 1], g.ctype) << 16;
+        // lanes 16 .. 31 and 48 .. 63 of the first for lanes 0 .. 15 and 32 .. 47 of the second: rows 0 .. 7 of
+        // fragment i, then of i + 1, rows 8 .. 15 of i, then of i + 1
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const auto x = __builtin_amdgcn_permlane16_swap(w[0][k], w[1][k], false, false);
+          w[0][k] = x[0];
+          w[1][k] = x[1];
+        }
+        const v4u8 v = {w[0][0], w[0][1], w[1][0], w[1][1]};
+        if (col0 + j * 16 < g.n) {
+          if (row + i * 16 + 8 <= g.m)
+            *reinterpret_cast<v4u_at2*>(to + i * 16) = v;
+          else if (row + i * 16 < g.m)
+            some(to + i * 16, v, 2 * (g.m - row - i * 16));
+        }
+      }
+    }
+    return p.m0 + BM <= g.m && p.n0 + BN <= g.n ? STORES : 0;
+  }
+
+  // The first bytes (a multiple of 2, under 16) of v; a loop, as code that few tiles run has to be fetched too.
+  static __device__ __forceinline__ void some(void* to, v4u8 v, int bytes) {
+    uint16_t* p = (uint16_t*)to;
+#pragma unroll 1
+    for (int k = 0; k < bytes; k += 2) {
+      *p++ = (uint16_t)v[0];
+      v = v4u8{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
     }
   }
 };
 
-template <class Tile, int BM, int BN>
-__global__ __launch_bounds__(Tile::THREADS) void scaled_tiles_kernel(Scaled8 g) {
+template <class Tile>
+__global__ __launch_bounds__(Tile::THREADS) void scaled_tiles_kernel(Scaled8 g, int tiles) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  const int tiles_m = (g.m + BM - 1) / BM, tiles_n = (g.n + BN - 1) / BN, whole = tiles_m * tiles_n;
-  const int part = blockIdx.x / whole;
-  int nj, mi;
-  panel_order<4>(xcd_order(blockIdx.x - part * whole, whole), tiles_n, tiles_m, nj, mi);
-  const int blocks = (g.q + 127) >> 7, each = (blocks + g.parts - 1) / g.parts;
-  const int k0 = min(part * each, blocks) * 128, k_end = min(g.q, k0 + each * 128);
-  v4f acc[Tile::FM][Tile::FN];
-  Tile::run(acc, smem, g, mi * BM, nj * BN, k0, k_end);
-  slice_barrier<0>();
-  const Target to = g.parts > 1 ? Target{g.partial + (long)part * g.n * g.m, OZGEMM_F32, g.m, mi * BM, g.m, nj * BN,
-                                         g.n, nullptr, nullptr}
-                                : Target{g.C, g.ctype, g.ldc, mi * BM, g.m, nj * BN, g.n, nullptr, nullptr};
-  Store<Tile>::run(acc, smem, to);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Tile::walk(g, smem, lane, wave, tiles);
 }
 
 // The sum of the parts, in their order: a block per column and 1024 rows.
-__global__ __launch_bounds__(256) void join_parts_kernel(Scaled8 g) {
+__global__ __launch_bounds__(256) void join_parts_kernel(Scaled8 g, int parts) {
   const int row = blockIdx.y * 1024 + threadIdx.x * 4;
   const long col = blockIdx.x;
   if (row >= g.m) return;
-  const v4f v = sum_parts(g.partial + col * g.m + row, (long)g.n * g.m, g.parts, g.m - row);
+  const v4f v = sum_parts(g.partial + col * g.m + row, (long)g.n * g.m, parts, g.m - row);
   const long to = col * g.ldc + row;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -320,10 +549,11 @@ __global__ __launch_bounds__(FEW8_WAVES * 64) void scaled_few_kernel(Scaled8 g) 
     if (left < 128 && (g.q & 15) != 0) {  // a piece that ends inside the last block
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        const v4u8 keep = first_bytes(left - h * 64);
 #pragma unroll
-        for (int i = 0; i < MR; ++i) ra[i][h] = first_bytes(ra[i][h], left - h * 64);
+        for (int i = 0; i < MR; ++i) ra[i][h] &= keep;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) rb[j][h] = first_bytes(rb[j][h], left - h * 64);
+        for (int j = 0; j < FN; ++j) rb[j][h] &= keep;
       }
     }
     Frag<TB, true> fb[FN];
@@ -333,12 +563,12 @@ __global__ __launch_bounds__(FEW8_WAVES * 64) void scaled_few_kernel(Scaled8 g) 
     for (int i = 0; i < MR; ++i) {
       Frag<TA, true> fa;
       fa.set(ra[i][0], ra[i][1]);
+      v4f d[FN];
+      block_products<TA, TB, true, FN>(d, fa, fb);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const v4f d = block_product<TA, TB, true>(fa, fb[j]);
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s4[i][r] * xb[j], acc[i][j][r]);
-      }
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[j][r], s4[i][r] * xb[j], acc[i][j][r]);
     }
   }
 #pragma unroll
@@ -380,15 +610,20 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const uint8_t* src, lon
 
 constexpr int FEW8_COLS = 64;
 
-template <int TA, int TB, bool WIDE, bool AROW, int B, int W>
+hipError_t join(const Scaled8& g, int parts, hipStream_t st) {
+  join_parts_kernel<<<dim3(g.n, (g.m + 1023) / 1024), 256, 0, st>>>(g, parts);
+  return hipGetLastError();
+}
+
+template <int TA, int TB, bool WIDE, bool AROW, int BM, int BN, int WM>
 hipError_t launch_tiles(const Scaled8& g, hipStream_t st) {
-  using Tile = Tile8<TA, TB, WIDE, AROW, B, B, 2, W>;
-  constexpr int SMEM = std::max(2 * Tile::BUF, Store<Tile>::BYTES);
-  const long tiles = (long)((g.m + B - 1) / B) * ((g.n + B - 1) / B) * g.parts;
-  auto kernel = scaled_tiles_kernel<Tile, B, B>;
-  const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  using Tile = Tile8<TA, TB, WIDE, AROW, BM, BN, WM, 8 / WM>;
+  const long tiles = (long)((g.m + BM - 1) / BM) * ((g.n + BN - 1) / BN) * g.parts;
+  const long room = 256 * (160 * 1024 / Tile::SMEM);  // blocks that the card holds
+  auto kernel = scaled_tiles_kernel<Tile>;
+  const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, Tile::SMEM);
   if (e != hipSuccess) return e;
-  kernel<<<(unsigned)tiles, Tile::THREADS, SMEM, st>>>(g);
+  kernel<<<(unsigned)std::min(tiles, room), Tile::THREADS, Tile::SMEM, st>>>(g, (int)tiles);
   return hipGetLastError();
 }
 
@@ -407,16 +642,15 @@ hipError_t launch_few(const Scaled8& g, hipStream_t st) {
 template <int TA, int TB, bool AROW>
 hipError_t launch_kind(const Scaled8& g, hipStream_t st) {
   if (g.n <= FEW8_COLS) return launch_few<TA, TB, AROW>(g, st);
+  if (g.q == 0) return join(g, 0, st);
   const long big = (long)((g.m + 255) / 256) * ((g.n + 255) / 256);
   const bool wide = g.ctype == OZGEMM_F32;
   hipError_t e;
   if (big >= 128)
-    e = wide ? launch_tiles<TA, TB, true, AROW, 256, 4>(g, st) : launch_tiles<TA, TB, false, AROW, 256, 4>(g, st);
+    e = wide ? launch_tiles<TA, TB, true, AROW, 256, 128, 4>(g, st) : launch_tiles<TA, TB, false, AROW, 256, 256, 2>(g, st);
   else
-    e = wide ? launch_tiles<TA, TB, true, AROW, 128, 2>(g, st) : launch_tiles<TA, TB, false, AROW, 128, 2>(g, st);
-  if (e != hipSuccess || g.parts == 1) return e;
-  join_parts_kernel<<<dim3(g.n, (g.m + 1023) / 1024), 256, 0, st>>>(g);
-  return hipGetLastError();
+    e = wide ? launch_tiles<TA, TB, true, AROW, 128, 128, 2>(g, st) : launch_tiles<TA, TB, false, AROW, 128, 128, 2>(g, st);
+  return e != hipSuccess || g.parts == 1 ? e : join(g, g.parts, st);
 }
 
 template <int TA, int TB>
@@ -428,10 +662,11 @@ hipError_t launch_types(const Scaled8& g, hipStream_t st) {
 
 int scaled_parts(int ctype, int m, int n, int q) {
   (void)ctype;
-  if (n <= FEW8_COLS) return 1;
+  if (n <= FEW8_COLS || q == 0) return 1;
   const long tiles = (long)((m + 127) / 128) * ((n + 127) / 128), blocks = (q + 127) / 128;
   if (tiles >= 256) return 1;
-  return (int)std::max(1L, std::min(512 / tiles, blocks / 4));
+  const long parts = std::max(1L, std::min(512 / tiles, blocks / 4)), each = (blocks + parts - 1) / parts;
+  return (int)((blocks + each - 1) / each);  // none of them empty
 }
 
 bool scaled_fits(int m, int n, int parts) {
