@@ -35,10 +35,10 @@ def _new_blocks(n: int, q: int, rows: int, dtype, like):
     boundaries, as the products read them in place; scales of a row each with
     those of one block next to one another, as they load them."""
     blocks = -(-q // BLOCK)
-    v = torch.empty((n, -(-q // 16) * 16), dtype=dtype, device=like.device)[:, :q]
+    v = like.new_empty_strided((n, q), (-(-q // 16) * 16, 1), dtype=dtype)
     if rows == 1:
-        return v, torch.empty((blocks, n), dtype=torch.float32, device=like.device).t()
-    return v, torch.empty((-(-n // rows), blocks), dtype=torch.float32, device=like.device)
+        return v, like.new_empty_strided((n, blocks), (1, n), dtype=torch.float32)
+    return v, like.new_empty((-(-n // rows), blocks), dtype=torch.float32)
 
 
 def quantize_blocks(X, rows: int = 1, both: bool = False, dtype=torch.float8_e4m3fn):
@@ -80,6 +80,8 @@ def _block_args(V, S):
 def _values(V, what: str):
     """8-bit rows with their entries next to each other, and their distance."""
     n, q = V.shape
+    if V.is_contiguous():
+        return V, max(1, q)
     if (q > 1 and V.stride(1) != 1) or (n > 1 and not max(1, q) <= V.stride(0) <= _LD_MAX):
         copy = torch.empty((n, -(-q // 16) * 16), dtype=V.dtype, device=V.device)[:, :q]
         V = copy.copy_(V)

@@ -41,6 +41,12 @@ int scaled_parts(int ctype, int m, int n, int q);
 bool scaled_fits(int m, int n, int parts);
 hipError_t launch_scaled(const Scaled8& g, hipStream_t st);
 
+// Whether a product of these sizes goes by the largest tiles.
+bool scaled_big(int m, int n);
+
+// the scales (row, block) of rows of q entries to block rows + row
+hipError_t launch_turn_scales(const float* src, long srow, long sblock, int rows, int q, float* dst, hipStream_t st);
+
 // rows x q bytes, rows ld apart, to rows up(q, 16) apart
 hipError_t launch_align_rows(const uint8_t* src, long ld, int rows, int q, uint8_t* dst, long dld, hipStream_t st);
 

@@ -499,8 +499,76 @@ constexpr int FEW8_WAVES = 8;
 
 // Bound by reading A once: a block takes 16 MR rows of it and all (up to 16
 // FN) columns; its eight wavefronts share the inner dimension block by block,
-// straight from HBM into MFMA operands, and their sums meet in LDS.  The
-// products are wide: next to the loads they cost nothing.
+// straight from HBM into MFMA operands, the next block's loads in flight while one is
+// multiplied, and their sums meet in LDS.  The products are wide: next to the loads
+// they cost little.  MR = 2 halves what the columns take from L2 (64 columns of
+// 8192 x 4096: 30 us with 1).
+template <int TA, int TB, bool AROW, int MR, int FN>
+struct Few8 {
+  v4u8 ra[MR][2], rb[FN][2];
+  float xb[FN], sa[MR][AROW ? 4 : 1];
+
+  __device__ __forceinline__ void load(const Scaled8& g, const uint8_t* const (&pa)[MR], const uint8_t* const (&pb)[FN],
+                                       const float* const (&sb)[FN], int m0, int lane, int b) {
+    const int k = b * 128, left = g.q - k - (lane >> 4) * 16;  // of this lane's first piece
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool any = left > h * 64;
+#pragma unroll
+      for (int i = 0; i < MR; ++i)
+        ra[i][h] = any ? *reinterpret_cast<const v4u8*>(pa[i] + k + h * 64) : v4u8{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        rb[j][h] = any ? *reinterpret_cast<const v4u8*>(pb[j] + k + h * 64) : v4u8{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) xb[j] = sb[j][b * g.B.sblock];
+#pragma unroll
+    for (int i = 0; i < MR; ++i)
+#pragma unroll
+      for (int r = 0; r < (AROW ? 4 : 1); ++r) {
+        const int row = min(m0 + i * 16 + (AROW ? 4 * (lane >> 4) + r : 0), g.m - 1) >> g.A.shift;
+        sa[i][r] = g.A.s[row * g.A.srow + b * g.A.sblock];
+      }
+  }
+
+  __device__ __forceinline__ void multiply(v4f (&acc)[MR][FN], int left) {
+    if (left < 128 && (left & 15) != 0) {  // a piece that ends inside the last block
+      const int lane = threadIdx.x & 63;
+      int have = left - (lane >> 4) * 16;
+      asm volatile("" : "+v"(have));  // (the masks are worked out here, not in every block)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v4u8 keep = first_bytes(have - h * 64);
+#pragma unroll
+        for (int i = 0; i < MR; ++i) ra[i][h] &= keep;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) rb[j][h] &= keep;
+      }
+    }
+    Frag<TA, true> fa[MR];
+#pragma unroll
+    for (int i = 0; i < MR; ++i) fa[i].set(ra[i][0], ra[i][1]);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      Frag<TB, true> fb;
+      fb.set(rb[j][0], rb[j][1]);
+      v4f d[MR];
+#pragma unroll
+      for (int i = 0; i < MR; ++i) d[i] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < MR; ++i) d[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fa[i].h[t], fb.h[t], d[i], 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < MR; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = __builtin_fmaf(d[i][r], sa[i][AROW ? r : 0] * xb[j], acc[i][j][r]);
+    }
+  }
+};
+
 template <int TA, int TB, bool AROW, int MR, int FN>
 __global__ __launch_bounds__(FEW8_WAVES * 64) void scaled_few_kernel(Scaled8 g) {
   __shared__ v4f sums[FEW8_WAVES][MR][FN][64];
@@ -520,55 +588,13 @@ __global__ __launch_bounds__(FEW8_WAVES * 64) void scaled_few_kernel(Scaled8 g) 
   }
   v4f acc[MR][FN] = {};
   const int blocks = (g.q + 127) >> 7;
-#pragma unroll 2
-  for (int b = wave; b < blocks; b += FEW8_WAVES) {
-    const int k = b * 128, left = g.q - k - piece * 16;  // of this lane's first piece
-    v4u8 ra[MR][2], rb[FN][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool any = left > h * 64;
-#pragma unroll
-      for (int i = 0; i < MR; ++i)
-        ra[i][h] = any ? *reinterpret_cast<const v4u8*>(pa[i] + k + h * 64) : v4u8{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        rb[j][h] = any ? *reinterpret_cast<const v4u8*>(pb[j] + k + h * 64) : v4u8{0, 0, 0, 0};
-    }
-    float xb[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) xb[j] = sb[j][b * g.B.sblock];
-    v4f s4[MR];
-#pragma unroll
-    for (int i = 0; i < MR; ++i) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = min(m0 + i * 16 + (AROW ? 4 * (lane >> 4) + r : 0), g.m - 1) >> g.A.shift;
-        s4[i][r] = AROW || r == 0 ? g.A.s[row * g.A.srow + b * g.A.sblock] : s4[i][0];
-      }
-    }
-    if (left < 128 && (g.q & 15) != 0) {  // a piece that ends inside the last block
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v4u8 keep = first_bytes(left - h * 64);
-#pragma unroll
-        for (int i = 0; i < MR; ++i) ra[i][h] &= keep;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) rb[j][h] &= keep;
-      }
-    }
-    Frag<TB, true> fb[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) fb[j].set(rb[j][0], rb[j][1]);
-#pragma unroll
-    for (int i = 0; i < MR; ++i) {
-      Frag<TA, true> fa;
-      fa.set(ra[i][0], ra[i][1]);
-      v4f d[FN];
-      block_products<TA, TB, true, FN>(d, fa, fb);
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[j][r], s4[i][r] * xb[j], acc[i][j][r]);
+  if (wave < blocks) {
+    Few8<TA, TB, AROW, MR, FN> now, next;
+    now.load(g, pa, pb, sb, m0, lane, wave);
+    for (int b = wave; b < blocks; b += FEW8_WAVES) {
+      if (b + FEW8_WAVES < blocks) next.load(g, pa, pb, sb, m0, lane, b + FEW8_WAVES);
+      now.multiply(acc, g.q - b * 128);
+      now = next;
     }
   }
 #pragma unroll
@@ -608,6 +634,22 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const uint8_t* src, lon
   *reinterpret_cast<v4u8*>(dst + blockIdx.x * dld + c) = v;
 }
 
+// 64 rows x 64 blocks by way of LDS, so that either side is read and written in runs.
+__global__ __launch_bounds__(256) void turn_scales_kernel(const float* src, long srow, long sblock, int rows, int blocks,
+                                                          float* dst) {
+  __shared__ float tile[64][65];
+  const int r0 = blockIdx.x * 64, b0 = blockIdx.y * 64, x = threadIdx.x & 63;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int y = k * 4 + (threadIdx.x >> 6);
+    if (r0 + y < rows && b0 + x < blocks) tile[y][x] = src[(r0 + y) * srow + (b0 + x) * sblock];
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int y = threadIdx.x >> 6; y < 64; y += 4)
+    if (b0 + y < blocks && r0 + x < rows) dst[(long)(b0 + y) * rows + r0 + x] = tile[x][y];
+}
+
 constexpr int FEW8_COLS = 64;
 
 hipError_t join(const Scaled8& g, int parts, hipStream_t st) {
@@ -627,26 +669,30 @@ hipError_t launch_tiles(const Scaled8& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int TA, int TB, bool AROW>
-hipError_t launch_few(const Scaled8& g, hipStream_t st) {
-  const unsigned threads = FEW8_WAVES * 64;
-  if (g.n <= 16)
-    scaled_few_kernel<TA, TB, AROW, 1, 1><<<(g.m + 15) / 16, threads, 0, st>>>(g);
-  else if (g.n <= 32)
-    scaled_few_kernel<TA, TB, AROW, 1, 2><<<(g.m + 15) / 16, threads, 0, st>>>(g);
-  else
-    scaled_few_kernel<TA, TB, AROW, 1, 4><<<(g.m + 15) / 16, threads, 0, st>>>(g);
+template <int TA, int TB, bool AROW, int MR, int FN>
+hipError_t few_kernel(const Scaled8& g, hipStream_t st) {
+  scaled_few_kernel<TA, TB, AROW, MR, FN><<<(g.m + 16 * MR - 1) / (16 * MR), FEW8_WAVES * 64, 0, st>>>(g);
   return hipGetLastError();
 }
+
+// 32 rows a block where that leaves a block for every compute unit.
+template <int TA, int TB, bool AROW>
+hipError_t launch_few(const Scaled8& g, hipStream_t st) {
+  if (g.n <= 16) return few_kernel<TA, TB, AROW, 1, 1>(g, st);
+  const bool two = g.m >= 32 * 256;
+  if (g.n <= 32) return two ? few_kernel<TA, TB, AROW, 2, 2>(g, st) : few_kernel<TA, TB, AROW, 1, 2>(g, st);
+  return two ? few_kernel<TA, TB, AROW, 2, 4>(g, st) : few_kernel<TA, TB, AROW, 1, 4>(g, st);
+}
+
+bool big_tiles(int m, int n) { return n > FEW8_COLS && (long)((m + 255) / 256) * ((n + 255) / 256) >= 128; }
 
 template <int TA, int TB, bool AROW>
 hipError_t launch_kind(const Scaled8& g, hipStream_t st) {
   if (g.n <= FEW8_COLS) return launch_few<TA, TB, AROW>(g, st);
   if (g.q == 0) return join(g, 0, st);
-  const long big = (long)((g.m + 255) / 256) * ((g.n + 255) / 256);
   const bool wide = g.ctype == OZGEMM_F32;
   hipError_t e;
-  if (big >= 128)
+  if (big_tiles(g.m, g.n))
     e = wide ? launch_tiles<TA, TB, true, AROW, 256, 128, 4>(g, st) : launch_tiles<TA, TB, false, AROW, 256, 256, 2>(g, st);
   else
     e = wide ? launch_tiles<TA, TB, true, AROW, 128, 128, 2>(g, st) : launch_tiles<TA, TB, false, AROW, 128, 128, 2>(g, st);
@@ -667,6 +713,14 @@ int scaled_parts(int ctype, int m, int n, int q) {
   if (tiles >= 256) return 1;
   const long parts = std::max(1L, std::min(512 / tiles, blocks / 4)), each = (blocks + parts - 1) / parts;
   return (int)((blocks + each - 1) / each);  // none of them empty
+}
+
+bool scaled_big(int m, int n) { return big_tiles(m, n); }
+
+hipError_t launch_turn_scales(const float* src, long srow, long sblock, int rows, int q, float* dst, hipStream_t st) {
+  const int blocks = (q + 127) / 128;
+  turn_scales_kernel<<<dim3((rows + 63) / 64, (blocks + 63) / 64), 256, 0, st>>>(src, srow, sblock, rows, blocks, dst);
+  return hipGetLastError();
 }
 
 bool scaled_fits(int m, int n, int parts) {

@@ -91,8 +91,8 @@ __device__ __forceinline__ void store_y(const Norm& g, long row, int c, int t, c
 }
 
 template <int TYPE, int OUT, int G, int P>
-__global__ __launch_bounds__(G > 256 ? G : 256) void norm_kernel(Norm g) {
-  constexpr int THREADS = G > 256 ? G : 256, RB = THREADS / G;
+__global__ __launch_bounds__(256) void norm_kernel(Norm g) {
+  constexpr int RB = 256 / G;
   __shared__ double meet[G / 64 + 1];
   const int t = threadIdx.x % G;
   float w[P][8];
@@ -194,13 +194,13 @@ struct NormGrads {
 };
 
 // Every group of G threads walks its rows and keeps their share of dw in
-// registers; join_weights adds the groups' in a fixed order.
+// registers; a block's groups meet in LDS, and join_weights adds the blocks' in a
+// fixed order.
 template <int TYPE, int G, int P>
-__global__ __launch_bounds__(G > 256 ? G : 256) void norm_grads_kernel(NormGrads g) {
-  constexpr int THREADS = G > 256 ? G : 256, RB = THREADS / G;
+__global__ __launch_bounds__(256) void norm_grads_kernel(NormGrads g) {
+  constexpr int RB = 256 / G;
   __shared__ double meet[G / 64 + 1], meet2[G / 64 + 1];
   const int t = threadIdx.x % G;
-  const long group = (long)blockIdx.x * RB + threadIdx.x / G;
   float w[P][8], dw[P][8];
 #pragma unroll
   for (int p = 0; p < P; ++p) load_weights<TYPE>(w[p], g.w, g.wf32, (p * G + t) * 8, g.q);
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_grads_kernel(NormGrads
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[p][k] = 0.f;
-  for (long row = group; row < g.n; row += (long)gridDim.x * RB) {
+  for (long row = (long)blockIdx.x * RB + threadIdx.x / G; row < g.n; row += (long)gridDim.x * RB) {
     Raw8<TYPE> h[P], dy[P], dh[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -257,9 +257,24 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_grads_kernel(NormGrads
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int c = (p * G + t) * 8;
+    if constexpr (RB > 1) {
+      __shared__ v4f8 sums[RB - 1][G][2];
+      const int group = threadIdx.x / G;
+      __syncthreads();  // (the piece before has been read)
+      if (group > 0) {
+        sums[group - 1][t][0] = v4f8{dw[p][0], dw[p][1], dw[p][2], dw[p][3]};
+        sums[group - 1][t][1] = v4f8{dw[p][4], dw[p][5], dw[p][6], dw[p][7]};
+      }
+      __syncthreads();
+      if (group > 0) continue;
+#pragma unroll
+      for (int o = 0; o < RB - 1; ++o)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dw[p][k] += sums[o][t][k >> 2][k & 3];
+    }
     Raw8<OZGEMM_F32> o;
     o.set(dw[p]);
-    if (c < g.q) o.store(g.partial, group * g.q + c, g.q - c);
+    if (c < g.q) o.store(g.partial, (long)blockIdx.x * g.q + c, g.q - c);
   }
 }
 
@@ -323,22 +338,21 @@ __global__ __launch_bounds__(256) void norm_grads_columns_kernel(NormGrads g) {
   o.store(g.partial, (long)blockIdx.y * g.q + c, g.q - c);
 }
 
-// dw = the groups' sums added in FP64: 16 wavefronts take every 16th group of
-// 64 columns each.
+// dw = the blocks' sums added in FP64: 32 half-wavefronts take every 32nd
+// block's, 32 columns each.
 __global__ __launch_bounds__(1024) void join_weights_kernel(const float* partial, int groups, int q, void* dw, int type) {
-  __shared__ double part[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  __shared__ double part[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
   double v = 0;
   if (c < q) {
 #pragma unroll 8
-    for (int i = wave; i < groups; i += 16) v += (double)partial[(long)i * q + c];
+    for (int i = y; i < groups; i += 32) v += (double)partial[(long)i * q + c];
   }
-  part[wave][lane] = v;
+  part[y][x] = v;
   __syncthreads();
-  if (wave > 0 || c >= q) return;
-  v = part[0][lane];
+  if (y > 0 || c >= q) return;
 #pragma unroll
-  for (int k = 1; k < 16; ++k) v += part[k][lane];
+  for (int k = 1; k < 32; ++k) v += part[k][x];
   const float f = to_odd(v);
   if (type == OZGEMM_F32)
     ((float*)dw)[c] = (float)v;
@@ -353,7 +367,7 @@ __global__ __launch_bounds__(1024) void join_weights_kernel(const float* partial
 struct Shape {
   int G, P;
 };
-constexpr Shape SHAPES[] = {{64, 1}, {64, 2}, {64, 4}, {256, 2}, {256, 4}};
+constexpr Shape SHAPES[] = {{64, 1}, {64, 2}, {256, 1}, {256, 2}, {256, 4}};
 
 Shape shape_of(int q) {
   for (const Shape& s : SHAPES)
@@ -367,17 +381,15 @@ bool with_shape(int q, const Call& call) {
   const Shape s = shape_of(q);
   if (s.G == 64 && s.P == 1) call.template run<64, 1>();
   if (s.G == 64 && s.P == 2) call.template run<64, 2>();
-  if (s.G == 64 && s.P == 4) call.template run<64, 4>();
+  if (s.G == 256 && s.P == 1) call.template run<256, 1>();
   if (s.G == 256 && s.P == 2) call.template run<256, 2>();
   if (s.G == 256 && s.P == 4) call.template run<256, 4>();
   return s.G > 0;
 }
 
-// Blocks for n rows: as many as the card's 256 compute units hold at once, which walk the rows.
-long blocks_for(int n, int G) {
-  const long threads = std::max(G, 256), rb = threads / G;
-  return std::min(((long)n + rb - 1) / rb, 256 * (2048 / threads));
-}
+// Blocks of 256 threads for n rows, which walk them: eight for each of the card's 256 compute units,
+// or (gradients, which have a row of dw to hand on each) four.
+long blocks_for(int n, int G, int each) { return std::min(((long)n * G + 255) / 256, 256L * each); }
 
 template <int TYPE, int OUT>
 struct Forward {
@@ -385,7 +397,7 @@ struct Forward {
   hipStream_t st;
   template <int G, int P>
   void run() const {
-    norm_kernel<TYPE, OUT, G, P><<<(unsigned)blocks_for(g.n, G), G > 256 ? G : 256, 0, st>>>(g);
+    norm_kernel<TYPE, OUT, G, P><<<(unsigned)blocks_for(g.n, G, 8), 256, 0, st>>>(g);
   }
 };
 
@@ -404,11 +416,11 @@ void forward_type(int ytype, const Norm& g, hipStream_t st) {
     forward<TYPE, TYPE>(g, st);
 }
 
-// Rows of the partial sums of dw: the groups of threads of a launch (long rows: its gridDim.y).
+// Rows of the partial sums of dw: the blocks of a launch (long rows: its gridDim.y).
 int grads_groups(int n, int q) {
   const Shape s = shape_of(q);
   if (s.G == 0) return (int)std::min<long>(n, std::max<long>(1, 2048 / ((q + 2047) / 2048)));
-  return (int)(blocks_for(n, s.G) * (std::max(s.G, 256) / s.G));
+  return (int)blocks_for(n, s.G, 4);
 }
 
 size_t grads_partial_bytes(int n, int q) { return up((size_t)grads_groups(n, q) * (size_t)q * sizeof(float), 256); }
@@ -423,7 +435,7 @@ struct Backward {
   hipStream_t st;
   template <int G, int P>
   void run() const {
-    norm_grads_kernel<TYPE, G, P><<<(unsigned)blocks_for(g.n, G), G > 256 ? G : 256, 0, st>>>(g);
+    norm_grads_kernel<TYPE, G, P><<<(unsigned)blocks_for(g.n, G, 4), 256, 0, st>>>(g);
   }
 };
 
@@ -550,7 +562,7 @@ int ozgemm_rms_norm_grads(int type, int wtype, int n, int q, const void* dY, int
       backward<OZGEMM_F16>(g, st);
   }
   if (dw != nullptr)
-    join_weights_kernel<<<(unsigned)((q + 63) / 64), 1024, 0, st>>>((const float*)workspace, groups, q, dw, wtype);
+    join_weights_kernel<<<(unsigned)((q + 31) / 32), 1024, 0, st>>>((const float*)workspace, groups, q, dw, wtype);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? OZGEMM_OK : record_hip_error(e);
 }

@@ -19,25 +19,50 @@ bool known8(int type) { return type == OZGEMM_E4M3 || type == OZGEMM_E5M2; }
 // behind the row, inside the same aligned 16 bytes.
 bool aligned8(const void* p, long ld) { return ((uintptr_t)p & 15) == 0 && ld % 16 == 0 && ld <= LD8_MAX; }
 
+// How the scales of one operand lie.
+struct Scales {
+  int rows, per;
+  long long srow, sblock;
+};
+
 struct Rooms {
-  bool a, b;  // copied
-  size_t a_at, b_at, partial, total;
+  bool a, b;    // copied
+  bool sa, sb;  // scales turned over
+  size_t a_at, b_at, sa_at, sb_at, partial, total;
   long ld;
   int parts;
 };
 
-Rooms rooms(int ctype, int m, int n, int q, const void* A, int lda, const void* B, int ldb) {
+// A tile loads its rows' scales of one block at a time: a line for each where
+// they lie block after block of a row.  Turning them over first costs a launch
+// (3 us), which pays where many tiles read them (8192 x 8192 x 4096: 288 us as
+// they lie, 250 so).
+bool turns(const Scales& s, int m, int n, int q) {
+  return s.per == 1 && s.srow != 1 && s.rows > 1 && q > BLOCK8 && scaled_big(m, n);
+}
+
+Rooms rooms(int ctype, int m, int n, int q, const void* A, int lda, const Scales& sa, const void* B, int ldb,
+            const Scales& sb) {
   Rooms r{};
   r.parts = 1;
   if (m < 1 || n < 1 || q < 1) return r;
   r.ld = (long)up(q, 16);
   r.a = !aligned8(A, lda);
   r.b = !aligned8(B, ldb);
-  r.a_at = 0;
-  r.b_at = r.a ? up((size_t)m * r.ld, WS_ALIGN) : 0;
-  r.partial = r.b_at + (r.b ? up((size_t)n * r.ld, WS_ALIGN) : 0);
+  r.sa = turns(sa, m, n, q);
+  r.sb = turns(sb, m, n, q);
+  const size_t blocks = (size_t)(q + BLOCK8 - 1) / BLOCK8;
+  auto take = [&](bool wanted, size_t bytes) {
+    const size_t at = r.total;
+    if (wanted) r.total += up(bytes, WS_ALIGN);
+    return at;
+  };
+  r.a_at = take(r.a, (size_t)m * r.ld);
+  r.b_at = take(r.b, (size_t)n * r.ld);
+  r.sa_at = take(r.sa, blocks * m * sizeof(float));
+  r.sb_at = take(r.sb, blocks * n * sizeof(float));
   r.parts = scaled_parts(ctype, m, n, q);
-  r.total = r.partial + (r.parts > 1 ? up((size_t)r.parts * m * n * sizeof(float), WS_ALIGN) : 0);
+  r.partial = take(r.parts > 1, (size_t)r.parts * m * n * sizeof(float));
   return r;
 }
 
@@ -54,10 +79,11 @@ using namespace oz;
 
 extern "C" {
 
-size_t ozgemm_scaled_gemm_workspace_bytes(int ctype, int m, int n, int q, const void* A, int lda, const void* B,
-                                          int ldb) {
+size_t ozgemm_scaled_gemm_workspace_bytes(int ctype, int m, int n, int q, const void* A, int lda, int rows_a,
+                                          long long sarow, long long sablock, const void* B, int ldb, long long sbrow,
+                                          long long sbblock) {
   if (m < 0 || n < 0 || q < 0 || m > OZGEMM_MAX_ROWS || n > OZGEMM_MAX_ROWS || q > OZGEMM_MAX_ROWS) return 0;
-  return rooms(ctype, m, n, q, A, lda, B, ldb).total;
+  return rooms(ctype, m, n, q, A, lda, Scales{m, rows_a, sarow, sablock}, B, ldb, Scales{n, 1, sbrow, sbblock}).total;
 }
 
 int ozgemm_scaled_gemm(int atype, int btype, int ctype, int m, int n, int q, const void* A, int lda, const float* SA,
@@ -91,7 +117,8 @@ int ozgemm_scaled_gemm(int atype, int btype, int ctype, int m, int n, int q, con
       overlap(C, cb, SA, scale_extent(m, rows_a, q, sarow, sablock)) ||
       overlap(C, cb, SB, scale_extent(n, 1, q, sbrow, sbblock)))
     return -18;
-  const Rooms r = rooms(ctype, m, n, q, A, lda, B, ldb);
+  const Rooms r =
+      rooms(ctype, m, n, q, A, lda, Scales{m, rows_a, sarow, sablock}, B, ldb, Scales{n, 1, sbrow, sbblock});
   if (r.total > 0 && (workspace == nullptr || ((uintptr_t)workspace & (WS_ALIGN - 1)))) return -20;
   if (workspace_bytes < r.total) return OZGEMM_WORKSPACE_TOO_SMALL;
   if (!scaled_fits(m, n, r.parts)) return OZGEMM_RANGE;
@@ -121,6 +148,18 @@ int ozgemm_scaled_gemm(int atype, int btype, int ctype, int m, int n, int q, con
     e = launch_align_rows(g.B.p, ldb, n, q, (uint8_t*)ws + r.b_at, r.ld, st);
     g.B.p = (const uint8_t*)ws + r.b_at;
     g.B.ld = r.ld;
+  }
+  if (e == hipSuccess && r.sa) {
+    e = launch_turn_scales(SA, g.A.srow, g.A.sblock, m, q, (float*)(ws + r.sa_at), st);
+    g.A.s = (const float*)(ws + r.sa_at);
+    g.A.srow = 1;
+    g.A.sblock = m;
+  }
+  if (e == hipSuccess && r.sb) {
+    e = launch_turn_scales(SB, g.B.srow, g.B.sblock, n, q, (float*)(ws + r.sb_at), st);
+    g.B.s = (const float*)(ws + r.sb_at);
+    g.B.srow = 1;
+    g.B.sblock = n;
   }
   if (e == hipSuccess) e = launch_scaled(g, st);
   return e == hipSuccess ? OZGEMM_OK : record_hip_error(e);

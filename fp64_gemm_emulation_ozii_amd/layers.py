@@ -28,12 +28,14 @@ def _no_grad(what: str, *tensors, instead: str = "") -> None:
     """Refuses tensors whose derivatives would get lost: those that autograd
     records (unless it is switched off), and those with a tangent of its forward
     mode (which torch.no_grad() does not switch off)."""
+    recorded = torch.is_grad_enabled()
+    tangents = getattr(forward_ad, "_current_level", 0) >= 0  # outside of every dual level there are none
     for t in tensors:
         if t is None:
             continue
-        if t.requires_grad and torch.is_grad_enabled():
+        if recorded and t.requires_grad:
             raise RuntimeError(f"{what} is not recorded by autograd: call it under torch.no_grad(){instead}")
-        if forward_ad.unpack_dual(t).tangent is not None:
+        if tangents and forward_ad.unpack_dual(t).tangent is not None:
             raise RuntimeError(f"{what} has no forward-mode derivative: call it on the primal of a dual tensor")
 
 
@@ -72,6 +74,8 @@ def _rows(t, what: str):
     if t.dim() != 2:
         raise ValueError(f"{what} must have two dimensions, got {tuple(t.shape)}")
     n, q = t.shape
+    if t.is_contiguous() and not t.is_neg():
+        return t, max(1, q)
     t = t.resolve_neg()
     if (q > 1 and t.stride(1) != 1) or (n > 1 and not max(1, q) <= t.stride(0) <= _LD_MAX):
         t = t.contiguous()
@@ -297,18 +301,30 @@ def _dense(t) -> bool:
 
 
 def _gradients(grads, what: str):
-    if isinstance(grads, torch.Tensor):
-        grads = (grads,)
-    grads = list(grads)
+    """(tensors, their types, their numbers of entries), checked."""
+    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
     if len(grads) > L.OZGEMM_ARRAYS_MAX:
         raise ValueError(f"{what}: up to {L.OZGEMM_ARRAYS_MAX} tensors, got {len(grads)}")
+    if not grads:
+        return grads, [], []
+    strided, device = torch.strided, grads[0].get_device()
+    types, sizes = [], []
     for g in grads:
-        if g.layout != torch.strided:
+        if g.layout is not strided:
             raise TypeError(f"{what}: {g.layout} tensors are not supported")
-        if g.device != grads[0].device:
+        if g.get_device() != device:
             raise ValueError(f"{what}: tensors on {grads[0].device} and {g.device}")
+        types.append(_TYPES.get(g.dtype, -1))
+        sizes.append(g.numel())
+    if -1 in types:
+        _type_of(grads[types.index(-1)], what, tuple(_TYPES))
     _no_grad(what, *grads)
-    return grads, [_type_of(g, what, tuple(_TYPES)) for g in grads]
+    return grads, types, sizes
+
+
+def _run(g):
+    """A tensor's entries as a run of memory: itself, or a copy."""
+    return g if g.is_contiguous() and not g.is_neg() or _dense(g) and not g.is_neg() else g.resolve_neg().contiguous()
 
 
 def gradient_norm(grads):
@@ -320,13 +336,12 @@ def gradient_norm(grads):
     together (the root of the sum of squares) and hand the result to
     :func:`clip_gradients`.
     """
-    grads, types = _gradients(grads, "gradient_norm")
+    grads, types, sizes = _gradients(grads, "gradient_norm")
     if not grads:
         return torch.zeros((), dtype=torch.float64)
     with _on_device(grads[0].device):
-        flat = [g if _dense(g) and not g.is_neg() else g.resolve_neg().contiguous() for g in grads]
         norm = torch.empty((), dtype=torch.float64, device=grads[0].device)
-        L.ozgemm_gradient_norm(types, flat, [g.numel() for g in flat], norm)
+        L.ozgemm_gradient_norm(types, [_run(g) for g in grads], sizes, norm)
     return norm
 
 
@@ -341,48 +356,49 @@ def clip_gradients(grads, max_norm: float, norm=None, eps: float = 1e-6, out=Non
     ``out``, tensors of the same shapes and types, receives the products instead.
     No two of the tensors that are written may share memory.
     """
-    grads, types = _gradients(grads, "clip_gradients")
+    grads, types, sizes = _gradients(grads, "clip_gradients")
     if not max_norm >= 0 or not eps >= 0:
         raise ValueError(f"max_norm and eps must not be negative, got {max_norm} and {eps}")
     if out is not None:
         out = [out] if isinstance(out, torch.Tensor) else list(out)
         if len(out) != len(grads):
             raise ValueError(f"out must be {len(grads)} tensors, got {len(out)}")
+        device = grads[0].get_device() if grads else -1
         for g, o in zip(grads, out):
-            if o.layout != torch.strided or o.shape != g.shape or o.dtype != g.dtype or o.device != g.device:
+            if o.shape != g.shape or o.dtype is not g.dtype or o.get_device() != device or o.layout is not torch.strided:
                 raise ValueError(f"out must be {tuple(g.shape)} of {g.dtype} on {g.device}, got {tuple(o.shape)} of "
                                  f"{o.dtype} on {o.device}")
         _no_grad("clip_gradients", *out)
-    if norm is not None and (norm.dtype != torch.float64 or norm.numel() != 1 or (
-            grads and norm.device != grads[0].device) or norm.is_neg()):
-        raise ValueError(f"norm must be one float64 value on the gradients' device, got {norm.numel()} of {norm.dtype} on "
-                         f"{norm.device}")
+    if norm is not None:
+        if norm.dtype != torch.float64 or norm.numel() != 1 or norm.is_neg() or (
+                grads and norm.device != grads[0].device):
+            raise ValueError(f"norm must be one float64 value on the gradients' device, got {norm.numel()} of "
+                             f"{norm.dtype} on {norm.device}")
+        _no_grad("clip_gradients", norm)
     to = grads if out is None else out
-    for o in to:
+    # Runs of memory, entry by entry alike on both sides; others by way of copies.
+    here, there = [], []
+    for g, o in zip(grads, to):
+        if g.is_contiguous() and not g.is_neg() and (g is o or o.is_contiguous() and not o.is_neg()):
+            here.append(g)
+            there.append(o)
+            continue
         if o.is_neg():
             raise ValueError("what is written must not be a negated view")
         if any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
             raise ValueError("what is written must not be an expanded tensor")
-    if norm is not None:
-        _no_grad("clip_gradients", norm)
+        alike = g.stride() == o.stride() and _dense(g) and not g.is_neg()
+        here.append(g if alike else g.resolve_neg().contiguous())
+        there.append(o if alike or g is not o and o.is_contiguous() else here[-1] if g is o else torch.empty_like(here[-1]))
     if not grads:
         return gradient_norm(grads) if norm is None else norm
     with _on_device(grads[0].device):
-        if norm is None:
-            norm = gradient_norm([g.detach() for g in grads])
-        # runs of memory, entry by entry alike on both sides; others by way of copies
-        here, there = [], []
-        for g, o in zip(grads, to):
-            if g is o:
-                g = o = g if _dense(g) else g.contiguous()
-            else:
-                alike = g.stride() == o.stride() and _dense(g) and not g.is_neg()
-                g = g if alike else g.resolve_neg().contiguous()
-                o = o if alike or o.is_contiguous() else torch.empty_like(g)
-            here.append(g)
-            there.append(o)
-        _written(*to)
-        L.ozgemm_clip_gradients(types, here, [g.numel() for g in here], there, norm, max_norm, eps)
+        own = norm is None
+        if own:
+            norm = torch.empty((), dtype=torch.float64, device=grads[0].device)
+        if to:
+            torch.autograd.graph.increment_version(to)
+        L.ozgemm_clip_gradients(types, here, sizes, there, norm, max_norm, eps, measured=not own)
         for o, t in zip(to, there):
             if o is not t:
                 o.copy_(t)

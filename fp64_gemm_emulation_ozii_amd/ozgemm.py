@@ -135,7 +135,7 @@ def lib():
         "ozgemm_quantize_blocks": (c_int, [c_int] * 5 + [vp, c_int] + [vp, c_int, vp, ll, ll] * 2 + [vp]),
         "ozgemm_scaled_gemm": (c_int, [c_int] * 6 + [vp, c_int, vp, c_int, ll, ll, vp, c_int, vp, ll, ll, vp, c_int, vp,
                                        c_size, vp]),
-        "ozgemm_scaled_gemm_workspace_bytes": (c_size, [c_int] * 4 + [vp, c_int, vp, c_int]),
+        "ozgemm_scaled_gemm_workspace_bytes": (c_size, [c_int] * 4 + [vp, c_int, c_int, ll, ll, vp, c_int, ll, ll]),
         "ozgemm_rms_norm": (c_int, [c_int] * 5 + [vp, c_int, vp, c_int, vp, f64, vp, c_int, vp, c_int, vp, ll, ll, vp]),
         "ozgemm_rms_norm_grads": (c_int, [c_int] * 4 + [vp, c_int, vp, c_int, vp, vp, c_int, f64, vp, c_int, vp, vp,
                                           c_size, vp]),
@@ -511,8 +511,9 @@ def ozgemm_quantize_blocks(type, qtype, rows, n, q, X, ldx, V, ldv, S, srow, sbl
 _SCALED_NO_WORKSPACE = -20
 
 
-def ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, A, lda, B, ldb) -> int:
-    return int(lib().ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, _ptr(A), lda, _ptr(B), ldb))
+def ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, A, lda, rows_a, sarow, sablock, B, ldb, sbrow, sbblock) -> int:
+    return int(lib().ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, _ptr(A), lda, rows_a, sarow, sablock, _ptr(B),
+                                                        ldb, sbrow, sbblock))
 
 
 def ozgemm_scaled_gemm(atype, btype, ctype, m, n, q, A, lda, SA, rows_a, sarow, sablock, B, ldb, SB, sbrow, sbblock, C,
@@ -525,7 +526,8 @@ def ozgemm_scaled_gemm(atype, btype, ctype, m, n, q, A, lda, SA, rows_a, sarow, 
     if workspace is None:  # operands are usually read in place
         st = L.ozgemm_scaled_gemm(*ops, None, 0, hs)
     if st == _SCALED_NO_WORKSPACE:
-        need = 0 if workspace is not None else ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, A, lda, B, ldb)
+        need = 0 if workspace is not None else ozgemm_scaled_gemm_workspace_bytes(
+            ctype, m, n, q, A, lda, rows_a, sarow, sablock, B, ldb, sbrow, sbblock)
         keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"), hs)
         st = L.ozgemm_scaled_gemm(*ops, ws, nbytes, hs)
     return _check(st, "ozgemm_scaled_gemm") if check else st
@@ -553,32 +555,39 @@ def ozgemm_rms_norm_grads(type, wtype, n, q, dY, lddy, H, ldh, w, dH, lddh, eps,
     return _check(st, "ozgemm_rms_norm_grads") if check else st
 
 
-def _arrays(types, sizes):
+def _arrays(types, tensors, sizes):
+    """C arrays of the types, addresses and sizes."""
     n = max(1, len(types))
-    return (ctypes.c_int * n)(*types), (ctypes.c_longlong * n)(*sizes)
-
-
-def _addresses(tensors):
-    return (ctypes.c_void_p * max(1, len(tensors)))(*[_ptr(t) for t in tensors])
+    return ((ctypes.c_int * n)(*types), (ctypes.c_void_p * n)(*[t if isinstance(t, int) else t.data_ptr() for t in tensors]),
+            (ctypes.c_longlong * n)(*sizes))
 
 
 def ozgemm_gradient_norm_workspace_bytes(types, sizes) -> int:
-    return int(lib().ozgemm_gradient_norm_workspace_bytes(len(types), *_arrays(types, sizes)))
+    t, _, s = _arrays(types, [], sizes)
+    return int(lib().ozgemm_gradient_norm_workspace_bytes(len(types), t, s))
+
+
+def _gradient_norm(count, t, p, s, norm, workspace, hs) -> int:
+    need = 0 if workspace is not None else int(lib().ozgemm_gradient_norm_workspace_bytes(count, t, s))
+    keep, ws, nbytes = _room(workspace, need, getattr(norm, "device", "cuda"), hs)
+    return lib().ozgemm_gradient_norm(count, t, p, s, _ptr(norm), ws, nbytes, hs)
 
 
 def ozgemm_gradient_norm(types, arrays, sizes, norm, workspace=None, stream=None, check: bool = True) -> int:
     """``types``, ``arrays`` (tensors or addresses) and ``sizes``: lists of one
     length.  Workspace as for :func:`ozgemm_grouped_gemm`."""
-    hs = _stream(stream)
-    t, s = _arrays(types, sizes)
-    need = 0 if workspace is not None else int(lib().ozgemm_gradient_norm_workspace_bytes(len(types), t, s))
-    keep, ws, nbytes = _room(workspace, need, getattr(norm, "device", "cuda"), hs)
-    st = lib().ozgemm_gradient_norm(len(types), t, _addresses(arrays), s, _ptr(norm), ws, nbytes, hs)
+    st = _gradient_norm(len(types), *_arrays(types, arrays, sizes), norm, workspace, _stream(stream))
     return _check(st, "ozgemm_gradient_norm") if check else st
 
 
-def ozgemm_clip_gradients(types, arrays, sizes, out, norm, most, eps, stream=None, check: bool = True) -> int:
-    t, s = _arrays(types, sizes)
-    st = lib().ozgemm_clip_gradients(len(types), t, _addresses(arrays), s, _addresses(out), _ptr(norm), most, eps,
-                                     _stream(stream))
+def ozgemm_clip_gradients(types, arrays, sizes, out, norm, most, eps, measured: bool = True, workspace=None,
+                          stream=None, check: bool = True) -> int:
+    """With ``measured=False`` the norm is worked out first (:func:`ozgemm_gradient_norm`, with that workspace)."""
+    hs = _stream(stream)
+    t, p, s = _arrays(types, arrays, sizes)
+    o = p if out is arrays else (ctypes.c_void_p * max(1, len(types)))(*[
+        x if isinstance(x, int) else x.data_ptr() for x in out])
+    st = OZGEMM_OK if measured else _gradient_norm(len(types), t, p, s, norm, workspace, hs)
+    if st == OZGEMM_OK:
+        st = lib().ozgemm_clip_gradients(len(types), t, p, s, o, _ptr(norm), most, eps, hs)
     return _check(st, "ozgemm_clip_gradients") if check else st

@@ -605,7 +605,8 @@ int ozgemm_quantize_blocks(int type, int qtype, int rows, int n, int q, const vo
  * Operands are read in place where they begin on 16-byte boundaries and their
  * leading dimension is a multiple of 16 up to 2^22 (then as whole aligned 16-byte
  * pieces, of which the last of a row may reach past q: read and not used);
- * others pass through the workspace.  Few tiles with a long inner dimension are
+ * others pass through the workspace, as do the scales of large products whose srow
+ * is not 1.  Few tiles with a long inner dimension are
  * summed in parts, in a fixed order, whose sums take room there too.
  * q = 0 gives zeros.  C must not overlap the operands or their scales.
  * Errors: -i for argument i; OZGEMM_RANGE for m, n or q above OZGEMM_MAX_ROWS or
@@ -617,8 +618,9 @@ int ozgemm_scaled_gemm(int atype, int btype, int ctype, int m, int n, int q,
 
 /* Bytes of workspace the call above needs (the pointers are looked at for their
  * alignment alone); 0 where it needs none or the arguments are invalid.  Host only. */
-size_t ozgemm_scaled_gemm_workspace_bytes(int ctype, int m, int n, int q, const void *A, int lda,
-                                          const void *B, int ldb);
+size_t ozgemm_scaled_gemm_workspace_bytes(int ctype, int m, int n, int q,
+                                          const void *A, int lda, int rows_a, long long sarow, long long sablock,
+                                          const void *B, int ldb, long long sbrow, long long sbblock);
 
 /* Y = H w / sqrt(mean over the row of H^2 + eps) for n rows of q entries, H = X + R.
  *   type   OZGEMM_F32, BF16 or F16: X's, R's and H's; wtype: w's, `type` or OZGEMM_F32
