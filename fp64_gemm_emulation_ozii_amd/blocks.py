@@ -111,12 +111,14 @@ def scaled_linear(X, xs, W, ws, out=None, out_dtype=None):
     Y [n, m] in bfloat16 (``out_dtype``: float16 or float32).
 
     Values are either 8-bit type; scales are any float32.  Rows on 16-byte
-    boundaries are read in place, others from a copy.  float32 results are summed
-    in float32; of those of 16 bits a block's 128 products are summed by the 8-bit
-    matrix cores, which is off by 1.5e-5 of the sums' norm, and blocks in
-    float32.  ``out`` must not overlap the operands.
+    boundaries are read in place, others from a copy.  float32 results, and those
+    of up to 16 rows of X, are summed in float32; of others a block's 128 products
+    are summed by the 8-bit matrix cores, which is off by 1.5e-5 of the sums' norm,
+    and blocks in float32.  ``out`` must not overlap the operands.
     """
-    tx, tw = _eight(X.dtype, "scaled_linear"), _eight(W.dtype, "scaled_linear")
+    tx, tw = _EIGHT.get(X.dtype), _EIGHT.get(W.dtype)
+    if tx is None or tw is None:
+        _eight(X.dtype, "scaled_linear"), _eight(W.dtype, "scaled_linear")
     _no_grad("scaled_linear", X, xs, W, ws, out, instead=" and take the gradients from scaled_linear_grads")
     if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
         raise ValueError(f"X {tuple(X.shape)} and W {tuple(W.shape)} do not go together")
@@ -126,16 +128,21 @@ def scaled_linear(X, xs, W, ws, out=None, out_dtype=None):
     _fits(n, m, q)
     xs, _ = _scales(xs, n, q, "xs", X, False)
     ws, wrows = _scales(ws, m, q, "ws", W, True)
-    dtypes = _OUT if out is not None else (out_dtype or torch.bfloat16,)
-    if dtypes[0] not in _OUT:
-        raise TypeError(f"scaled_linear: results are bfloat16, float16 or float32, not {dtypes[0]}")
-    Y = _target(out, (n, m), dtypes, X, "out")
+    if out is None:
+        out_dtype = out_dtype or torch.bfloat16
+        if out_dtype not in _OUT:
+            raise TypeError(f"scaled_linear: results are bfloat16, float16 or float32, not {out_dtype}")
+        Y, ldy = X.new_empty((n, m), dtype=out_dtype), max(1, m)
+    else:
+        Y = _target(out, (n, m), _OUT, X, "out")
+        ldy = _ld(Y)
     with _on_device(X.device):
         X, ldx = _values(X, "X")
         W, ldw = _values(W, "W")
-        _written(out)
-        L.ozgemm_scaled_gemm(tw, tx, _TYPES[Y.dtype], m, n, q, W, ldw, ws, wrows, ws.stride(0), ws.stride(1), X, ldx, xs,
-                             xs.stride(0), xs.stride(1), Y, _ld(Y))
+        if out is not None:
+            _written(out)
+        L.ozgemm_scaled_gemm(tw, tx, _TYPES[Y.dtype], m, n, q, W, ldw, ws, wrows, *ws.stride(), X, ldx, xs, *xs.stride(),
+                             Y, ldy)
     return Y
 
 

@@ -1,17 +1,19 @@
 // Products of 8-bit operands in scaled blocks (gemm8.h) on gfx950 matrix cores.
 //
 // Two ways to sum a block's 128 products:
-//   narrow  one v_mfma_f32_16x16x128_f8f6f4, for results of 16 bits.  Within the
+//   narrow  one v_mfma_f32_16x16x128_f8f6f4, for results of 16 bits and more than 16 columns.  Within the
 //           products that one lane holds the matrix core keeps what lies above
 //           2^-13 of the largest: blocks of gaussian entries come out with an
 //           error of 1.5e-5 of their sum's norm, a fifteenth of float16's
 //           rounding and a hundredth of bfloat16's.
 //   wide    four v_mfma_f32_16x16x32_f16 of the same entries as half precision
-//           (both 8-bit types are exact there), for float32 results: the sums are
-//           float32 throughout, at half the rate.
+//           (both 8-bit types are exact there), for float32 results, whose sums are
+//           float32 throughout, at half the rate; and for 16 columns and fewer, where
+//           the weights' bytes count and not the products.
 // A block's sum is then multiplied by its scales and added to the accumulators
 // in float32.
 #include <algorithm>
+#include <atomic>
 
 #include "block8.h"
 #include "gemm8.h"
@@ -495,130 +497,152 @@ __global__ __launch_bounds__(256) void join_parts_kernel(Scaled8 g, int parts) {
 // Few columns
 // ---------------------------------------------------------------------------
 
-constexpr int FEW8_WAVES = 8;
-
-// Bound by reading A once: a block takes 16 MR rows of it and all (up to 16
-// FN) columns; its eight wavefronts share the inner dimension block by block,
-// straight from HBM into MFMA operands, the next block's loads in flight while one is
-// multiplied, and their sums meet in LDS.  The products are wide: next to the loads
-// they cost little.  MR = 2 halves what the columns take from L2 (64 columns of
-// 8192 x 4096: 30 us with 1).
-template <int TA, int TB, bool AROW, int MR, int FN>
+// Bound by reading A once.  A block takes 16 RG rows of it and all (up to 16 FN)
+// columns; its eight wavefronts are RG of rows by KG of the inner dimension, of which
+// KG blocks of 128 make a step.  A step's operands go to LDS through NB buffers, whole
+// rows' 128 bytes by eight lanes each: read straight into MFMA operands, 16 neighbouring
+// lanes would ask for 16 different lines (64 columns of 8192 x 4096: 19 us so, 15
+// by way of LDS, both with wide products).  The KG sums meet in LDS, in a fixed order.
+template <int TA, int TB, bool WIDE, bool AROW, int RG, int FN>
 struct Few8 {
-  v4u8 ra[MR][2], rb[FN][2];
-  float xb[FN], sa[MR][AROW ? 4 : 1];
-
-  __device__ __forceinline__ void load(const Scaled8& g, const uint8_t* const (&pa)[MR], const uint8_t* const (&pb)[FN],
-                                       const float* const (&sb)[FN], int m0, int lane, int b) {
-    const int k = b * 128, left = g.q - k - (lane >> 4) * 16;  // of this lane's first piece
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool any = left > h * 64;
-#pragma unroll
-      for (int i = 0; i < MR; ++i)
-        ra[i][h] = any ? *reinterpret_cast<const v4u8*>(pa[i] + k + h * 64) : v4u8{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        rb[j][h] = any ? *reinterpret_cast<const v4u8*>(pb[j] + k + h * 64) : v4u8{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int j = 0; j < FN; ++j) xb[j] = sb[j][b * g.B.sblock];
-#pragma unroll
-    for (int i = 0; i < MR; ++i)
-#pragma unroll
-      for (int r = 0; r < (AROW ? 4 : 1); ++r) {
-        const int row = min(m0 + i * 16 + (AROW ? 4 * (lane >> 4) + r : 0), g.m - 1) >> g.A.shift;
-        sa[i][r] = g.A.s[row * g.A.srow + b * g.A.sblock];
-      }
+  static constexpr int KG = 8 / RG, ROWS = RG + FN;  // sixteens of rows in a block's tile
+  static constexpr int TILE = ROWS * 2048, STAGE = KG * TILE + 8 * 256;
+  static constexpr int LOADS = ROWS * 2 / RG + 1;  // of a wavefront in a step
+  static constexpr int NB = 150 * 1024 / STAGE < 4 ? 150 * 1024 / STAGE : 4;
+  static constexpr int SUMS = KG * RG * FN * 1024;
+  static constexpr int SMEM = NB * STAGE > SUMS ? NB * STAGE : SUMS;
+  static_assert(ROWS * 2 % RG == 0 && NB >= 3, "whole wave loads, two steps ahead");
+  static __device__ __forceinline__ int swz(int row) { return ((row >> 1) ^ (row << 2)) & 7; }
+  template <class V>
+  static __device__ __forceinline__ V read(const char* __restrict__ p) {
+    return *reinterpret_cast<const V*>(p);
   }
 
-  __device__ __forceinline__ void multiply(v4f (&acc)[MR][FN], int left) {
-    if (left < 128 && (left & 15) != 0) {  // a piece that ends inside the last block
-      const int lane = threadIdx.x & 63;
-      int have = left - (lane >> 4) * 16;
-      asm volatile("" : "+v"(have));  // (the masks are worked out here, not in every block)
+  static __device__ __forceinline__ void run(const Scaled8& g, char* smem) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = wave / RG, rg = wave % RG, m0 = blockIdx.x * 16 * RG;
+    const int steps = (((g.q + 127) >> 7) + KG - 1) / KG;
+    // the loads of this wavefront's block, which its RG wavefronts share out
+    const uint8_t* pa = g.A.p + (long)m0 * g.A.ld + kg * 128;
+    const uint8_t* pb = g.B.p + kg * 128;
+    const int len = (g.q + 15) / 16 * 16 - kg * 128;
+    int reca = (min(g.m - m0, 16 * RG) - 1) * (int)g.A.ld + len, recb = (g.n - 1) * (int)g.B.ld + len;
+    const bool a = rg == 0;  // which scales
+    const int srow = a ? min(m0 + lane, g.m - 1) >> g.A.shift : 0;
+    const int scol = min(lane, g.n - 1);
+    const int past = (g.q - 1) >> 7;  // the last block
+    int issued = 0;
+    auto issue = [&]() {
+      const int k = (issued * KG + kg) * 128, left = g.q - k;
+      char* to = smem + issued % NB * STAGE + kg * TILE;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v4u8 keep = first_bytes(have - h * 64);
+      for (int li = 0; li < LOADS - 1; ++li) {
+        const int idx = li * RG + rg, r = lane >> 3;
+        const bool of_a = idx < RG * 2;
+        const int row0 = of_a ? idx * 8 : (idx - RG * 2) * 8;
+        const int kin = ((lane & 7) ^ swz((idx & 1) * 8 + r)) * 16;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(of_a ? pa : pb), 0, left > 0 ? (of_a ? reca : recb) : 0, 0x00020000);
+        const int at = kin < left ? (row0 + r) * (int)(of_a ? g.A.ld : g.B.ld) + kin : (int)0x80000000;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(to + idx * 1024), 16, at,
+                                                 0, 0, 0);
+      }
+      const int b = min(issued * KG + kg, past);
+      const float* s = RG > 1 ? (a ? g.A.s + srow * g.A.srow + b * g.A.sblock : g.B.s + scol * g.B.srow + b * g.B.sblock)
+                              : (lane < 32 ? g.A.s + (min(m0 + (lane & 15), g.m - 1) >> g.A.shift) * g.A.srow +
+                                                 b * g.A.sblock
+                                           : g.B.s + min(lane - 32, g.n - 1) * g.B.srow + b * g.B.sblock);
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)s,
+          (__attribute__((address_space(3))) void*)(smem + issued % NB * STAGE + KG * TILE + wave * 256), 4, 0, 0);
+      ++issued;
+      pa += KG * 128;
+      pb += KG * 128;
+      reca -= KG * 128;
+      recb -= KG * 128;
+    };
 #pragma unroll
-        for (int i = 0; i < MR; ++i) ra[i][h] &= keep;
+    for (int b = 0; b < NB - 1; ++b) issue();
+    v4f acc[FN] = {};
+    const int at0 = (lane & 15) * 128 + (((lane >> 4) ^ swz(lane & 15)) * 16), at1 = at0 ^ 64;
+    // where the two kinds of scales lie, from a block's first wavefront's place on
+    const int sa_at = (AROW ? rg * 16 + 4 * (lane >> 4) : rg * 16) * 4, sb_at = (RG > 1 ? 64 : 32) * 4 + (lane & 15) * 4;
+    for (int t = 0; t < steps; ++t) {
+      slice_barrier<(NB - 2) * LOADS>();  // step t has landed, and everybody has read step t - 1
+      issue();
+      const char* tile = smem + t % NB * STAGE + kg * TILE;
+      const char* scales = smem + t % NB * STAGE + KG * TILE + kg * RG * 256;
+      v4u8 ra[2], rb[FN][2];
+      ra[0] = read<v4u8>(tile + rg * 2048 + at0);
+      ra[1] = read<v4u8>(tile + rg * 2048 + at1);
+      float xb[FN];
+      v4f s4;
+      if (AROW)
+        s4 = read<v4f>(scales + sa_at);
+      else
+        s4[0] = s4[1] = s4[2] = s4[3] = read<float>(scales + sa_at);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) rb[j][h] &= keep;
+      for (int j = 0; j < FN; ++j) {
+        rb[j][0] = read<v4u8>(tile + (RG + j) * 2048 + at0);
+        rb[j][1] = read<v4u8>(tile + (RG + j) * 2048 + at1);
+        xb[j] = read<float>(scales + sb_at + j * 64);
+      }
+      const int left = g.q - (t * KG + kg) * 128;
+      if (left < 128 && (left & 15) != 0) {  // the rows' last piece ends inside it
+        int have = left - (lane >> 4) * 16;
+        asm volatile("" : "+v"(have));  // (the masks are worked out here, not in every step)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const v4u8 keep = first_bytes(have - h * 64);
+          ra[h] &= keep;
+#pragma unroll
+          for (int j = 0; j < FN; ++j) rb[j][h] &= keep;
+        }
+      }
+      Frag<TA, WIDE> fa;
+      Frag<TB, WIDE> fb[FN];
+      fa.set(ra[0], ra[1]);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[j].set(rb[j][0], rb[j][1]);
+      v4f d[FN];
+      block_products<TA, TB, WIDE, FN>(d, fa, fb);
+      if (left > 0) {  // (scales past the end may be anything)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(d[j][r], s4[r] * xb[j], acc[j][r]);
       }
     }
-    Frag<TA, true> fa[MR];
+    slice_barrier<0>();
+    v4f* sums = reinterpret_cast<v4f*>(smem);
 #pragma unroll
-    for (int i = 0; i < MR; ++i) fa[i].set(ra[i][0], ra[i][1]);
+    for (int j = 0; j < FN; ++j) sums[(wave * FN + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    for (int u = (int)threadIdx.x; u < RG * FN * 64; u += 512) {
+      const int l = u & 63, j = u / 64 % FN, i = u / 64 / FN;
+      v4f v = sums[(i * FN + j) * 64 + l];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      Frag<TB, true> fb;
-      fb.set(rb[j][0], rb[j][1]);
-      v4f d[MR];
+      for (int w = 1; w < KG; ++w) v += sums[((w * RG + i) * FN + j) * 64 + l];
+      const int col = j * 16 + (l & 15), row = m0 + i * 16 + 4 * (l >> 4);
+      if (col >= g.n) continue;
+      const long to = col * g.ldc + row;
 #pragma unroll
-      for (int i = 0; i < MR; ++i) d[i] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < MR; ++i) d[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fa[i].h[t], fb.h[t], d[i], 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < MR; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = __builtin_fmaf(d[i][r], sa[i][AROW ? r : 0] * xb[j], acc[i][j][r]);
+      for (int r = 0; r < 4; ++r) {
+        if (row + r >= g.m) break;
+        if (g.ctype == OZGEMM_F32)
+          ((float*)g.C)[to + r] = v[r];
+        else
+          ((uint16_t*)g.C)[to + r] = round16(v[r], g.ctype);
+      }
     }
   }
 };
 
-template <int TA, int TB, bool AROW, int MR, int FN>
-__global__ __launch_bounds__(FEW8_WAVES * 64) void scaled_few_kernel(Scaled8 g) {
-  __shared__ v4f sums[FEW8_WAVES][MR][FN][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m0 = blockIdx.x * 16 * MR, piece = lane >> 4;
-  const uint8_t* pa[MR];
-  const uint8_t* pb[FN];
-  const float* sb[FN];
-#pragma unroll
-  for (int i = 0; i < MR; ++i) pa[i] = g.A.p + (long)min(m0 + i * 16 + (lane & 15), g.m - 1) * g.A.ld + piece * 16;
-#pragma unroll
-  for (int j = 0; j < FN; ++j) {
-    const int col = min(j * 16 + (lane & 15), g.n - 1);
-    pb[j] = g.B.p + (long)col * g.B.ld + piece * 16;
-    sb[j] = g.B.s + col * g.B.srow;
-  }
-  v4f acc[MR][FN] = {};
-  const int blocks = (g.q + 127) >> 7;
-  if (wave < blocks) {
-    Few8<TA, TB, AROW, MR, FN> now, next;
-    now.load(g, pa, pb, sb, m0, lane, wave);
-    for (int b = wave; b < blocks; b += FEW8_WAVES) {
-      if (b + FEW8_WAVES < blocks) next.load(g, pa, pb, sb, m0, lane, b + FEW8_WAVES);
-      now.multiply(acc, g.q - b * 128);
-      now = next;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MR; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j) sums[wave][i][j][lane] = acc[i][j];
-  __syncthreads();
-  for (int u = threadIdx.x; u < MR * FN * 64; u += FEW8_WAVES * 64) {
-    const int l = u & 63, j = u / 64 % FN, i = u / 64 / FN;
-    v4f v = sums[0][i][j][l];
-#pragma unroll
-    for (int w = 1; w < FEW8_WAVES; ++w) v += sums[w][i][j][l];
-    const int col = j * 16 + (l & 15), row = m0 + i * 16 + 4 * (l >> 4);
-    if (col >= g.n) continue;
-    const long to = col * g.ldc + row;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (row + r >= g.m) break;
-      if (g.ctype == OZGEMM_F32)
-        ((float*)g.C)[to + r] = v[r];
-      else
-        ((uint16_t*)g.C)[to + r] = round16(v[r], g.ctype);
-    }
-  }
+template <class Few>
+__global__ __launch_bounds__(512) void scaled_few_kernel(Scaled8 g) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  Few::run(g, smem);
 }
 
 __global__ __launch_bounds__(256) void align_rows_kernel(const uint8_t* src, long ld, int q, uint8_t* dst, long dld) {
@@ -634,20 +658,17 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const uint8_t* src, lon
   *reinterpret_cast<v4u8*>(dst + blockIdx.x * dld + c) = v;
 }
 
-// 64 rows x 64 blocks by way of LDS, so that either side is read and written in runs.
+// A lane takes four blocks of a row, so that neighbouring lanes write next to each other.
 __global__ __launch_bounds__(256) void turn_scales_kernel(const float* src, long srow, long sblock, int rows, int blocks,
                                                           float* dst) {
-  __shared__ float tile[64][65];
-  const int r0 = blockIdx.x * 64, b0 = blockIdx.y * 64, x = threadIdx.x & 63;
+  const int r = blockIdx.x * 64 + (threadIdx.x & 63), b = (blockIdx.y * 4 + (threadIdx.x >> 6)) * 4;
+  if (r >= rows) return;
+  float v[4];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int y = k * 4 + (threadIdx.x >> 6);
-    if (r0 + y < rows && b0 + x < blocks) tile[y][x] = src[(r0 + y) * srow + (b0 + x) * sblock];
-  }
-  __syncthreads();
-#pragma unroll 4
-  for (int y = threadIdx.x >> 6; y < 64; y += 4)
-    if (b0 + y < blocks && r0 + x < rows) dst[(long)(b0 + y) * rows + r0 + x] = tile[x][y];
+  for (int k = 0; k < 4; ++k) v[k] = src[r * srow + min(b + k, blocks - 1) * sblock];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (b + k < blocks) dst[(long)(b + k) * rows + r] = v[k];
 }
 
 constexpr int FEW8_COLS = 64;
@@ -657,39 +678,66 @@ hipError_t join(const Scaled8& g, int parts, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Lets a kernel have that much LDS, once for every device (a bit each).
+hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& known) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (known.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) known.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <int TA, int TB, bool WIDE, bool AROW, int BM, int BN, int WM>
 hipError_t launch_tiles(const Scaled8& g, hipStream_t st) {
   using Tile = Tile8<TA, TB, WIDE, AROW, BM, BN, WM, 8 / WM>;
   const long tiles = (long)((g.m + BM - 1) / BM) * ((g.n + BN - 1) / BN) * g.parts;
   const long room = 256 * (160 * 1024 / Tile::SMEM);  // blocks that the card holds
   auto kernel = scaled_tiles_kernel<Tile>;
-  const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, Tile::SMEM);
+  static std::atomic<uint64_t> known{0};
+  const hipError_t e = allow_lds((const void*)kernel, Tile::SMEM, known);
   if (e != hipSuccess) return e;
   kernel<<<(unsigned)std::min(tiles, room), Tile::THREADS, Tile::SMEM, st>>>(g, (int)tiles);
   return hipGetLastError();
 }
 
-template <int TA, int TB, bool AROW, int MR, int FN>
-hipError_t few_kernel(const Scaled8& g, hipStream_t st) {
-  scaled_few_kernel<TA, TB, AROW, MR, FN><<<(g.m + 16 * MR - 1) / (16 * MR), FEW8_WAVES * 64, 0, st>>>(g);
+template <class Few>
+hipError_t few_kernel(const Scaled8& g, int rows, hipStream_t st) {
+  auto kernel = scaled_few_kernel<Few>;
+  static std::atomic<uint64_t> known{0};
+  const hipError_t e = allow_lds((const void*)kernel, Few::SMEM, known);
+  if (e != hipSuccess) return e;
+  kernel<<<(g.m + rows - 1) / rows, 512, Few::SMEM, st>>>(g);
   return hipGetLastError();
 }
 
-// 32 rows a block where that leaves a block for every compute unit.
+// 32 rows a block where that leaves a block for every compute unit, or where
+// LDS has no room for the columns of eight blocks.
+template <int TA, int TB, bool WIDE, bool AROW>
+hipError_t few_columns(const Scaled8& g, hipStream_t st) {
+  const bool two = g.m >= 32 * 256;
+  if (g.n <= 32)
+    return two ? few_kernel<Few8<TA, TB, WIDE, AROW, 2, 2>>(g, 32, st)
+               : few_kernel<Few8<TA, TB, WIDE, AROW, 1, 2>>(g, 16, st);
+  return few_kernel<Few8<TA, TB, WIDE, AROW, 2, 4>>(g, 32, st);
+}
+
 template <int TA, int TB, bool AROW>
 hipError_t launch_few(const Scaled8& g, hipStream_t st) {
-  if (g.n <= 16) return few_kernel<TA, TB, AROW, 1, 1>(g, st);
-  const bool two = g.m >= 32 * 256;
-  if (g.n <= 32) return two ? few_kernel<TA, TB, AROW, 2, 2>(g, st) : few_kernel<TA, TB, AROW, 1, 2>(g, st);
-  return two ? few_kernel<TA, TB, AROW, 2, 4>(g, st) : few_kernel<TA, TB, AROW, 1, 4>(g, st);
+  if (g.n <= 16)
+    return g.m >= 32 * 256 ? few_kernel<Few8<TA, TB, true, AROW, 2, 1>>(g, 32, st)
+                           : few_kernel<Few8<TA, TB, true, AROW, 1, 1>>(g, 16, st);
+  return g.ctype == OZGEMM_F32 ? few_columns<TA, TB, true, AROW>(g, st) : few_columns<TA, TB, false, AROW>(g, st);
 }
 
 bool big_tiles(int m, int n) { return n > FEW8_COLS && (long)((m + 255) / 256) * ((n + 255) / 256) >= 128; }
 
 template <int TA, int TB, bool AROW>
 hipError_t launch_kind(const Scaled8& g, hipStream_t st) {
-  if (g.n <= FEW8_COLS) return launch_few<TA, TB, AROW>(g, st);
   if (g.q == 0) return join(g, 0, st);
+  if (g.n <= FEW8_COLS) return launch_few<TA, TB, AROW>(g, st);
   const bool wide = g.ctype == OZGEMM_F32;
   hipError_t e;
   if (big_tiles(g.m, g.n))
@@ -719,7 +767,7 @@ bool scaled_big(int m, int n) { return big_tiles(m, n); }
 
 hipError_t launch_turn_scales(const float* src, long srow, long sblock, int rows, int q, float* dst, hipStream_t st) {
   const int blocks = (q + 127) / 128;
-  turn_scales_kernel<<<dim3((rows + 63) / 64, (blocks + 63) / 64), 256, 0, st>>>(src, srow, sblock, rows, blocks, dst);
+  turn_scales_kernel<<<dim3((rows + 63) / 64, (blocks + 15) / 16), 256, 0, st>>>(src, srow, sblock, rows, blocks, dst);
   return hipGetLastError();
 }
 

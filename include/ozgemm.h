@@ -594,11 +594,11 @@ int ozgemm_quantize_blocks(int type, int qtype, int rows, int n, int q, const vo
  * makes them): dX from dY and W turned over, dW from dY and X turned over.
  *
  * Sums.  OZGEMM_F32 results: products are exact and everything is summed in
- * FP32.  BF16 and F16 results of more than 64 columns: the 128 products of a
+ * FP32.  BF16 and F16 results of more than 16 columns: the 128 products of a
  * block are summed by the 8-bit matrix cores, which keep of each term what lies
  * above 2^-13 of the largest of the terms next to it (an error of 1.5e-5 of the
  * sums' norm for gaussian entries; F16 rounds to 2e-4, BF16 to 1.7e-3); blocks
- * are scaled and added in FP32.  64 columns and fewer: as F32.  Results are
+ * are scaled and added in FP32.  16 columns and fewer: as F32.  Results are
  * rounded once, to nearest-even, and do not depend on the order of blocks.
  * NaN anywhere in a row makes the outputs it touches NaN.
  *

@@ -5,7 +5,7 @@ Tolerances.  Blocks are exact: a power of two and one rounding.  A product's
 entry is a sum of q products in blocks of 128: 128 + 4 additions in a block,
 two roundings of its scaling and one addition per block, none off by more than
 2^-23 of the sum of the magnitudes so far (matrix cores may cut instead of
-round).  The 8-bit matrix cores drop what lies under 2^-13 of the largest of the
+round).  The 8-bit matrix cores (results of 16 bits and more than 16 columns) drop what lies under 2^-13 of the largest of the
 products that they add at once, so at most that per product.  A result of 16 bits
 is then off by half a step."""
 import pytest
@@ -151,7 +151,7 @@ def test_products_of_any_scales(n, q, m, t, rows):
     w, ws = oz.quantize_blocks(normal(g, m, q), rows=rows)
     xs, ws = (s * (1 + torch.rand(s.shape, generator=g, device="cuda")) for s in (xs, ws))
     got = oz.scaled_linear(x, xs, w, ws, out_dtype=TYPES[t])
-    check_product(got, x, xs, w, ws, rows, t == "f32" or n <= 64)
+    check_product(got, x, xs, w, ws, rows, t == "f32" or n <= 16)
     # the same from rows off the 16-byte grid, bit for bit
     for a, b in ((x.clone().contiguous()[:, :], w), (x, odd_rows(w)), (odd_rows(x), odd_rows(w))):
         assert torch.equal(oz.scaled_linear(a, xs, b, ws, out_dtype=TYPES[t]), got)
@@ -230,7 +230,7 @@ def test_gradients(n, q, m, t):
         dX, dW = oz.scaled_linear_grads(dY, Xt, xts, Wt, wts, dw_dtype=torch.float32, dtype=dtype)
         assert dX.dtype == dY.dtype and dX.shape == (n, q) and dW.shape == (m, q)
         v, s = blocks(dY, 1, dtype)
-        check_product(dX, v, s, Wt, wts, 128, t == "f32" or n <= 64)
+        check_product(dX, v, s, Wt, wts, 128, t == "f32" or n <= 16)
         v, s = blocks(dY.t(), 1, dtype)
         check_product(dW, v, s, Xt, xts, 1, True)
 
