@@ -167,11 +167,33 @@ __device__ __forceinline__ void store_bytes(uint8_t* p, v2u v, int left) {
   }
 }
 
+// The value of the lane N on, around the row of 16 lanes.
+template <int N>
+__device__ __forceinline__ uint32_t rotated(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xf, 0xf, false);
+}
+template <int N>
+__device__ __forceinline__ double rotated(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)rotated<N>((uint32_t)u) | (uint64_t)rotated<N>((uint32_t)(u >> 32)) << 32);
+}
+
 // The largest of 16 neighbouring lanes, in all of them.
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d, 64));
-  return v;
+  v = max(v, rotated<8>(v));
+  v = max(v, rotated<4>(v));
+  v = max(v, rotated<2>(v));
+  return max(v, rotated<1>(v));
+}
+
+// The sum of a wavefront, the same bits in all of its lanes.
+__device__ __forceinline__ double sum64(double v) {
+  v += rotated<8>(v);
+  v += rotated<4>(v);
+  v += rotated<2>(v);
+  v += rotated<1>(v);
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
 }
 
 }  // namespace oz

@@ -76,8 +76,7 @@ __device__ __forceinline__ double square_sum64(const double* p, long size, int c
 template <int THREADS>
 __device__ __forceinline__ double block_sum(double s) {
   __shared__ double meet[THREADS / 64];
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+  s = sum64(s);
   if ((threadIdx.x & 63) == 0) meet[threadIdx.x >> 6] = s;
   __syncthreads();
   s = meet[0];

@@ -36,7 +36,7 @@ struct Scaled8 {
 constexpr long LD8_MAX = 1L << 22;
 
 // Parts of the inner dimension a product of these sizes is summed in.
-int scaled_parts(int ctype, int m, int n, int q);
+int scaled_parts(int m, int n, int q);
 // Whether the launches have at most 2^32 - 1 threads each.
 bool scaled_fits(int m, int n, int parts);
 hipError_t launch_scaled(const Scaled8& g, hipStream_t st);

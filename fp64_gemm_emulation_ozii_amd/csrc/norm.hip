@@ -28,8 +28,7 @@ struct Norm {
 
 template <int G>
 __device__ __forceinline__ double row_sum(double v, double* meet) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  v = sum64(v);
   if (G > 64) {
     __syncthreads();  // (the row before has been read)
     if ((threadIdx.x & 63) == 0) meet[threadIdx.x >> 6] = v;

@@ -41,7 +41,7 @@ bool turns(const Scales& s, int m, int n, int q) {
   return s.per == 1 && s.srow != 1 && s.rows > 1 && q > BLOCK8 && scaled_big(m, n);
 }
 
-Rooms rooms(int ctype, int m, int n, int q, const void* A, int lda, const Scales& sa, const void* B, int ldb,
+Rooms rooms(int m, int n, int q, const void* A, int lda, const Scales& sa, const void* B, int ldb,
             const Scales& sb) {
   Rooms r{};
   r.parts = 1;
@@ -61,7 +61,7 @@ Rooms rooms(int ctype, int m, int n, int q, const void* A, int lda, const Scales
   r.b_at = take(r.b, (size_t)n * r.ld);
   r.sa_at = take(r.sa, blocks * m * sizeof(float));
   r.sb_at = take(r.sb, blocks * n * sizeof(float));
-  r.parts = scaled_parts(ctype, m, n, q);
+  r.parts = scaled_parts(m, n, q);
   r.partial = take(r.parts > 1, (size_t)r.parts * m * n * sizeof(float));
   return r;
 }
@@ -79,11 +79,11 @@ using namespace oz;
 
 extern "C" {
 
-size_t ozgemm_scaled_gemm_workspace_bytes(int ctype, int m, int n, int q, const void* A, int lda, int rows_a,
+size_t ozgemm_scaled_gemm_workspace_bytes(int m, int n, int q, const void* A, int lda, int rows_a,
                                           long long sarow, long long sablock, const void* B, int ldb, long long sbrow,
                                           long long sbblock) {
   if (m < 0 || n < 0 || q < 0 || m > OZGEMM_MAX_ROWS || n > OZGEMM_MAX_ROWS || q > OZGEMM_MAX_ROWS) return 0;
-  return rooms(ctype, m, n, q, A, lda, Scales{m, rows_a, sarow, sablock}, B, ldb, Scales{n, 1, sbrow, sbblock}).total;
+  return rooms(m, n, q, A, lda, Scales{m, rows_a, sarow, sablock}, B, ldb, Scales{n, 1, sbrow, sbblock}).total;
 }
 
 int ozgemm_scaled_gemm(int atype, int btype, int ctype, int m, int n, int q, const void* A, int lda, const float* SA,
@@ -118,7 +118,7 @@ int ozgemm_scaled_gemm(int atype, int btype, int ctype, int m, int n, int q, con
       overlap(C, cb, SB, scale_extent(n, 1, q, sbrow, sbblock)))
     return -18;
   const Rooms r =
-      rooms(ctype, m, n, q, A, lda, Scales{m, rows_a, sarow, sablock}, B, ldb, Scales{n, 1, sbrow, sbblock});
+      rooms(m, n, q, A, lda, Scales{m, rows_a, sarow, sablock}, B, ldb, Scales{n, 1, sbrow, sbblock});
   if (r.total > 0 && (workspace == nullptr || ((uintptr_t)workspace & (WS_ALIGN - 1)))) return -20;
   if (workspace_bytes < r.total) return OZGEMM_WORKSPACE_TOO_SMALL;
   if (!scaled_fits(m, n, r.parts)) return OZGEMM_RANGE;

@@ -135,7 +135,7 @@ def lib():
         "ozgemm_quantize_blocks": (c_int, [c_int] * 5 + [vp, c_int] + [vp, c_int, vp, ll, ll] * 2 + [vp]),
         "ozgemm_scaled_gemm": (c_int, [c_int] * 6 + [vp, c_int, vp, c_int, ll, ll, vp, c_int, vp, ll, ll, vp, c_int, vp,
                                        c_size, vp]),
-        "ozgemm_scaled_gemm_workspace_bytes": (c_size, [c_int] * 4 + [vp, c_int, c_int, ll, ll, vp, c_int, ll, ll]),
+        "ozgemm_scaled_gemm_workspace_bytes": (c_size, [c_int] * 3 + [vp, c_int, c_int, ll, ll, vp, c_int, ll, ll]),
         "ozgemm_rms_norm": (c_int, [c_int] * 5 + [vp, c_int, vp, c_int, vp, f64, vp, c_int, vp, c_int, vp, ll, ll, vp]),
         "ozgemm_rms_norm_grads": (c_int, [c_int] * 4 + [vp, c_int, vp, c_int, vp, vp, c_int, f64, vp, c_int, vp, vp,
                                           c_size, vp]),
@@ -511,8 +511,8 @@ def ozgemm_quantize_blocks(type, qtype, rows, n, q, X, ldx, V, ldv, S, srow, sbl
 _SCALED_NO_WORKSPACE = -20
 
 
-def ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, A, lda, rows_a, sarow, sablock, B, ldb, sbrow, sbblock) -> int:
-    return int(lib().ozgemm_scaled_gemm_workspace_bytes(ctype, m, n, q, _ptr(A), lda, rows_a, sarow, sablock, _ptr(B),
+def ozgemm_scaled_gemm_workspace_bytes(m, n, q, A, lda, rows_a, sarow, sablock, B, ldb, sbrow, sbblock) -> int:
+    return int(lib().ozgemm_scaled_gemm_workspace_bytes(m, n, q, _ptr(A), lda, rows_a, sarow, sablock, _ptr(B),
                                                         ldb, sbrow, sbblock))
 
 
@@ -527,7 +527,7 @@ def ozgemm_scaled_gemm(atype, btype, ctype, m, n, q, A, lda, SA, rows_a, sarow, 
         st = L.ozgemm_scaled_gemm(*ops, None, 0, hs)
     if st == _SCALED_NO_WORKSPACE:
         need = 0 if workspace is not None else ozgemm_scaled_gemm_workspace_bytes(
-            ctype, m, n, q, A, lda, rows_a, sarow, sablock, B, ldb, sbrow, sbblock)
+            m, n, q, A, lda, rows_a, sarow, sablock, B, ldb, sbrow, sbblock)
         keep, ws, nbytes = _room(workspace, need, getattr(B, "device", "cuda"), hs)
         st = L.ozgemm_scaled_gemm(*ops, ws, nbytes, hs)
     return _check(st, "ozgemm_scaled_gemm") if check else st

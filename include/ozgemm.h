@@ -618,7 +618,7 @@ int ozgemm_scaled_gemm(int atype, int btype, int ctype, int m, int n, int q,
 
 /* Bytes of workspace the call above needs (the pointers are looked at for their
  * alignment alone); 0 where it needs none or the arguments are invalid.  Host only. */
-size_t ozgemm_scaled_gemm_workspace_bytes(int ctype, int m, int n, int q,
+size_t ozgemm_scaled_gemm_workspace_bytes(int m, int n, int q,
                                           const void *A, int lda, int rows_a, long long sarow, long long sablock,
                                           const void *B, int ldb, long long sbrow, long long sbblock);
 
