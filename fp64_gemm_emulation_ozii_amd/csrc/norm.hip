@@ -3,6 +3,8 @@
 //
 //   H = X + R (each entry rounded to their type),  r = 1 / sqrt(sum H^2 / q + eps),  Y = H r w
 //   g = dY w,  dX = r g - H r^3 (sum g H) / q + dH,  dw = sum over the rows of dY H r
+// The middle term is formed as (H r) (r^2 sum g H / q): with a third r in its second factor that would leave
+// float32's range for rows below 1e-19 (where eps is 0).
 //
 // G threads hold a row of up to 8192 entries in registers, eight entries P times
 // each, so it is read once.  Sums over a row and Y itself are FP64: that costs nothing next to the
@@ -186,7 +188,7 @@ struct NormGrads {
   const void *dy, *h, *w, *dh;
   void* dx;
   float* partial;  // [groups][q]; nullptr: no dw
-  float* rows;     // long rows: [n][2], r and r^3 (sum g H) / q
+  float* rows;     // long rows: [n][2], r and r^2 (sum g H) / q
   long lddy, ldh, lddh, lddx;
   int n, q, wf32;
   double eps;
@@ -234,7 +236,7 @@ __global__ __launch_bounds__(256) void norm_grads_kernel(NormGrads g) {
     s1 = row_sum<G>(s1, meet);
     s2 = row_sum<G>(s2, meet2);
     const double r = 1.0 / sqrt(s1 / (double)g.q + g.eps);
-    const float a = (float)r, b = (float)(r * r * r * (s2 / (double)g.q));
+    const float a = (float)r, b = (float)(r * r * (s2 / (double)g.q));
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = (p * G + t) * 8;
@@ -242,10 +244,10 @@ __global__ __launch_bounds__(256) void norm_grads_kernel(NormGrads g) {
       float v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float hk = h[p].get(k), dk = dy[p].get(k);
+        const float hk = a * h[p].get(k), dk = dy[p].get(k);
         v[k] = a * (dk * w[p][k]) - b * hk;
         if (g.dh != nullptr) v[k] += dh[p].get(k);
-        dw[p][k] = __builtin_fmaf(dk, a * hk, dw[p][k]);
+        dw[p][k] = __builtin_fmaf(dk, hk, dw[p][k]);
       }
       Raw8<TYPE> o;
       o.set(v);
@@ -302,7 +304,7 @@ __global__ __launch_bounds__(LONG) void norm_grads_rows_kernel(NormGrads g) {
   const double r = 1.0 / sqrt(s1 / (double)g.q + g.eps);
   if (threadIdx.x == 0) {
     g.rows[2 * row] = (float)r;
-    g.rows[2 * row + 1] = (float)(r * r * r * (s2 / (double)g.q));
+    g.rows[2 * row + 1] = (float)(r * r * (s2 / (double)g.q));
   }
 }
 
@@ -322,10 +324,10 @@ __global__ __launch_bounds__(256) void norm_grads_columns_kernel(NormGrads g) {
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float hk = h.get(k), dk = dy.get(k);
+      const float hk = a * h.get(k), dk = dy.get(k);
       v[k] = a * (dk * w[k]) - b * hk;
       if (g.dh != nullptr) v[k] += dh.get(k);
-      dw[k] = __builtin_fmaf(dk, a * hk, dw[k]);
+      dw[k] = __builtin_fmaf(dk, hk, dw[k]);
     }
     Raw8<TYPE> o;
     o.set(v);

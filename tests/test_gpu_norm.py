@@ -159,6 +159,21 @@ def test_rows_without_a_norm(q):
     assert dX[1].isfinite().all() and dX[2].isnan().any() and dX[3].isnan().all() and dw.isnan().any()
 
 
+@pytest.mark.parametrize("q", [300, 9000])
+@pytest.mark.parametrize("size", [1e-30, 1e-19, 1e15])
+def test_gradients_of_small_and_large_rows(q, size):
+    g = torch.Generator(device="cuda").manual_seed(q)
+    H, dY = (torch.randn(5, q, generator=g, device="cuda") * f for f in (size, 1e-3))
+    w = torch.ones(q, device="cuda")
+    dX, dw = oz.rms_norm_grads(dY, H, w, eps=0.0)
+    h, d = H.double(), dY.double()
+    r = 1 / h.square().mean(1, keepdim=True).sqrt()
+    a, b = r * d, h * r ** 3 * (d * h).mean(1, keepdim=True)
+    assert ((dX.double() - (a - b)).abs() <= 6.06 * 2.0 ** -24 * (a.abs() + b.abs()) + half_step(a - b, H.dtype)).all()
+    terms = d * h * r
+    assert ((dw.double() - terms.sum(0)).abs() <= 7.07 * 2.0 ** -24 * terms.abs().sum(0) + half_step(terms.sum(0), H.dtype)).all()
+
+
 def test_no_rows():
     for q in (40, 9000):
         w = torch.ones(q, device="cuda")
