@@ -486,6 +486,7 @@ int ozgemm_rms_norm(int type, int ytype, int wtype, int n, int q, const void* X,
   if (eight && sblock < 0) return -18;
   if (n > OZGEMM_MAX_ROWS || q > OZGEMM_MAX_ROWS) return OZGEMM_RANGE;
   if (!any) return OZGEMM_OK;
+  if (eight && !places_differ(n, (q - 1) / BLOCK8 + 1, srow, sblock)) return -17;
   const size_t size = elem_bytes(type);
   const size_t xb = extent(q, n, ldx, 0, 1, size), rb = R ? extent(q, n, ldr, 0, 1, size) : 0;
   const size_t wb = (size_t)q * elem_bytes(wtype), hb = R ? extent(q, n, ldh, 0, 1, size) : 0;

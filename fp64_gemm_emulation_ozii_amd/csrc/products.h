@@ -28,6 +28,13 @@ inline bool overlap(const void* a, size_t abytes, const void* b, size_t bbytes) 
   return abytes && bbytes && pa < pb + bbytes && pb < pa + abytes;
 }
 
+// Whether the entries (row, block) of an array that is written, at row srow + block sblock, are all different ones.
+inline bool places_differ(long rows, long blocks, long long srow, long long sblock) {
+  if (rows > 1 && blocks > 1)
+    return (srow > 0 && sblock > (rows - 1) * srow) || (sblock > 0 && srow > (blocks - 1) * sblock);
+  return (rows <= 1 || srow > 0) && (blocks <= 1 || sblock > 0);
+}
+
 // An operand of a 16-bit product as the kernels read it.
 struct Operand16 {
   const uint16_t* p;

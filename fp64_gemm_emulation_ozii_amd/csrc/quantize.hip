@@ -188,6 +188,8 @@ extern "C" int ozgemm_quantize_blocks(int type, int qtype, int rows, int n, int 
   const size_t rb = (n - 1) / rows, qb = (q - 1) / BLOCK8;  // last row and block of the scales
   const size_t sb = V ? (rb * srow + qb * sblock + 1) * sizeof(float) : 0;
   const size_t stb = Vt ? ((q - 1) / rows * (size_t)strow + (n - 1) / BLOCK8 * (size_t)stblock + 1) * sizeof(float) : 0;
+  if (V && !places_differ((n - 1) / rows + 1, (q - 1) / BLOCK8 + 1, srow, sblock)) return -11;
+  if (Vt && !places_differ((q - 1) / rows + 1, (n - 1) / BLOCK8 + 1, strow, stblock)) return -16;
   if (overlap(V, vb, X, xb)) return -8;
   if (overlap(S, sb, X, xb) || overlap(S, sb, V, vb)) return -10;
   if (overlap(Vt, vtb, X, xb) || overlap(Vt, vtb, V, vb) || overlap(Vt, vtb, S, sb)) return -13;

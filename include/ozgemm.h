@@ -570,7 +570,10 @@ size_t ozgemm_orthogonalize_workspace_bytes(int type, int batch, int m, int n, i
  * The scales that these calls make are powers of two: the least 2^e >= 2^-126
  * with |x| <= MAX 2^e for all finite x of the block (MAX = 448 for E4M3, 57344 for
  * E5M2), 1 for a block of zeros; every value is x 2^-e rounded once, to
- * nearest-even.  Inf and NaN become NaN.  The products take any scales. */
+ * nearest-even.  Inf and NaN become NaN.  The products take any scales, whose
+ * product, of a row's and a column's block, is taken in FP32.
+ *
+ * Every array begins at a multiple of its entries' size. */
 
 /* V, S = the n x q matrix X in blocks, and Vt, St = its transpose in blocks (of
  * `rows` x 128 of the transpose), either or both (V or Vt NULL: not that one).
@@ -578,8 +581,9 @@ size_t ozgemm_orthogonalize_workspace_bytes(int type, int batch, int m, int n, i
  *   rows   1 or 128
  *   X      n rows of q entries, ldx >= max(1, q) apart
  *   V      n rows of q bytes, ldv >= max(1, q) apart; Vt q rows of n, ldvt >= max(1, n)
- * No array that is written may overlap another.  Errors: -i for argument i; OZGEMM_RANGE for n or q
- * above OZGEMM_MAX_ROWS or 2^24 and more tiles of 128 x 128. */
+ * No array that is written may overlap another, and no two scales may have one place.
+ * Errors: -i for argument i; OZGEMM_RANGE for n or q above OZGEMM_MAX_ROWS or
+ * 2^24 and more tiles of 128 x 128. */
 int ozgemm_quantize_blocks(int type, int qtype, int rows, int n, int q, const void *X, int ldx,
                            void *V, int ldv, float *S, long long srow, long long sblock,
                            void *Vt, int ldvt, float *St, long long strow, long long stblock,
@@ -625,7 +629,7 @@ size_t ozgemm_scaled_gemm_workspace_bytes(int m, int n, int q,
 /* Y = H w / sqrt(mean over the row of H^2 + eps) for n rows of q entries, H = X + R.
  *   type   OZGEMM_F32, BF16 or F16: X's, R's and H's; wtype: w's, `type` or OZGEMM_F32
  *   ytype  `type` itself, or OZGEMM_E4M3 or E5M2: then Y is values in blocks (rows = 1)
- *          with scales S (not looked at otherwise)
+ *          with scales S, no two of them in one place (not looked at otherwise)
  *   R      the residual; NULL: H = X.  H receives the sum, each entry added in FP32
  *          and rounded to its type, which is what the norm is taken of; not looked
  *          at without R

@@ -166,6 +166,8 @@ def test_quantize_arguments():
         (1, L.OZGEMM_F64), (1, 9), (2, L.OZGEMM_F16), (3, 0), (3, 64), (4, -1), (5, -1), (6, None), (7, 199), (9, 199),
         (10, None), (11, -1), (12, -1), (14, 299), (15, None), (16, -1), (17, -1), (4, big + 1, -14),
         (8, at(0) + 64), (10, at(0) + 64), (13, at(1) + 64), (13, at(2) + 64), (15, at(3) + 64), (10, at(1) + 64)])
+    # scales of different blocks in one place
+    call("ozgemm_quantize_blocks", good, [(11, 0), (11, 300), (12, 0, -11), (12, 299, -11), (16, 0), (16, 2), (17, 0, -16)])
     f = L.lib().ozgemm_quantize_blocks
     assert f(*(good[:7] + [None, 0, None, 0, 0, None, 0, None, 0, 0, None])) == -8  # neither result
     # 2^24 tiles and more
@@ -221,6 +223,7 @@ def test_norm_arguments():
         (11, -1.0), (11, float("nan")), (12, None), (13, 199), (14, None), (15, 199), (16, None), (17, -1), (18, -1),
         (4, big + 1, L.OZGEMM_RANGE), (12, at(0) + 8), (12, at(1) + 8), (12, at(2)), (14, at(0)), (14, at(3)), (16, at(4)),
         (16, at(0)), (12, at(0) + 2)])
+    call("ozgemm_rms_norm", good, [(17, 0), (17, 30), (18, 29, -17), (18, 0, -17)])  # scales in one place
     assert L.lib().ozgemm_rms_norm(*good[:3], 0, *good[4:]) == 0
     good = [L.OZGEMM_F16, L.OZGEMM_F16, 30, 200, at(0), 200, at(1), 200, at(2), at(3), 200, 1e-6, at(4), 200, at(5), at(6),
             1 << 40, None]
