@@ -17,7 +17,7 @@ from __future__ import annotations
 import torch
 
 from . import ozgemm as L
-from .layers import _LD_MAX, _TYPES, _fits, _ld, _no_grad, _on_device, _overlap, _rows, _same, _target, _type_of, _written
+from .layers import _LD_MAX, _TYPES, _fits, _ld, _no_grad, _on_device, _overlap, _rows, _target, _type_of, _written
 
 BLOCK = 128
 _EIGHT = {torch.float8_e4m3fn: L.OZGEMM_E4M3, torch.float8_e5m2: L.OZGEMM_E5M2}
@@ -50,23 +50,27 @@ def quantize_blocks(X, rows: int = 1, both: bool = False, dtype=torch.float8_e4m
     scale is the least power of two that keeps its finite entries within the
     type's range, and an entry is rounded once; Inf and NaN become NaN.
     """
-    t = _type_of(X, "quantize_blocks")
-    e = _eight(dtype, "quantize_blocks")
+    _type_of(X, "quantize_blocks")
+    _eight(dtype, "quantize_blocks")
     if rows not in (1, BLOCK):
         raise ValueError(f"blocks have 1 or {BLOCK} rows, not {rows}")
     if X.dim() != 2:
         raise ValueError(f"X must have two dimensions, got {tuple(X.shape)}")
     _no_grad("quantize_blocks", X)
-    n, q = X.shape
-    _fits(n, q)
+    _fits(*X.shape)
     with _on_device(X.device):
-        V, S = _new_blocks(n, q, rows, dtype, X)
-        Vt, St = _new_blocks(q, n, rows, dtype, X) if both else (None, None)
-        plain, turned = (V, S), (Vt, St)
-        if n > 1 and q > 1 and X.stride(0) == 1 and X.stride(1) >= n:  # the transpose lies row by row
-            X, (n, q), plain, turned = X.t(), (q, n), turned, plain
-        X, ldx = _rows(X, "X")
-        L.ozgemm_quantize_blocks(t, e, rows, n, q, X, ldx, *_block_args(*plain), *_block_args(*turned))
+        return _quantize(X, rows, both, dtype)
+
+
+def _quantize(X, rows: int, both: bool, dtype):
+    n, q = X.shape
+    V, S = _new_blocks(n, q, rows, dtype, X)
+    Vt, St = _new_blocks(q, n, rows, dtype, X) if both else (None, None)
+    plain, turned, t = (V, S), (Vt, St), _TYPES[X.dtype]
+    if n > 1 and q > 1 and X.stride(0) == 1 and X.stride(1) >= n:  # the transpose lies row by row
+        X, (n, q), plain, turned = X.t(), (q, n), turned, plain
+    X, ldx = _rows(X, "X")
+    L.ozgemm_quantize_blocks(t, _EIGHT[dtype], rows, n, q, X, ldx, *_block_args(*plain), *_block_args(*turned))
     return (V, S, Vt, St) if both else (V, S)
 
 
@@ -116,9 +120,8 @@ def scaled_linear(X, xs, W, ws, out=None, out_dtype=None):
     are summed by the 8-bit matrix cores, which is off by 1.5e-5 of the sums' norm,
     and blocks in float32.  ``out`` must not overlap the operands.
     """
-    tx, tw = _EIGHT.get(X.dtype), _EIGHT.get(W.dtype)
-    if tx is None or tw is None:
-        _eight(X.dtype, "scaled_linear"), _eight(W.dtype, "scaled_linear")
+    _eight(X.dtype, "scaled_linear")
+    _eight(W.dtype, "scaled_linear")
     _no_grad("scaled_linear", X, xs, W, ws, out, instead=" and take the gradients from scaled_linear_grads")
     if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
         raise ValueError(f"X {tuple(X.shape)} and W {tuple(W.shape)} do not go together")
@@ -137,13 +140,18 @@ def scaled_linear(X, xs, W, ws, out=None, out_dtype=None):
         Y = _target(out, (n, m), _OUT, X, "out")
         ldy = _ld(Y)
     with _on_device(X.device):
-        X, ldx = _values(X, "X")
-        W, ldw = _values(W, "W")
         if out is not None:
             _written(out)
-        L.ozgemm_scaled_gemm(tw, tx, _TYPES[Y.dtype], m, n, q, W, ldw, ws, wrows, *ws.stride(), X, ldx, xs, *xs.stride(),
-                             Y, ldy)
+        _product(X, xs, W, ws, wrows, Y, ldy)
     return Y
+
+
+def _product(X, xs, W, ws, wrows: int, Y, ldy: int) -> None:
+    (n, q), m = X.shape, W.shape[0]
+    tx, tw = _EIGHT[X.dtype], _EIGHT[W.dtype]
+    X, ldx = _values(X, "X")
+    W, ldw = _values(W, "W")
+    L.ozgemm_scaled_gemm(tw, tx, _TYPES[Y.dtype], m, n, q, W, ldw, ws, wrows, *ws.stride(), X, ldx, xs, *xs.stride(), Y, ldy)
 
 
 def scaled_linear_grads(dY, Xt, xts, Wt, wts, dX=None, dW=None, dx_dtype=None, dw_dtype=None, dtype=torch.float8_e4m3fn):
@@ -169,22 +177,24 @@ def scaled_linear_grads(dY, Xt, xts, Wt, wts, dX=None, dW=None, dx_dtype=None, d
         raise ValueError(f"dY, Xt and Wt are on {dY.device}, {Xt.device} and {Wt.device}")
     (n, m), q = dY.shape, Xt.shape[0]
     _fits(n, m, q)
-    _scales(xts, q, n, "xts", Xt, True)
-    _scales(wts, q, m, "wts", Wt, True)
+    xts, xrows = _scales(xts, q, n, "xts", Xt, True)
+    wts, wrows = _scales(wts, q, m, "wts", Wt, True)
     given = dX, dW
-    for t, want in ((given[0], dx_dtype), (given[1], dw_dtype)):
+    for t, want in ((dX, dx_dtype), (dW, dw_dtype)):
         if t is None and (want or dY.dtype) not in _OUT:
             raise TypeError(f"scaled_linear_grads: results are bfloat16, float16 or float32, not {want}")
     dX = _target(dX, (n, q), _OUT if dX is not None else (dx_dtype or dY.dtype,), dY, "dX")
     dW = _target(dW, (m, q), _OUT if dW is not None else (dw_dtype or dY.dtype,), dY, "dW")
-    # dX is written before Xt is read for dW
-    if _overlap(dX, dW) or any(_overlap(d, t) for d in (dX, dW) for t in (Xt, xts, Wt, wts)):
+    # dX is written before Xt is read for dW (new tensors overlap nothing)
+    held = (Xt, xts, Wt, wts) if given[1] is None else (Xt, xts, Wt, wts, dW)
+    if (given[0] is not None and any(_overlap(dX, t) for t in held)) or (
+            given[1] is not None and any(_overlap(dW, t) for t in held[:4])):
         raise ValueError("dX and dW must not overlap the operands or each other")
-    V, S, Vt, St = quantize_blocks(dY.detach(), both=True, dtype=dtype)
-    Xt, xts, Wt, wts = Xt.detach(), xts.detach(), Wt.detach(), wts.detach()
-    with torch.no_grad():
-        scaled_linear(V, S, Wt, wts, out=dX)
-        scaled_linear(Vt, St, Xt, xts, out=dW)
+    with _on_device(dY.device):
+        V, S, Vt, St = _quantize(dY, 1, True, dtype)
+        _written(*given)
+        _product(V, S, Wt, wts, wrows, dX, _ld(dX))
+        _product(Vt, St, Xt, xts, xrows, dW, _ld(dW))
     return dX, dW
 
 
