@@ -42,7 +42,7 @@ bool scaled_fits(int m, int n, int parts);
 hipError_t launch_scaled(const Scaled8& g, hipStream_t st);
 
 // Whether a product of these sizes goes by the largest tiles.
-bool scaled_big(int m, int n);
+bool scaled_big(int m, int n, int q);
 
 // the scales (row, block) of rows of q entries to block rows + row
 hipError_t launch_turn_scales(const float* src, long srow, long sblock, int rows, int q, float* dst, hipStream_t st);

@@ -494,18 +494,19 @@ __global__ __launch_bounds__(256) void join_parts_kernel(Scaled8 g, int parts) {
 }
 
 // ---------------------------------------------------------------------------
-// Few columns
+// Few columns, and few results of any shape
 // ---------------------------------------------------------------------------
 
-// Bound by reading A once.  A block takes 16 RG rows of it and all (up to 16 FN)
-// columns; its eight wavefronts are RG of rows by KG of the inner dimension, of which
+// Few columns are bound by reading A once, few results by the time from one slice to the
+// next: a tile above takes 0.7 us for each, however small it is.  A block takes 16 RG rows
+// and up to 16 FN columns; its eight wavefronts are RG of rows by KG of the inner dimension, of which
 // KG blocks of 128 make a step.  A step's operands go to LDS through NB buffers, whole
 // rows' 128 bytes by eight lanes each: read straight into MFMA operands, 16 neighbouring
 // lanes would ask for 16 different lines (64 columns of 8192 x 4096: 19 us so, 15
 // by way of LDS, both with wide products).  The KG sums meet in LDS, in a fixed order.
 template <int TA, int TB, bool WIDE, bool AROW, int RG, int FN>
 struct Few8 {
-  static constexpr int KG = 8 / RG, ROWS = RG + FN;  // sixteens of rows in a block's tile
+  static constexpr int KG = 8 / RG, COLS = 16 * FN, ROWS = RG + FN;  // sixteens of rows in a block's tile
   static constexpr int TILE = ROWS * 2048, STAGE = KG * TILE + 8 * 256;
   static constexpr int LOADS = ROWS * 2 / RG + 1;  // of a wavefront in a step
   static constexpr int NB = 150 * 1024 / STAGE < 4 ? 150 * 1024 / STAGE : 4;
@@ -521,16 +522,16 @@ struct Few8 {
   static __device__ __forceinline__ void run(const Scaled8& g, char* smem) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int kg = wave / RG, rg = wave % RG, m0 = blockIdx.x * 16 * RG;
+    const int kg = wave / RG, rg = wave % RG, m0 = blockIdx.x * 16 * RG, n0 = blockIdx.y * 16 * FN;
     const int steps = (((g.q + 127) >> 7) + KG - 1) / KG;
     // the loads of this wavefront's block, which its RG wavefronts share out
     const uint8_t* pa = g.A.p + (long)m0 * g.A.ld + kg * 128;
-    const uint8_t* pb = g.B.p + kg * 128;
+    const uint8_t* pb = g.B.p + (long)n0 * g.B.ld + kg * 128;
     const int len = (g.q + 15) / 16 * 16 - kg * 128;
-    int reca = (min(g.m - m0, 16 * RG) - 1) * (int)g.A.ld + len, recb = (g.n - 1) * (int)g.B.ld + len;
+    int reca = (min(g.m - m0, 16 * RG) - 1) * (int)g.A.ld + len, recb = (min(g.n - n0, 16 * FN) - 1) * (int)g.B.ld + len;
     const bool a = rg == 0;  // which scales
     const int srow = a ? min(m0 + lane, g.m - 1) >> g.A.shift : 0;
-    const int scol = min(lane, g.n - 1);
+    const int scol = min(n0 + lane, g.n - 1);
     const int past = (g.q - 1) >> 7;  // the last block
     int issued = 0;
     auto issue = [&]() {
@@ -552,7 +553,7 @@ struct Few8 {
       const float* s = RG > 1 ? (a ? g.A.s + srow * g.A.srow + b * g.A.sblock : g.B.s + scol * g.B.srow + b * g.B.sblock)
                               : (lane < 32 ? g.A.s + (min(m0 + (lane & 15), g.m - 1) >> g.A.shift) * g.A.srow +
                                                  b * g.A.sblock
-                                           : g.B.s + min(lane - 32, g.n - 1) * g.B.srow + b * g.B.sblock);
+                                           : g.B.s + min(n0 + lane - 32, g.n - 1) * g.B.srow + b * g.B.sblock);
       __builtin_amdgcn_global_load_lds(
           (const __attribute__((address_space(1))) void*)s,
           (__attribute__((address_space(3))) void*)(smem + issued % NB * STAGE + KG * TILE + wave * 256), 4, 0, 0);
@@ -624,9 +625,9 @@ struct Few8 {
       v4f v = sums[(i * FN + j) * 64 + l];
 #pragma unroll
       for (int w = 1; w < KG; ++w) v += sums[((w * RG + i) * FN + j) * 64 + l];
-      const int col = j * 16 + (l & 15), row = m0 + i * 16 + 4 * (l >> 4);
+      const int col = n0 + j * 16 + (l & 15), row = m0 + i * 16 + 4 * (l >> 4);
       if (col >= g.n) continue;
-      const long to = col * g.ldc + row;
+      const long to = (long)col * g.ldc + row;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (row + r >= g.m) break;
@@ -671,7 +672,7 @@ __global__ __launch_bounds__(256) void turn_scales_kernel(const float* src, long
     if (b + k < blocks) dst[(long)(b + k) * rows + r] = v[k];
 }
 
-constexpr int FEW8_COLS = 64;
+constexpr int FEW8_COLS = 64;  // of one block
 
 hipError_t join(const Scaled8& g, int parts, hipStream_t st) {
   join_parts_kernel<<<dim3(g.n, (g.m + 1023) / 1024), 256, 0, st>>>(g, parts);
@@ -709,38 +710,83 @@ hipError_t few_kernel(const Scaled8& g, int rows, hipStream_t st) {
   static std::atomic<uint64_t> known{0};
   const hipError_t e = allow_lds((const void*)kernel, Few::SMEM, known);
   if (e != hipSuccess) return e;
-  kernel<<<(g.m + rows - 1) / rows, 512, Few::SMEM, st>>>(g);
+  kernel<<<dim3((g.m + rows - 1) / rows, (g.n + Few::COLS - 1) / Few::COLS), 512, Few::SMEM, st>>>(g);
   return hipGetLastError();
 }
 
-// 32 rows a block where that leaves a block for every compute unit, or where
-// LDS has no room for the columns of eight blocks.
+// How a product is worked out.
+enum class Way {
+  FEW,     // up to 64 columns: blocks of 16 or 32 rows
+  FEW32,   // blocks of 32 rows and 64 columns
+  FEW64,   // blocks of 64 rows and 64 columns
+  TILES,   // 128 x 128
+  BIG,     // 256 x 256, wide products 256 x 128
+};
+
+// Above 64 columns: what takes the least time by measured costs, in us, where a unit is a
+// block at once on each of the 256 compute units (TILES: two, the second one at 0.57).
+//   FEW32   2 and, a round of units, 1.9 and 0.73 a step of four slices
+//   FEW64   2 and 2.8 and 0.57 a step of two slices
+//   TILES   3.3 and 0.72 a slice, 0.57 more for every further unit; for parts of the inner
+//           dimension 4 and their sums written and read at 4 TB/s
+//   BIG     5 and 1.8 a slice
+// Measured, of 4096 x 4096, FEW32 / FEW64 / TILES / BIG: 128 columns 9.7 / 13.4 / 17.3 (4 parts) / 49,
+// 200 of them 17.5 / 13.6 / 20 / 49, 512 of them 33 / 26 / 27 / 51; 2048 columns of 4096 x 4096
+// 131 / 98 / 43 / 53; 1000 columns of 16384 x 4096 - / 209 / 86 / 62.
+// Wide products take 1.5 to 1.9 times as long each way, so the choice is the same but for further
+// units of TILES, which cost them as much as the first: 1000 columns of 8192 x 4096 81 by those, 63 by BIG.
+Way way_of(int m, int n, int q, int* parts) {
+  *parts = 1;
+  if (n <= FEW8_COLS) return Way::FEW;
+  const auto per = [](long a, long b) { return (a + b - 1) / b; };
+  const auto units = [&](int rows, int cols, long p) { return (double)per(per(m, rows) * per(n, cols) * p, 256); };
+  const long slices = per(q, 128);
+  Way way = Way::FEW32;
+  double best = 2.0 + units(32, 64, 1) * (1.9 + 0.73 * (double)per(slices, 4));
+  const auto offer = [&](double t, Way w, long p) {
+    if (t >= best) return;
+    best = t;
+    way = w;
+    *parts = (int)p;
+  };
+  offer(2.0 + units(64, 64, 1) * (2.8 + 0.57 * (double)per(slices, 2)), Way::FEW64, 1);
+  for (long p = 1; p <= 16 && p * 2 <= std::max(2L, slices); ++p) {
+    const long each = per(slices, p);
+    const double sums = p > 1 ? 4.0 + (double)p * m * n * 8.0 / 4e6 : 0.0;
+    offer(3.3 + (0.15 + 0.57 * units(128, 128, p)) * (double)each + sums, Way::TILES, per(slices, each));  // (no empty part)
+  }
+  offer(5.0 + 1.8 * units(256, 256, 1) * (double)slices, Way::BIG, 1);
+  return way;
+}
+
+// Few columns: 32 rows a block where that leaves a block for every compute unit, or where
+// LDS has no room for the columns of eight blocks of the inner dimension.
 template <int TA, int TB, bool WIDE, bool AROW>
-hipError_t few_columns(const Scaled8& g, hipStream_t st) {
+hipError_t few_columns(const Scaled8& g, Way way, hipStream_t st) {
   const bool two = g.m >= 32 * 256;
-  if (g.n <= 32)
-    return two ? few_kernel<Few8<TA, TB, WIDE, AROW, 2, 2>>(g, 32, st)
-               : few_kernel<Few8<TA, TB, WIDE, AROW, 1, 2>>(g, 16, st);
-  return few_kernel<Few8<TA, TB, WIDE, AROW, 2, 4>>(g, 32, st);
+  if (way == Way::FEW64) return few_kernel<Few8<TA, TB, WIDE, AROW, 4, 4>>(g, 64, st);
+  if (g.n > 32) return few_kernel<Few8<TA, TB, WIDE, AROW, 2, 4>>(g, 32, st);
+  return two ? few_kernel<Few8<TA, TB, WIDE, AROW, 2, 2>>(g, 32, st) : few_kernel<Few8<TA, TB, WIDE, AROW, 1, 2>>(g, 16, st);
 }
 
 template <int TA, int TB, bool AROW>
-hipError_t launch_few(const Scaled8& g, hipStream_t st) {
+hipError_t launch_few(const Scaled8& g, Way way, hipStream_t st) {
   if (g.n <= 16)
     return g.m >= 32 * 256 ? few_kernel<Few8<TA, TB, true, AROW, 2, 1>>(g, 32, st)
                            : few_kernel<Few8<TA, TB, true, AROW, 1, 1>>(g, 16, st);
-  return g.ctype == OZGEMM_F32 ? few_columns<TA, TB, true, AROW>(g, st) : few_columns<TA, TB, false, AROW>(g, st);
+  return g.ctype == OZGEMM_F32 ? few_columns<TA, TB, true, AROW>(g, way, st) : few_columns<TA, TB, false, AROW>(g, way, st);
 }
-
-bool big_tiles(int m, int n) { return n > FEW8_COLS && (long)((m + 255) / 256) * ((n + 255) / 256) >= 128; }
 
 template <int TA, int TB, bool AROW>
 hipError_t launch_kind(const Scaled8& g, hipStream_t st) {
   if (g.q == 0) return join(g, 0, st);
-  if (g.n <= FEW8_COLS) return launch_few<TA, TB, AROW>(g, st);
+  int parts;
+  const Way way = way_of(g.m, g.n, g.q, &parts);
+  if (way <= Way::FEW64) return launch_few<TA, TB, AROW>(g, way, st);
   const bool wide = g.ctype == OZGEMM_F32;
   hipError_t e;
-  if (big_tiles(g.m, g.n))
+  const bool more = (long)((g.m + 127) / 128) * ((g.n + 127) / 128) > 256;
+  if (way == Way::BIG || (wide && more && parts == 1))
     e = wide ? launch_tiles<TA, TB, true, AROW, 256, 128, 4>(g, st) : launch_tiles<TA, TB, false, AROW, 256, 256, 2>(g, st);
   else
     e = wide ? launch_tiles<TA, TB, true, AROW, 128, 128, 2>(g, st) : launch_tiles<TA, TB, false, AROW, 128, 128, 2>(g, st);
@@ -754,26 +800,16 @@ hipError_t launch_types(const Scaled8& g, hipStream_t st) {
 
 }  // namespace
 
-// Parts that take the least time by measured costs of 128 x 128 tiles, two of them
-// on a compute unit (2048 x 2048 x 4096: 31 us; the sums of the parts 6.6 us for 3 of
-// 2049 x 1001): 0.72 us a slice, and for parts 4 us and their sums written and read at 4 TB/s.
 int scaled_parts(int m, int n, int q) {
-  if (n <= FEW8_COLS || q == 0 || big_tiles(m, n)) return 1;
-  const long tiles = (long)((m + 127) / 128) * ((n + 127) / 128), blocks = (q + 127) / 128;
-  double best = 0;
-  long parts = 1;
-  for (long p = 1; p <= 16 && p * 2 <= std::max(2L, blocks); ++p) {
-    const long each = (blocks + p - 1) / p, rounds = (tiles * p + 511) / 512;
-    const double t = 0.72 * (double)(rounds * each) + (p > 1 ? 4.0 + (double)p * m * n * 8.0 / 4e6 : 0.0);
-    if (p == 1 || t < best) {
-      best = t;
-      parts = (blocks + each - 1) / each;  // none of them empty
-    }
-  }
-  return (int)parts;
+  int parts;
+  way_of(m, n, q, &parts);
+  return parts;
 }
 
-bool scaled_big(int m, int n) { return big_tiles(m, n); }
+bool scaled_big(int m, int n, int q) {
+  int parts;
+  return way_of(m, n, q, &parts) == Way::BIG;
+}
 
 hipError_t launch_turn_scales(const float* src, long srow, long sblock, int rows, int q, float* dst, hipStream_t st) {
   const int blocks = (q + 127) / 128;

@@ -38,7 +38,7 @@ struct Rooms {
 // (3 us), which pays where many tiles read them (8192 x 8192 x 4096: 288 us as
 // they lie, 250 so).
 bool turns(const Scales& s, int m, int n, int q) {
-  return s.per == 1 && s.srow != 1 && s.rows > 1 && q > BLOCK8 && scaled_big(m, n);
+  return s.per == 1 && s.srow != 1 && s.rows > 1 && q > BLOCK8 && scaled_big(m, n, q);
 }
 
 Rooms rooms(int m, int n, int q, const void* A, int lda, const Scales& sa, const void* B, int ldb,
