@@ -7,6 +7,11 @@
 // chunks; a block sums one in FP64 (squares of the 16- and 32-bit types are
 // exact there) into a place of its own, and one block adds those up in a
 // fixed order.
+//
+// Bound by HBM: 48 arrays of BF16, 957 MB together, 193 us for the norm (5.0 TB/s) and
+// 345 us for the scaling (5.5 TB/s); nothing can be scaled before all of it is read, and
+// the caches hold a quarter of it at best: going through the arrays backwards the second time
+// gained nothing.  40 small ones: 5.5, 1.7 and 8 us in three launches.
 #include <algorithm>
 #include <vector>
 

@@ -119,6 +119,14 @@ __device__ __forceinline__ v4u8 first_bytes(int left) {
 // every wavefront has then read the slice, whose buffer the loads of the slice
 // after the next go to, and the next slice, asked for a slice's time ago, has landed.
 // The stream of slices runs on over the tiles' ends.
+//
+// Measured: 8192 x 8192 x 4096 narrow 245 to 260 us, the matrix cores busy for 51% of the cycles at
+// 2.0 GHz; LDS is written and read for about as many, and the rest goes by between them.
+// 4096 x 4096 x 8192 wide 284 us with scales for every row of both, 239 where 128 rows
+// share one: the conversions to half precision and the scaling take more issue slots than
+// the products.  Accumulating by the scaled form of the instruction (for scales that are
+// powers of two) took 6% less at best, two groups of wavefronts in turn at
+// products and scaling more than this.
 template <int TA, int TB, bool WIDE, bool AROW, int BM, int BN, int WM, int WN>
 struct Tile8 {
   static constexpr int NW = WM * WN, THREADS = NW * 64;
