@@ -218,3 +218,49 @@ def test_whole_numbers_over_large_tiles(n, q, m, rows):
     for a, b in ((xs, ws), (xs.contiguous(), ws.contiguous())):
         for t in (torch.float32, torch.bfloat16):
             assert torch.equal(oz.scaled_linear(x, a, w, b, out_dtype=t), want.to(t))
+
+
+def test_offsets_past_32_bits():
+    # 1024 rows over and over: every piece of a result is the first one's, bit by bit
+    times, rows, q, m = 1075, 1024, 4096, 2100
+    n = times * rows
+    g = torch.Generator(device="cuda").manual_seed(6)
+    base = torch.randn(rows, q, generator=g, device="cuda").bfloat16()
+    X = base.repeat(times, 1)
+    assert X.numel() > 2 ** 32
+
+    def again(t, first, dim=0):
+        t = t.view(torch.uint8) if t.dtype == E4M3 else t
+        first = first.view(torch.uint8) if first.dtype == E4M3 else first
+        size = first.shape[dim]
+        return all(torch.equal(t.narrow(dim, k * size, size), first) for k in range(t.shape[dim] // size))
+
+    V, S, Vt, St = oz.quantize_blocks(X, both=True)
+    v, s, vt, st = oz.quantize_blocks(base, both=True)
+    assert again(V, v) and again(S, s) and again(Vt, vt, 1) and again(St, st, 1)
+    del Vt, St
+    w, ws = oz.quantize_blocks(torch.randn(m, q, generator=g, device="cuda"), rows=128)
+    Y = oz.scaled_linear(V, S, w, ws)
+    assert Y.numel() * 2 > 2 ** 32
+    check_product(Y[:rows], v, s, w, ws, 128, False)
+    assert again(Y, Y[:rows])
+    del Y
+    few = oz.scaled_linear(v[:3], s[:3], V, S)  # as weights
+    check_product(few[:, :rows], v[:3], s[:3], v, s, 1, True)
+    assert again(few, few[:, :rows], 1)
+    del V, S, few
+    gain = torch.randn(q, generator=g, device="cuda")
+    V, S, _ = oz.rms_norm_quantized(X, gain)
+    v, s, _ = oz.rms_norm_quantized(base, gain)
+    assert again(V, v) and again(S, s)
+    del V, S
+    dX, _ = oz.rms_norm_grads(X, X, gain)
+    assert again(dX, oz.rms_norm_grads(base, base, gain)[0])
+    norm = oz.clip_gradients([X], 1.0, out=[dX])
+    want = math.sqrt(times * base.double().square().sum().item())
+    assert abs(norm.item() - want) <= 1e-13 * want
+    assert again(dX, dX[:rows])
+    want = base.double() * (1 / (want + 1e-6))
+    assert ((dX[:rows].double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.01 * 2.0 ** -24)).all()
+    del X, dX
+    torch.cuda.empty_cache()
