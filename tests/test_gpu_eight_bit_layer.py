@@ -264,3 +264,36 @@ def test_offsets_past_32_bits():
     assert ((dX[:rows].double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.01 * 2.0 ** -24)).all()
     del X, dX
     torch.cuda.empty_cache()
+
+
+def test_operands_and_scales_that_lie_otherwise():
+    g = torch.Generator(device="cuda").manual_seed(9)
+
+    def eight(*s):
+        return torch.randn(*s, generator=g, device="cuda").to(E4M3)
+
+    def same_as_contiguous(x, xs, w, ws, **kw):
+        want = oz.scaled_linear(x.contiguous(), xs.contiguous(), w.contiguous(), ws.contiguous(), **kw)
+        assert torch.equal(oz.scaled_linear(x, xs, w, ws, **kw), want)
+
+    xs, ws = (torch.rand(n, 5, generator=g, device="cuda") + 0.5 for n in (300, 4))
+    x, w = eight(600, 300).t(), eight(400, 600)
+    for t in (torch.float32, torch.bfloat16):
+        same_as_contiguous(x, xs, w, ws, out_dtype=t)
+        same_as_contiguous(x, xs, w[:1].expand(400, 600), ws, out_dtype=t)  # one row of weights for all
+        same_as_contiguous(x, xs[:1, :1].expand(300, 5), w, ws, out_dtype=t)  # one scale for all
+        same_as_contiguous(x, torch.rand(5, 300, generator=g, device="cuda").t(), w, ws[:, :1].expand(4, 5), out_dtype=t)
+        same_as_contiguous(x[:2], xs[:2], w, xs[0].expand(400, 5), out_dtype=t)
+    big, one = eight(4000, 608)[:, :600], torch.full((1, 1), 0.25, device="cuda").expand(4000, 5)
+    same_as_contiguous(big, one, big, one)  # tiles whose scales are turned over first
+    same_as_contiguous(big, torch.rand(4000, 10, generator=g, device="cuda")[:, ::2], big, one)
+
+
+def test_serving_in_inference_mode():
+    with torch.inference_mode():
+        layer = Layer(5, 512, 512, 3)
+        z, zs, H = oz.rms_norm_quantized(layer.X, layer.gain, layer.R, H=layer.R)
+        assert H is layer.R
+        check_product(oz.scaled_linear(z, zs, *layer.blocks[:2]), z, zs, *layer.blocks[:2], 128, True)
+        grads = [torch.ones(100, device="cuda")]
+        assert oz.clip_gradients(grads, 5.0).item() == 10 and (grads[0] - 0.5).abs().max() <= 1e-6
