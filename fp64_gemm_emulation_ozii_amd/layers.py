@@ -352,7 +352,8 @@ def clip_gradients(grads, max_norm: float, norm=None, eps: float = 1e-6, out=Non
 
     The host waits for nothing.  Entries are multiplied in float32 (float64 ones
     in float64) and rounded once; where the factor is 1 they stay as they are.  A norm of
-    Inf makes finite entries 0 and infinite ones NaN, one of NaN makes all of them NaN.
+    Inf makes finite entries 0 and infinite ones NaN, one of NaN makes all of them NaN
+    (as do ``max_norm`` and ``norm + eps`` both 0 or both Inf).
     ``out``, tensors of the same shapes and types, receives the products instead.
     No two of the tensors that are written may share memory.
     """

@@ -116,7 +116,8 @@ def check_product(got, x, xs, w, ws, rows, wide):
 
 PRODUCTS = [(1, 128, 16), (1, 4096, 1000), (5, 130, 33), (16, 1, 1), (17, 100, 129), (33, 257, 31), (64, 2048, 512),
             (65, 128, 128), (100, 1531, 77), (128, 64, 300), (200, 8192, 130), (300, 16, 257), (512, 500, 4100),
-            (1001, 1531, 2049), (3000, 260, 3000), (100, 300, 2000), (200, 1100, 4001), (1000, 1000, 1000), (4097, 700, 3333)]
+            (1001, 1531, 2049), (3000, 260, 3000), (100, 300, 2000), (200, 1100, 4001), (1000, 1000, 1000), (4097, 700, 3333),
+            (3000, 200, 1), (2000, 600, 17), (70, 1, 70), (65, 2000, 5000)]
 
 
 @pytest.mark.parametrize("rows", [1, 128])
