@@ -19,6 +19,9 @@ bool known8(int type) { return type == OZGEMM_E4M3 || type == OZGEMM_E5M2; }
 // behind the row, inside the same aligned 16 bytes.
 bool aligned8(const void* p, long ld) { return ((uintptr_t)p & 15) == 0 && ld % 16 == 0 && ld <= LD8_MAX; }
 
+// The leading dimension of rows of q entries; one row alone has none, and takes that of rows laid out here.
+long ld8(int rows, long ld, int q) { return rows == 1 ? (long)up(q, 16) : ld; }
+
 // How the scales of one operand lie.
 struct Scales {
   int rows, per;
@@ -47,8 +50,8 @@ Rooms rooms(int m, int n, int q, const void* A, int lda, const Scales& sa, const
   r.parts = 1;
   if (m < 1 || n < 1 || q < 1) return r;
   r.ld = (long)up(q, 16);
-  r.a = !aligned8(A, lda);
-  r.b = !aligned8(B, ldb);
+  r.a = !aligned8(A, ld8(m, lda, q));
+  r.b = !aligned8(B, ld8(n, ldb, q));
   r.sa = turns(sa, m, n, q);
   r.sb = turns(sb, m, n, q);
   const size_t blocks = (size_t)(q + BLOCK8 - 1) / BLOCK8;
@@ -126,8 +129,8 @@ int ozgemm_scaled_gemm(int atype, int btype, int ctype, int m, int n, int q, con
   hipStream_t st = (hipStream_t)hip_stream;
   char* ws = (char*)workspace;
   Scaled8 g{};
-  g.A = Operand8{(const uint8_t*)A, lda, SA, (long)sarow, (long)sablock, rows_a == 1 ? 0 : 7};
-  g.B = Operand8{(const uint8_t*)B, ldb, SB, (long)sbrow, (long)sbblock, 0};
+  g.A = Operand8{(const uint8_t*)A, ld8(m, lda, q), SA, (long)sarow, (long)sablock, rows_a == 1 ? 0 : 7};
+  g.B = Operand8{(const uint8_t*)B, ld8(n, ldb, q), SB, (long)sbrow, (long)sbblock, 0};
   g.atype = atype;
   g.btype = btype;
   g.m = m;

@@ -607,7 +607,7 @@ int ozgemm_quantize_blocks(int type, int qtype, int rows, int n, int q, const vo
  * NaN anywhere in a row makes the outputs it touches NaN.
  *
  * Operands are read in place where they begin on 16-byte boundaries and their
- * leading dimension is a multiple of 16 up to 2^22 (then as whole aligned 16-byte
+ * leading dimension, unless they have one row, is a multiple of 16 up to 2^22 (then as whole aligned 16-byte
  * pieces, of which the last of a row may reach past q: read and not used);
  * others pass through the workspace, as do the scales of large products whose srow
  * is not 1.  Few tiles with a long inner dimension are

@@ -213,6 +213,16 @@ def test_scaled_gemm_workspace():
     assert room(128, 128, 1 << 20, 0, 1 << 20, 128, 1 << 13, 1, 0, 1 << 20, 1, 128) >= 2 * 128 * 128 * 4
 
 
+def test_one_row_needs_no_leading_dimension():
+    room = L.ozgemm_scaled_gemm_workspace_bytes
+    for ld in (1531, 1540, (1 << 22) + 16, 1 << 30):  # never used
+        assert room(8192, 1, 1531, 0, 1536, 128, 12, 1, 0, ld, 1, 1) == 0
+        assert room(1, 1, 1531, 0, ld, 1, 12, 1, 0, 1531, 1, 1) == 0
+    assert room(8192, 1, 1531, 0, 1536, 128, 12, 1, 8, 1536, 1, 1) == 1536  # off the 16-byte grid
+    assert room(8192, 2, 1531, 0, 1536, 128, 12, 1, 0, 1531, 1, 2) == 3072  # two rows
+    assert room(1, 0, 1531, 0, 1531, 1, 12, 1, 0, 1531, 1, 1) == 0 and room(0, 1, 1531, 0, 1531, 1, 12, 1, 0, 1531, 1, 1) == 0
+
+
 @no_gpu_only
 def test_norm_arguments():
     big = L.OZGEMM_MAX_ROWS

@@ -164,6 +164,20 @@ def odd_rows(v):
 
 
 @pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("n, q, m", [(1, 1531, 8192), (1, 1, 40), (1, 130, 9000), (100, 1531, 1), (1, 77, 1), (3000, 517, 1)])
+def test_one_row_of_any_length(n, q, m, t):
+    # a row alone, its leading dimension its length: in place, NaN behind it in its last 16 bytes
+    g = gen(n + q)
+    x, w = (torch.randint(-8, 9, s, generator=g, device="cuda").float() for s in ((n, q), (m, q)))
+    xs, ws = (torch.rand(s.shape[0], -(-q // 128), generator=g, device="cuda") + 0.5 for s in (x, w))
+    rows = [aligned(v, E4M3, float("nan")) for v in (x, w)]
+    alone = [v.as_strided(v.shape, (q, 1)) if v.shape[0] == 1 else v for v in rows]
+    got = oz.scaled_linear(alone[0], xs, alone[1], ws, out_dtype=TYPES[t])
+    check_product(got, x, xs, w, ws, 1, t == "f32" or n <= 16)
+    assert torch.equal(got, oz.scaled_linear(odd_rows(x.to(E4M3)), xs, odd_rows(w.to(E4M3)), ws, out_dtype=TYPES[t]))
+
+
+@pytest.mark.parametrize("t", list(TYPES))
 @pytest.mark.parametrize("n", [3, 300])
 def test_sums_of_gaussian_entries_keep_their_digits(n, t):
     # the 8-bit matrix cores are off by 1.5e-5 of the sums' norm; twice that, and the result's own rounding
