@@ -114,11 +114,18 @@ def scaled_linear(X, xs, W, ws, out=None, out_dtype=None):
     every row and 128 columns, W [m, q] with those or one for every 128 x 128 tile,
     Y [n, m] in bfloat16 (``out_dtype``: float16 or float32).
 
-    Values are either 8-bit type; scales are any float32.  Rows on 16-byte
-    boundaries are read in place, others from a copy.  float32 results, and those
-    of up to 16 rows of X, are summed in float32; of others a block's 128 products
-    are summed by the 8-bit matrix cores, which is off by 1.5e-5 of the sums' norm,
-    and blocks in float32.  ``out`` must not overlap the operands.
+    Values are either 8-bit type; scales are any float32, and so must be the product of a
+    row's of X and one of W, which is taken first (1e20 and 1e20 make NaN of a block of zeros).
+    Rows on 16-byte boundaries are read in place, others from a copy.  ``out`` must not overlap the operands.
+
+    float32 results, and those of up to 16 rows of X, are summed in float32.  Of others a
+    block's 128 products are summed by the 8-bit matrix cores, which drop what lies below
+    2^-13 of the largest product next to it, and blocks in float32.  Over all results that
+    is 1.5e-5 of their norm for gaussian entries and 4.6e-5 where one column of X in a
+    hundred is 21 times larger (float16 rounds to 2.1e-4, bfloat16 to 1.7e-3); it is not bounded relative
+    to a single result whose products cancel, for which ``out_dtype=torch.float32`` is there.
+    A row's last bits depend on how many rows come with it: of those two ways, and
+    by the order of sums, which follows the sizes.
     """
     _eight(X.dtype, "scaled_linear")
     _eight(W.dtype, "scaled_linear")

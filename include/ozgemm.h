@@ -600,10 +600,15 @@ int ozgemm_quantize_blocks(int type, int qtype, int rows, int n, int q, const vo
  * Sums.  OZGEMM_F32 results: products are exact and everything is summed in
  * FP32.  BF16 and F16 results of more than 16 columns: the 128 products of a
  * block are summed by the 8-bit matrix cores, which keep of each term what lies
- * above 2^-13 of the largest of the terms next to it (an error of 1.5e-5 of the
- * sums' norm for gaussian entries; F16 rounds to 2e-4, BF16 to 1.7e-3); blocks
- * are scaled and added in FP32.  16 columns and fewer: as F32.  Results are
- * rounded once, to nearest-even, and do not depend on the order of blocks.
+ * above 2^-13 of the largest of the 32 terms next to it; blocks are scaled and
+ * added in FP32.  What goes so is measured by the terms, not by their sum: over
+ * a matrix of results 1.5e-5 of its norm for gaussian entries, 4.6e-5 with one
+ * column of B's in a hundred 21 times larger, 8.6e-5 with it 301 times larger (F16
+ * rounds to 2.1e-4, BF16 to 1.7e-3), and without a bound relative to a result
+ * whose terms cancel.  F32 results do not lose it.  16 columns and fewer: as F32,
+ * so a column's results have other last bits in a call of 16 columns than of 17 (and by
+ * the order of sums, which follows m, n and q, elsewhere too).  Results are rounded
+ * once, to nearest-even, and the same call gives the same bits.
  * NaN anywhere in a row makes the outputs it touches NaN.
  *
  * Operands are read in place where they begin on 16-byte boundaries and their

@@ -190,6 +190,85 @@ def test_sums_of_gaussian_entries_keep_their_digits(n, t):
     assert off <= (1e-6 if t == "f32" else 3e-5 + torch.finfo(TYPES[t]).eps / 2)
 
 
+# The k of a block that one lane holds, of each of the four that share a result.
+LANES = [[*range(16 * h, 16 * h + 16), *range(64 + 16 * h, 80 + 16 * h)] for h in range(4)]
+
+
+def dropped(x, xs, w, ws, rows):
+    """What the sums lose where every product of a lane loses what lies below 2^-13 of the lane's largest."""
+    lost = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64, device=x.device)
+    per = ws.double() if rows == 1 else ws.double().repeat_interleave(128, 0)[:w.shape[0]]
+    for b in range(xs.shape[1]):
+        for lane in LANES:
+            k = torch.tensor(lane, device=x.device) + 128 * b
+            k = k[k < x.shape[1]]
+            p = x[:, None, k].double() * w[None, :, k].double()
+            most = p.abs().amax(-1, keepdim=True)
+            cut = torch.where(most == 0, 1.0, torch.exp2(torch.floor(torch.log2(most)) - 13))
+            lost += (p - torch.trunc(p / cut) * cut).sum(-1) * xs[:, b, None].double() * per[None, :, b]
+    return lost
+
+
+def rms(t):
+    return t.double().square().mean().sqrt().item()
+
+
+@pytest.mark.parametrize("far", [1, 21, 301])
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("n, q, m", [(3, 2048, 600), (40, 2048, 600), (130, 2100, 4096), (512, 2048, 4096), (1000, 1531, 1100), (3000, 1024, 3000)])
+def test_sums_of_entries_with_far_columns_keep_their_digits(n, q, m, t, rows, far):
+    # Activations as layers have them: rows of different size, one column in a hundred `far` times larger, scales that are no
+    # powers of two.  The mean square of the error, over 64 x 64 results (3 x 64) spread over all, is at most that of
+    #   the result's own rounding, uniform within a step: step^2 / 12 on average;
+    #   what the 8-bit matrix cores drop, at most what the model above loses (the two are independent);
+    #   float32 sums: 2^-23 of the magnitudes for each of the additions of a block's four parts and of the blocks, sqrt of their number at random.
+    # The square of an error uniform within a step has the variance step^4 (1/80 - 1/144) = step^4 / 180 about its mean, so the mean of
+    # N of them scatters by sqrt(sum of step^4 / 180) / N, more than N alike ones by as much as their steps differ: six times that.
+    g = gen(n + q + far)
+    X = normal(g, n, q) * torch.exp(0.3 * normal(g, n, 1)) * (1 + (far - 1) * (torch.rand(1, q, generator=g, device="cuda") < 0.01))
+    x, xs = oz.quantize_blocks(X)
+    w, ws = oz.quantize_blocks(normal(g, m, q) / q ** 0.5, rows=rows)
+    xs, ws = (s * (1 + torch.rand(s.shape, generator=g, device="cuda")) for s in (xs, ws))
+    got = oz.scaled_linear(x, xs, w, ws, out_dtype=TYPES[t])
+    at, to = torch.arange(min(n, 64), device="cuda") * max(1, n // 64), torch.arange(64, device="cuda") * (m // 64)
+    x, xs, w, ws = x.float()[at], xs[at], w.float()[to], ws[to] if rows == 1 else ws[to // 128].contiguous()
+    got = got[at][:, to].double()
+    a, b = value(x, xs, 1), value(w, ws, 1)
+    want = a @ b.T.contiguous()
+    bound = rms(a.abs() @ b.abs().T.contiguous()) ** 2 * (4 + -(-q // 128)) * 2.0 ** -46
+    if t != "f32":
+        step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0 ** -14)))) * torch.finfo(TYPES[t]).eps
+        bound += rms(step) ** 2 / 12 + 6 * rms(step.square()) / (180 * step.numel()) ** 0.5
+        if n > 16:
+            bound += rms(dropped(x, xs, w, ws, 1)) ** 2
+    off = rms(got - want) ** 2
+    assert off <= bound
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("tx, tw", [(E4M3, E4M3), (E5M2, E4M3), (E4M3, E5M2), (E5M2, E5M2)], ids=str)
+@pytest.mark.parametrize("n, q, m", [(1, 300, 70), (9, 4096, 130), (40, 300, 200), (200, 700, 3000), (1000, 513, 1100), (2500, 300, 2500)])
+def test_subnormal_entries_count(n, q, m, tx, tw, rows):
+    # whole multiples of the least subnormal value, up to the second binade of normal ones: products are whole numbers up to 225
+    # of the least product, none of them under 2^-13 of another, and sums stay below 2^24: exact in every way
+    g = gen(n + q + m + 1)
+
+    def least(a, b, t):
+        most, unit = (15, 2.0 ** -9) if t == E4M3 else (7, 2.0 ** -16)
+        k = torch.randint(-most, most + 1, (a, b), generator=g, device="cuda").float()
+        held = aligned(k * unit, t, float("nan"))
+        assert torch.equal(held.float(), k * unit)
+        return held, unit
+
+    (x, ux), (w, uw) = least(n, q, tx), least(m, q, tw)
+    xs, ws = torch.full((n, -(-q // 128)), 1 / ux, device="cuda"), torch.full((-(-m // rows), -(-q // 128)), 1 / uw, device="cuda")
+    want = value(x, xs, 1) @ value(w, ws, rows).T.contiguous()
+    assert want.abs().amax() > 0
+    for t in TYPES.values():
+        assert torch.equal(oz.scaled_linear(x, xs, w, ws, out_dtype=t), want.to(t))
+
+
 @pytest.mark.parametrize("n, m", [(3, 40), (300, 200), (1000, 9000)])
 @pytest.mark.parametrize("t", list(TYPES))
 def test_nan_and_infinities_stay_in_their_rows(n, m, t):
