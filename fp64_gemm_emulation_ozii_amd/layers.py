@@ -327,6 +327,52 @@ def _run(g):
     return g if g.is_contiguous() and not g.is_neg() or _dense(g) and not g.is_neg() else g.resolve_neg().contiguous()
 
 
+_MEET_STEPS = 1 << 14  # of the search below: some 10 ms
+
+
+def _meet(a, b) -> bool:
+    """Whether two tensors with entries have a byte in common, by their strides
+    (True also where that takes too long to find out)."""
+    # Byte u of a's entry i and byte v of b's entry j are one where  a0 + sum i s + u = b0 + sum j t + v.  Counted from the
+    # other end, j and v go to the left side: a sum of positive steps, each up to its number of times, that is to reach `goal`.
+    counts = {1: a.element_size() + b.element_size() - 2}
+    goal = b.data_ptr() - a.data_ptr() + b.element_size() - 1
+    for t, turned in ((a, 0), (b, 1)):
+        for n, s in zip(t.shape, t.stride()):
+            s *= t.element_size()
+            if n > 1 and s > 0:
+                counts[s] = counts.get(s, 0) + n - 1
+                goal += turned * (n - 1) * s
+    steps = sorted(counts, reverse=True)
+    reach = [sum(s * counts[s] for s in steps[k:]) for k in range(len(steps) + 1)]
+    tries = _MEET_STEPS
+
+    def reaches(k, goal):
+        nonlocal tries
+        if k == len(steps):
+            return goal == 0
+        tries -= 1
+        s = steps[k]
+        least, most = max(0, -((reach[k + 1] - goal) // s)), min(counts[s], goal // s)
+        return tries < 0 or any(reaches(k + 1, goal - x * s) for x in range(most, least - 1, -1))
+
+    return 0 <= goal <= reach[0] and reaches(0, goal)
+
+
+def _lie_apart(written, copied) -> None:
+    """Refuses tensors that share memory, of which one at least is written from a
+    copy (``copied``, by their places; of the others the library call sees to it itself)."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size(), k)
+                   for k, t in enumerate(written) if t.numel() > 0)
+    open_spans = []
+    for start, end, k in spans:
+        open_spans = [(e, o) for e, o in open_spans if e > start]
+        for _, o in open_spans:
+            if (k in copied or o in copied) and _meet(written[k], written[o]):
+                raise ValueError("no two of the tensors that are written may share memory, nor one with the norm")
+        open_spans.append((end, k))
+
+
 def gradient_norm(grads):
     """The norm over all entries of ``grads`` (a tensor or several, of float64,
     float32, bfloat16 and float16 together): a float64 tensor of one value on
@@ -378,8 +424,8 @@ def clip_gradients(grads, max_norm: float, norm=None, eps: float = 1e-6, out=Non
         _no_grad("clip_gradients", norm)
     to = grads if out is None else out
     # Runs of memory, entry by entry alike on both sides; others by way of copies.
-    here, there = [], []
-    for g, o in zip(grads, to):
+    here, there, copied = [], [], set()
+    for k, (g, o) in enumerate(zip(grads, to)):
         if g.is_contiguous() and not g.is_neg() and (g is o or o.is_contiguous() and not o.is_neg()):
             here.append(g)
             there.append(o)
@@ -391,6 +437,10 @@ def clip_gradients(grads, max_norm: float, norm=None, eps: float = 1e-6, out=Non
         alike = g.stride() == o.stride() and _dense(g) and not g.is_neg()
         here.append(g if alike else g.resolve_neg().contiguous())
         there.append(o if alike or g is not o and o.is_contiguous() else here[-1] if g is o else torch.empty_like(here[-1]))
+        if there[-1] is not o:
+            copied.add(k)
+    if copied:
+        _lie_apart(to if norm is None else [*to, norm], copied)
     if not grads:
         return gradient_norm(grads) if norm is None else norm
     with _on_device(grads[0].device):

@@ -2,6 +2,7 @@
 ask of a workspace: host checks, no GPU needed."""
 import ctypes
 import os
+import time
 
 import pytest
 import torch
@@ -9,7 +10,7 @@ from torch.autograd import forward_ad
 
 import fp64_gemm_emulation_ozii_amd as oz
 from fp64_gemm_emulation_ozii_amd import ozgemm as L
-from fp64_gemm_emulation_ozii_amd.layers import _dense
+from fp64_gemm_emulation_ozii_amd.layers import _dense, _meet
 
 E4M3 = torch.float8_e4m3fn
 
@@ -221,6 +222,87 @@ def test_one_row_needs_no_leading_dimension():
     assert room(8192, 1, 1531, 0, 1536, 128, 12, 1, 8, 1536, 1, 1) == 1536  # off the 16-byte grid
     assert room(8192, 2, 1531, 0, 1536, 128, 12, 1, 0, 1531, 1, 2) == 3072  # two rows
     assert room(1, 0, 1531, 0, 1531, 1, 12, 1, 0, 1531, 1, 1) == 0 and room(0, 1, 1531, 0, 1531, 1, 12, 1, 0, 1531, 1, 1) == 0
+
+
+ROOM = torch.zeros(4000)
+
+
+def view(size, stride, at=0, dtype=torch.float32):
+    return ROOM.view(dtype).as_strided(size, stride, at)
+
+
+#: (two views of one storage, whether they have an entry in common)
+PAIRS = [((view((10, 20), (40, 2)), view((10, 20), (40, 2))), True), ((view((10, 20), (40, 2)), view((10, 20), (40, 2), 1)), False),
+         ((view((10, 20), (40, 2)), view((10, 20), (40, 2), 42)), True), ((view((10, 20), (40, 2)), view((20, 10), (2, 40), 80)), True),
+         ((view((10, 5), (40, 1)), view((10, 5), (40, 1), 5)), False), ((view((10, 6), (40, 1)), view((10, 6), (40, 1), 5)), True),
+         ((view((10, 5), (40, 1)), view((10, 5), (40, 1), 35)), False), ((view((10, 5), (40, 1)), view((10, 5), (40, 1), 36)), True),
+         ((view((50,), (2,)), view((30,), (3,))), True), ((view((50,), (4,)), view((30,), (6,), 1)), False),
+         ((view((50,), (4,)), view((30,), (6,), 2)), True), ((view((50,), (2,)), view((99,), (1,), 1)), True),
+         ((view((50,), (2,)), view((1,), (1,), 97)), False), ((view((50,), (2,)), view((1,), (1,), 98)), True),
+         ((view((3, 4, 5), (200, 10, 2)), view((3, 4, 5), (200, 10, 2), 40)), False),
+         ((view((3, 4, 5), (200, 10, 2)), view((3, 4, 5), (200, 10, 2), 38)), True),
+         ((view((50,), (2,)), view((20,), (4,), 2, torch.bfloat16)), False), ((view((50,), (2,)), view((20,), (4,), 1, torch.bfloat16)), True),
+         ((view((50,), (2,)), view((10,), (1,), 3000)), False), ((view((0, 5), (2, 40)), view((10, 5), (2, 40))), False)]
+
+
+@pytest.mark.parametrize("pair, shared", PAIRS)
+def test_what_is_written_by_way_of_copies_must_lie_apart_too(pair, shared):
+    # both orders, in place and into `out`; tensors that lie apart get as far as their device
+    for a, b in (pair, pair[::-1]):
+        dense = a.is_contiguous() and b.is_contiguous()
+        assert not dense
+        with pytest.raises(ValueError, match="share memory" if shared else "GPU only"):
+            oz.clip_gradients([a, b], 1.0)
+        with pytest.raises(ValueError, match="share memory" if shared else "GPU only"):
+            oz.clip_gradients([torch.zeros_like(a), torch.zeros(3), torch.zeros_like(b)], 1.0, out=[a, torch.zeros(3), b])
+    for a in pair:
+        if a.numel() > 1 and not a.is_contiguous():
+            with pytest.raises(ValueError, match="share memory"):
+                oz.clip_gradients([a, a], 1.0)
+
+
+def test_sharing_is_what_every_byte_says():
+    def memory(t):
+        at = torch.zeros((), dtype=torch.int64)
+        for n, s in zip(t.shape, t.stride()):
+            at = at[..., None] + torch.arange(n) * s
+        at = at.reshape(-1) * t.element_size() + t.storage_offset() * t.element_size()
+        return {x for k in range(t.element_size()) for x in (at + k).tolist()}
+
+    rng = torch.Generator().manual_seed(3)
+
+    def pick(*choices):
+        return choices[int(torch.randint(len(choices), (), generator=rng))]
+
+    met = 0
+    for _ in range(600):
+        pair = []
+        for _ in range(2):
+            dims = pick(1, 2, 2, 3)
+            size, stride = [pick(1, 2, 3, 4, 7) for _ in range(dims)], [pick(1, 2, 3, 4, 6, 8, 12, 20, 40, 100) for _ in range(dims)]
+            pair.append(view(size, stride, pick(0, 1, 2, 3, 7, 17, 50), pick(torch.float32, torch.bfloat16, torch.float64)))
+        a, b = pair
+        got = _meet(a, b)
+        assert got == _meet(b, a) == bool(memory(a) & memory(b)), (a.shape, a.stride(), b.shape, b.stride())
+        met += got
+    assert 100 < met < 500
+
+
+def test_sharing_that_takes_long_to_find_counts_as_shared():
+    strides = [2 * p for p in (10007, 10009, 10037, 10039, 10061)]
+    a = b = torch.empty(6000000).as_strided([60] * 5, strides)
+    assert _meet(a, b)  # the same
+    start = time.perf_counter()
+    _meet(a, b.as_strided([60] * 5, strides, 1))
+    assert time.perf_counter() - start < 5
+
+
+def test_the_norm_is_not_written_over():
+    norm = torch.zeros(10, dtype=torch.float64)
+    out = [norm[::2]]
+    for k, words in ((4, "share memory"), (5, "GPU only")):
+        with pytest.raises(ValueError, match=words):
+            oz.clip_gradients([torch.zeros(5, dtype=torch.float64)], 1.0, norm=norm[k], out=out)
 
 
 @no_gpu_only

@@ -122,3 +122,22 @@ def test_writing_counts_as_a_change():
         was = t._version, o._version
         oz.clip_gradients([t], 0.5, out=None if k else [o])
         assert (t._version > was[0]) == (k == 1) and (o._version > was[1]) == (k == 0)
+
+
+def test_interleaved_tensors_are_not_shared_memory():
+    t, o = torch.ones(64, 100, device="cuda"), torch.zeros(64, 100, device="cuda")
+    parts = [t[:, ::2], t[:, 1::2]]
+    want = 1.0 / (80.0 + 1e-6)
+    oz.clip_gradients(parts, 1.0, out=[o[:, 1::2], o[:, ::2]])
+    check([o], [torch.ones_like(t)], want)
+    assert (t == 1).all()
+    for out in ([o[:, ::2], o[:, ::2]], [o[:, ::2], o[:, 2::2].as_strided((64, 50), (100, 2), 2)], [o[:, ::2], o.view(-1)[:3200].view(64, 50)]):
+        before = o.clone()
+        with pytest.raises(ValueError, match="share memory"):
+            oz.clip_gradients(parts, 1.0, out=out)
+        assert torch.equal(o, before)
+    with pytest.raises(ValueError, match="share memory"):
+        oz.clip_gradients([t[:, ::2], t[:, :2]], 1.0)
+    assert (t == 1).all()
+    oz.clip_gradients(parts, 1.0)
+    check([t], [torch.ones_like(t)], want)
