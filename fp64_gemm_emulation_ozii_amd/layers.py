@@ -307,9 +307,11 @@ def _gradients(grads, what: str):
         raise ValueError(f"{what}: up to {L.OZGEMM_ARRAYS_MAX} tensors, got {len(grads)}")
     if not grads:
         return grads, [], []
-    strided, device = torch.strided, grads[0].get_device()
+    strided, device = torch.strided, grads[0].get_device() if isinstance(grads[0], torch.Tensor) else -1
     types, sizes = [], []
     for g in grads:
+        if not isinstance(g, torch.Tensor):
+            raise TypeError(f"{what}: a gradient must be a tensor, not {type(g).__name__}")
         if g.layout is not strided:
             raise TypeError(f"{what}: {g.layout} tensors are not supported")
         if g.get_device() != device:
@@ -375,7 +377,7 @@ def _lie_apart(written, copied) -> None:
 
 def gradient_norm(grads):
     """The norm over all entries of ``grads`` (a tensor or several, of float64,
-    float32, bfloat16 and float16 together): a float64 tensor of one value on
+    float32, bfloat16 and float16 together, parameters without a gradient left out): a float64 tensor of one value on
     their device, summed in float64 in a fixed order.
 
     Where a model's gradients are spread over processes, bring their norms
@@ -412,6 +414,8 @@ def clip_gradients(grads, max_norm: float, norm=None, eps: float = 1e-6, out=Non
             raise ValueError(f"out must be {len(grads)} tensors, got {len(out)}")
         device = grads[0].get_device() if grads else -1
         for g, o in zip(grads, out):
+            if not isinstance(o, torch.Tensor):
+                raise TypeError(f"clip_gradients: out must be tensors, not {type(o).__name__}")
             if o.shape != g.shape or o.dtype is not g.dtype or o.get_device() != device or o.layout is not torch.strided:
                 raise ValueError(f"out must be {tuple(g.shape)} of {g.dtype} on {g.device}, got {tuple(o.shape)} of "
                                  f"{o.dtype} on {o.device}")

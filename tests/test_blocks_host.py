@@ -305,6 +305,15 @@ def test_the_norm_is_not_written_over():
             oz.clip_gradients([torch.zeros(5, dtype=torch.float64)], 1.0, norm=norm[k], out=out)
 
 
+@pytest.mark.parametrize("call", [lambda g: oz.gradient_norm(g), lambda g: oz.clip_gradients(g, 1.0),
+                                  lambda g: oz.clip_gradients([torch.zeros(2)] * len(g), 1.0, out=g)])
+@pytest.mark.parametrize("grads", [[None], [torch.zeros(2), None], [None, torch.zeros(2)], [1.0]])
+def test_gradients_that_are_none(call, grads):
+    # a parameter without a gradient has to be left out
+    with pytest.raises(TypeError, match="tensor"):
+        call(grads)
+
+
 @no_gpu_only
 def test_norm_arguments():
     big = L.OZGEMM_MAX_ROWS
