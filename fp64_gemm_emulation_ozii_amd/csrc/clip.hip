@@ -115,8 +115,17 @@ __global__ __launch_bounds__(1024) void join_norm_kernel(const double* sums, lon
   if (threadIdx.x == 0) *norm = sqrt(s);
 }
 
+// A factor's 24 bits for entries of up to 32 bits: x times it is ((x step) f) step, where
+// the step is 1, or 2^-100 for factors below that, which FP32 holds in fewer bits or not at all.
+struct Factor {
+  float f, step;
+  __device__ __forceinline__ explicit Factor(double v)
+      : f((float)(v < 0x1p-100 ? v * 0x1p200 : v)), step(v < 0x1p-100 ? 0x1p-100f : 1.f) {}
+  __device__ __forceinline__ float times(float x) const { return x * step * f * step; }
+};
+
 template <int TYPE>
-__device__ __forceinline__ void scale_chunk(const void* in, void* out, long size, int chunk, float f) {
+__device__ __forceinline__ void scale_chunk(const void* in, void* out, long size, int chunk, Factor f) {
   constexpr int PER = CHUNK_BYTES / Entry<TYPE>::BYTES, STEP = 256 * 8;
   const long at = (long)chunk * PER;
   const int left = (int)min((long)PER, size - at);
@@ -126,7 +135,7 @@ __device__ __forceinline__ void scale_chunk(const void* in, void* out, long size
     v.load(in, at + k, left - k);
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = v.get(i) * f;
+    for (int i = 0; i < 8; ++i) x[i] = f.times(v.get(i));
     v.set(x);
     v.store(out, at + k, left - k);
   }
@@ -140,11 +149,11 @@ __global__ __launch_bounds__(256) void scale_kernel(Table t, const double* norm,
   if (f == 1.0 && t.in[a] == t.out[a]) return;  // x 1 is x
   const int type = t.type[a];
   if (type == OZGEMM_F32) {
-    scale_chunk<OZGEMM_F32>(t.in[a], t.out[a], t.size[a], chunk, (float)f);
+    scale_chunk<OZGEMM_F32>(t.in[a], t.out[a], t.size[a], chunk, Factor(f));
   } else if (type == OZGEMM_BF16) {
-    scale_chunk<OZGEMM_BF16>(t.in[a], t.out[a], t.size[a], chunk, (float)f);
+    scale_chunk<OZGEMM_BF16>(t.in[a], t.out[a], t.size[a], chunk, Factor(f));
   } else if (type == OZGEMM_F16) {
-    scale_chunk<OZGEMM_F16>(t.in[a], t.out[a], t.size[a], chunk, (float)f);
+    scale_chunk<OZGEMM_F16>(t.in[a], t.out[a], t.size[a], chunk, Factor(f));
   } else {
     constexpr int PER = CHUNK_BYTES / 8;
     const double* p = (const double*)t.in[a];

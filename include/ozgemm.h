@@ -677,7 +677,7 @@ int ozgemm_gradient_norm(int count, const int *types, const void *const *in, con
 size_t ozgemm_gradient_norm_workspace_bytes(int count, const int *types, const long long *sizes);
 
 /* out[k] = in[k] min(1, most / (*norm + eps)), most >= 0, eps >= 0: the factor is
- * FP64, rounded to FP32 for arrays other than OZGEMM_F64, whose entries are rounded
+ * FP64, rounded to 24 bits (also below FP32's range) for arrays other than OZGEMM_F64, whose entries are rounded
  * once.  A norm of NaN makes every entry NaN, as do 0 / 0 and Inf / Inf.
  * out[k] may be in[k] (then nothing is read or written where the
  * factor is 1), and must share no memory with any other array or the norm;

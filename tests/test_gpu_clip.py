@@ -141,3 +141,22 @@ def test_interleaved_tensors_are_not_shared_memory():
     assert (t == 1).all()
     oz.clip_gradients(parts, 1.0)
     check([t], [torch.ones_like(t)], want)
+
+
+@pytest.mark.parametrize("bound", [1e30, 1.0, 1e-3, 1e-20])
+@pytest.mark.parametrize("types", [[t] for t in TYPES] + [TYPES], ids=str)
+def test_factors_below_the_range_of_float32(types, bound):
+    # entries up to 3e38 (float64: 1e100) under a small bound: the factor underflows float32, the products do not have to
+    g = torch.Generator(device="cuda").manual_seed(8)
+    grads = []
+    for k, size in enumerate((40, 70000, 9)):
+        t = types[k % len(types)]
+        top = {torch.float64: 1e100, torch.float16: 6e4}.get(t, 3e38)
+        grads.append((torch.rand(size, generator=g, device="cuda", dtype=torch.float64) * top * 10.0 ** -torch.randint(0, 4, (size,), generator=g, device="cuda")).to(t))
+    want = norm_of(grads)
+    out = [torch.full_like(x, 9.0) for x in grads]
+    norm = oz.clip_gradients(grads, bound, out=out)
+    assert abs(norm.item() - want) <= 1e-13 * want
+    check(out, grads, min(1.0, bound / (norm.item() + 1e-6)))
+    if any(t is torch.float32 for t in types) and torch.float64 not in types:
+        assert bound < 1e-3 or any(o.abs().amax() > 0 for o in out)
