@@ -8,10 +8,10 @@
 // exact there) into a place of its own, and one block adds those up in a
 // fixed order.
 //
-// Bound by HBM: 48 arrays of BF16, 957 MB together, 193 us for the norm (5.0 TB/s) and
-// 345 us for the scaling (5.5 TB/s); nothing can be scaled before all of it is read, and
+// Bound by HBM: 48 arrays of BF16, 957 MB together, 196 us for the norm (4.9 TB/s) and
+// 347 us for the scaling (5.5 TB/s); nothing can be scaled before all of it is read, and
 // the caches hold a quarter of it at best: going through the arrays backwards the second time
-// gained nothing.  40 small ones: 5.5, 1.7 and 8 us in three launches.
+// gained nothing.  40 small ones: 5.8, 1.8 and 8.6 us in three launches.
 #include <algorithm>
 #include <vector>
 

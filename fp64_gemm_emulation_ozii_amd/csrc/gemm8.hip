@@ -123,10 +123,12 @@ __device__ __forceinline__ v4u8 first_bytes(int left) {
 // after the next go to, and the next slice, asked for a slice's time ago, has landed.
 // The stream of slices runs on over the tiles' ends.
 //
-// Measured: 8192 x 8192 x 4096 narrow 245 to 260 us, the matrix cores busy for 51% of the cycles at
-// 2.0 GHz; LDS is written and read for about as many, and the rest goes by between them.
-// 4096 x 4096 x 8192 wide 284 us with scales for every row of both, 239 where 128 rows
-// share one: the conversions to half precision and the scaling take more issue slots than
+// Measured: 8192 x 8192 x 4096 narrow 251 to 322 us over twenty calls in a row (290 on average: the clock
+// gives way to the power), 255 over four, the matrix cores busy for 51% of the cycles at 2.0 GHz.
+// Of a wavefront's cycles 38% issue, 32% wait for an issue slot and 30% for loads, LDS or the barrier; of
+// its 390 instructions a slice 32 are products, 179 others of the vector units, 91 scalar.
+// 4096 x 4096 x 8192 wide 290 to 363 us with scales for every row of both (twenty calls; 284 in a shorter run,
+// and 239 there where 128 rows share one): the conversions to half precision and the scaling take more issue slots than
 // the products.  Accumulating by the scaled form of the instruction (for scales that are
 // powers of two) took 6% less at best, two groups of wavefronts in turn at
 // products and scaling more than this.
@@ -796,6 +798,8 @@ hipError_t launch_kind(const Scaled8& g, hipStream_t st) {
   if (way <= Way::FEW64) return launch_few<TA, TB, AROW>(g, way, st);
   const bool wide = g.ctype == OZGEMM_F32;
   hipError_t e;
+  // A second tile of a unit costs wide products as much as the first (way_of), so they go by the larger ones from there
+  // on; scaled_big, which knows no type of results, does not say so, and their scales are read as they lie.
   const bool more = (long)((g.m + 127) / 128) * ((g.n + 127) / 128) > 256;
   if (way == Way::BIG || (wide && more && parts == 1))
     e = wide ? launch_tiles<TA, TB, true, AROW, 256, 128, 4>(g, st) : launch_tiles<TA, TB, false, AROW, 256, 256, 2>(g, st);

@@ -650,7 +650,8 @@ int ozgemm_rms_norm(int type, int ytype, int wtype, int n, int q, const void *X,
  *   dH     the gradient that reaches H from elsewhere; NULL: none
  *   dX     may be dY, H or dH itself (with its leading dimension)
  *   dw     q entries of wtype; NULL: not wanted
- * Statistics of a row are FP64, entries FP32 and rounded once; dw is summed in
+ * Statistics of a row are FP64, entries FP32 and rounded once (rows below 3e-39, whose r with eps = 0 FP32
+ * does not hold, give Inf or NaN); dw is summed in
  * FP32 over every row of a few thousand groups and in FP64 over those, in a fixed
  * order.  n = 0 gives dw = 0.  Errors as above. */
 int ozgemm_rms_norm_grads(int type, int wtype, int n, int q, const void *dY, int lddy, const void *H, int ldh,
