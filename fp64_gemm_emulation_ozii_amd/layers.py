@@ -361,18 +361,55 @@ def _meet(a, b) -> bool:
     return 0 <= goal <= reach[0] and reaches(0, goal)
 
 
+def _meetings(spans):
+    """The pairs of (start, end, what) that overlap."""
+    at = []
+    for start, end, k in sorted(spans, key=lambda span: span[:2]):
+        at = [span for span in at if span[1] > start]
+        for span in at:
+            yield span[2], k
+        at.append((start, end, k))
+
+
+def _row_spans(spans, written):
+    """Where tensors are rows equally far apart, their rows' spans within that distance (a span over its
+    end as two): slices of one matrix, whose whole spans all overlap, come apart so.  Else the spans as they are."""
+    steps = {max((s * written[k].element_size() for n, s in zip(written[k].shape, written[k].stride()) if n > 1), default=0)
+             for _, _, k in spans}
+    step = steps.pop()
+    if steps or step == 0:
+        return spans
+    rows = []
+    for start, end, k in spans:
+        t = written[k]
+        n = max(n for n, s in zip(t.shape, t.stride()) if n > 1 and s * t.element_size() == step)
+        length, at = end - start - (n - 1) * step, start % step
+        if length > step:
+            return spans
+        rows.append((at, min(at + length, step), k))
+        if at + length > step:
+            rows.append((0, at + length - step, k))
+    return rows
+
+
 def _lie_apart(written, copied) -> None:
     """Refuses tensors that share memory, of which one at least is written from a
     copy (``copied``, by their places; of the others the library call sees to it itself)."""
     spans = sorted((t.data_ptr(), t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size(), k)
                    for k, t in enumerate(written) if t.numel() > 0)
-    open_spans = []
-    for start, end, k in spans:
-        open_spans = [(e, o) for e, o in open_spans if e > start]
-        for _, o in open_spans:
-            if (k in copied or o in copied) and _meet(written[k], written[o]):
+    runs, reach = [], 0  # of spans that overlap from one to the next
+    for span in spans:
+        if runs and span[0] < reach:
+            runs[-1].append(span)
+        else:
+            runs.append([span])
+        reach = max(reach, span[1])
+    for run in runs:
+        if len(run) == 1 or copied.isdisjoint(k for _, _, k in run):
+            continue
+        for o, k in _meetings(_row_spans(run, written)):
+            if o != k and (k in copied or o in copied) and _meet(written[k], written[o]):
                 raise ValueError("no two of the tensors that are written may share memory, nor one with the norm")
-        open_spans.append((end, k))
 
 
 def gradient_norm(grads):

@@ -10,7 +10,7 @@ from torch.autograd import forward_ad
 
 import fp64_gemm_emulation_ozii_amd as oz
 from fp64_gemm_emulation_ozii_amd import ozgemm as L
-from fp64_gemm_emulation_ozii_amd.layers import _dense, _meet
+from fp64_gemm_emulation_ozii_amd.layers import _dense, _lie_apart, _meet
 
 E4M3 = torch.float8_e4m3fn
 
@@ -286,6 +286,48 @@ def test_sharing_is_what_every_byte_says():
         assert got == _meet(b, a) == bool(memory(a) & memory(b)), (a.shape, a.stride(), b.shape, b.stride())
         met += got
     assert 100 < met < 500
+
+
+def test_slices_of_one_matrix_are_told_apart_quickly():
+    w = torch.zeros(64, 4096)
+    experts = torch.zeros(16, 512, 8)
+    for parts in (list(w.chunk(2048, 1)), [experts[:, e] for e in range(512)], list(w[:, 1:].chunk(819, 1)),
+                  [v for r in w.chunk(8) for v in r.chunk(256, 1)], [experts[..., k] for k in range(8)]):
+        start = time.perf_counter()
+        _lie_apart(parts, set(range(len(parts))))
+        assert time.perf_counter() - start < 1  # (1000 of them pair by pair: 4 s)
+        for twice in (parts[0], parts[len(parts) // 2], parts[-1]):
+            with pytest.raises(ValueError, match="share memory"):
+                _lie_apart([*parts, twice], {len(parts)})
+            _lie_apart([*parts, twice], set())  # others see to it
+
+
+def test_lists_of_views_are_apart_as_their_bytes_are():
+    rng = torch.Generator().manual_seed(11)
+
+    def pick(*choices):
+        return choices[int(torch.randint(len(choices), (), generator=rng))]
+
+    def memory(t):
+        at = torch.zeros((), dtype=torch.int64)
+        for n, s in zip(t.shape, t.stride()):
+            at = at[..., None] + torch.arange(n) * s
+        return set((at.reshape(-1) + t.storage_offset()).tolist())
+
+    refused = 0
+    for _ in range(400):
+        step = pick(20, 40, 100)
+        views = [view((pick(1, 2, 5), pick(1, 2, 3, 6)), (step if pick(0, 0, 0, 1) == 0 else pick(20, 30), pick(1, 1, 2)), pick(*range(0, 200, 3)))
+                 for _ in range(pick(2, 3, 4))]
+        bytes_of = [memory(v) for v in views]
+        shared = any(a & b for k, a in enumerate(bytes_of) for b in bytes_of[:k])
+        refused += shared
+        if shared:
+            with pytest.raises(ValueError, match="share memory"):
+                _lie_apart(views, set(range(len(views))))
+        else:
+            _lie_apart(views, set(range(len(views))))
+    assert 50 < refused < 350  # both among them
 
 
 def test_sharing_that_takes_long_to_find_counts_as_shared():
