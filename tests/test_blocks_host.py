@@ -220,7 +220,7 @@ def test_one_row_needs_no_leading_dimension():
         assert room(8192, 1, 1531, 0, 1536, 128, 12, 1, 0, ld, 1, 1) == 0
         assert room(1, 1, 1531, 0, ld, 1, 12, 1, 0, 1531, 1, 1) == 0
     assert room(8192, 1, 1531, 0, 1536, 128, 12, 1, 8, 1536, 1, 1) == 1536  # off the 16-byte grid
-    assert room(8192, 2, 1531, 0, 1536, 128, 12, 1, 0, 1531, 1, 2) == 3072  # two rows
+    assert room(8192, 2, 1531, 0, 1536, 128, 12, 1, 0, 1531, 1, 2) == 2 * 1536  # two rows
     assert room(1, 0, 1531, 0, 1531, 1, 12, 1, 0, 1531, 1, 1) == 0 and room(0, 1, 1531, 0, 1531, 1, 12, 1, 0, 1531, 1, 1) == 0
 
 
